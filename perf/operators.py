@@ -283,7 +283,8 @@ def _accept(p, q, drafts, u, count):
     w = units(target - other)
     w = torch.where(w.sum(1, keepdim=True) == 0, units(target), w)
     total = w.sum(1)
-    goal = (u[rows, n].double() * total.double()).to(torch.int64).clamp(max=total - 1)
+    # the tests' numbers are used up: given a rejection they are no longer uniform
+    goal = (u[:, K].double() * total.double()).to(torch.int64).clamp(max=total - 1)
     token = (w.cumsum(1) <= goal[:, None]).sum(1)
     token = torch.where(total > 0, token, -1)
     steps = torch.arange(K1, device=dev)
