@@ -1,0 +1,227 @@
+// gdn_accept.cu -- verification of drafted tokens against the target's
+// probabilities, from given random numbers (speculative sampling).
+//
+// Row b has c_b drafts x_0 .. x_{c-1}, the target's distributions p_0 .. p_K
+// and the drafts' q_0 .. q_{K-1} (without them q_i(x_i) = 1: a lookup's or a
+// greedy draft's certainty):
+//   n      = the first i < c with u_i q_i(x_i) >= p_i(x_i), else c
+//   weight = max(p_n - q_n, 0) if n < c, else p_c;  p_n where that is 0 everywhere
+//   token  = the first j with weight_0 + .. + weight_j > goal
+// The weights are taken in whole units of 2^-40, so that their sums are exact
+// 64-bit integers and do not depend on the order or the split of the work:
+// goal = floor(u_K * total) is the same for every launch shape.  The token has a
+// random number of its own: given a rejection, the tests' ones are no longer
+// uniform.
+//
+// Of B (2K + 1) rows of V probabilities only two rows a request are read, by
+// a cluster of CTAs: each warp sums a contiguous segment, the warps' sums are
+// shared through distributed shared memory, and the CTA that owns the segment
+// with the goal scans it again (from L2) for the token.  Bound by HBM for many
+// requests and by the chain of dependent reads (drafts, their probabilities,
+// the rows, the segment) for few.
+#include <cooperative_groups.h>
+
+#include "gdn_internal.cuh"
+
+namespace gdn {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kWarps = 16;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxCluster = 8;
+constexpr int kUnroll = 8;
+
+// A weight in units of 2^-40; not above 1 and 0 for NaN.
+__device__ __forceinline__ long long units(float x) {
+    return x > 0.f ? __float2ll_rz(fminf(x, 1.f) * 1099511627776.f) : 0ll;
+}
+
+template <typename T>
+struct Row {
+    const T *p, *q;   // q: nullptr if nothing is taken off
+    int drop;         // token whose weight is 0 (the rejected one of a certain draft), or -1
+    __device__ __forceinline__ long long at(int j) const {
+        const float t = ld_f(p + j);
+        const long long w = units(q != nullptr ? t - ld_f(q + j) : t);
+        return j == drop ? 0ll : w;
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ long long segment_sum(const Row<T> &row, int lo, int hi, int lane) {
+    long long s = 0;
+    int j = lo + lane;
+    for (; j + (kUnroll - 1) * 32 < hi; j += kUnroll * 32) {
+        long long w[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) w[i] = row.at(j + i * 32);
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) s += w[i];
+    }
+    for (; j < hi; j += 32) s += row.at(j);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams p) {
+    __shared__ long long seg[kWarps];                 // this CTA's segment sums, read by the cluster
+    __shared__ long long all[kMaxCluster * kWarps];   // the cluster's, in token order
+    __shared__ long long part[kWarps];
+    __shared__ int n_sh;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
+    const int b = blockIdx.x / cs;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int K = p.K, V = p.V;
+    const T *P = reinterpret_cast<const T *>(p.p), *Q = reinterpret_cast<const T *>(p.q);
+    const int32_t *x = p.drafts + (long)b * K;
+    const float *u = p.u + (long)b * (K + 1);
+    int c = K;
+    if (p.count != nullptr) c = min(max(p.count[b], 0), K);
+
+    if (warp == 0) {
+        int n = c;
+        for (int i0 = 0; i0 < c; i0 += 32) {
+            const int i = i0 + lane;
+            bool ok = true;
+            if (i < c) {
+                const int tok = x[i];
+                ok = false;
+                if (tok >= 0 && tok < V) {
+                    const float pt = ld_f(P + ((int64_t)b * (K + 1) + i) * p.ps + tok);
+                    const float qt = Q != nullptr ? ld_f(Q + ((int64_t)b * K + i) * p.qs + tok) : 1.f;
+                    ok = u[i] * qt < pt;
+                } else if (rank == 0) {
+                    atomicOr(p.err, (uint32_t)GDN_DEVERR_BAD_INDEX);
+                }
+            }
+            const unsigned bad = __ballot_sync(0xffffffffu, !ok);
+            if (bad != 0) {
+                n = i0 + __ffs(bad) - 1;
+                break;
+            }
+        }
+        if (lane == 0) n_sh = n;
+    }
+    __syncthreads();
+    const int n = n_sh;
+    Row<T> row;
+    row.p = P + ((int64_t)b * (K + 1) + n) * p.ps;
+    row.q = (n < c && Q != nullptr) ? Q + ((int64_t)b * K + n) * p.qs : nullptr;
+    row.drop = (n < c && Q == nullptr) ? x[n] : -1;
+    const int nseg = cs * kWarps;
+    const int len = (V + nseg - 1) / nseg;
+    const int mine = rank * kWarps + warp;
+    const int lo = min((int64_t)mine * len, (int64_t)V), hi = min(lo + len, V);
+
+    long long total = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        const long long s = segment_sum(row, lo, hi, lane);
+        if (lane == 0) seg[warp] = s;
+        cluster.sync();
+        for (int i = threadIdx.x; i < nseg; i += kThreads) all[i] = cluster.map_shared_rank(seg, i / kWarps)[i % kWarps];
+        cluster.sync();  // every CTA has its copy: seg may be written again, or its CTA end
+        total = 0;
+        for (int i = lane; i < nseg; i += 32) total += all[i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        if (total > 0 || (row.q == nullptr && row.drop < 0)) break;
+        // nothing is left of the target: it is sampled as it is
+        row.q = nullptr;
+        row.drop = -1;
+    }
+
+    int32_t *out = p.tokens + (long)b * (K + 1);
+    if (rank == 0) {
+        for (int i = threadIdx.x; i <= K; i += kThreads)
+            if (i != n || total == 0) out[i] = i < n ? x[i] : -1;
+        if (threadIdx.x == 0) p.emitted[b] = n + 1;
+    }
+    if (total == 0) return;
+    long long goal = (long long)((double)u[K] * (double)total);
+    goal = goal < 0 ? 0 : (goal >= total ? total - 1 : goal);
+    // the segment whose running sum first exceeds the goal
+    long long before = 0;
+    int hit = 0;
+    for (int i0 = 0; i0 < nseg; i0 += 32) {
+        long long v = i0 + lane < nseg ? all[i0 + lane] : 0;
+        const long long own = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += t;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, before + v > goal);
+        if (over != 0) {
+            const int l = __ffs(over) - 1;
+            hit = i0 + l;
+            before += __shfl_sync(0xffffffffu, v - own, l);
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (hit / kWarps != rank) return;
+    // its tokens, a run of consecutive ones for each thread
+    const int s_lo = min((int64_t)hit * len, (int64_t)V), s_hi = min(s_lo + len, V);
+    const int per = (len + kThreads - 1) / kThreads;
+    const int t_lo = min(s_lo + (int)threadIdx.x * per, s_hi), t_hi = min(t_lo + per, s_hi);
+    long long s = 0;
+    for (int j = t_lo; j < t_hi; ++j) s += row.at(j);
+    long long incl = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) part[warp] = incl;
+    __syncthreads();
+    long long run = before + incl - s;
+    for (int w = 0; w < warp; ++w) run += part[w];
+    if (run <= goal && run + s > goal) {  // one thread: the running sum crosses the goal in its run
+        for (int j = t_lo; j < t_hi; ++j) {
+            run += row.at(j);
+            if (run > goal) {
+                out[n] = j;
+                break;
+            }
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_t(const AcceptParams &p, cudaStream_t stream) {
+    // CTAs a row: more while the grid leaves multiprocessors without work for
+    // four CTAs and each warp still sums a few hundred tokens
+    int cs = 1;
+    const long slots = 4l * sm_count_of_current_device();
+    while (cs < kMaxCluster && (long)p.B * cs * 2 <= slots && p.V / (2 * cs * kWarps) >= 128) cs *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p.B * cs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)cs;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, accept_kernel<T>, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_accept(const AcceptParams &p, cudaStream_t stream) {
+    switch (p.dt) {
+        case GDN_F32: return launch_t<float>(p, stream);
+        case GDN_F16: return launch_t<__half>(p, stream);
+        default: return launch_t<__nv_bfloat16>(p, stream);
+    }
+}
+
+}  // namespace gdn

@@ -103,6 +103,17 @@ bool mul_ok(size_t a, size_t b, size_t *out) {
     return true;
 }
 
+// Bytes from the first to the last element of n rows of `width` elements, `stride` apart.
+bool rows_bytes(int64_t n, int64_t stride, int64_t width, size_t elem, size_t *out) {
+    if (n <= 0) {
+        *out = 0;
+        return true;
+    }
+    size_t body;
+    if (!mul_ok((size_t)(n - 1), (size_t)stride, &body)) return false;
+    return mul_ok(body + (size_t)width, elem, out);
+}
+
 // Sizes shared by prefill and recurrent calls.
 struct Shapes {
     size_t total_T, qk_bytes, v_bytes, gate_bytes, s0_bytes, sf_bytes;
@@ -112,7 +123,7 @@ int check_common(const void *q, const void *k, const void *v, const void *alpha,
                  const void *beta, const int32_t *cu, const float *s0,
                  const int32_t *s0_idx, int n_s0, const float *sf, const void *out,
                  int B, int T, int Hq, int Hk, int Hv, int dk, int dv, int dt_qkv,
-                 int dt_gate, Shapes *sh) {
+                 int dt_gate, Shapes *sh, bool linear = false, bool alpha_per_head = false) {
     if (B < 0 || T < 0 || Hk <= 0 || Hv <= 0 || dk <= 0 || dv <= 0) return GDN_ERR_INVALID_ARG;
     if (Hq != Hk || Hv % Hk != 0) return GDN_ERR_INVALID_ARG;
     if (dtype_bytes(dt_qkv) == 0 || dtype_bytes(dt_gate) == 0) return GDN_ERR_INVALID_ARG;
@@ -121,7 +132,7 @@ int check_common(const void *q, const void *k, const void *v, const void *alpha,
     if (B > 65535 || Hv > 65535) return GDN_ERR_UNSUPPORTED;
     size_t total_T = (cu == nullptr) ? (size_t)B * (size_t)T : (size_t)T;
     if (B > 0 && total_T > 0) {
-        if (!q || !k || !v || !alpha || !beta || !out) return GDN_ERR_INVALID_ARG;
+        if (!q || !k || !v || !alpha || (!beta && !linear) || !out) return GDN_ERR_INVALID_ARG;
     }
     if (s0_idx != nullptr && s0 == nullptr) return GDN_ERR_INVALID_ARG;
     if (s0 != nullptr) {
@@ -137,7 +148,8 @@ int check_common(const void *q, const void *k, const void *v, const void *alpha,
     sh->total_T = total_T;
     if (!mul_ok(total_T, (size_t)Hk * dk * dtype_bytes(dt_qkv), &sh->qk_bytes)) return GDN_ERR_INVALID_ARG;
     if (!mul_ok(total_T, (size_t)Hv * dv * dtype_bytes(dt_qkv), &sh->v_bytes)) return GDN_ERR_INVALID_ARG;
-    if (!mul_ok(total_T, (size_t)Hv * dtype_bytes(dt_gate), &sh->gate_bytes)) return GDN_ERR_INVALID_ARG;
+    if (!mul_ok(alpha_per_head ? 1 : total_T, (size_t)Hv * dtype_bytes(dt_gate), &sh->gate_bytes))
+        return GDN_ERR_INVALID_ARG;
     sh->s0_bytes = s0 ? (size_t)(s0_idx ? n_s0 : (n_s0 > B ? n_s0 : B)) * st : 0;
     sh->sf_bytes = sf ? (size_t)B * st : 0;
     return GDN_OK;
@@ -228,6 +240,205 @@ int gdn_recurrent_capture(const void *q, const void *k, const void *v, const voi
     p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     if (error_word(&p.err) != cudaSuccess) return GDN_ERR_CUDA;
     return launch_recurrent(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+int gdn_linear_recurrent(const void *q, const void *k, const void *v, const void *alpha,
+                         const int32_t *cu_seqlens, const float *initial_state,
+                         const int32_t *initial_state_indices, int num_initial_states,
+                         float *final_state, void *out, int B, int T, int Hq, int Hk, int Hv, int dk,
+                         int dv, float scale, int dtype_qkv, int dtype_gate,
+                         int state_update_capacity, const int32_t *capture_count,
+                         const int32_t *state_update_active, float *state_update, void *stream) {
+    int conv = 0, dtq = 0, dtg = 0;
+    if (!split_dtype(dtype_qkv, 0, &dtq, &conv) ||
+        !split_dtype(dtype_gate, GDN_ALPHA_LOG | GDN_ALPHA_PER_HEAD, &dtg, &conv))
+        return GDN_ERR_INVALID_ARG;
+    Shapes sh;
+    int st = check_common(q, k, v, alpha, nullptr, cu_seqlens, initial_state, initial_state_indices,
+                          num_initial_states, final_state, out, B, T, Hq, Hk, Hv, dk, dv, dtq, dtg, &sh,
+                          true, (conv & GDN_ALPHA_PER_HEAD) != 0);
+    if (st != GDN_OK) return st;
+    const int cap = state_update_capacity;
+    if (cap < 0) return GDN_ERR_INVALID_ARG;
+    if (cap > 0 && (capture_count == nullptr || state_update == nullptr)) return GDN_ERR_INVALID_ARG;
+    if (state_update && !aligned(state_update, 16)) return GDN_ERR_ALIGN;
+    if ((capture_count && !aligned(capture_count, 4)) ||
+        (state_update_active && !aligned(state_update_active, 4)))
+        return GDN_ERR_ALIGN;
+    if (final_state != nullptr && final_state == initial_state && initial_state_indices != nullptr)
+        return GDN_ERR_ALIAS;
+    size_t su_bytes = 0;
+    if (cap > 0 && !mul_ok((size_t)B * cap, GDN_STATE_UPDATE_SLOT(Hk, Hv, dk, dv) * sizeof(float), &su_bytes))
+        return GDN_ERR_INVALID_ARG;
+    const size_t sf_in_place = (final_state == initial_state) ? sh.sf_bytes : 0;
+    Span spans[] = {
+        {q, sh.qk_bytes, false},
+        {k, sh.qk_bytes, false},
+        {v, sh.v_bytes, false},
+        {alpha, sh.gate_bytes, false},
+        {cu_seqlens, cu_seqlens ? (size_t)(B + 1) * 4 : 0, false},
+        {initial_state, sf_in_place ? sf_in_place : sh.s0_bytes, false},  // 5
+        {initial_state_indices, initial_state_indices ? (size_t)B * 4 : 0, false},
+        {capture_count, cap > 0 ? (size_t)B * 4 : 0, false},
+        {state_update_active, state_update_active ? 4u : 0u, false},
+        {final_state, sh.sf_bytes, true},                                 // 9
+        {out, sh.v_bytes, true},
+        {state_update, su_bytes, true},
+    };
+    st = check_alias(spans, (int)(sizeof(spans) / sizeof(spans[0])), 5, 9);
+    if (st != GDN_OK) return st;
+    if (B == 0) return GDN_OK;
+
+    RecurrentParams p{};
+    p.q = q; p.k = k; p.v = v; p.alpha = alpha;
+    p.cu_seqlens = cu_seqlens;
+    p.s0 = initial_state; p.s0_idx = initial_state_indices; p.n_s0 = num_initial_states;
+    p.s_final = final_state; p.out = out;
+    p.B = B; p.T = T; p.Hk = Hk; p.Hv = Hv; p.dk = dk; p.dv = dv;
+    p.scale = scale; p.dt_qkv = dtq; p.dt_gate = dtg; p.conv = conv; p.linear = true;
+    p.capacity = cap; p.capture_count = capture_count; p.active = state_update_active;
+    p.su = cap > 0 ? state_update : nullptr;
+    p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+    if (error_word(&p.err) != cudaSuccess) return GDN_ERR_CUDA;
+    return launch_recurrent(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+size_t gdn_linear_prefill_workspace_size(int B, int T, int Hk, int Hv, int dk, int dv, int dtype_qkv,
+                                         int varlen) {
+    (void)varlen;
+    if (B < 0 || T < 0 || Hk <= 0 || Hv <= 0 || dk <= 0 || dv <= 0 || dtype_bytes(dtype_qkv) == 0)
+        return (size_t)-1;
+    return 0;
+}
+
+int gdn_linear_prefill(const void *q, const void *k, const void *v, const void *alpha,
+                       const int32_t *cu_seqlens, const float *initial_state,
+                       const int32_t *initial_state_indices, int num_initial_states,
+                       float *final_state, void *out, int B, int T, int Hq, int Hk, int Hv, int dk,
+                       int dv, float scale, int dtype_qkv, int dtype_gate, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+    (void)workspace;
+    (void)workspace_bytes;
+    return gdn_linear_recurrent(q, k, v, alpha, cu_seqlens, initial_state, initial_state_indices,
+                                num_initial_states, final_state, out, B, T, Hq, Hk, Hv, dk, dv, scale,
+                                dtype_qkv, dtype_gate, 0, nullptr, nullptr, nullptr, stream);
+}
+
+int gdn_gated_norm(const void *x, const void *z, const void *weight, void *out, int64_t N, int H, int d,
+                   int64_t x_stride, int64_t z_stride, int64_t out_stride, float eps, int gate,
+                   int dtype_x, int dtype_w, void *stream) {
+    const int act = gate & 0xF;
+    if (N < 0 || H <= 0 || d <= 0 || !(eps >= 0.f)) return GDN_ERR_INVALID_ARG;
+    if ((gate & ~(0xF | GDN_GATE_FIRST | GDN_NORM_UNIT_OFFSET)) || act > GDN_GATE_SIGMOID)
+        return GDN_ERR_INVALID_ARG;
+    if (dtype_bytes(dtype_x) == 0 || dtype_bytes(dtype_w) == 0) return GDN_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)H * d;
+    if (x_stride < row || out_stride < row || (act != GDN_GATE_NONE && z_stride < row))
+        return GDN_ERR_INVALID_ARG;
+    if (d > kNormMaxWidth || N > INT32_MAX / H) return GDN_ERR_UNSUPPORTED;
+    if (N == 0) return GDN_OK;
+    if (!x || !out || (act != GDN_GATE_NONE) != (z != nullptr)) return GDN_ERR_INVALID_ARG;
+    const size_t ex = dtype_bytes(dtype_x), ew = dtype_bytes(dtype_w);
+    if (!aligned(x, ex) || !aligned(z, ex) || !aligned(out, ex) || !aligned(weight, ew)) return GDN_ERR_ALIGN;
+    size_t xb, zb, ob;
+    if (!rows_bytes(N, x_stride, row, ex, &xb) || !rows_bytes(N, z_stride, row, ex, &zb) ||
+        !rows_bytes(N, out_stride, row, ex, &ob))
+        return GDN_ERR_INVALID_ARG;
+    Span spans[] = {
+        {x, xb, false},
+        {z, z ? zb : 0, false},
+        {weight, weight ? (size_t)d * ew : 0, false},
+        {out, ob, true},
+    };
+    const int st = check_alias(spans, 4, x_stride == out_stride ? 0 : -1, 3);
+    if (st != GDN_OK) return st;
+    GatedNormParams p{};
+    p.x = x; p.z = z; p.w = weight; p.out = out;
+    p.N = N; p.H = H; p.d = d;
+    p.xs = x_stride; p.zs = z_stride; p.os = out_stride;
+    p.eps = eps; p.gate = gate; p.dt_x = dtype_x; p.dt_w = dtype_w;
+    return launch_gated_norm(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+int gdn_residual_norm(const void *y, const void *residual, const void *gate, const void *post_weight,
+                      const void *pre_weight, void *residual_out, void *out, int64_t N, int D,
+                      int64_t y_stride, int64_t gate_stride, float res_scale, float eps, int flags,
+                      int dtype_x, int dtype_res, int dtype_w, void *stream) {
+    const int act = flags & 0xF;
+    if (N < 0 || D <= 0 || !(eps >= 0.f)) return GDN_ERR_INVALID_ARG;
+    if ((flags & ~(0xF | GDN_NORM_UNIT_OFFSET)) || act > GDN_GATE_SIGMOID) return GDN_ERR_INVALID_ARG;
+    if (dtype_bytes(dtype_x) == 0 || dtype_bytes(dtype_w) == 0 || dtype_bytes(dtype_res) == 0)
+        return GDN_ERR_INVALID_ARG;
+    if (dtype_res != dtype_x && dtype_res != GDN_F32) return GDN_ERR_UNSUPPORTED;
+    if (y_stride < D || (act != GDN_GATE_NONE && gate_stride < D)) return GDN_ERR_INVALID_ARG;
+    if (D > kNormMaxWidth || N > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    if (N == 0) return GDN_OK;
+    if (!y || (!residual_out && !out) || (act != GDN_GATE_NONE) != (gate != nullptr)) return GDN_ERR_INVALID_ARG;
+    const size_t ex = dtype_bytes(dtype_x), er = dtype_bytes(dtype_res), ew = dtype_bytes(dtype_w);
+    if (!aligned(y, ex) || !aligned(gate, ex) || !aligned(out, ex) || !aligned(residual, er) ||
+        !aligned(residual_out, er) || !aligned(post_weight, ew) || !aligned(pre_weight, ew))
+        return GDN_ERR_ALIGN;
+    size_t yb, gb, rb, ob;
+    if (!rows_bytes(N, y_stride, D, ex, &yb) || !rows_bytes(N, gate_stride, D, ex, &gb) ||
+        !rows_bytes(N, D, D, er, &rb) || !rows_bytes(N, D, D, ex, &ob))
+        return GDN_ERR_INVALID_ARG;
+    Span spans[] = {
+        {y, yb, false},
+        {residual, residual ? rb : 0, false},  // 1
+        {gate, gate ? gb : 0, false},
+        {post_weight, post_weight ? (size_t)D * ew : 0, false},
+        {pre_weight, pre_weight ? (size_t)D * ew : 0, false},
+        {residual_out, residual_out ? rb : 0, true},  // 5
+        {out, out ? ob : 0, true},
+    };
+    const int st = check_alias(spans, 7, 1, 5);
+    if (st != GDN_OK) return st;
+    ResidualNormParams p{};
+    p.y = y; p.x = residual; p.z = gate; p.w_post = post_weight; p.w_pre = pre_weight;
+    p.x_out = residual_out; p.out = out;
+    p.N = N; p.D = D; p.ys = y_stride; p.zs = gate_stride;
+    p.scale = res_scale; p.eps = eps; p.flags = flags;
+    p.dt_x = dtype_x; p.dt_res = dtype_res; p.dt_w = dtype_w;
+    return launch_residual_norm(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+int gdn_accept_drafts(const void *target_probs, const void *draft_probs, const int32_t *draft_tokens,
+                      const float *uniform, const int32_t *draft_count, int32_t *tokens,
+                      int32_t *emitted_count, int B, int K, int V, int64_t target_stride,
+                      int64_t draft_stride, int dtype_probs, void *stream) {
+    if (B < 0 || K < 0 || V <= 0) return GDN_ERR_INVALID_ARG;
+    const size_t e = dtype_bytes(dtype_probs);
+    if (e == 0) return GDN_ERR_INVALID_ARG;
+    if (target_stride < V || (draft_probs && draft_stride < V)) return GDN_ERR_INVALID_ARG;
+    if (V > kAcceptMaxVocab || B > 65535 || K > kAcceptMaxDrafts) return GDN_ERR_UNSUPPORTED;
+    if (B == 0) return GDN_OK;
+    if (!target_probs || !uniform || !tokens || !emitted_count || (K > 0 && !draft_tokens))
+        return GDN_ERR_INVALID_ARG;
+    if (!aligned(target_probs, e) || !aligned(draft_probs, e) || !aligned(draft_tokens, 4) ||
+        !aligned(uniform, 4) || !aligned(draft_count, 4) || !aligned(tokens, 4) || !aligned(emitted_count, 4))
+        return GDN_ERR_ALIGN;
+    size_t tb, db;
+    if (!rows_bytes((int64_t)B * (K + 1), target_stride, V, e, &tb) ||
+        !rows_bytes((int64_t)B * K, draft_probs ? draft_stride : V, V, e, &db))
+        return GDN_ERR_INVALID_ARG;
+    const size_t n = (size_t)B * (K + 1) * 4;
+    Span spans[] = {
+        {target_probs, tb, false},
+        {draft_probs, draft_probs ? db : 0, false},
+        {draft_tokens, K > 0 ? (size_t)B * K * 4 : 0, false},
+        {uniform, n, false},
+        {draft_count, draft_count ? (size_t)B * 4 : 0, false},
+        {tokens, n, true},
+        {emitted_count, (size_t)B * 4, true},
+    };
+    const int st = check_alias(spans, 7, -1, -1);
+    if (st != GDN_OK) return st;
+    AcceptParams p{};
+    p.p = target_probs; p.q = draft_probs; p.drafts = draft_tokens; p.u = uniform; p.count = draft_count;
+    p.tokens = tokens; p.emitted = emitted_count;
+    p.B = B; p.K = K; p.V = V; p.ps = target_stride; p.qs = draft_stride; p.dt = dtype_probs;
+    if (error_word(&p.err) != cudaSuccess) return GDN_ERR_CUDA;
+    return launch_accept(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 int gdn_replay_verify(const void *q, const void *k, const void *v, const void *alpha,

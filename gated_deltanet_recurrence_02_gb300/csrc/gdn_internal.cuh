@@ -33,7 +33,8 @@ struct RecurrentParams {
     int B, T, Hk, Hv, dk, dv;
     float scale;
     int dt_qkv, dt_gate;
-    int conv;  // GDN_QK_L2NORM | GDN_ALPHA_LOG | GDN_BETA_LOGIT bits
+    int conv;  // GDN_QK_L2NORM | GDN_ALPHA_LOG | GDN_BETA_LOGIT | GDN_ALPHA_PER_HEAD bits
+    bool linear;  // linear attention: no beta, delta = v
     int capacity;
     const int32_t *capture_count;
     const int32_t *active;
@@ -95,6 +96,45 @@ struct PrefillParams {
     uint32_t *err;
 };
 
+// Rows are (token n, head h): element i of row (n, h) of x is x[n * xs + h * d + i].
+struct GatedNormParams {
+    const void *x, *z, *w;
+    void *out;
+    int64_t N;
+    int H, d;
+    int64_t xs, zs, os;
+    float eps;
+    int gate;  // GDN_GATE_* | GDN_GATE_FIRST | GDN_NORM_UNIT_OFFSET
+    int dt_x, dt_w;
+};
+
+struct ResidualNormParams {
+    const void *y, *x, *z, *w_post, *w_pre;
+    void *x_out, *out;
+    int64_t N;
+    int D;
+    int64_t ys, zs;
+    float scale, eps;
+    int flags;  // GDN_GATE_* | GDN_NORM_UNIT_OFFSET
+    int dt_x, dt_res, dt_w;
+};
+
+struct AcceptParams {
+    const void *p, *q;
+    const int32_t *drafts;
+    const float *u;
+    const int32_t *count;
+    int32_t *tokens, *emitted;
+    int B, K, V;
+    int64_t ps, qs;
+    int dt;
+    uint32_t *err;
+};
+
+constexpr int kNormMaxWidth = 16384;
+constexpr int kAcceptMaxVocab = 1 << 22;   // sums of 2^40 units a token stay below 2^62
+constexpr int kAcceptMaxDrafts = 1024;
+
 // Captured tokens of row b (row length len): n_b = clamp(count, 0, min(capacity, len)),
 // 0 when capture is off or inactive.
 __device__ __forceinline__ int prefill_ncap(const PrefillParams &p, int b, int len) {
@@ -133,6 +173,10 @@ bool prefill_simt_supported(int dk, int dv, int chunk);
 cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t stream);
 bool prefill_tc_supported(int dk, int dv, int chunk, int dt_qkv);
 size_t prefill_tc_workspace_bytes(int B, int T, int Hk, int Hv, bool varlen);
+
+cudaError_t launch_gated_norm(const GatedNormParams &p, cudaStream_t stream);
+cudaError_t launch_residual_norm(const ResidualNormParams &p, cudaStream_t stream);
+cudaError_t launch_accept(const AcceptParams &p, cudaStream_t stream);
 
 // Raises kernel Kern's dynamic shared-memory limit to `bytes`, once per device
 // (function attributes belong to the device's context): later calls make no

@@ -32,6 +32,14 @@
 // capture are replayed on the registers, S <- decay S + delta key^T, with the
 // same fp32 operations as the token update, and the committed state is
 // written out; the drafts then run from it.
+//
+// Linear attention with a decay for each head (LIN = true) is the same stream
+// without the delta rule's correction: delta = v, so S <- alpha S_old + v k^T
+// and o = alpha (S_old q) + v (k . q).  It has no S k reduction and no beta;
+// alpha is a gate of each (token, head) or, with GDN_ALPHA_PER_HEAD, of each
+// head.  A capture holds decay, key and v, which the replay of the delta rule
+// rebuilds the state from unchanged.  It moves the same bytes as the delta
+// rule and is bound by them.
 #include "gdn_internal.cuh"
 #include "tc_ptx.cuh"
 
@@ -73,6 +81,12 @@ __device__ __forceinline__ void store_row(float *dst, const float2 (&Sr)[2 * F4]
 
 constexpr int kStages = 3;       // tiles in flight per CTA
 
+// Linear attention: the decay of (token, head) element gi, or of head h when
+// one decay per head is given.
+__device__ __forceinline__ float linear_alpha(const RecurrentParams &p, long gi, int h) {
+    return conv_alpha(ld_gate(p.alpha, (p.conv & GDN_ALPHA_PER_HEAD) ? h : gi, p.dt_gate), p.conv);
+}
+
 // Per-stage header, written by the producer before it arrives on the stage.
 struct TileHeader {
     long tok0;
@@ -104,7 +118,8 @@ struct StageLayout {
 // TS tokens and RS replayed slots per tile are staged in shared memory by the
 // producer; later ones (long rows, large acceptance counts) are read by the
 // compute warps straight from memory.  CPS = resident CTAs per SM.
-template <int DK, typename TQ, int TS, int RS, int CPS, int CW>
+// LIN: linear attention instead of the gated delta rule.
+template <int DK, typename TQ, int TS, int RS, int CPS, int CW, bool LIN>
 __global__ void __launch_bounds__(CW * 32 + 32, CPS)
 recurrent_kernel(const RecurrentParams p) {
     using L = StageLayout<DK, TQ, TS, RS>;
@@ -190,8 +205,12 @@ recurrent_kernel(const RecurrentParams p) {
             float *sg = reinterpret_cast<float *>(st + L::oG);
             if (lane < nts) {
                 const long gi = (hd.tok0 + lane) * Hv + hd.h;
-                sg[lane] = conv_alpha(ld_gate(p.alpha, gi, p.dt_gate), p.conv);
-                sg[TS + lane] = conv_beta(ld_gate(p.beta, gi, p.dt_gate), p.conv);
+                if constexpr (LIN) {
+                    sg[lane] = linear_alpha(p, gi, hd.h);
+                } else {
+                    sg[lane] = conv_alpha(ld_gate(p.alpha, gi, p.dt_gate), p.conv);
+                    sg[TS + lane] = conv_beta(ld_gate(p.beta, gi, p.dt_gate), p.conv);
+                }
             }
             if constexpr (RS > 0) {
                 // the first RS replayed slots (all loads issued, then stored)
@@ -282,15 +301,19 @@ recurrent_kernel(const RecurrentParams p) {
                 load_pairs<F4>(reinterpret_cast<const TQ *>(st + L::oQ + t * L::kVec), l8, qf);
                 const float *sg = reinterpret_cast<const float *>(st + L::oG);
                 a = sg[t];
-                bt = sg[TS + t];
+                if constexpr (!LIN) bt = sg[TS + t];
             } else {
                 const long tok = hd.tok0 + t;
                 load_pairs<F4>(kb + (tok * Hk + hk) * DK, l8, kf);
                 load_pairs<F4>(qb + (tok * Hk + hk) * DK, l8, qf);
-                a = conv_alpha(ld_gate(p.alpha, tok * Hv + h, p.dt_gate), p.conv);
-                bt = conv_beta(ld_gate(p.beta, tok * Hv + h, p.dt_gate), p.conv);
+                if constexpr (LIN) {
+                    a = linear_alpha(p, tok * Hv + h, h);
+                } else {
+                    a = conv_alpha(ld_gate(p.alpha, tok * Hv + h, p.dt_gate), p.conv);
+                    bt = conv_beta(ld_gate(p.beta, tok * Hv + h, p.dt_gate), p.conv);
+                }
             }
-            if (p.conv & GDN_QK_L2NORM) {
+            if (!LIN && (p.conv & GDN_QK_L2NORM)) {
                 // q and k normalised in the kernel (8-lane sums of squares)
                 const float nk = l2norm_factor(group_sum<kLanesPerRow>(dot_pairs<F2>(kf, kf)));
                 const float nq = l2norm_factor(group_sum<kLanesPerRow>(dot_pairs<F2>(qf, qf)));
@@ -306,12 +329,13 @@ recurrent_kernel(const RecurrentParams p) {
         // update, the readout with the updated state and the captured delta.
         auto row_step = [&](float2(&Sr)[F2], int r, int t, const float2(&kf)[F2], const float2(&qf)[F2],
                             float a, float bt, float kq, float *su_t) {
-            const float sk = group_sum<kLanesPerRow>(dot_pairs<F2>(Sr, kf));
+            float sk = 0.f;
+            if constexpr (!LIN) sk = group_sum<kLanesPerRow>(dot_pairs<F2>(Sr, kf));
             const float sq = group_sum<kLanesPerRow>(dot_pairs<F2>(Sr, qf)) * scale;
             const long tok = hd.tok0 + t;
             const float vi = (t < TS) ? ld_f(reinterpret_cast<const TQ *>(st + L::oV + t * L::kV) + lrow[r])
                                       : ld_f(vb + (tok * Hv + h) * (long)dv + row0 + lrow[r]);
-            const float delta = bt * (vi - a * sk);
+            const float delta = LIN ? vi : bt * (vi - a * sk);
             const float2 a2 = make_float2(a, a), d2 = make_float2(delta, delta);
 #pragma unroll
             for (int i = 0; i < F2; ++i) Sr[i] = __ffma2_rn(a2, Sr[i], __fmul2_rn(d2, kf[i]));
@@ -376,7 +400,7 @@ recurrent_kernel(const RecurrentParams p) {
             // Replay of the accepted prefix, S <- decay S + delta key^T per
             // slot, then the committed state (skipped in place when nothing
             // changed).
-            if (hd.m > 0) {
+            if (RS > 0 && hd.m > 0) {
                 const float *su_b = p.rp_su + (long)b * p.rp_capacity * slot;
                 for (int j = 0; j < hd.m; ++j) {
                     float dec, dl[NP];
@@ -422,7 +446,7 @@ recurrent_kernel(const RecurrentParams p) {
 
             for (int t = 0; t < Tb; ++t) {
                 float2 kf[F2], qf[F2];
-                float a, bt, vi[NP];
+                float a, bt = 0.f, vi[NP];
                 token_in(t, kf, qf, a, bt);
                 const long tok = hd.tok0 + t;
                 if (t < TS) {
@@ -439,20 +463,21 @@ recurrent_kernel(const RecurrentParams p) {
                 float kq = dot_pairs<F2>(kf, qf), sk[NP], sq[NP];
 #pragma unroll
                 for (int r = 0; r < NP; ++r) {
-                    sk[r] = dot_pairs<F2>(S[r], kf);
+                    if constexpr (!LIN) sk[r] = dot_pairs<F2>(S[r], kf);
                     sq[r] = dot_pairs<F2>(S[r], qf);
                 }
                 kq = group_sum<kLanesPerRow>(kq) * scale;
 #pragma unroll
                 for (int r = 0; r < NP; ++r) {
-                    sk[r] = group_sum<kLanesPerRow>(sk[r]);
+                    if constexpr (!LIN) sk[r] = group_sum<kLanesPerRow>(sk[r]);
                     sq[r] = group_sum<kLanesPerRow>(sq[r]) * scale;
                 }
                 float *su_t = (t < hd.ncap) ? su_row + (long)t * slot : nullptr;
                 const float2 a2 = make_float2(a, a);
 #pragma unroll
                 for (int r = 0; r < NP; ++r) {
-                    const float delta = bt * (vi[r] - a * sk[r]);
+                    float delta = vi[r];
+                    if constexpr (!LIN) delta = bt * (vi[r] - a * sk[r]);
                     const float2 d2 = make_float2(delta, delta);
 #pragma unroll
                     for (int i = 0; i < F2; ++i) S[r][i] = __ffma2_rn(a2, S[r][i], __fmul2_rn(d2, kf[i]));
@@ -473,11 +498,11 @@ recurrent_kernel(const RecurrentParams p) {
     }
 }
 
-template <int DK, typename TQ, int TS, int RS, int CPS, int CW>
+template <int DK, typename TQ, int TS, int RS, int CPS, int CW, bool LIN>
 cudaError_t launch_v(const RecurrentParams &p, cudaStream_t stream) {
-    auto kern = recurrent_kernel<DK, TQ, TS, RS, CPS, CW>;
+    auto kern = recurrent_kernel<DK, TQ, TS, RS, CPS, CW, LIN>;
     const size_t bytes = (size_t)kStages * StageLayout<DK, TQ, TS, RS>::kBytes + 2 * kStages * sizeof(uint64_t);
-    cudaError_t e = set_smem_once<recurrent_kernel<DK, TQ, TS, RS, CPS, CW>>((int)bytes);
+    cudaError_t e = set_smem_once<recurrent_kernel<DK, TQ, TS, RS, CPS, CW, LIN>>((int)bytes);
     if (e != cudaSuccess) return e;
     const long tiles = (long)p.B * p.Hv * (p.dv / kRowsPerCta);
     const long cap = (long)sm_count_of_current_device() * CPS;
@@ -491,9 +516,10 @@ cudaError_t launch_v(const RecurrentParams &p, cudaStream_t stream) {
 // four tokens and four slots staged, three CTAs per SM.
 template <int DK, typename TQ>
 cudaError_t launch_t(const RecurrentParams &p, cudaStream_t stream) {
-    if (p.rp_capacity == 0 && p.cu_seqlens == nullptr && p.T <= 1)
-        return launch_v<DK, TQ, 1, 0, 4, 4>(p, stream);
-    return launch_v<DK, TQ, 4, 4, 3, 4>(p, stream);
+    const bool single = p.rp_capacity == 0 && p.cu_seqlens == nullptr && p.T <= 1;
+    if (p.linear)
+        return single ? launch_v<DK, TQ, 1, 0, 4, 4, true>(p, stream) : launch_v<DK, TQ, 4, 0, 3, 4, true>(p, stream);
+    return single ? launch_v<DK, TQ, 1, 0, 4, 4, false>(p, stream) : launch_v<DK, TQ, 4, 4, 3, 4, false>(p, stream);
 }
 
 template <int DK>

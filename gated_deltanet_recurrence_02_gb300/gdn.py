@@ -23,6 +23,10 @@ GDN_F32, GDN_F16, GDN_BF16 = 0, 1, 2
 GDN_DEVERR_BAD_INDEX, GDN_DEVERR_TIMEOUT = 1, 2
 # input conventions (include/gdn.h): OR'd into dtype_qkv / dtype_gate
 GDN_QK_L2NORM, GDN_ALPHA_LOG, GDN_BETA_LOGIT = 0x100, 0x200, 0x400
+GDN_ALPHA_PER_HEAD = 0x800
+# gates of the norms
+GDN_GATE_NONE, GDN_GATE_SILU, GDN_GATE_SIGMOID = 0, 1, 2
+GDN_GATE_FIRST, GDN_NORM_UNIT_OFFSET = 0x10, 0x20
 _DT = {torch.float32: GDN_F32, torch.float16: GDN_F16, torch.bfloat16: GDN_BF16}
 
 _lib = None
@@ -64,6 +68,20 @@ def lib() -> ctypes.CDLL:
     L.gdn_replay_verify.argtypes = ([vp] * 9 + [i] + [vp] * 3 + [i] * 7 + [f, i, i, i]
                                     + [vp] * 4)
     L.gdn_replay_verify.restype = i
+    L.gdn_linear_prefill_workspace_size.argtypes = [i] * 8
+    L.gdn_linear_prefill_workspace_size.restype = sz
+    L.gdn_linear_prefill.argtypes = [vp] * 7 + [i, vp, vp] + [i] * 7 + [f, i, i, vp, sz, vp]
+    L.gdn_linear_prefill.restype = i
+    L.gdn_linear_recurrent.argtypes = ([vp] * 7 + [i, vp, vp] + [i] * 7 + [f, i, i]
+                                       + [i, vp, vp, vp, vp])
+    L.gdn_linear_recurrent.restype = i
+    i64 = ctypes.c_int64
+    L.gdn_gated_norm.argtypes = [vp] * 4 + [i64, i, i, i64, i64, i64, f, i, i, i, vp]
+    L.gdn_gated_norm.restype = i
+    L.gdn_residual_norm.argtypes = [vp] * 7 + [i64, i, i64, i64, f, f, i, i, i, i, vp]
+    L.gdn_residual_norm.restype = i
+    L.gdn_accept_drafts.argtypes = [vp] * 7 + [i, i, i, i64, i64, i, vp]
+    L.gdn_accept_drafts.restype = i
     L.gdn_device_errors.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
     L.gdn_device_errors.restype = i
     L.gdn_status_string.argtypes = [i]
@@ -295,6 +313,173 @@ def gdn_replay_verify(q, k, v, alpha, beta, *, B: int, T: Optional[int] = None,
         _p(state_update_active), _p(state_update), _stream(stream))
     _check(st, "gdn_replay_verify")
     return out, state_out, state_update, draft_final_state
+
+
+def gdn_linear_prefill_workspace_size(B, T, Hk, Hv, dk, dv, dtype_qkv, varlen=False) -> int:
+    return int(lib().gdn_linear_prefill_workspace_size(B, T, Hk, Hv, dk, dv,
+                                                       _DT.get(dtype_qkv, dtype_qkv),
+                                                       int(bool(varlen))))
+
+
+def gdn_linear_prefill(q, k, v, alpha, *, B: int, T: Optional[int] = None, cu_seqlens=None,
+                       initial_state=None, initial_state_indices=None, final_state=None,
+                       out=None, scale: float = 1.0, workspace=None,
+                       want_final_state: bool = True, conventions: int = 0, stream=None):
+    """Linear attention with a decay for each head, chunked form.  alpha is
+    [total_T, Hv], or [Hv] with GDN_ALPHA_PER_HEAD in conventions.  Returns
+    (out, final_state)."""
+    T, Hk, dk, Hv, dv = _dims(q, v, B, T, cu_seqlens)
+    if out is None:
+        out = torch.empty_like(v)
+    if final_state is None and want_final_state:
+        final_state = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=v.device)
+    n0 = initial_state.shape[0] if initial_state is not None else 0
+    if workspace is None:
+        need = gdn_linear_prefill_workspace_size(B, T, Hk, Hv, dk, dv, q.dtype,
+                                                 varlen=cu_seqlens is not None)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = lib().gdn_linear_prefill(
+        _p(q), _p(k), _p(v), _p(alpha), _p(cu_seqlens), _p(initial_state),
+        _p(initial_state_indices), n0, _p(final_state), _p(out), B, T, Hk, Hk, Hv, dk, dv,
+        scale, _DT[q.dtype], _DT[alpha.dtype] | conventions, _p(workspace), ws_bytes,
+        _stream(stream))
+    _check(st, "gdn_linear_prefill")
+    return out, final_state
+
+
+def gdn_linear_recurrent(q, k, v, alpha, *, B: int, T: Optional[int] = None, cu_seqlens=None,
+                         initial_state=None, initial_state_indices=None, final_state=None,
+                         out=None, scale: float = 1.0, state_update_capacity: int = 0,
+                         capture_count=None, state_update_active=None, state_update=None,
+                         want_final_state: bool = True, conventions: int = 0, stream=None):
+    """Linear attention token by token, with the compact capture (delta = v).
+    Returns (out, final_state, state_update).  final_state may be
+    initial_state itself (in place)."""
+    T, Hk, dk, Hv, dv = _dims(q, v, B, T, cu_seqlens)
+    if out is None:
+        out = torch.empty_like(v)
+    if final_state is None and want_final_state:
+        final_state = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=v.device)
+    cap = int(state_update_capacity)
+    if cap > 0 and state_update is None:
+        state_update = torch.empty((B, cap, slot_width(Hk, Hv, dk, dv)),
+                                   dtype=torch.float32, device=v.device)
+    n0 = initial_state.shape[0] if initial_state is not None else 0
+    st = lib().gdn_linear_recurrent(
+        _p(q), _p(k), _p(v), _p(alpha), _p(cu_seqlens), _p(initial_state),
+        _p(initial_state_indices), n0, _p(final_state), _p(out), B, T, Hk, Hk, Hv, dk, dv,
+        scale, _DT[q.dtype], _DT[alpha.dtype] | conventions, cap, _p(capture_count),
+        _p(state_update_active), _p(state_update), _stream(stream))
+    _check(st, "gdn_linear_recurrent")
+    return out, final_state, state_update
+
+
+def _rows(t, width_dims: int):
+    """Pointer and row stride (elements) of a tensor whose rows (the last
+    width_dims dimensions) are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("libgdn takes device tensors")
+    want = 1
+    for d in range(t.dim() - 1, t.dim() - 1 - width_dims, -1):
+        if t.shape[d] != 1 and t.stride(d) != want:
+            raise ValueError("the elements of a row must be contiguous")
+        want *= t.shape[d]
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else want)
+
+
+def gdn_gated_norm(x, z=None, weight=None, *, eps: float = 1e-6, gate: int = GDN_GATE_SILU,
+                   out=None, stream=None):
+    """Norm of each head of x [N, H, d], fused with its gate z: rmsnorm(x) *
+    weight * act(z), or with GDN_GATE_FIRST rmsnorm(x * act(z)) * weight.  x, z
+    and out may be slices of wider rows.  Without z the gate is none."""
+    N, H, d = x.shape
+    if z is None:
+        gate &= ~0xF
+    elif z.shape != x.shape or z.dtype != x.dtype:
+        raise ValueError("z must have the shape and the dtype of x")
+    if weight is not None and weight.shape != (d,):
+        raise ValueError("weight must have one element for each of a head")
+    if out is None:
+        out = torch.empty((N, H, d), dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have the shape and the dtype of x")
+    xp, xs = _rows(x, 2)
+    zp, zs = _rows(z, 2) if z is not None else (None, H * d)
+    op, os_ = _rows(out, 2)
+    st = lib().gdn_gated_norm(xp, zp, _p(weight), op, N, H, d, xs, zs, os_, eps, gate,
+                              _DT[x.dtype], _DT[weight.dtype] if weight is not None else GDN_F32,
+                              _stream(stream))
+    _check(st, "gdn_gated_norm")
+    return out
+
+
+def gdn_residual_norm(y, residual=None, *, post_weight=None, gate=None,
+                      gate_act: int = GDN_GATE_SIGMOID, res_scale: float = 1.0, pre_weight=None,
+                      eps: float = 1e-6, unit_offset: bool = False, residual_out=None, out=None,
+                      residual_dtype=None, stream=None):
+    """From one block to the next: x' = residual + res_scale * act(gate) *
+    [rmsnorm(y) * post_weight], and rmsnorm(x') * pre_weight.  y and gate are
+    [N, D] (rows may be slices).  Returns (x', out); residual_out may be
+    residual itself."""
+    N, D = y.shape
+    if residual is not None and residual.shape != y.shape:
+        raise ValueError("residual must have the shape of y")
+    if gate is not None and (gate.shape != y.shape or gate.dtype != y.dtype):
+        raise ValueError("gate must have the shape and the dtype of y")
+    for w in (post_weight, pre_weight):
+        if w is not None and w.shape != (D,):
+            raise ValueError("a norm's weight must have one element for each of a row")
+    if post_weight is not None and pre_weight is not None and post_weight.dtype != pre_weight.dtype:
+        raise ValueError("the two weights must have one dtype")
+    rdt = residual.dtype if residual is not None else (residual_dtype or y.dtype)
+    if residual_out is None:
+        residual_out = torch.empty((N, D), dtype=rdt, device=y.device)
+    if out is None:
+        out = torch.empty((N, D), dtype=y.dtype, device=y.device)
+    if (residual_out.shape != y.shape or residual_out.dtype != rdt or out.shape != y.shape
+            or out.dtype != y.dtype):
+        raise ValueError("outputs must have the shape of y and their input's dtype")
+    yp, ys = _rows(y, 1)
+    gp, gs = _rows(gate, 1) if gate is not None else (None, D)
+    w = post_weight if post_weight is not None else pre_weight
+    flags = (gate_act if gate is not None else GDN_GATE_NONE) | (GDN_NORM_UNIT_OFFSET if unit_offset else 0)
+    st = lib().gdn_residual_norm(yp, _p(residual), gp, _p(post_weight), _p(pre_weight),
+                                 _p(residual_out), _p(out), N, D, ys, gs, res_scale, eps, flags,
+                                 _DT[y.dtype], _DT[rdt],
+                                 _DT[w.dtype] if w is not None else GDN_F32, _stream(stream))
+    _check(st, "gdn_residual_norm")
+    return residual_out, out
+
+
+def gdn_accept_drafts(target_probs, draft_probs, draft_tokens, uniform, *, draft_count=None,
+                      tokens=None, emitted_count=None, stream=None):
+    """Verify drafts [B, K] against target_probs [B, K + 1, V] (draft_probs
+    [B, K, V], or None for certain drafts) with uniform [B, K + 1].  Returns
+    (tokens [B, K + 1], emitted_count [B]): the accepted drafts, one sampled
+    token, then -1; emitted_count is the accepted_count of a replay."""
+    B, K1, V = target_probs.shape
+    K = K1 - 1
+    if draft_tokens.shape != (B, K) or uniform.shape != (B, K1):
+        raise ValueError("draft_tokens must be [B, K] and uniform [B, K + 1]")
+    if draft_probs is not None and (draft_probs.shape != (B, K, V)
+                                    or draft_probs.dtype != target_probs.dtype):
+        raise ValueError("draft_probs must be [B, K, V] in target_probs' dtype")
+    if tokens is None:
+        tokens = torch.empty((B, K1), dtype=torch.int32, device=target_probs.device)
+    if emitted_count is None:
+        emitted_count = torch.empty((B,), dtype=torch.int32, device=target_probs.device)
+    for t in (draft_tokens, draft_count, tokens, emitted_count):
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError("tokens and counts are int32")
+    if uniform.dtype != torch.float32:
+        raise ValueError("uniform is float32")
+    st = lib().gdn_accept_drafts(
+        _p(target_probs), _p(draft_probs), _p(draft_tokens), _p(uniform), _p(draft_count),
+        _p(tokens), _p(emitted_count), B, K, V, V, V, _DT[target_probs.dtype], _stream(stream))
+    _check(st, "gdn_accept_drafts")
+    return tokens, emitted_count
 
 
 def gdn_set_wait_limit_ns(ns: int) -> None:

@@ -313,6 +313,136 @@ GDN_API int gdn_replay_verify(const void *q, const void *k, const void *v,
                               void *stream);
 
 /*
+ * Linear attention with a decay for each head -- the layer that hybrid
+ * backbones place next to the gated delta rule.  Per (row b, value head h):
+ *     S <- alpha_t S + v_t k_t^T          S: fp32 [dv, dk], S[i][j] += v[i] k[j]
+ *     o_t = S (scale * q_t)               readout with the updated S
+ * Layouts, packed rows, states, snapshots, alignment and errors are those of
+ * the delta-rule calls; beta does not exist.  Extra convention bit:
+ *  GDN_ALPHA_PER_HEAD  in dtype_gate: alpha is [Hv], one decay for each head
+ *                      (else [total_T, Hv], one for each token and head).
+ * GDN_ALPHA_LOG applies to both forms; no other bit is taken.  alpha = 0 is
+ * allowed (the state is dropped).  Inputs that are not finite reach the
+ * tokens after them in the same row and, in the chunked form, the up to 127
+ * tokens before them that share their chunk; they touch no other row, and
+ * values of one head touch no other head.
+ */
+#define GDN_ALPHA_PER_HEAD 0x800
+
+/*
+ * gdn_linear_prefill -- chunked form, for prompts of any length.
+ *  final_state may be NULL (not written), or exactly initial_state when
+ *  initial_state_indices is NULL.  workspace: device buffer of
+ *  gdn_linear_prefill_workspace_size() bytes (same B, T, sizes and dtype_qkv;
+ *  varlen != 0 when cu_seqlens is passed; NULL allowed when 0), scratch.
+ *  Other arguments as in gdn_prefill_chunked.
+ */
+GDN_API size_t gdn_linear_prefill_workspace_size(int B, int T, int Hk, int Hv, int dk, int dv,
+                                                 int dtype_qkv, int varlen);
+GDN_API int gdn_linear_prefill(const void *q, const void *k, const void *v, const void *alpha,
+                               const int32_t *cu_seqlens, const float *initial_state,
+                               const int32_t *initial_state_indices, int num_initial_states,
+                               float *final_state, void *out, int B, int T, int Hq, int Hk, int Hv,
+                               int dk, int dv, float scale, int dtype_qkv, int dtype_gate,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_linear_recurrent -- recurrent form, token by token (decode, verify).
+ * The capture is gdn_recurrent_capture's with delta = v, so
+ * gdn_replay_state_updates rebuilds the state after an accepted prefix from
+ * it.  Other arguments as in gdn_recurrent_capture.
+ */
+GDN_API int gdn_linear_recurrent(const void *q, const void *k, const void *v, const void *alpha,
+                                 const int32_t *cu_seqlens, const float *initial_state,
+                                 const int32_t *initial_state_indices, int num_initial_states,
+                                 float *final_state, void *out, int B, int T, int Hq, int Hk, int Hv,
+                                 int dk, int dv, float scale, int dtype_qkv, int dtype_gate,
+                                 int state_update_capacity, const int32_t *capture_count,
+                                 const int32_t *state_update_active, float *state_update,
+                                 void *stream);
+
+/* Gates of the norms below: silu(z) = z / (1 + e^-z), sigmoid(z) = 1 / (1 + e^-z). */
+enum { GDN_GATE_NONE = 0, GDN_GATE_SILU = 1, GDN_GATE_SIGMOID = 2 };
+#define GDN_GATE_FIRST 0x10        /* the gate is applied before the norm, not after it */
+#define GDN_NORM_UNIT_OFFSET 0x20  /* weights are stored as w - 1 */
+
+/*
+ * gdn_gated_norm -- the mixer's output norm of each head, fused with its gate:
+ *     out = x / sqrt(mean(x^2) + eps) * weight * act(z)
+ * or, with GDN_GATE_FIRST, the norm of x * act(z), times weight.  The mean is
+ * over the d elements of one head; sums are fp32, the result is rounded once.
+ *  x, z, out   dtype_x, element (n, h, i) at [n * stride + h * d + i]: a stride
+ *              (in elements, >= H * d) for each, so x and z may be slices of
+ *              wider rows.  Aligned to their element (16-byte aligned rows of
+ *              multiples of 16 bytes take the vector path).  z is NULL exactly
+ *              when the gate is GDN_GATE_NONE.  out may be exactly x (same
+ *              stride), and overlaps nothing else.
+ *  weight      [d] of dtype_w, or NULL (ones).
+ *  gate        GDN_GATE_* | GDN_GATE_FIRST | GDN_NORM_UNIT_OFFSET.
+ *  d           1 .. 16384.
+ */
+GDN_API int gdn_gated_norm(const void *x, const void *z, const void *weight, void *out, int64_t N,
+                           int H, int d, int64_t x_stride, int64_t z_stride, int64_t out_stride,
+                           float eps, int gate, int dtype_x, int dtype_w, void *stream);
+
+/*
+ * gdn_residual_norm -- from one block to the next in one pass:
+ *     u            = y / sqrt(mean(y^2) + eps) * post_weight   (u = y if post_weight is NULL)
+ *     x'           = residual + res_scale * act(gate) * u      -> residual_out
+ *     out          = x' / sqrt(mean(x'^2) + eps) * pre_weight
+ * out is formed from x' in fp32, before residual_out's rounding.
+ *  y, gate        [N, D] of dtype_x with a row stride each (elements, >= D);
+ *                 gate is NULL exactly when flags hold GDN_GATE_NONE.
+ *  residual       [N, D] of dtype_res, dense, or NULL (zeros).
+ *  residual_out   [N, D] of dtype_res, dense, or NULL (not written); may be
+ *                 exactly residual.
+ *  out            [N, D] of dtype_x, dense, or NULL (not written; not both).
+ *  post_weight, pre_weight   [D] of dtype_w; pre_weight NULL: ones.
+ *  flags          GDN_GATE_* | GDN_NORM_UNIT_OFFSET.
+ *  dtype_res      dtype_x or GDN_F32.     D: 1 .. 16384.
+ */
+GDN_API int gdn_residual_norm(const void *y, const void *residual, const void *gate,
+                              const void *post_weight, const void *pre_weight, void *residual_out,
+                              void *out, int64_t N, int D, int64_t y_stride, int64_t gate_stride,
+                              float res_scale, float eps, int flags, int dtype_x, int dtype_res,
+                              int dtype_w, void *stream);
+
+/*
+ * gdn_accept_drafts -- verification of drafted tokens against the target's
+ * probabilities, from given random numbers (speculative sampling).  Row b has
+ * c_b drafts x_i, i < c_b:
+ *     n      = the first i < c_b with  uniform_i * q_i(x_i) >= p_i(x_i),  else c_b
+ *     weight = max(p_n - q_n, 0) if n < c_b, else p_n
+ *     token  = the first j whose running sum of weights exceeds uniform_K * total
+ * Weights are held in whole units of 2^-40 (rounded down, at most 1, NaN as 0),
+ * so sums are exact and the token does not depend on how the work is split:
+ * it exceeds floor(uniform_K * total) as whole numbers.  Where every weight is
+ * 0, p_n itself is sampled; where that is 0 too, the token is -1.
+ *  target_probs   p: [B, K + 1, V] of dtype_probs, rows target_stride elements apart.
+ *  draft_probs    q: [B, K, V], rows draft_stride apart, or NULL: the drafts
+ *                 were certain, q_i(x_i) = 1 and 0 elsewhere.
+ *  draft_tokens   int32 [B, K].  One outside [0, V) is rejected and sets
+ *                 GDN_DEVERR_BAD_INDEX.
+ *  uniform        fp32 [B, K + 1], in [0, 1): one number for the test of each
+ *                 draft, and the last one for the token (given a rejection, the
+ *                 tests' numbers are no longer uniform).
+ *  draft_count    int32 [B] (clamped to [0, K]) or NULL: K drafts in each row.
+ *  tokens         int32 [B, K + 1] (output): the n accepted drafts, the token,
+ *                 then -1.
+ *  emitted_count  int32 [B] (output): n + 1, the tokens of the row.  A verify
+ *                 pass over the last token and its drafts captured as many
+ *                 state updates to commit, so this is what
+ *                 gdn_replay_state_updates and gdn_replay_verify take as
+ *                 accepted_count.
+ *  K <= 1024, V <= 2^22.
+ */
+GDN_API int gdn_accept_drafts(const void *target_probs, const void *draft_probs,
+                              const int32_t *draft_tokens, const float *uniform,
+                              const int32_t *draft_count, int32_t *tokens, int32_t *emitted_count,
+                              int B, int K, int V, int64_t target_stride, int64_t draft_stride,
+                              int dtype_probs, void *stream);
+
+/*
  * gdn_prefill_chunked_noalloc -- gdn_prefill_chunked for callers that cannot
  * allocate device memory: runtimes with their own memory planner that forbid
  * hidden allocations, or latency-critical paths that must never enter the
