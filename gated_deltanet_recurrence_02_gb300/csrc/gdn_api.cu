@@ -305,10 +305,9 @@ int gdn_linear_recurrent(const void *q, const void *k, const void *v, const void
 
 size_t gdn_linear_prefill_workspace_size(int B, int T, int Hk, int Hv, int dk, int dv, int dtype_qkv,
                                          int varlen) {
-    (void)varlen;
     if (B < 0 || T < 0 || Hk <= 0 || Hv <= 0 || dk <= 0 || dv <= 0 || dtype_bytes(dtype_qkv) == 0)
         return (size_t)-1;
-    return 0;
+    return linear_tc_supported(dk, dv, dtype_qkv) ? linear_tc_workspace_bytes(B, T, Hv, dk, dv, varlen != 0) : 0;
 }
 
 int gdn_linear_prefill(const void *q, const void *k, const void *v, const void *alpha,
@@ -317,11 +316,52 @@ int gdn_linear_prefill(const void *q, const void *k, const void *v, const void *
                        float *final_state, void *out, int B, int T, int Hq, int Hk, int Hv, int dk,
                        int dv, float scale, int dtype_qkv, int dtype_gate, void *workspace,
                        size_t workspace_bytes, void *stream) {
-    (void)workspace;
-    (void)workspace_bytes;
-    return gdn_linear_recurrent(q, k, v, alpha, cu_seqlens, initial_state, initial_state_indices,
-                                num_initial_states, final_state, out, B, T, Hq, Hk, Hv, dk, dv, scale,
-                                dtype_qkv, dtype_gate, 0, nullptr, nullptr, nullptr, stream);
+    int conv = 0, dtq = 0, dtg = 0;
+    if (!split_dtype(dtype_qkv, 0, &dtq, &conv) ||
+        !split_dtype(dtype_gate, GDN_ALPHA_LOG | GDN_ALPHA_PER_HEAD, &dtg, &conv))
+        return GDN_ERR_INVALID_ARG;
+    Shapes sh;
+    int st = check_common(q, k, v, alpha, nullptr, cu_seqlens, initial_state, initial_state_indices,
+                          num_initial_states, final_state, out, B, T, Hq, Hk, Hv, dk, dv, dtq, dtg, &sh,
+                          true, (conv & GDN_ALPHA_PER_HEAD) != 0);
+    if (st != GDN_OK) return st;
+    if (final_state != nullptr && final_state == initial_state && initial_state_indices != nullptr)
+        return GDN_ERR_ALIAS;
+    const size_t need =
+        gdn_linear_prefill_workspace_size(B, T, Hk, Hv, dk, dv, dtq, cu_seqlens != nullptr);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+    if (workspace && !aligned(workspace, 16)) return GDN_ERR_ALIGN;
+    const size_t sf_in_place = (final_state == initial_state) ? sh.sf_bytes : 0;
+    Span spans[] = {
+        {q, sh.qk_bytes, false},
+        {k, sh.qk_bytes, false},
+        {v, sh.v_bytes, false},
+        {alpha, sh.gate_bytes, false},
+        {cu_seqlens, cu_seqlens ? (size_t)(B + 1) * 4 : 0, false},
+        {initial_state, sf_in_place ? sf_in_place : sh.s0_bytes, false},  // 5
+        {initial_state_indices, initial_state_indices ? (size_t)B * 4 : 0, false},
+        {final_state, sh.sf_bytes, true},                                 // 7
+        {out, sh.v_bytes, true},
+        {workspace, need, true},
+    };
+    st = check_alias(spans, (int)(sizeof(spans) / sizeof(spans[0])), 5, 7);
+    if (st != GDN_OK) return st;
+    if (B == 0) return GDN_OK;
+    if (!linear_tc_supported(dk, dv, dtq))
+        return gdn_linear_recurrent(q, k, v, alpha, cu_seqlens, initial_state, initial_state_indices,
+                                    num_initial_states, final_state, out, B, T, Hq, Hk, Hv, dk, dv, scale,
+                                    dtype_qkv, dtype_gate, 0, nullptr, nullptr, nullptr, stream);
+    PrefillParams p{};
+    p.q = q; p.k = k; p.v = v; p.alpha = alpha;
+    p.cu_seqlens = cu_seqlens;
+    p.s0 = initial_state; p.s0_idx = initial_state_indices; p.n_s0 = num_initial_states;
+    p.s_final = final_state; p.out = out;
+    p.B = B; p.T = T; p.Hk = Hk; p.Hv = Hv; p.dk = dk; p.dv = dv;
+    p.scale = scale; p.dt_qkv = dtq; p.dt_gate = dtg; p.conv = conv;
+    p.ws = workspace; p.ws_bytes = workspace_bytes;
+    p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+    if (error_word(&p.err) != cudaSuccess) return GDN_ERR_CUDA;
+    return launch_linear_tc(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 int gdn_gated_norm(const void *x, const void *z, const void *weight, void *out, int64_t N, int H, int d,

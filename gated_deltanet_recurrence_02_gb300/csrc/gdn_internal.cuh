@@ -174,6 +174,11 @@ cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t stream);
 bool prefill_tc_supported(int dk, int dv, int chunk, int dt_qkv);
 size_t prefill_tc_workspace_bytes(int B, int T, int Hk, int Hv, bool varlen);
 
+// Linear attention, chunked form on the 5th-generation tensor cores (16-bit
+// inputs).  PrefillParams without beta, chunk, checkpoints and capture.
+cudaError_t launch_linear_tc(const PrefillParams &p, cudaStream_t stream);
+bool linear_tc_supported(int dk, int dv, int dt_qkv);
+size_t linear_tc_workspace_bytes(int B, int T, int Hv, int dk, int dv, bool varlen);
 cudaError_t launch_gated_norm(const GatedNormParams &p, cudaStream_t stream);
 cudaError_t launch_residual_norm(const ResidualNormParams &p, cudaStream_t stream);
 cudaError_t launch_accept(const AcceptParams &p, cudaStream_t stream);

@@ -120,34 +120,7 @@ __device__ __forceinline__ void unpack8(uint4 u, float *v) {
     v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y; v[4] = c.x; v[5] = c.y; v[6] = d.x; v[7] = d.y;
 }
 
-// 2^x by the PTX ISA's base-2 exponential instruction, flushing subnormal
-// results to zero.  Phase A evaluates e^{g_t - g_i} as 2^{(g_t - g_i) log2 e}
-// with both terms pre-scaled by log2 e; every argument it keeps is <= 0, so
-// the values lie in (0, 1], and results below 2^-126 (flushed) are negligible
-// against the other terms.  Its accuracy is covered by the parity tests
-// (per chunk and head against the fp64 oracle).  The accurate library paths
-// (expf, exp2f) handle subnormals and cost this kernel ~6 us at T=4100.
-__device__ __forceinline__ float ex2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-constexpr float kLog2e = 1.4426950408889634f;
-
-// The 1024-byte aligned start of a kernel's dynamic shared memory, found by
-// pointer arithmetic on the __shared__ array itself: through an integer round
-// trip the compiler no longer sees that the pointer, and every pointer derived
-// from it, addresses shared memory, and each access becomes a generic one
-// (slower, and a measured ~1.3k cycles of every chunk-parallel unit).
-__device__ __forceinline__ uint8_t *smem_align1k(uint8_t *raw) {
-    return raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-}
-
-// Byte offset of the 16-byte chunk holding elements [8*q, 8*q+8) of row r.
-__device__ __forceinline__ uint32_t sw128_chunk(int r, int q) {
-    return (uint32_t)(r * 128 + (((q ^ (r & 7)) & 7) << 4));
-}
-// Same for the 64-byte rows of a 32-column U tile (chunks swizzled by row % 4).
+// sw128_chunk for the 64-byte rows of a 32-column U tile (chunks swizzled by row % 4).
 __device__ __forceinline__ uint32_t u32_chunk(int r, int q) {
     return (uint32_t)(r * 64 + (((q ^ (r & 3)) & 3) << 4));
 }
@@ -1321,6 +1294,10 @@ long max_chunks_of(int B, int T, bool varlen) {
 }
 
 }  // namespace
+
+bool encode_token_map(CUtensorMap *m, const void *ptr, int H, long total_T, bool bf16, int width) {
+    return make_map(m, ptr, H, total_T, bf16, width);
+}
 
 bool prefill_tc_supported(int dk, int dv, int chunk, int dt_qkv) {
     auto width_ok = [](int d) { return d == 32 || d == 64 || d == D; };

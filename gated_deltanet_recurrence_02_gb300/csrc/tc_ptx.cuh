@@ -23,6 +23,34 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// 2^x by the PTX ISA's base-2 exponential instruction, flushing subnormal
+// results to zero.  The chunked kernels evaluate e^{g_t - g_i} as 2^{(g_t - g_i) log2 e}
+// with both terms pre-scaled by log2 e; every argument it keeps is <= 0, so
+// the values lie in (0, 1], and results below 2^-126 (flushed) are negligible
+// against the other terms.  Its accuracy is covered by the parity tests
+// (per chunk and head against the fp64 oracle).  The accurate library paths
+// (expf, exp2f) handle subnormals and cost the delta rule's prefill ~6 us at T=4100.
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The 1024-byte aligned start of a kernel's dynamic shared memory, found by
+// pointer arithmetic on the __shared__ array itself: through an integer round
+// trip the compiler no longer sees that the pointer, and every pointer derived
+// from it, addresses shared memory, and each access becomes a generic one
+// (slower, and a measured ~1.3k cycles of every chunk-parallel unit).
+__device__ __forceinline__ uint8_t *smem_align1k(uint8_t *raw) {
+    return raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+}
+
+// Byte offset of the 16-byte chunk holding elements [8*q, 8*q+8) of row r.
+__device__ __forceinline__ uint32_t sw128_chunk(int r, int q) {
+    return (uint32_t)(r * 128 + (((q ^ (r & 7)) & 7) << 4));
+}
+
 // ------------------------------------------------------------ mbarrier ---
 
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
@@ -204,6 +232,16 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// The same with A in TMEM: lane = row of A, each 32-bit column two 16-bit
+// elements along K (one K = 16 step is eight columns), K-major.
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 // Arrive once on `bar` when every MMA this thread issued so far has completed.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -253,6 +291,29 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The calling warp's 32 lanes x 16 consecutive 32-bit columns, the inverse of
+// the loads above; tmem_wait_st completes the thread's stores.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Moves the calling warpgroup's register limit (a multiple of 8) up or down;
+// every warp of the warpgroup executes it.  An increase waits for registers
+// that other warpgroups of the CTA have given up.
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Shared-memory matrix descriptor, 128-byte swizzle, start / LBO / SBO in bytes.
