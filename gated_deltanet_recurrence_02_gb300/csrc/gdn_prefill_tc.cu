@@ -1220,16 +1220,18 @@ EncodeTiledFn encode_fn() {
 // [total_T, H, width] 16-bit tensor, box {64 features, 1 head, 64 tokens},
 // 128-byte swizzle.  A head narrower than 128 features reads as zero-padded
 // to 128: the box parts past `width` are out of bounds and come back as zeros.
-bool make_map(CUtensorMap *m, const void *ptr, int H, long total_T, bool bf16, int width) {
+// (or, for stores, `box_width` features under `swizzle`).
+bool make_map(CUtensorMap *m, const void *ptr, int H, long total_T, bool bf16, int width, int box_width = 64,
+              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     EncodeTiledFn enc = encode_fn();
     if (enc == nullptr) return false;
     cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)H, (cuuint64_t)total_T};
     cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)H * width * 2};
-    cuuint32_t box[3] = {64, 1, 64};
+    cuuint32_t box[3] = {(cuuint32_t)box_width, 1, 64};
     cuuint32_t es[3] = {1, 1, 1};
     return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                const_cast<void *>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1297,6 +1299,9 @@ long max_chunks_of(int B, int T, bool varlen) {
 
 bool encode_token_map(CUtensorMap *m, const void *ptr, int H, long total_T, bool bf16, int width) {
     return make_map(m, ptr, H, total_T, bf16, width);
+}
+bool encode_store_map(CUtensorMap *m, void *ptr, int H, long total_T, bool bf16, int width) {
+    return make_map(m, ptr, H, total_T, bf16, width, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 bool prefill_tc_supported(int dk, int dv, int chunk, int dt_qkv) {
