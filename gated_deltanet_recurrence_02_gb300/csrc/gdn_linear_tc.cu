@@ -31,9 +31,8 @@
 //   warps 4-7   W: values (ldmatrix, transposed), scaled and split, -> TMEM
 //   warps 8-11  outputs: O1 + 2^{b} O2, transposed through shared memory (stmatrix), TMA stores
 //   warp 12     tiles (TMA) and the chunk's decay sums
-//   warp 13     issues every MMA, in the order dS, O2, O1 of a chunk, then R of
-//               the next one: the threads' part of each product is done while
-//               the others run
+//   warp 13     issues every MMA: dS and O2 of a chunk, R of the next one, O1; the
+//               threads' part of each is done while the others run
 //   warps 14-15 P
 // Few rows are cut into segments of whole chunks, so that every SM has one: a
 // first pass (kStateOnly) forms each segment's end state from its start on,
@@ -73,8 +72,14 @@ constexpr uint32_t kStageV = 2 * kBlock;
 constexpr uint32_t kStage = kStageV + 16384;
 constexpr uint32_t oP = NS * kStage;
 constexpr uint32_t oOut = oP + 8192;               // [4 warps][64 tokens][32 features] on their way out
-constexpr uint32_t oGate = oOut + 16384;           // per stage: b, scale 2^b, 2^s (64 floats each), 2^b_63
+constexpr uint32_t oGate = oOut + 16384;           // per stage (kGate bytes), the words below
 constexpr uint32_t kGate = 1024;
+constexpr int gSum = 0;                            // [64] b_t (decays of at least 2^-40 each)
+constexpr int gScaled = 64;                        // [64] scale 2^{b_t}
+constexpr int gW = 128;                            // [64] 2^{s_t}
+constexpr int gLast = 192;                         // 2^{b_63}
+constexpr int gN = 193, gTok = 194, gHead = 195;   // ints: the chunk's tokens (0: no more chunks), first token, head
+constexpr int gLeft = 200;                         // [32] 2^{b_31 - b_t}
 constexpr uint32_t oWInv = oGate + NS * kGate;     // [2][128] 1 / scale of a lane of W
 constexpr uint32_t oSInv = oWInv + 1024;           // [2][128] 1 / scale of a lane of the image
 constexpr uint32_t oPInv = oSInv + 1024;           // [2][64]  1 / scale of a row of P
@@ -95,6 +100,8 @@ enum Mode {
 struct LinearParams : PrefillParams {
     int G;             // segments a row
     int G_run;         // segments of this pass
+    unsigned n_units;  // B Hv G_run
+    uint32_t spins;    // limit of a wait
     float *seg_state;  // [B, Hv, G, dv, dk]
     float *seg_decay;  // [B, Hv, G]
 };
@@ -137,41 +144,18 @@ struct Unit {
     int b, h, g, len, c0, c1;
     long tok0;
 };
-__device__ __forceinline__ Unit unit_at(const LinearParams &p, long u) {
+__device__ __forceinline__ Unit unit_at(const LinearParams &p, unsigned u) {
     Unit x;
-    const unsigned r = (unsigned)((unsigned long)u / (unsigned)p.Hv);
-    x.h = (int)(u - (long)r * p.Hv);
+    const unsigned r = u / (unsigned)p.Hv;
+    x.h = (int)(u - r * (unsigned)p.Hv);
     x.b = (int)(r / (unsigned)p.G_run);
     x.g = (int)(r - (unsigned)x.b * (unsigned)p.G_run);
     row_range(p.cu_seqlens, x.b, p.T, x.tok0, x.len);
-    const int nc = (x.len + C - 1) / C, per = (nc + p.G - 1) / p.G;
-    x.c0 = min(x.g * per, nc);
-    x.c1 = min(x.c0 + per, nc);
+    const unsigned nc = (unsigned)(x.len + C - 1) / C, per = (nc + p.G - 1) / (unsigned)p.G;
+    x.c0 = (int)min((unsigned)x.g * per, nc);
+    x.c1 = (int)min((unsigned)x.c0 + per, nc);
     return x;
 }
-__device__ __forceinline__ long n_units(const LinearParams &p) { return (long)p.B * p.Hv * p.G_run; }
-
-// The CTA's chunks, unit after unit.
-struct Cursor {
-    long u;
-    int c;
-    Unit x;
-    __device__ __forceinline__ void start() {
-        u = (long)blockIdx.x - gridDim.x;
-        c = 0;
-        x.c1 = 0;
-    }
-    __device__ __forceinline__ bool next(const LinearParams &p) {
-        ++c;
-        while (c >= x.c1) {
-            u += gridDim.x;
-            if (u >= n_units(p)) return false;
-            x = unit_at(p, u);
-            c = x.c0;
-        }
-        return true;
-    }
-};
 
 template <typename E, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -184,24 +168,25 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_align1k(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + oBar), *empty = full + NS;
-    uint64_t *r_done = empty + NS, *r_free = r_done + 1, *p_ready = r_done + 2, *w_ready = r_done + 3,
-             *ds_done = r_done + 4, *ds_free = r_done + 5, *qs_done = r_done + 6, *s_ready = r_done + 7,
-             *o_done = r_done + 8, *o_free = r_done + 9, *drain = r_done + 10;
-    uint32_t *slot = reinterpret_cast<uint32_t *>(r_done + 11);
+    uint64_t *ds_done = empty + NS;  // [4]: after each 16 tokens of the product
+    uint64_t *r_done = ds_done + 4, *r_free = r_done + 1, *p_ready = r_done + 2, *w_ready = r_done + 3,
+             *ds_free = r_done + 4, *qs_done = r_done + 5, *s_ready = r_done + 6, *o_done = r_done + 7,
+             *o_free = r_done + 8, *drain = r_done + 9;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(r_done + 10);
     // (through a shuffle: known to be the same in every lane)
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int dk = p.dk, dv = p.dv, Hv = p.Hv, Hk = p.Hk;
+    const int dk = p.dk, dv = p.dv, Hv = p.Hv;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&full[s], 2);                  // the copies' thread, the decay sums
+            mbar_init(&full[s], 2);                          // the copies' bytes, the decay sums
             mbar_init(&empty[s], kOut ? 1 + 4 + 4 : 1 + 4);  // MMAs, state warps, output warps
         }
+        for (int j = 0; j < 4; ++j) mbar_init(&ds_done[j], 1);
         mbar_init(r_done, 1);
         mbar_init(r_free, 2);
         mbar_init(p_ready, 2);
         mbar_init(w_ready, 4);
-        mbar_init(ds_done, 1);
         mbar_init(ds_free, 4);
         mbar_init(qs_done, 1);
         mbar_init(s_ready, 4);
@@ -222,10 +207,15 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     // A wait of a whole warp: the outcome is the same in every lane, so that
     // the warp-wide TMEM accesses behind it stay converged.
     auto wait = [&](uint64_t *bar, int it) {
-        const bool done = mbar_wait(bar, (uint32_t)it & 1u, p.wait_ns);
-        return __all_sync(0xffffffffu, done) != 0;
+        return __all_sync(0xffffffffu, mbar_wait_spins(bar, (uint32_t)it & 1u, p.spins)) != 0;
     };
-    auto wait_full = [&](int it) { return wait(&full[it % NS], it / NS); };
+    auto gate_of = [&](int it) { return reinterpret_cast<float *>(sm + oGate + (it % NS) * kGate); };
+    // The chunk's tiles and sums are there; its tokens n, or 0 past the last one
+    // (and -1 where the wait ran out).
+    auto chunk = [&](int it) {
+        if (!wait(&full[it % NS], it / NS)) return -1;
+        return reinterpret_cast<const int *>(gate_of(it))[gN];
+    };
     auto arrive = [&](uint64_t *bar) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
@@ -261,7 +251,8 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
 #pragma unroll 1
             for (int s = 0; s < n; ++s) add_row(p.seg_state + (seg0 + s) * mat, p.seg_decay[seg0 + s]);
         };
-        for (long u = blockIdx.x; ok && u < n_units(p); u += gridDim.x) {
+#pragma unroll 1
+        for (unsigned u = blockIdx.x; ok && u < p.n_units; u += gridDim.x) {
             const Unit x = unit_at(p, u);
             const size_t seg0 = ((size_t)x.b * Hv + x.h) * p.G;
             clear();
@@ -276,16 +267,18 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             for (int c = x.c0; c < x.c1; ++c, ++it) {
                 if constexpr (kOut) {
                     // this chunk's start state as an MMA operand
-                    float sc = 1.f;
+                    float sc = 1.f, inv = 1.f;
                     if constexpr (!kBf) {
-                        float m = 0.f, inv;
+                        float m = 0.f;
 #pragma unroll
                         for (int j = 0; j < 64; ++j) m = fmaxf(m, fmaxf(fabsf(S[j].x), fabsf(S[j].y)));
                         half_scale(m, sc, inv);
-                        sinv[(it & 1) * 128 + i] = inv;
                     }
                     if (it > 0 && !(ok = wait(qs_done, it - 1))) break;
                     fence_after_sync();
+                    // (the outputs two chunks back have read their scales: that
+                    // product was issued after them)
+                    if constexpr (!kBf) sinv[(it & 1) * 128 + i] = inv;
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         if (g * 32 < dk) {
@@ -302,22 +295,27 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     arrive(s_ready);
                 }
                 // S <- 2^b_63 S + dS
-                if (!(ok = wait_full(it)) || !(ok = wait(ds_done, it))) break;
+                if (!(ok = chunk(it) > 0) || !(ok = wait(&ds_done[3], it))) break;
                 fence_after_sync();
-                const float gam = reinterpret_cast<const float *>(sm + oGate + (it % NS) * kGate)[192];
+                const float gam = gate_of(it)[gLast];
                 const float wi = kBf ? 1.f : winv[(it & 1) * 128 + i];
                 const float2 gam2 = make_float2(gam, gam), wi2 = make_float2(wi, wi);
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
+                for (int g = 0; g < 4; g += 2) {
                     if (g * 32 < dk) {
-                        float v[32];
-                        tmem_ld32(lane_base + tDS + 32 * g, v);
+                        uint32_t v[2][32];
+                        tmem_ld32_async(lane_base + tDS + 32 * g, v[0]);
+                        if (g * 32 + 32 < dk) tmem_ld32_async(lane_base + tDS + 32 * g + 32, v[1]);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float2 d = make_float2(v[2 * j], v[2 * j + 1]);
-                            if constexpr (!kBf) d = __fmul2_rn(wi2, d);
-                            S[16 * g + j] = __ffma2_rn(gam2, S[16 * g + j], d);
-                        }
+                        for (int h = 0; h < 2; ++h)
+                            if (g * 32 + h * 32 < dk)
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) {
+                                    float2 d = make_float2(__uint_as_float(v[h][2 * j]), __uint_as_float(v[h][2 * j + 1]));
+                                    if constexpr (!kBf) d = __fmul2_rn(wi2, d);
+                                    S[16 * (g + h) + j] = __ffma2_rn(gam2, S[16 * (g + h) + j], d);
+                                }
                     }
                 }
                 kept *= gam;
@@ -349,26 +347,25 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
         }
     } else if (warp < 8) {
         // ============================== W ================================
-        const int wq = warp - 4, tid = threadIdx.x - 128;
+        const int wq = warp - 4;
         const uint32_t lane_base = tm + ((uint32_t)(wq * 32) << 16);
-        float *winv = reinterpret_cast<float *>(sm + oWInv);
+        float *winv = reinterpret_cast<float *>(sm + oWInv) + wq * 32 + (lane >> 2);
         // ldmatrix: this lane's row of the four 8 x 8 matrices (tokens 0-7 and
         // 8-15 of 16, features 0-7 and 8-15 of 16)
         const int row = (lane & 7) + ((lane >> 4) << 3), cg = (wq & 1) * 4 + ((lane >> 3) & 1);
         const uint32_t v_off = kStageV + (wq >> 1) * 8192 + row * 128;
-        Cursor k;
-        k.start();
 #pragma unroll 1
-        for (int it = 0; k.next(p); ++it) {
-            const int n = min(C, k.x.len - k.c * C);
-            if (!(ok = wait_full(it))) break;
+        for (int it = 0;; ++it) {
+            const int n = chunk(it);
+            ok = n >= 0;
+            if (n <= 0) break;
             uint8_t *st = sm + (it % NS) * kStage;
-            const float *w = reinterpret_cast<const float *>(sm + oGate + (it % NS) * kGate) + 128 + 2 * (lane & 3);
+            const float *w = gate_of(it) + gW + 2 * (lane & 3);
             if (n < C) {
                 // K and V rows past the row's end: zeros, whatever was loaded
 #pragma unroll 1
-                for (int e = tid; e < (C - n) * 8; e += 128) {
-                    const int r = n + (e >> 3), off = r * 128 + (e & 7) * 16;
+                for (int e = threadIdx.x - 128; e < (C - n) * 8; e += 128) {
+                    const int off = (n + (e >> 3)) * 128 + (e & 7) * 16;
                     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
                     *reinterpret_cast<uint4 *>(st + off) = z;
                     *reinterpret_cast<uint4 *>(st + kBlock + off) = z;
@@ -378,79 +375,91 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 fence_proxy_async();
                 named_bar(kBarW, 128);
             }
-            // 16 features at a time: lanes g and g + 8 of them, tokens 2 t, 2 t + 1
-            // of each eight, in the layout of the TMEM store
-#pragma unroll 1
-            for (int hh = 0; hh < 2; ++hh) {
-                uint32_t part[NT][16];
-                float2 x[16];
+            // 16 tokens (j), 16 features (hh): features g and g + 8, tokens 2 t, 2 t + 1
+            // of each eight, which is the layout of the TMEM store
+            auto scaled = [&](int j, int hh, float2 (&x)[4]) {
+                uint32_t v[4];
+                ldsm_x4_trans(v, st + v_off + j * 2048 + (((cg + 2 * hh) ^ (lane & 7)) << 4));
+                const float2 w0 = *reinterpret_cast<const float2 *>(w + 16 * j);
+                const float2 w1 = *reinterpret_cast<const float2 *>(w + 16 * j + 8);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t v[4];
-                    ldsm_x4_trans(v, st + v_off + j * 2048 + (((cg + 2 * hh) ^ (lane & 7)) << 4));
+                for (int e = 0; e < 4; ++e) x[e] = __fmul2_rn(e < 2 ? w0 : w1, H::unpack2(v[e]));
+            };
+            float sc[4] = {1.f, 1.f, 1.f, 1.f}, inv[4];
+            if constexpr (!kBf) {
+                // the largest magnitude of each feature gives its scale; the four
+                // lanes of a group hold a feature's tokens
+                float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        float2 x[4];
+                        scaled(j, hh, x);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            m[2 * hh + (e & 1)] = fmaxf(m[2 * hh + (e & 1)], fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+                    }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], 1));
+                    m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], 2));
+                    half_scale(m[e], sc[e], inv[e]);
+                }
+            }
+            // Each 16 tokens of W are replaced as soon as the last chunk's product
+            // has read theirs.
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                uint32_t part[2][NT][4];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    float2 x[4];
+                    scaled(j, hh, x);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 w2 = *reinterpret_cast<const float2 *>(w + 16 * j + 8 * (e >> 1));
-                        x[4 * j + e] = __fmul2_rn(w2, H::unpack2(v[e]));
-                    }
-                }
-                if constexpr (kBf) {
-                    // the upper 16 bits are a bf16 by truncation; what is left is exact
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
                         float2 r = x[e];
+                        if constexpr (kBf) {
+                            // the upper 16 bits are a bf16 by truncation; what is left is exact
 #pragma unroll
-                        for (int m = 0; m < NT - 1; ++m) {
-                            const uint32_t a = __float_as_uint(r.x), b = __float_as_uint(r.y);
-                            part[m][e] = __byte_perm(a, b, 0x7632);
-                            r = __fadd2_rn(r, make_float2(__uint_as_float((a & 0xffff0000u) ^ 0x80000000u),
-                                                          __uint_as_float((b & 0xffff0000u) ^ 0x80000000u)));
+                            for (int m = 0; m < NT - 1; ++m) {
+                                const uint32_t a = __float_as_uint(r.x), b = __float_as_uint(r.y);
+                                part[hh][m][e] = __byte_perm(a, b, 0x7632);
+                                r = __fadd2_rn(r, make_float2(__uint_as_float((a & 0xffff0000u) ^ 0x80000000u),
+                                                              __uint_as_float((b & 0xffff0000u) ^ 0x80000000u)));
+                            }
+                            part[hh][NT - 1][e] = H::pack2(r.x, r.y);
+                        } else {
+                            const float s = sc[2 * hh + (e & 1)];
+                            r = __fmul2_rn(make_float2(s, s), r);
+                            part[hh][0][e] = H::pack2(r.x, r.y);
+                            const float2 h = H::unpack2(part[hh][0][e]);
+                            part[hh][1][e] = H::pack2(r.x - h.x, r.y - h.y);
                         }
-                        part[NT - 1][e] = H::pack2(r.x, r.y);
-                    }
-                } else {
-                    // the largest magnitude of each of the two features, over its
-                    // four lanes, gives its scale
-                    float m0 = 0.f, m1 = 0.f, s0, s1, i0, i1;
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        m0 = fmaxf(m0, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
-                        m1 = fmaxf(m1, fmaxf(fabsf(x[e + 1].x), fabsf(x[e + 1].y)));
-                    }
-#pragma unroll
-                    for (int o = 1; o < 4; o <<= 1) {
-                        m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-                        m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
-                    }
-                    half_scale(m0, s0, i0);
-                    half_scale(m1, s1, i1);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float s = (e & 1) ? s1 : s0;
-                        const float2 y = __fmul2_rn(make_float2(s, s), x[e]);
-                        part[0][e] = H::pack2(y.x, y.y);
-                        const float2 h = H::unpack2(part[0][e]);
-                        part[1][e] = H::pack2(y.x - h.x, y.y - h.y);
-                    }
-                    if (hh == 0 && it > 0 && !(ok = wait(ds_done, it - 1))) break;
-                    if ((lane & 3) == 0) {
-                        winv[(it & 1) * 128 + wq * 32 + 16 * hh + (lane >> 2)] = i0;
-                        winv[(it & 1) * 128 + wq * 32 + 16 * hh + (lane >> 2) + 8] = i1;
                     }
                 }
-                if (kBf && hh == 0 && it > 0 && !(ok = wait(ds_done, it - 1))) break;
+                if (it > 0 && !(ok = wait(&ds_done[j], it - 1))) break;
                 fence_after_sync();
 #pragma unroll
-                for (int m = 0; m < NT; ++m) tmem_st_16x32(lane_base + ((uint32_t)(16 * hh) << 16) + tW + 32 * m, part[m]);
+                for (int m = 0; m < NT; ++m)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh)
+                        tmem_st_16x8(lane_base + ((uint32_t)(16 * hh) << 16) + tW + 32 * m + 8 * j, part[hh][m]);
             }
             if (!ok) break;
+            // (the last wait was for the whole of the last product, which was
+            // issued after the state warps had read the scales before its own)
+            if constexpr (!kBf)
+                if ((lane & 3) == 0)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) winv[(it & 1) * 128 + 8 * e] = inv[e];
             tmem_wait_st();
             fence_before_sync();
             arrive(w_ready);
         }
     } else if (warp < 12) {
         // ============================ outputs ============================
-        regs_dec<96>();
+        regs_dec<80>();
         if constexpr (kOut) {
             const int wq = warp - 8;
             const uint32_t lane_base = tm + ((uint32_t)(wq * 32) << 16);
@@ -460,15 +469,15 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             // stmatrix: this lane's row (token) of the four 8 x 8 matrices (features
             // 0-7 and 8-15 of 16, tokens 0-7 and 8-15 of 16)
             const int row = (lane & 7) + ((lane >> 4) << 3), cg = (lane >> 3) & 1;
-            const bool mine = wq * 32 < dv;
-            Cursor k;
-            k.start();
 #pragma unroll 1
-            for (int it = 0; k.next(p); ++it) {
-                const int n = min(C, k.x.len - k.c * C);
-                if (!(ok = wait_full(it)) || !(ok = wait(o_done, it))) break;
+            for (int it = 0;; ++it) {
+                const int n = chunk(it);
+                ok = n >= 0;
+                if (n <= 0 || !(ok = wait(o_done, it))) break;
                 fence_after_sync();
-                const float *eb = reinterpret_cast<const float *>(sm + oGate + (it % NS) * kGate) + 64 + 2 * (lane & 3);
+                const float *eb = gate_of(it) + gScaled + 2 * (lane & 3);
+                const int t0 = reinterpret_cast<const int *>(gate_of(it))[gTok];
+                const int h = reinterpret_cast<const int *>(gate_of(it))[gHead];
                 if (lane == 0) bulk_wait_read_all();  // the last chunk's tile has left
                 __syncwarp();
 #pragma unroll 1
@@ -509,20 +518,20 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 fence_before_sync();
                 arrive(o_free);
                 arrive(&empty[it % NS]);
-                const long t0 = k.x.tok0 + (long)k.c * C;
-                if (mine && n == C) {
+                if (wq * 32 >= dv) continue;
+                if (n == C) {
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_3d(&mo, wq * 32, k.x.h, (int)t0, buf);
+                        tma_store_3d(&mo, wq * 32, h, t0, buf);
                         bulk_commit();
                     }
-                } else if (mine) {  // the next row's tokens stay untouched
+                } else {  // the next row's tokens stay untouched
                     __syncwarp();
 #pragma unroll 1
                     for (int e = lane; e < n * 4; e += 32) {
                         const int t = e >> 2, q = e & 3;
-                        *reinterpret_cast<uint4 *>(reinterpret_cast<E *>(p.out) + ((t0 + t) * Hv + k.x.h) * dv + wq * 32 + 8 * q) =
+                        *reinterpret_cast<uint4 *>(reinterpret_cast<E *>(p.out) + ((long)(t0 + t) * Hv + h) * dv + wq * 32 + 8 * q) =
                             *reinterpret_cast<const uint4 *>(buf + t * 64 + ((q ^ ((t >> 1) & 3)) << 4));
                     }
                     __syncwarp();
@@ -531,210 +540,274 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             if (lane == 0) bulk_wait_all();
         }
     } else {
-        regs_dec<88>();
+        regs_dec<104>();
+        const uint32_t leader = elect_leader();
         if (warp == 12) {
             // ====================== tiles, decay sums ====================
-            int issued = 0;
-            Cursor k;
-            k.start();
             const bool per_head = (p.conv & GDN_ALPHA_PER_HEAD) != 0;
-            float raw[2] = {0.f, 0.f};
-            auto fetch = [&]() {  // the chunk's decays of tokens 2 lane, 2 lane + 1 as they are stored
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = k.c * C + 2 * lane + e;
-                    if (t < k.x.len)
-                        raw[e] = ld_gate_early(p.alpha, per_head ? (long)k.x.h : (k.x.tok0 + t) * Hv + k.x.h, p.dt_gate);
+            const int G = Hv / p.Hk;
+            unsigned u = blockIdx.x - gridDim.x;  // (wraps to blockIdx.x at the first step)
+            Unit x;
+            x.c1 = 0;
+            int c = 0, t0 = 0, n = 0, h = 0;  // the chunk that is next: first token, tokens, head
+            float raw[2] = {0.f, 0.f};        // its decays of tokens 2 lane, 2 lane + 1, as stored
+            int it = -1;
+#pragma unroll 1
+            for (;; ++it) {
+                const int t0_ = t0, n_ = n, h_ = h;
+                float a[2] = {raw[0], raw[1]};
+                // the one after it, and its decays: they arrive while this one is worked on
+                n = 0;
+                ++c;
+#pragma unroll 1
+                while (c >= x.c1) {
+                    u += gridDim.x;
+                    if (u >= p.n_units) break;
+                    x = unit_at(p, u);
+                    c = x.c0;
                 }
-            };
-            bool more = k.next(p);
-            if (more) fetch();
-            for (int it = 0; more; ++it) {
+                if (u < p.n_units) {
+                    t0 = (int)(x.tok0 + (long)c * C);
+                    n = min(C, x.len - c * C);
+                    h = x.h;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (2 * lane + e < n)
+                            raw[e] = ld_gate_early(p.alpha, per_head ? (long)h : (long)(t0 + 2 * lane + e) * Hv + h, p.dt_gate);
+                }
+                if (it < 0) continue;
                 const int s = it % NS;
                 uint8_t *st = sm + s * kStage;
                 if (it >= NS && !(ok = wait(&empty[s], it / NS - 1))) break;
+                float *gate = gate_of(it);
                 if (lane == 0) {
-                    const int hk = k.x.h / (Hv / Hk), t0 = (int)(k.x.tok0 + (long)k.c * C);
-                    const int kb = dk > 64 ? 2 : 1, vb = dv > 64 ? 2 : 1;
-                    mbar_arrive_expect_tx(&full[s], 8192u * (kb * (kOut ? 2 : 1) + vb));
-                    for (int j = 0; j < kb; ++j) {
-                        tma_load_3d(st + j * kBlock, &mk, 64 * j, hk, t0, &full[s]);
-                        if constexpr (kOut) tma_load_3d(st + j * kBlock + 8192, &mq, 64 * j, hk, t0, &full[s]);
-                    }
-                    for (int j = 0; j < vb; ++j) tma_load_3d(st + kStageV + j * 8192, &mv, 64 * j, k.x.h, t0, &full[s]);
+                    reinterpret_cast<int *>(gate)[gN] = n_;
+                    reinterpret_cast<int *>(gate)[gTok] = t0_;
+                    reinterpret_cast<int *>(gate)[gHead] = h_;
+                    mbar_arrive_expect_tx(
+                        &full[s], n_ == 0 ? 0u : 8192u * ((dk > 64 ? 2 : 1) * (kOut ? 2 : 1) + (dv > 64 ? 2 : 1)));
                 }
-                ++issued;
-                float a[2];
+                __syncwarp();
+                if (n_ == 0) {  // past the last chunk
+                    arrive(&full[s]);
+                    break;
+                }
+                const int hk = h_ / G;
+#pragma unroll 1
+                for (int j = 0; j < 2; ++j) {
+                    if (64 * j < dk) {
+                        tma_load_3d_warp(leader, st + j * kBlock, &mk, 64 * j, hk, t0_, &full[s]);
+                        if constexpr (kOut) tma_load_3d_warp(leader, st + j * kBlock + 8192, &mq, 64 * j, hk, t0_, &full[s]);
+                    }
+                    if (64 * j < dv) tma_load_3d_warp(leader, st + kStageV + j * 8192, &mv, 64 * j, h_, t0_, &full[s]);
+                }
+                // Inclusive sums over the lanes from both ends; the exclusive ones
+                // are the neighbours' (a difference would lose what a strong decay
+                // has in front of it, and be no number after a decay of 0).  For
+                // P's differences a decay below 2^-40 (0 among them) counts as 2^-40,
+                // far below the scores' own rounding: the sums stay finite, and small
+                // enough for their differences to be exact to 2^-12.
+                float held[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    a[e] = (p.conv & GDN_ALPHA_LOG) ? raw[e] * kLog2e : log2f(raw[e]);
-                    if (k.c * C + 2 * lane + e >= k.x.len) a[e] = 0.f;
+                    a[e] = 2 * lane + e >= n_ ? 0.f : (p.conv & GDN_ALPHA_LOG) ? a[e] * kLog2e : log2f(a[e]);
+                    held[e] = a[e] < -40.f ? -40.f : a[e];
                 }
-                more = k.next(p);
-                if (more) fetch();
-                // inclusive sums over the lanes from both ends; the exclusive ones
-                // are the neighbours' (a difference would lose what a strong decay
-                // has in front of it, and be no number after a decay of 0)
-                auto scan = [&](float v, bool up) {
+                float up = a[0] + a[1], down = up, hup = held[0] + held[1];
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const float y = up ? __shfl_up_sync(0xffffffffu, v, o) : __shfl_down_sync(0xffffffffu, v, o);
-                        if (up ? lane >= o : lane + o < 32) v += y;
-                    }
-                    return v;
-                };
-                float *gate = reinterpret_cast<float *>(sm + oGate + s * kGate);
-                const float inc = scan(a[0] + a[1], true);
-                float ex = __shfl_up_sync(0xffffffffu, inc, 1);
-                if (lane == 0) ex = 0.f;
-                float suf = __shfl_down_sync(0xffffffffu, scan(a[0] + a[1], false), 1);
-                if (lane == 31) suf = 0.f;
-                float2 bc = make_float2(ex + a[0], inc);
-                gate[64 + 2 * lane] = p.scale * exp2f(bc.x);
-                gate[64 + 2 * lane + 1] = p.scale * exp2f(bc.y);
-                gate[128 + 2 * lane] = exp2f(suf + a[1]);
-                gate[128 + 2 * lane + 1] = exp2f(suf);
-                if (lane == 31) gate[192] = exp2f(inc);
-                // For P's differences a decay below 2^-40 (0 among them) counts as
-                // 2^-40, far below the scores' own rounding: the sums stay finite,
-                // and small enough for their differences to be exact to 2^-12.
-                const bool strong = a[0] < -40.f || a[1] < -40.f;
-                if (__any_sync(0xffffffffu, strong)) {
-                    const float c0 = a[0] < -40.f ? -40.f : a[0], c1 = a[1] < -40.f ? -40.f : a[1];
-                    const float ic = scan(c0 + c1, true);
-                    float ec = __shfl_up_sync(0xffffffffu, ic, 1);
-                    if (lane == 0) ec = 0.f;
-                    bc = make_float2(ec + c0, ic);
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float y0 = __shfl_up_sync(0xffffffffu, up, o), y1 = __shfl_down_sync(0xffffffffu, down, o);
+                    const float y2 = __shfl_up_sync(0xffffffffu, hup, o);
+                    if (lane >= o) up += y0, hup += y2;
+                    if (lane + o < 32) down += y1;
                 }
-                *reinterpret_cast<float2 *>(gate + 2 * lane) = bc;
+                float ex = __shfl_up_sync(0xffffffffu, up, 1), eh = __shfl_up_sync(0xffffffffu, hup, 1);
+                float suf = __shfl_down_sync(0xffffffffu, down, 1);
+                if (lane == 0) ex = eh = 0.f;
+                if (lane == 31) suf = 0.f;
+                const float b31 = __shfl_sync(0xffffffffu, hup, 15);
+                const float2 b2 = make_float2(eh + held[0], hup);
+                *reinterpret_cast<float2 *>(gate + gSum + 2 * lane) = b2;
+                *reinterpret_cast<float2 *>(gate + gScaled + 2 * lane) =
+                    make_float2(p.scale * ex2_approx(ex + a[0]), p.scale * ex2_approx(up));
+                *reinterpret_cast<float2 *>(gate + gW + 2 * lane) = make_float2(ex2_approx(suf + a[1]), ex2_approx(suf));
+                if (lane < 16)
+                    *reinterpret_cast<float2 *>(gate + gLeft + 2 * lane) =
+                        make_float2(ex2_approx(b31 - b2.x), ex2_approx(b31 - b2.y));
+                if (lane == 31) gate[gLast] = ex2_approx(up);
                 arrive(&full[s]);
             }
             if (!ok)  // the copies in flight must land before the CTA ends
-                for (int j = issued > NS ? issued - NS : 0; j < issued; ++j)
+                for (int j = it > NS ? it - NS : 0; j < it; ++j)
                     mbar_wait(&full[j % NS], (uint32_t)(j / NS) & 1u, kDefaultWaitNs);
         } else if (warp == 13) {
             // =========================== MMAs ============================
             const uint32_t id_r = idesc_f16(128, 64, false, false, kBf);
             const uint32_t id_o1 = idesc_f16(128, 64, true, false, kBf);
-            const uint32_t id_o2 = idesc_f16(128, 64, false, false, kBf);
             const uint32_t id_ds = idesc_f16(128, dk, false, true, kBf);
             const int ks = dk / 16;  // K = 16 steps over dk
             const uint32_t s0 = smem_u32(sm);
+            // (loops are kept rolled: an MMA takes longer than its turn)
             auto raw_scores = [&](int it) {
-                if (!wait_full(it) || (it > 0 && !wait(r_free, it - 1))) return false;
+                if (it > 0 && !wait(r_free, it - 1)) return false;
                 fence_after_sync();
-                const uint64_t kq = desc_sw128(s0 + (it % NS) * kStage, 16, 1024);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if (k >= ks) break;
-                    const uint64_t d = desc_add(kq, (k >> 2) * kBlock + (k & 3) * 32);
-                    mma_f16_elect(tm + tR, d, d, id_r, k > 0);
+                uint64_t d = desc_sw128(s0 + (it % NS) * kStage, 16, 1024);
+#pragma unroll 1
+                for (int k = 0; k < ks; ++k) {
+                    mma_f16_warp(leader, tm + tR, d, d, id_r, k > 0);
+                    d = desc_add(d, k == 3 ? kBlock - 96 : 32);
                 }
-                mma_commit_elect(r_done);
+                mma_commit_warp(leader, r_done);
                 return true;
             };
-            Cursor k;
-            k.start();
-            bool more = k.next(p);
-            if constexpr (kOut) ok = !more || raw_scores(0);
+            int n = chunk(0);
+            ok = n >= 0;
+            if (kOut && n > 0) ok = raw_scores(0);
 #pragma unroll 1
-            for (int it = 0; ok && more; ++it) {
+            for (int it = 0; ok && n > 0; ++it) {
                 const uint32_t st = s0 + (it % NS) * kStage;
-                // dS = W^T K, every part of W
-                if (!(ok = wait_full(it)) || !(ok = wait(w_ready, it)) || (it > 0 && !(ok = wait(ds_free, it - 1)))) break;
+                // dS = W^T K, 16 tokens of every part of W at a time
+                if (!(ok = wait(w_ready, it)) || (it > 0 && !(ok = wait(ds_free, it - 1)))) break;
                 fence_after_sync();
-                const uint64_t kn = desc_sw128(st, kBlock, 1024);
+                uint64_t kn = desc_sw128(st, kBlock, 1024);
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
 #pragma unroll
-                for (int m = 0; m < NT; ++m)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_f16_ta_elect(tm + tDS, tm + tW + 32 * m + 8 * j, desc_add(kn, j * 2048), id_ds, m + j > 0);
-                mma_commit_elect(ds_done);
+                    for (int m = 0; m < NT; ++m)
+                        mma_f16_ta_warp(leader, tm + tDS, tm + tW + 32 * m + 8 * j, kn, id_ds, m + j > 0);
+                    mma_commit_warp(leader, &ds_done[j]);
+                    kn = desc_add(kn, 2048);
+                }
                 if constexpr (kOut) {
                     // O2^T = S Q^T
                     if (!(ok = wait(s_ready, it)) || (it > 0 && !(ok = wait(o_free, it - 1)))) break;
                     fence_after_sync();
-                    const uint64_t qd = desc_sw128(st + 8192, 16, 1024);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        if (j >= ks) break;
-                        mma_f16_ta_elect(tm + tO2, tm + tS + 8 * j, desc_add(qd, (j >> 2) * kBlock + (j & 3) * 32), id_o2,
-                                         j > 0);
+                    uint64_t qd = desc_sw128(st + 8192, 16, 1024);
+#pragma unroll 1
+                    for (int k = 0; k < ks; ++k) {
+                        mma_f16_ta_warp(leader, tm + tO2, tm + tS + 8 * k, qd, id_r, k > 0);
+                        qd = desc_add(qd, k == 3 ? kBlock - 96 : 32);
                     }
-                    mma_commit_elect(qs_done);
+                    mma_commit_warp(leader, qs_done);
+                    // R of the next chunk
+                    n = chunk(it + 1);
+                    if (!(ok = n >= 0) || (n > 0 && !(ok = raw_scores(it + 1)))) break;
                     // O1^T = V^T P^T
                     if (!(ok = wait(p_ready, it))) break;
                     fence_after_sync();
-                    const uint64_t vd = desc_sw128(st + kStageV, 8192, 1024), pd = desc_sw128(s0 + oP, 16, 1024);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_f16_elect(tm + tO1, desc_add(vd, j * 2048), desc_add(pd, j * 32), id_o1, j > 0);
-                    mma_commit_elect(o_done);
+                    uint64_t vd = desc_sw128(st + kStageV, 8192, 1024), pd = desc_sw128(s0 + oP, 16, 1024);
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j) {
+                        mma_f16_warp(leader, tm + tO1, vd, pd, id_o1, j > 0);
+                        vd = desc_add(vd, 2048);
+                        pd = desc_add(pd, 32);
+                    }
+                    mma_commit_warp(leader, o_done);
+                    mma_commit_warp(leader, &empty[it % NS]);
+                } else {
+                    mma_commit_warp(leader, &empty[it % NS]);
+                    n = chunk(it + 1);
+                    ok = n >= 0;
                 }
-                mma_commit_elect(&empty[it % NS]);
-                more = k.next(p);
-                if constexpr (kOut)
-                    if (more && !(ok = raw_scores(it + 1))) break;
             }
-            mma_commit_elect(drain);  // nothing may be in flight when TMEM is given back
+            mma_commit_warp(leader, drain);  // nothing may be in flight when TMEM is given back
             mbar_wait(drain, 0, kDefaultWaitNs);
-        } else {
+        } else if constexpr (kOut) {
             // ============================= P =============================
-            if constexpr (kOut) {
-                const int i = (warp - 14) * 32 + lane;  // token of the chunk
-                const uint32_t lane_base = tm + ((uint32_t)(64 + (warp - 14) * 32) << 16);
-                float *pinv = reinterpret_cast<float *>(sm + oPInv);
-                Cursor k;
-                k.start();
-                for (int it = 0; k.next(p); ++it) {
-                    if (!(ok = wait_full(it)) || !(ok = wait(r_done, it))) break;
-                    fence_after_sync();
-                    const float *b = reinterpret_cast<const float *>(sm + oGate + (it % NS) * kGate);
-                    const float bi = b[i];
-                    // 16 columns of the row: zero above the diagonal
-                    auto columns = [&](int cb, float (&x)[16]) {
-                        tmem_ld16(lane_base + tR + 16 * cb, x);
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 b4 = *reinterpret_cast<const float4 *>(b + 16 * cb + j);
-                            const float bs[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                x[j + e] = 16 * cb + j + e <= i ? x[j + e] * p.scale * ex2_approx(bi - bs[e]) : 0.f;
-                        }
-                    };
-                    const int blocks = 2 * (warp - 14) + 2;  // the warp's rows end in column 16 blocks - 1
-                    float sc = 1.f;
-                    if constexpr (!kBf) {
-                        float m = 0.f, inv;
+            const int diag = 32 * (warp - 14);  // the rows' diagonal block of 32 columns
+            const int i = diag + lane;          // token of the chunk
+            const uint32_t lane_base = tm + ((uint32_t)(64 + diag) << 16);
+            float *pinv = reinterpret_cast<float *>(sm + oPInv);
+            const float2 scale2 = make_float2(p.scale, p.scale);
+            if (diag == 0)  // right of the first rows' diagonal block: zeros, once
 #pragma unroll 1
-                        for (int cb = 0; cb < blocks; ++cb) {
-                            float x[16];
-                            columns(cb, x);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(x[j]));
-                        }
-                        half_scale(m, sc, inv);
-                        pinv[(it & 1) * 64 + i] = inv;
-                    }
+                for (int q = 4; q < 8; ++q)
+                    *reinterpret_cast<uint4 *>(sm + oP + sw128_chunk(i, q)) = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
-                    for (int cb = 0; cb < 4; ++cb) {
-                        uint32_t v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-                        if (cb < blocks) {
-                            float x[16];
-                            columns(cb, x);
+            for (int it = 0;; ++it) {
+                const int n = chunk(it);
+                ok = n >= 0;
+                if (n <= 0 || !(ok = wait(r_done, it))) break;
+                fence_after_sync();
+                const float *gate = gate_of(it);
+                const float bi = gate[gSum + i];
+                // 2^{b_i - b_31} of the columns left of the diagonal block: with
+                // 2^{b_31 - b_j} two factors of at most 1 where no decay is above 1
+                const float l = p.scale * ex2_approx(bi - gate[gSum + 31]);
+                const float2 l2 = make_float2(l, l);
+                // 16 columns from diag + 16 hh on, and the 16 from 16 hh on
+                auto columns = [&](int hh, uint32_t (&x)[16], uint32_t (&y)[16]) {
+                    tmem_ld16_async(lane_base + tR + diag + 16 * hh, x);
+                    if (diag > 0) tmem_ld16_async(lane_base + tR + 16 * hh, y);
+                    tmem_wait_ld();
+                };
+                auto decayed = [&](int hh, uint32_t (&x)[16], uint32_t (&y)[16], float &m) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                v[j] = kBf ? H::pack2(x[2 * j], x[2 * j + 1]) : H::pack2(sc * x[2 * j], sc * x[2 * j + 1]);
-                        }
-                        *reinterpret_cast<uint4 *>(sm + oP + sw128_chunk(i, 2 * cb)) = make_uint4(v[0], v[1], v[2], v[3]);
-                        *reinterpret_cast<uint4 *>(sm + oP + sw128_chunk(i, 2 * cb + 1)) = make_uint4(v[4], v[5], v[6], v[7]);
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 b2 = *reinterpret_cast<const float2 *>(gate + gSum + diag + 16 * hh + j);
+                        float2 v = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                        v = __fmul2_rn(__fmul2_rn(v, scale2), make_float2(ex2_approx(bi - b2.x), ex2_approx(bi - b2.y)));
+                        v.x = 16 * hh + j <= lane ? v.x : 0.f;
+                        v.y = 16 * hh + j + 1 <= lane ? v.y : 0.f;
+                        if constexpr (!kBf) m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
+                        x[j] = __float_as_uint(v.x);
+                        x[j + 1] = __float_as_uint(v.y);
                     }
-                    fence_before_sync();
-                    arrive(r_free);
-                    fence_proxy_async();
-                    arrive(p_ready);
+                    if (diag > 0)
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 c2 = *reinterpret_cast<const float2 *>(gate + gLeft + 16 * hh + j);
+                            const float2 v =
+                                __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), c2), l2);
+                            if constexpr (!kBf) m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
+                            y[j] = __float_as_uint(v.x);
+                            y[j + 1] = __float_as_uint(v.y);
+                        }
+                };
+                float sc = 1.f, inv = 1.f, m = 0.f;
+                if constexpr (!kBf) {
+#pragma unroll 1
+                    for (int hh = 0; hh < 2; ++hh) {
+                        uint32_t x[16], y[16];
+                        columns(hh, x, y);
+                        decayed(hh, x, y, m);
+                    }
+                    half_scale(m, sc, inv);
                 }
+                auto store = [&](int q, const uint32_t *z) {  // eight columns from 8 q on
+                    uint32_t v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float a = __uint_as_float(z[2 * e]), b = __uint_as_float(z[2 * e + 1]);
+                        v[e] = kBf ? H::pack2(a, b) : H::pack2(sc * a, sc * b);
+                    }
+                    *reinterpret_cast<uint4 *>(sm + oP + sw128_chunk(i, q)) = make_uint4(v[0], v[1], v[2], v[3]);
+                };
+#pragma unroll 1
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t x[16], y[16];
+                    columns(hh, x, y);
+                    if (hh == 1) {
+                        fence_before_sync();
+                        arrive(r_free);
+                    }
+                    decayed(hh, x, y, m);
+                    if (hh == 0) {
+                        // the products with the last chunk's P are done (and so are
+                        // the reads of the scales of the one before)
+                        if (it > 0 && !(ok = wait(o_done, it - 1))) break;
+                        if constexpr (!kBf) pinv[(it & 1) * 64 + i] = inv;
+                    }
+                    store(diag / 8 + 2 * hh, x);
+                    store(diag / 8 + 2 * hh + 1, x + 8);
+                    if (diag > 0) {
+                        store(2 * hh, y);
+                        store(2 * hh + 1, y + 8);
+                    }
+                }
+                if (!ok) break;
+                fence_proxy_async();
+                arrive(p_ready);
             }
         }
     }
@@ -763,6 +836,10 @@ cudaError_t launch_mode(LinearParams p, int g_run, const CUtensorMap &mq, const 
     p.G_run = g_run;
     const long units = (long)p.B * p.Hv * g_run, sms = sm_count_of_current_device();
     if (units == 0) return cudaSuccess;
+    if (units > 0x7fffffffL - sms) return cudaErrorInvalidValue;
+    p.n_units = (unsigned)units;
+    // a turn of a wait takes some 20 ns at least
+    p.spins = p.wait_ns < 1000 ? 1u : (uint32_t)(p.wait_ns / 16 < 0xffffffffull ? p.wait_ns / 16 : 0xffffffffull);
     cudaError_t e = set_smem_once<linear_kernel<E, MODE>>((int)kSmem);
     if (e != cudaSuccess) return e;
     linear_kernel<E, MODE><<<(unsigned)(units < sms ? units : sms), kThreads, kSmem, stream>>>(p, mq, mk, mv, mo);
