@@ -30,10 +30,12 @@
 //   warps 0-3   state: dS -> fp32 registers -> the next chunk's image
 //   warps 4-7   W: values (ldmatrix, transposed), scaled and split, -> TMEM
 //   warps 8-11  outputs: O1 + 2^{b} O2, transposed through shared memory (stmatrix), TMA stores
-//   warp 12     tiles (TMA) and the chunk's decay sums
-//   warp 13     issues every MMA: dS and O2 of a chunk, R of the next one, O1; the
-//               threads' part of each is done while the others run
+//   warp 12     tiles (TMA)
+//   warp 13     issues dS and O2
 //   warps 14-15 P
+//   warp 16     issues R, one chunk ahead, and O1 (two issuing warps: an MMA costs
+//               its issuer some 55 cycles, and half of them run for 32)
+//   warp 17     the chunk's decay sums
 // Few rows are cut into segments of whole chunks, so that every SM has one: a
 // first pass (kStateOnly) forms each segment's end state from its start on,
 // and the second takes each segment's start state from those.
@@ -62,7 +64,7 @@ using namespace tc;
 
 constexpr int C = 64;        // chunk
 constexpr int NS = 4;        // stages
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 
 // Shared memory: per stage two blocks (dk 0-63, 64-127) of [K 64 rows | Q 64
 // rows] and two blocks of V; then P, the outputs, the stages' decay sums, the power-of-two
@@ -180,7 +182,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], 2);                          // the copies' bytes, the decay sums
-            mbar_init(&empty[s], kOut ? 1 + 4 + 4 : 1 + 4);  // MMAs, state warps, output warps
+            mbar_init(&empty[s], kOut ? 2 + 4 + 4 : 1 + 4);  // MMA warps, state warps, output warps
         }
         for (int j = 0; j < 4; ++j) mbar_init(&ds_done[j], 1);
         mbar_init(r_done, 1);
@@ -190,9 +192,9 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
         mbar_init(ds_free, 4);
         mbar_init(qs_done, 1);
         mbar_init(s_ready, 4);
-        mbar_init(o_done, 1);
+        mbar_init(o_done, 2);
         mbar_init(o_free, 4);
-        mbar_init(drain, 1);
+        mbar_init(drain, kOut ? 2 : 1);
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -223,7 +225,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
 
     if (warp < 4) {
         // ============================ state ==============================
-        regs_inc<200>();
+        regs_inc<184>();
         const int i = warp * 32 + lane;  // value feature
         const uint32_t lane_base = tm + ((uint32_t)(warp * 32) << 16);
         const float *winv = reinterpret_cast<const float *>(sm + oWInv);
@@ -301,21 +303,17 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 const float wi = kBf ? 1.f : winv[(it & 1) * 128 + i];
                 const float2 gam2 = make_float2(gam, gam), wi2 = make_float2(wi, wi);
 #pragma unroll
-                for (int g = 0; g < 4; g += 2) {
+                for (int g = 0; g < 4; ++g) {
                     if (g * 32 < dk) {
-                        uint32_t v[2][32];
-                        tmem_ld32_async(lane_base + tDS + 32 * g, v[0]);
-                        if (g * 32 + 32 < dk) tmem_ld32_async(lane_base + tDS + 32 * g + 32, v[1]);
+                        uint32_t v[32];
+                        tmem_ld32_async(lane_base + tDS + 32 * g, v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            if (g * 32 + h * 32 < dk)
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) {
-                                    float2 d = make_float2(__uint_as_float(v[h][2 * j]), __uint_as_float(v[h][2 * j + 1]));
-                                    if constexpr (!kBf) d = __fmul2_rn(wi2, d);
-                                    S[16 * (g + h) + j] = __ffma2_rn(gam2, S[16 * (g + h) + j], d);
-                                }
+                        for (int j = 0; j < 16; ++j) {
+                            float2 d = make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                            if constexpr (!kBf) d = __fmul2_rn(wi2, d);
+                            S[16 * g + j] = __ffma2_rn(gam2, S[16 * g + j], d);
+                        }
                     }
                 }
                 kept *= gam;
@@ -459,7 +457,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
         }
     } else if (warp < 12) {
         // ============================ outputs ============================
-        regs_dec<80>();
+        regs_dec<72>();
         if constexpr (kOut) {
             const int wq = warp - 8;
             const uint32_t lane_base = tm + ((uint32_t)(wq * 32) << 16);
@@ -539,133 +537,55 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             }
             if (lane == 0) bulk_wait_all();
         }
-    } else {
-        regs_dec<104>();
+    } else if (warp < 16) {
+        regs_dec<80>();
         const uint32_t leader = elect_leader();
         if (warp == 12) {
-            // ====================== tiles, decay sums ====================
-            const bool per_head = (p.conv & GDN_ALPHA_PER_HEAD) != 0;
-            const int G = Hv / p.Hk;
-            unsigned u = blockIdx.x - gridDim.x;  // (wraps to blockIdx.x at the first step)
-            Unit x;
-            x.c1 = 0;
-            int c = 0, t0 = 0, n = 0, h = 0;  // the chunk that is next: first token, tokens, head
-            float raw[2] = {0.f, 0.f};        // its decays of tokens 2 lane, 2 lane + 1, as stored
-            int it = -1;
+            // ============================ tiles ==========================
+            const int G = Hv / p.Hk, bytes = 8192 * ((dk > 64 ? 2 : 1) * (kOut ? 2 : 1) + (dv > 64 ? 2 : 1));
+            unsigned u = blockIdx.x;
+            int it = 0;
 #pragma unroll 1
-            for (;; ++it) {
-                const int t0_ = t0, n_ = n, h_ = h;
-                float a[2] = {raw[0], raw[1]};
-                // the one after it, and its decays: they arrive while this one is worked on
-                n = 0;
-                ++c;
+            for (; ok && u < p.n_units; u += gridDim.x) {
+                const Unit x = unit_at(p, u);
+                const int hk = x.h / G;
 #pragma unroll 1
-                while (c >= x.c1) {
-                    u += gridDim.x;
-                    if (u >= p.n_units) break;
-                    x = unit_at(p, u);
-                    c = x.c0;
-                }
-                if (u < p.n_units) {
-                    t0 = (int)(x.tok0 + (long)c * C);
-                    n = min(C, x.len - c * C);
-                    h = x.h;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (2 * lane + e < n)
-                            raw[e] = ld_gate_early(p.alpha, per_head ? (long)h : (long)(t0 + 2 * lane + e) * Hv + h, p.dt_gate);
-                }
-                if (it < 0) continue;
-                const int s = it % NS;
-                uint8_t *st = sm + s * kStage;
-                if (it >= NS && !(ok = wait(&empty[s], it / NS - 1))) break;
-                float *gate = gate_of(it);
-                if (lane == 0) {
-                    reinterpret_cast<int *>(gate)[gN] = n_;
-                    reinterpret_cast<int *>(gate)[gTok] = t0_;
-                    reinterpret_cast<int *>(gate)[gHead] = h_;
-                    mbar_arrive_expect_tx(
-                        &full[s], n_ == 0 ? 0u : 8192u * ((dk > 64 ? 2 : 1) * (kOut ? 2 : 1) + (dv > 64 ? 2 : 1)));
-                }
-                __syncwarp();
-                if (n_ == 0) {  // past the last chunk
-                    arrive(&full[s]);
-                    break;
-                }
-                const int hk = h_ / G;
+                for (int c = x.c0; c < x.c1; ++c, ++it) {
+                    const int s = it % NS, t0 = (int)(x.tok0 + (long)c * C);
+                    if (it >= NS && !(ok = wait(&empty[s], it / NS - 1))) break;
+                    uint8_t *st = sm + s * kStage;
+                    if (leader) mbar_arrive_expect_tx(&full[s], bytes);
+                    __syncwarp();
 #pragma unroll 1
-                for (int j = 0; j < 2; ++j) {
-                    if (64 * j < dk) {
-                        tma_load_3d_warp(leader, st + j * kBlock, &mk, 64 * j, hk, t0_, &full[s]);
-                        if constexpr (kOut) tma_load_3d_warp(leader, st + j * kBlock + 8192, &mq, 64 * j, hk, t0_, &full[s]);
+                    for (int j = 0; j < 2; ++j) {
+                        if (64 * j < dk) {
+                            tma_load_3d_warp(leader, st + j * kBlock, &mk, 64 * j, hk, t0, &full[s]);
+                            if constexpr (kOut) tma_load_3d_warp(leader, st + j * kBlock + 8192, &mq, 64 * j, hk, t0, &full[s]);
+                        }
+                        if (64 * j < dv) tma_load_3d_warp(leader, st + kStageV + j * 8192, &mv, 64 * j, x.h, t0, &full[s]);
                     }
-                    if (64 * j < dv) tma_load_3d_warp(leader, st + kStageV + j * 8192, &mv, 64 * j, h_, t0_, &full[s]);
                 }
-                // Inclusive sums over the lanes from both ends; the exclusive ones
-                // are the neighbours' (a difference would lose what a strong decay
-                // has in front of it, and be no number after a decay of 0).  For
-                // P's differences a decay below 2^-40 (0 among them) counts as 2^-40,
-                // far below the scores' own rounding: the sums stay finite, and small
-                // enough for their differences to be exact to 2^-12.
-                float held[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    a[e] = 2 * lane + e >= n_ ? 0.f : (p.conv & GDN_ALPHA_LOG) ? a[e] * kLog2e : log2f(a[e]);
-                    held[e] = a[e] < -40.f ? -40.f : a[e];
-                }
-                float up = a[0] + a[1], down = up, hup = held[0] + held[1];
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float y0 = __shfl_up_sync(0xffffffffu, up, o), y1 = __shfl_down_sync(0xffffffffu, down, o);
-                    const float y2 = __shfl_up_sync(0xffffffffu, hup, o);
-                    if (lane >= o) up += y0, hup += y2;
-                    if (lane + o < 32) down += y1;
-                }
-                float ex = __shfl_up_sync(0xffffffffu, up, 1), eh = __shfl_up_sync(0xffffffffu, hup, 1);
-                float suf = __shfl_down_sync(0xffffffffu, down, 1);
-                if (lane == 0) ex = eh = 0.f;
-                if (lane == 31) suf = 0.f;
-                const float b31 = __shfl_sync(0xffffffffu, hup, 15);
-                const float2 b2 = make_float2(eh + held[0], hup);
-                *reinterpret_cast<float2 *>(gate + gSum + 2 * lane) = b2;
-                *reinterpret_cast<float2 *>(gate + gScaled + 2 * lane) =
-                    make_float2(p.scale * ex2_approx(ex + a[0]), p.scale * ex2_approx(up));
-                *reinterpret_cast<float2 *>(gate + gW + 2 * lane) = make_float2(ex2_approx(suf + a[1]), ex2_approx(suf));
-                if (lane < 16)
-                    *reinterpret_cast<float2 *>(gate + gLeft + 2 * lane) =
-                        make_float2(ex2_approx(b31 - b2.x), ex2_approx(b31 - b2.y));
-                if (lane == 31) gate[gLast] = ex2_approx(up);
-                arrive(&full[s]);
             }
-            if (!ok)  // the copies in flight must land before the CTA ends
+            if (ok) {  // the end of the chunks
+                if (it >= NS) ok = wait(&empty[it % NS], it / NS - 1);
+                if (ok) arrive(&full[it % NS]);
+            }
+            // the copies in flight must land before the CTA ends
+            if (!ok)
                 for (int j = it > NS ? it - NS : 0; j < it; ++j)
-                    mbar_wait(&full[j % NS], (uint32_t)(j / NS) & 1u, kDefaultWaitNs);
+                    mbar_wait(&full[j % NS], (uint32_t)(j / NS) & 1u, kDefaultWaitNs / 8);
         } else if (warp == 13) {
-            // =========================== MMAs ============================
-            const uint32_t id_r = idesc_f16(128, 64, false, false, kBf);
-            const uint32_t id_o1 = idesc_f16(128, 64, true, false, kBf);
+            // ======================= MMAs of the state ===================
+            const uint32_t id_o2 = idesc_f16(128, 64, false, false, kBf);
             const uint32_t id_ds = idesc_f16(128, dk, false, true, kBf);
             const int ks = dk / 16;  // K = 16 steps over dk
-            const uint32_t s0 = smem_u32(sm);
             // (loops are kept rolled: an MMA takes longer than its turn)
-            auto raw_scores = [&](int it) {
-                if (it > 0 && !wait(r_free, it - 1)) return false;
-                fence_after_sync();
-                uint64_t d = desc_sw128(s0 + (it % NS) * kStage, 16, 1024);
 #pragma unroll 1
-                for (int k = 0; k < ks; ++k) {
-                    mma_f16_warp(leader, tm + tR, d, d, id_r, k > 0);
-                    d = desc_add(d, k == 3 ? kBlock - 96 : 32);
-                }
-                mma_commit_warp(leader, r_done);
-                return true;
-            };
-            int n = chunk(0);
-            ok = n >= 0;
-            if (kOut && n > 0) ok = raw_scores(0);
-#pragma unroll 1
-            for (int it = 0; ok && n > 0; ++it) {
-                const uint32_t st = s0 + (it % NS) * kStage;
+            for (int it = 0;; ++it) {
+                const int n = chunk(it);
+                ok = n >= 0;
+                if (n <= 0) break;
+                const uint32_t st = smem_u32(sm) + (it % NS) * kStage;
                 // dS = W^T K, 16 tokens of every part of W at a time
                 if (!(ok = wait(w_ready, it)) || (it > 0 && !(ok = wait(ds_free, it - 1)))) break;
                 fence_after_sync();
@@ -685,30 +605,13 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     uint64_t qd = desc_sw128(st + 8192, 16, 1024);
 #pragma unroll 1
                     for (int k = 0; k < ks; ++k) {
-                        mma_f16_ta_warp(leader, tm + tO2, tm + tS + 8 * k, qd, id_r, k > 0);
+                        mma_f16_ta_warp(leader, tm + tO2, tm + tS + 8 * k, qd, id_o2, k > 0);
                         qd = desc_add(qd, k == 3 ? kBlock - 96 : 32);
                     }
                     mma_commit_warp(leader, qs_done);
-                    // R of the next chunk
-                    n = chunk(it + 1);
-                    if (!(ok = n >= 0) || (n > 0 && !(ok = raw_scores(it + 1)))) break;
-                    // O1^T = V^T P^T
-                    if (!(ok = wait(p_ready, it))) break;
-                    fence_after_sync();
-                    uint64_t vd = desc_sw128(st + kStageV, 8192, 1024), pd = desc_sw128(s0 + oP, 16, 1024);
-#pragma unroll 1
-                    for (int j = 0; j < 4; ++j) {
-                        mma_f16_warp(leader, tm + tO1, vd, pd, id_o1, j > 0);
-                        vd = desc_add(vd, 2048);
-                        pd = desc_add(pd, 32);
-                    }
                     mma_commit_warp(leader, o_done);
-                    mma_commit_warp(leader, &empty[it % NS]);
-                } else {
-                    mma_commit_warp(leader, &empty[it % NS]);
-                    n = chunk(it + 1);
-                    ok = n >= 0;
                 }
+                mma_commit_warp(leader, &empty[it % NS]);
             }
             mma_commit_warp(leader, drain);  // nothing may be in flight when TMEM is given back
             mbar_wait(drain, 0, kDefaultWaitNs);
@@ -729,6 +632,15 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 ok = n >= 0;
                 if (n <= 0 || !(ok = wait(r_done, it))) break;
                 fence_after_sync();
+                if (n < C) {  // V rows past the row's end: zeros, whatever was loaded
+                    uint8_t *v = sm + (it % NS) * kStage + kStageV;
+#pragma unroll 1
+                    for (int e = i; e < (C - n) * 8; e += 64) {
+                        const int off = (n + (e >> 3)) * 128 + (e & 7) * 16;
+                        *reinterpret_cast<uint4 *>(v + off) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(v + 8192 + off) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
                 const float *gate = gate_of(it);
                 const float bi = gate[gSum + i];
                 // 2^{b_i - b_31} of the columns left of the diagonal block: with
@@ -808,6 +720,131 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 if (!ok) break;
                 fence_proxy_async();
                 arrive(p_ready);
+            }
+        }
+    } else {
+        regs_dec<48>();
+        const uint32_t leader = elect_leader();
+        if (warp == 16) {
+            // ====================== MMAs of the scores ===================
+            if constexpr (kOut) {
+                const uint32_t id_r = idesc_f16(128, 64, false, false, kBf);
+                const uint32_t id_o1 = idesc_f16(128, 64, true, false, kBf);
+                const int ks = dk / 16;
+                const uint32_t s0 = smem_u32(sm);
+#pragma unroll 1
+                for (int it = 0;; ++it) {
+                    const int n = chunk(it);
+                    ok = n >= 0;
+                    if (n > 0) {
+                        // R = [K;Q] K^T
+                        if (it > 0 && !(ok = wait(r_free, it - 1))) break;
+                        fence_after_sync();
+                        uint64_t d = desc_sw128(s0 + (it % NS) * kStage, 16, 1024);
+#pragma unroll 1
+                        for (int k = 0; k < ks; ++k) {
+                            mma_f16_warp(leader, tm + tR, d, d, id_r, k > 0);
+                            d = desc_add(d, k == 3 ? kBlock - 96 : 32);
+                        }
+                        mma_commit_warp(leader, r_done);
+                    }
+                    if (it > 0 && ok) {
+                        // O1^T = V^T P^T of the chunk before
+                        const int pt = it - 1;
+                        if (!(ok = wait(p_ready, pt)) || (pt > 0 && !(ok = wait(o_free, pt - 1)))) break;
+                        fence_after_sync();
+                        uint64_t vd = desc_sw128(s0 + (pt % NS) * kStage + kStageV, 8192, 1024);
+                        uint64_t pd = desc_sw128(s0 + oP, 16, 1024);
+#pragma unroll 1
+                        for (int j = 0; j < 4; ++j) {
+                            mma_f16_warp(leader, tm + tO1, vd, pd, id_o1, j > 0);
+                            vd = desc_add(vd, 2048);
+                            pd = desc_add(pd, 32);
+                        }
+                        mma_commit_warp(leader, o_done);
+                        mma_commit_warp(leader, &empty[pt % NS]);
+                    }
+                    if (n <= 0) break;
+                }
+                mma_commit_warp(leader, drain);
+                mbar_wait(drain, 0, kDefaultWaitNs);
+            }
+        } else if (warp == 17) {
+            // ========================= decay sums ========================
+            const bool per_head = (p.conv & GDN_ALPHA_PER_HEAD) != 0;
+            unsigned u = blockIdx.x - gridDim.x;  // (wraps to blockIdx.x at the first step)
+            Unit x;
+            x.c1 = 0;
+            int c = 0, t0 = 0, n = 0, h = 0;  // the chunk that is next: first token, tokens, head
+            float raw[2] = {0.f, 0.f};        // its decays of tokens 2 lane, 2 lane + 1, as stored
+#pragma unroll 1
+            for (int it = -1;; ++it) {
+                const int t0_ = t0, n_ = n, h_ = h;
+                float a[2] = {raw[0], raw[1]};
+                // the one after it, and its decays: they arrive while this one is worked on
+                n = 0;
+                ++c;
+#pragma unroll 1
+                while (c >= x.c1) {
+                    u += gridDim.x;
+                    if (u >= p.n_units) break;
+                    x = unit_at(p, u);
+                    c = x.c0;
+                }
+                if (u < p.n_units) {
+                    t0 = (int)(x.tok0 + (long)c * C);
+                    n = min(C, x.len - c * C);
+                    h = x.h;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (2 * lane + e < n)
+                            raw[e] = ld_gate_early(p.alpha, per_head ? (long)h : (long)(t0 + 2 * lane + e) * Hv + h, p.dt_gate);
+                }
+                if (it < 0) continue;
+                const int s = it % NS;
+                if (it >= NS && !(ok = wait(&empty[s], it / NS - 1))) break;
+                float *gate = gate_of(it);
+                if (lane == 0) {
+                    reinterpret_cast<int *>(gate)[gN] = n_;
+                    reinterpret_cast<int *>(gate)[gTok] = t0_;
+                    reinterpret_cast<int *>(gate)[gHead] = h_;
+                }
+                // Inclusive sums over the lanes from both ends; the exclusive ones
+                // are the neighbours' (a difference would lose what a strong decay
+                // has in front of it, and be no number after a decay of 0).  For
+                // P's differences a decay below 2^-40 (0 among them) counts as 2^-40,
+                // far below the scores' own rounding: the sums stay finite, and small
+                // enough for their differences to be exact to 2^-12.
+                float held[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    a[e] = 2 * lane + e >= n_ ? 0.f : (p.conv & GDN_ALPHA_LOG) ? a[e] * kLog2e : log2f(a[e]);
+                    held[e] = a[e] < -40.f ? -40.f : a[e];
+                }
+                float up = a[0] + a[1], down = up, hup = held[0] + held[1];
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float y0 = __shfl_up_sync(0xffffffffu, up, o), y1 = __shfl_down_sync(0xffffffffu, down, o);
+                    const float y2 = __shfl_up_sync(0xffffffffu, hup, o);
+                    if (lane >= o) up += y0, hup += y2;
+                    if (lane + o < 32) down += y1;
+                }
+                float ex = __shfl_up_sync(0xffffffffu, up, 1), eh = __shfl_up_sync(0xffffffffu, hup, 1);
+                float suf = __shfl_down_sync(0xffffffffu, down, 1);
+                if (lane == 0) ex = eh = 0.f;
+                if (lane == 31) suf = 0.f;
+                const float b31 = __shfl_sync(0xffffffffu, hup, 15);
+                const float2 b2 = make_float2(eh + held[0], hup);
+                *reinterpret_cast<float2 *>(gate + gSum + 2 * lane) = b2;
+                *reinterpret_cast<float2 *>(gate + gScaled + 2 * lane) =
+                    make_float2(p.scale * ex2_approx(ex + a[0]), p.scale * ex2_approx(up));
+                *reinterpret_cast<float2 *>(gate + gW + 2 * lane) = make_float2(ex2_approx(suf + a[1]), ex2_approx(suf));
+                if (lane < 16)
+                    *reinterpret_cast<float2 *>(gate + gLeft + 2 * lane) =
+                        make_float2(ex2_approx(b31 - b2.x), ex2_approx(b31 - b2.y));
+                if (lane == 31) gate[gLast] = ex2_approx(up);
+                arrive(&full[s]);
+                if (n_ == 0) break;  // past the last chunk
             }
         }
     }
