@@ -28,14 +28,14 @@
 // waits for the threads.  One persistent CTA a SM, warp-specialised, four
 // stages of tiles in flight; every hand-off between the roles is an mbarrier:
 //   warps 0-3   state: dS -> fp32 registers -> the next chunk's image
-//   warps 4-7   W: values (ldmatrix, transposed), scaled and split, -> TMEM
+//   warps 4-7, 20-23  W: values (ldmatrix, transposed), scaled and split, -> TMEM
 //   warps 8-11  outputs: O1 + 2^{b} O2, transposed through shared memory (stmatrix), TMA stores
 //   warp 12     tiles (TMA)
 //   warp 13     issues dS and O2
 //   warps 14-15 P
 //   warp 16     issues R, one chunk ahead, and O1 (two issuing warps: an MMA costs
 //               its issuer some 55 cycles, and half of them run for 32)
-//   warp 17     the chunk's decay sums
+//   warps 17-19 the chunks' decay sums
 // Few rows are cut into segments of whole chunks, so that every SM has one: a
 // first pass (kStateOnly) forms each segment's end state from its start on,
 // and the second takes each segment's start state from those.
@@ -64,7 +64,7 @@ using namespace tc;
 
 constexpr int C = 64;        // chunk
 constexpr int NS = 4;        // stages
-constexpr int kThreads = 640;
+constexpr int kThreads = 768;
 
 // Shared memory: per stage two blocks (dk 0-63, 64-127) of [K 64 rows | Q 64
 // rows] and two blocks of V; then P, the outputs, the stages' decay sums, the power-of-two
@@ -78,7 +78,7 @@ constexpr uint32_t oGate = oOut + 16384;           // per stage (kGate bytes), t
 constexpr uint32_t kGate = 1024;
 constexpr int gSum = 0;                            // [64] b_t (decays of at least 2^-40 each)
 constexpr int gScaled = 64;                        // [64] scale 2^{b_t}
-constexpr int gW = 128;                            // [64] 2^{s_t}
+constexpr int gW = 128;                            // [64] 2^{s_t}, or (two bf16 parts) [32][2] pairs of both parts
 constexpr int gLast = 192;                         // 2^{b_63}
 constexpr int gN = 193, gTok = 194, gHead = 195;   // ints: the chunk's tokens (0: no more chunks), first token, head
 constexpr int gLeft = 200;                         // [32] 2^{b_31 - b_t}
@@ -103,7 +103,6 @@ struct LinearParams : PrefillParams {
     int G;             // segments a row
     int G_run;         // segments of this pass
     unsigned n_units;  // B Hv G_run
-    uint32_t spins;    // limit of a wait
     float *seg_state;  // [B, Hv, G, dv, dk]
     float *seg_decay;  // [B, Hv, G]
 };
@@ -130,6 +129,17 @@ struct Half16<__half> {
     }
     __device__ static float2 unpack2(uint32_t u) { return __half22float2(*reinterpret_cast<__half2 *>(&u)); }
 };
+
+__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
 
 // A power of two that brings a largest magnitude m into [2^13, 2^14), and its
 // inverse (fp16 holds 2^-14 .. 2^15 in full precision).
@@ -170,11 +180,10 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_align1k(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + oBar), *empty = full + NS;
-    uint64_t *ds_done = empty + NS;  // [4]: after each 16 tokens of the product
-    uint64_t *r_done = ds_done + 4, *r_free = r_done + 1, *p_ready = r_done + 2, *w_ready = r_done + 3,
-             *ds_free = r_done + 4, *qs_done = r_done + 5, *s_ready = r_done + 6, *o_done = r_done + 7,
-             *o_free = r_done + 8, *drain = r_done + 9;
-    uint32_t *slot = reinterpret_cast<uint32_t *>(r_done + 10);
+    uint64_t *r_done = empty + NS, *r_free = r_done + 1, *p_ready = r_done + 2, *w_ready = r_done + 3,
+             *ds_done = r_done + 4, *ds_free = r_done + 5, *qs_done = r_done + 6, *s_ready = r_done + 7,
+             *pv_done = r_done + 8, *o_done = r_done + 9, *o_free = r_done + 10, *drain = r_done + 11;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(r_done + 12);
     // (through a shuffle: known to be the same in every lane)
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int dk = p.dk, dv = p.dv, Hv = p.Hv;
@@ -184,11 +193,12 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             mbar_init(&full[s], 2);                          // the copies' bytes, the decay sums
             mbar_init(&empty[s], kOut ? 2 + 4 + 4 : 1 + 4);  // MMA warps, state warps, output warps
         }
-        for (int j = 0; j < 4; ++j) mbar_init(&ds_done[j], 1);
+        mbar_init(ds_done, 1);
+        mbar_init(pv_done, 1);
         mbar_init(r_done, 1);
         mbar_init(r_free, 2);
         mbar_init(p_ready, 2);
-        mbar_init(w_ready, 4);
+        mbar_init(w_ready, 8);
         mbar_init(ds_free, 4);
         mbar_init(qs_done, 1);
         mbar_init(s_ready, 4);
@@ -206,16 +216,21 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     fence_after_sync();
     const uint32_t tm = __shfl_sync(0xffffffffu, *slot, 0);
     bool ok = true;
+    // Waits run out p.wait_ns after the warp's last chunk came (a limit below a
+    // microsecond at the first check that finds a phase incomplete).
+    auto limit = [&]() { return p.wait_ns < 1000 ? 0ull : globaltimer_ns() + p.wait_ns; };
+    uint64_t deadline = limit();
     // A wait of a whole warp: the outcome is the same in every lane, so that
     // the warp-wide TMEM accesses behind it stay converged.
     auto wait = [&](uint64_t *bar, int it) {
-        return __all_sync(0xffffffffu, mbar_wait_spins(bar, (uint32_t)it & 1u, p.spins)) != 0;
+        return __all_sync(0xffffffffu, mbar_wait_until(bar, (uint32_t)it & 1u, deadline)) != 0;
     };
     auto gate_of = [&](int it) { return reinterpret_cast<float *>(sm + oGate + (it % NS) * kGate); };
     // The chunk's tiles and sums are there; its tokens n, or 0 past the last one
     // (and -1 where the wait ran out).
     auto chunk = [&](int it) {
         if (!wait(&full[it % NS], it / NS)) return -1;
+        deadline = limit();
         return reinterpret_cast<const int *>(gate_of(it))[gN];
     };
     auto arrive = [&](uint64_t *bar) {
@@ -225,7 +240,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
 
     if (warp < 4) {
         // ============================ state ==============================
-        regs_inc<184>();
+        regs_inc<168>();
         const int i = warp * 32 + lane;  // value feature
         const uint32_t lane_base = tm + ((uint32_t)(warp * 32) << 16);
         const float *winv = reinterpret_cast<const float *>(sm + oWInv);
@@ -297,7 +312,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     arrive(s_ready);
                 }
                 // S <- 2^b_63 S + dS
-                if (!(ok = chunk(it) > 0) || !(ok = wait(&ds_done[3], it))) break;
+                if (!(ok = chunk(it) > 0) || !(ok = wait(ds_done, it))) break;
                 fence_after_sync();
                 const float gam = gate_of(it)[gLast];
                 const float wi = kBf ? 1.f : winv[(it & 1) * 128 + i];
@@ -343,15 +358,17 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                             make_float4(S[2 * q].x, S[2 * q].y, S[2 * q + 1].x, S[2 * q + 1].y);
             }
         }
-    } else if (warp < 8) {
+    } else if (warp < 8 || warp >= 20) {
         // ============================== W ================================
-        const int wq = warp - 4;
-        const uint32_t lane_base = tm + ((uint32_t)(wq * 32) << 16);
-        float *winv = reinterpret_cast<float *>(sm + oWInv) + wq * 32 + (lane >> 2);
+        // Two warps for each 32 features, 16 of them each.
+        regs_dec<72>();
+        const int wq = warp & 3, hh = warp >= 20 ? 1 : 0;
+        const uint32_t lane_base = tm + ((uint32_t)(wq * 32 + 16 * hh) << 16);
+        float *winv = reinterpret_cast<float *>(sm + oWInv) + wq * 32 + 16 * hh + (lane >> 2);
         // ldmatrix: this lane's row of the four 8 x 8 matrices (tokens 0-7 and
         // 8-15 of 16, features 0-7 and 8-15 of 16)
-        const int row = (lane & 7) + ((lane >> 4) << 3), cg = (wq & 1) * 4 + ((lane >> 3) & 1);
-        const uint32_t v_off = kStageV + (wq >> 1) * 8192 + row * 128;
+        const int row = (lane & 7) + ((lane >> 4) << 3), cg = (wq & 1) * 4 + 2 * hh + ((lane >> 3) & 1);
+        const uint32_t v_off = kStageV + (wq >> 1) * 8192 + row * 128 + ((cg ^ (lane & 7)) << 4);
 #pragma unroll 1
         for (int it = 0;; ++it) {
             const int n = chunk(it);
@@ -362,7 +379,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             if (n < C) {
                 // K and V rows past the row's end: zeros, whatever was loaded
 #pragma unroll 1
-                for (int e = threadIdx.x - 128; e < (C - n) * 8; e += 128) {
+                for (int e = (wq + 4 * hh) * 32 + lane; e < (C - n) * 8; e += 256) {
                     const int off = (n + (e >> 3)) * 128 + (e & 7) * 16;
                     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
                     *reinterpret_cast<uint4 *>(st + off) = z;
@@ -371,49 +388,57 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     *reinterpret_cast<uint4 *>(st + kStageV + 8192 + off) = z;
                 }
                 fence_proxy_async();
-                named_bar(kBarW, 128);
+                named_bar(kBarW, 256);
             }
-            // 16 tokens (j), 16 features (hh): features g and g + 8, tokens 2 t, 2 t + 1
-            // of each eight, which is the layout of the TMEM store
-            auto scaled = [&](int j, int hh, float2 (&x)[4]) {
+            // 16 tokens (j): features g and g + 8, tokens 2 t, 2 t + 1 of each eight,
+            // which is the layout of the TMEM store
+            auto values = [&](int j, uint32_t (&v)[4]) { ldsm_x4_trans(v, st + v_off + j * 2048); };
+            auto scaled = [&](int j, float2 (&x)[4]) {
                 uint32_t v[4];
-                ldsm_x4_trans(v, st + v_off + j * 2048 + (((cg + 2 * hh) ^ (lane & 7)) << 4));
+                values(j, v);
                 const float2 w0 = *reinterpret_cast<const float2 *>(w + 16 * j);
                 const float2 w1 = *reinterpret_cast<const float2 *>(w + 16 * j + 8);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] = __fmul2_rn(e < 2 ? w0 : w1, H::unpack2(v[e]));
             };
-            float sc[4] = {1.f, 1.f, 1.f, 1.f}, inv[4];
+            float sc[2] = {1.f, 1.f}, inv[2];
             if constexpr (!kBf) {
                 // the largest magnitude of each feature gives its scale; the four
                 // lanes of a group hold a feature's tokens
-                float m[4] = {0.f, 0.f, 0.f, 0.f};
+                float m[2] = {0.f, 0.f};
 #pragma unroll 1
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 4; ++j) {
+                    float2 x[4];
+                    scaled(j, x);
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        float2 x[4];
-                        scaled(j, hh, x);
+                    for (int e = 0; e < 4; ++e) m[e & 1] = fmaxf(m[e & 1], fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+                }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            m[2 * hh + (e & 1)] = fmaxf(m[2 * hh + (e & 1)], fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
-                    }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 2; ++e) {
                     m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], 1));
                     m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], 2));
                     half_scale(m[e], sc[e], inv[e]);
                 }
             }
-            // Each 16 tokens of W are replaced as soon as the last chunk's product
-            // has read theirs.
-#pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-                uint32_t part[2][NT][4];
+            // All of W is formed in registers while the last chunk's product still
+            // reads TMEM: the stores alone stand between that product and the next.
+            uint32_t part[NT][16];
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (kBf && NT == 2) {
+                    // w = wh + wl to 16 bits: wh v = p + r exactly in two bf16 numbers,
+                    // and wl v joins the second, in packed bf16 arithmetic
+                    uint32_t v[4];
+                    values(j, v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint2 ww = *reinterpret_cast<const uint2 *>(w + 16 * j + 8 * (e >> 1));
+                        part[0][4 * j + e] = bf2_mul(ww.x, v[e]);
+                        part[1][4 * j + e] = bf2_fma(ww.y, v[e], bf2_fma(ww.x, v[e], part[0][4 * j + e] ^ 0x80008000u));
+                    }
+                } else {
                     float2 x[4];
-                    scaled(j, hh, x);
+                    scaled(j, x);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float2 r = x[e];
@@ -422,42 +447,37 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
 #pragma unroll
                             for (int m = 0; m < NT - 1; ++m) {
                                 const uint32_t a = __float_as_uint(r.x), b = __float_as_uint(r.y);
-                                part[hh][m][e] = __byte_perm(a, b, 0x7632);
+                                part[m][4 * j + e] = __byte_perm(a, b, 0x7632);
                                 r = __fadd2_rn(r, make_float2(__uint_as_float((a & 0xffff0000u) ^ 0x80000000u),
                                                               __uint_as_float((b & 0xffff0000u) ^ 0x80000000u)));
                             }
-                            part[hh][NT - 1][e] = H::pack2(r.x, r.y);
+                            part[NT - 1][4 * j + e] = H::pack2(r.x, r.y);
                         } else {
-                            const float s = sc[2 * hh + (e & 1)];
-                            r = __fmul2_rn(make_float2(s, s), r);
-                            part[hh][0][e] = H::pack2(r.x, r.y);
-                            const float2 h = H::unpack2(part[hh][0][e]);
-                            part[hh][1][e] = H::pack2(r.x - h.x, r.y - h.y);
+                            r = __fmul2_rn(make_float2(sc[e & 1], sc[e & 1]), r);
+                            part[0][4 * j + e] = H::pack2(r.x, r.y);
+                            const float2 h = H::unpack2(part[0][4 * j + e]);
+                            part[1][4 * j + e] = H::pack2(r.x - h.x, r.y - h.y);
                         }
                     }
                 }
-                if (it > 0 && !(ok = wait(&ds_done[j], it - 1))) break;
-                fence_after_sync();
-#pragma unroll
-                for (int m = 0; m < NT; ++m)
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh)
-                        tmem_st_16x8(lane_base + ((uint32_t)(16 * hh) << 16) + tW + 32 * m + 8 * j, part[hh][m]);
             }
-            if (!ok) break;
-            // (the last wait was for the whole of the last product, which was
-            // issued after the state warps had read the scales before its own)
+            if (it > 0 && !(ok = wait(ds_done, it - 1))) break;
+            fence_after_sync();
+#pragma unroll
+            for (int m = 0; m < NT; ++m) tmem_st_16x32(lane_base + tW + 32 * m, part[m]);
+            // (the last product was issued after the state warps had read the
+            // scales of the one before it)
             if constexpr (!kBf)
                 if ((lane & 3) == 0)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) winv[(it & 1) * 128 + 8 * e] = inv[e];
+                    for (int e = 0; e < 2; ++e) winv[(it & 1) * 128 + 8 * e] = inv[e];
             tmem_wait_st();
             fence_before_sync();
             arrive(w_ready);
         }
     } else if (warp < 12) {
         // ============================ outputs ============================
-        regs_dec<72>();
+        regs_dec<64>();
         if constexpr (kOut) {
             const int wq = warp - 8;
             const uint32_t lane_base = tm + ((uint32_t)(wq * 32) << 16);
@@ -538,7 +558,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             if (lane == 0) bulk_wait_all();
         }
     } else if (warp < 16) {
-        regs_dec<80>();
+        regs_dec<64>();
         const uint32_t leader = elect_leader();
         if (warp == 12) {
             // ============================ tiles ==========================
@@ -553,6 +573,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 for (int c = x.c0; c < x.c1; ++c, ++it) {
                     const int s = it % NS, t0 = (int)(x.tok0 + (long)c * C);
                     if (it >= NS && !(ok = wait(&empty[s], it / NS - 1))) break;
+                    deadline = limit();
                     uint8_t *st = sm + s * kStage;
                     if (leader) mbar_arrive_expect_tx(&full[s], bytes);
                     __syncwarp();
@@ -595,9 +616,9 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
 #pragma unroll
                     for (int m = 0; m < NT; ++m)
                         mma_f16_ta_warp(leader, tm + tDS, tm + tW + 32 * m + 8 * j, kn, id_ds, m + j > 0);
-                    mma_commit_warp(leader, &ds_done[j]);
                     kn = desc_add(kn, 2048);
                 }
+                mma_commit_warp(leader, ds_done);
                 if constexpr (kOut) {
                     // O2^T = S Q^T
                     if (!(ok = wait(s_ready, it)) || (it > 0 && !(ok = wait(o_free, it - 1)))) break;
@@ -707,7 +728,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     if (hh == 0) {
                         // the products with the last chunk's P are done (and so are
                         // the reads of the scales of the one before)
-                        if (it > 0 && !(ok = wait(o_done, it - 1))) break;
+                        if (it > 0 && !(ok = wait(pv_done, it - 1))) break;
                         if constexpr (!kBf) pinv[(it & 1) * 64 + i] = inv;
                     }
                     store(diag / 8 + 2 * hh, x);
@@ -723,7 +744,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             }
         }
     } else {
-        regs_dec<48>();
+        regs_dec<40>();
         const uint32_t leader = elect_leader();
         if (warp == 16) {
             // ====================== MMAs of the scores ===================
@@ -761,6 +782,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                             vd = desc_add(vd, 2048);
                             pd = desc_add(pd, 32);
                         }
+                        mma_commit_warp(leader, pv_done);
                         mma_commit_warp(leader, o_done);
                         mma_commit_warp(leader, &empty[pt % NS]);
                     }
@@ -769,29 +791,39 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 mma_commit_warp(leader, drain);
                 mbar_wait(drain, 0, kDefaultWaitNs);
             }
-        } else if (warp == 17) {
+        } else {
             // ========================= decay sums ========================
+            // Three warps take the chunks in turn: a chunk's decays are loaded while
+            // the warp's last one is worked on, and take longer than a chunk does.
             const bool per_head = (p.conv & GDN_ALPHA_PER_HEAD) != 0;
             unsigned u = blockIdx.x - gridDim.x;  // (wraps to blockIdx.x at the first step)
             Unit x;
             x.c1 = 0;
             int c = 0, t0 = 0, n = 0, h = 0;  // the chunk that is next: first token, tokens, head
             float raw[2] = {0.f, 0.f};        // its decays of tokens 2 lane, 2 lane + 1, as stored
+            int steps = warp - 16;            // to the warp's next chunk
+            bool end = false;                 // the next one would be the first past the last
+            bool over = false;                // no more chunks
 #pragma unroll 1
-            for (int it = -1;; ++it) {
+            for (int it = warp - 20;; it += 3) {
                 const int t0_ = t0, n_ = n, h_ = h;
+                const bool end_ = end;
                 float a[2] = {raw[0], raw[1]};
-                // the one after it, and its decays: they arrive while this one is worked on
                 n = 0;
-                ++c;
 #pragma unroll 1
-                while (c >= x.c1) {
-                    u += gridDim.x;
-                    if (u >= p.n_units) break;
-                    x = unit_at(p, u);
-                    c = x.c0;
+                for (; steps > 0 && !over; --steps) {
+                    ++c;
+#pragma unroll 1
+                    while (c >= x.c1) {
+                        u += gridDim.x;
+                        if ((over = u >= p.n_units)) break;
+                        x = unit_at(p, u);
+                        c = x.c0;
+                    }
+                    end = over && steps == 1;
                 }
-                if (u < p.n_units) {
+                steps = 3;
+                if (!over) {
                     t0 = (int)(x.tok0 + (long)c * C);
                     n = min(C, x.len - c * C);
                     h = x.h;
@@ -801,8 +833,10 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                             raw[e] = ld_gate_early(p.alpha, per_head ? (long)h : (long)(t0 + 2 * lane + e) * Hv + h, p.dt_gate);
                 }
                 if (it < 0) continue;
+                if (n_ == 0 && !end_) break;
                 const int s = it % NS;
                 if (it >= NS && !(ok = wait(&empty[s], it / NS - 1))) break;
+                deadline = limit();
                 float *gate = gate_of(it);
                 if (lane == 0) {
                     reinterpret_cast<int *>(gate)[gN] = n_;
@@ -838,7 +872,14 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 *reinterpret_cast<float2 *>(gate + gSum + 2 * lane) = b2;
                 *reinterpret_cast<float2 *>(gate + gScaled + 2 * lane) =
                     make_float2(p.scale * ex2_approx(ex + a[0]), p.scale * ex2_approx(up));
-                *reinterpret_cast<float2 *>(gate + gW + 2 * lane) = make_float2(ex2_approx(suf + a[1]), ex2_approx(suf));
+                const float2 w2 = make_float2(ex2_approx(suf + a[1]), ex2_approx(suf));
+                if constexpr (kBf && NT == 2) {
+                    const uint32_t wh = H::pack2(w2.x, w2.y);
+                    const float2 u = H::unpack2(wh);
+                    *reinterpret_cast<uint2 *>(gate + gW + 2 * lane) = make_uint2(wh, H::pack2(w2.x - u.x, w2.y - u.y));
+                } else {
+                    *reinterpret_cast<float2 *>(gate + gW + 2 * lane) = w2;
+                }
                 if (lane < 16)
                     *reinterpret_cast<float2 *>(gate + gLeft + 2 * lane) =
                         make_float2(ex2_approx(b31 - b2.x), ex2_approx(b31 - b2.y));
@@ -875,8 +916,6 @@ cudaError_t launch_mode(LinearParams p, int g_run, const CUtensorMap &mq, const 
     if (units == 0) return cudaSuccess;
     if (units > 0x7fffffffL - sms) return cudaErrorInvalidValue;
     p.n_units = (unsigned)units;
-    // a turn of a wait takes some 20 ns at least
-    p.spins = p.wait_ns < 1000 ? 1u : (uint32_t)(p.wait_ns / 16 < 0xffffffffull ? p.wait_ns / 16 : 0xffffffffull);
     cudaError_t e = set_smem_once<linear_kernel<E, MODE>>((int)kSmem);
     if (e != cudaSuccess) return e;
     linear_kernel<E, MODE><<<(unsigned)(units < sms ? units : sms), kThreads, kSmem, stream>>>(p, mq, mk, mv, mo);

@@ -114,13 +114,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
         if (globaltimer_ns() - t0 > limit_ns) return false;
     }
 }
-// The same with a limit of `spins` turns of the (suspending) wait, for kernels
-// with many waits in their instruction cache.
-__device__ __forceinline__ bool mbar_wait_spins(uint64_t *bar, uint32_t parity, uint32_t spins) {
+// The same until a time of the global timer, for kernels with many waits in
+// their instruction cache (0: gives up at the first incomplete check).
+__device__ __forceinline__ bool mbar_wait_until(uint64_t *bar, uint32_t parity, uint64_t deadline_ns) {
 #pragma unroll 1
     do {
         if (mbar_try_wait(bar, parity)) return true;
-    } while (--spins != 0);
+    } while (globaltimer_ns() < deadline_ns);
     return false;
 }
 
@@ -380,13 +380,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
-// 16 lanes x 8 columns in the layout of the warp-level MMA's fragments (g =
+// 16 lanes x 32 columns in the layout of the warp-level MMA's fragments (g =
 // lane / 4, t = lane % 4): v[2 r] = (lane g, column 4 r + t), v[2 r + 1] =
-// (lane g + 8, column 4 r + t), r < 2.
-__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&v)[4]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3])
-                 : "memory");
+// (lane g + 8, column 4 r + t), r < 8.
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
 }
 // 16 lanes x 32 columns of 32 bits as accumulator fragments: v[4 r], v[4 r + 1]
 // = (lane g, columns 8 r + 2 t, + 1), v[4 r + 2], v[4 r + 3] the same of lane
