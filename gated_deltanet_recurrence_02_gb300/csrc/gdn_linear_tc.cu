@@ -31,11 +31,11 @@
 //   warps 4-7, 20-23  W: values (ldmatrix, transposed), scaled and split, -> TMEM
 //   warps 8-11  outputs: O1 + 2^{b} O2, transposed through shared memory (stmatrix), TMA stores
 //   warp 12     tiles (TMA)
-//   warp 13     issues dS and O2
-//   warps 14-15 P
-//   warp 16     issues R, one chunk ahead, and O1 (two issuing warps: an MMA costs
-//               its issuer some 55 cycles, and half of them run for 32)
-//   warps 17-19 the chunks' decay sums
+//   warp 13     issues dS
+//   warps 14, 15, 19  P
+//   warp 16     issues R, one chunk ahead, O2 and O1 (two issuing warps: an MMA
+//               costs its issuer some 55 cycles, and half of them run for 32)
+//   warps 17-18 the chunks' decay sums
 // Few rows are cut into segments of whole chunks, so that every SM has one: a
 // first pass (kStateOnly) forms each segment's end state from its start on,
 // and the second takes each segment's start state from those.
@@ -75,23 +75,25 @@ constexpr uint32_t kStage = kStageV + 16384;
 constexpr uint32_t oP = NS * kStage;
 constexpr uint32_t oOut = oP + 8192;               // [4 warps][64 tokens][32 features] on their way out
 constexpr uint32_t oGate = oOut + 16384;           // per stage (kGate bytes), the words below
-constexpr uint32_t kGate = 1024;
+constexpr uint32_t kGate = 1280;
 constexpr int gSum = 0;                            // [64] b_t (decays of at least 2^-40 each)
 constexpr int gScaled = 64;                        // [64] scale 2^{b_t}
-constexpr int gW = 128;                            // [64] 2^{s_t}, or (two bf16 parts) [32][2] pairs of both parts
-constexpr int gLast = 192;                         // 2^{b_63}
-constexpr int gN = 193, gTok = 194, gHead = 195;   // ints: the chunk's tokens (0: no more chunks), first token, head
-constexpr int gLeft = 200;                         // [32] 2^{b_31 - b_t}
+constexpr int gW = 128;                            // 2^{s_t}: fp32 [64], or for bf16 [32 pairs][its three parts, 0]
+constexpr int gLast = 256;                         // 2^{b_63}
+constexpr int gN = 257, gTok = 258, gHead = 259;   // ints: the chunk's tokens (0: no more chunks), first token, head
+constexpr int gLeft = 264;                         // [32] 2^{b_31 - b_t}
 constexpr uint32_t oWInv = oGate + NS * kGate;     // [2][128] 1 / scale of a lane of W
 constexpr uint32_t oSInv = oWInv + 1024;           // [2][128] 1 / scale of a lane of the image
 constexpr uint32_t oPInv = oSInv + 1024;           // [2][64]  1 / scale of a row of P
-constexpr uint32_t oBar = oPInv + 512;
+constexpr uint32_t oPMax = oPInv + 512;            // [64] maxima of both parts of the later rows of P
+constexpr uint32_t oBar = oPMax + 256;
 constexpr uint32_t kSmem = oBar + 256 + 1024;      // + alignment slack
 
 // TMEM columns
 constexpr uint32_t tR = 0, tO1 = 64, tO2 = 128, tDS = 192, tS = 320, tW = 384;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kBarW = 1;  // named barrier: the W warps
+constexpr uint32_t kBarW = 1;  // named barriers: the W warps, and the two of the later rows of P
+constexpr uint32_t kBarP = 2;
 
 enum Mode {
     kWhole,      // a unit is a whole row: outputs and final state
@@ -140,6 +142,12 @@ __device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) 
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
+// a b - c: the rest of a product c = a b that was rounded to bf16, exactly.
+__device__ __forceinline__ uint32_t bf2_rest(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("{\n\t.reg .b32 t;\n\tneg.bf16x2 t, %3;\n\tfma.rn.bf16x2 %0, %1, %2, t;\n}\n" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
 
 // A power of two that brings a largest magnitude m into [2^13, 2^14), and its
 // inverse (fp16 holds 2^-14 .. 2^15 in full precision).
@@ -176,13 +184,13 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     using H = Half16<E>;
     constexpr bool kBf = H::kBf16;
     constexpr bool kOut = MODE != kStateOnly;
-    constexpr int NT = kBf && MODE != kOutputs ? 3 : 2;  // 16-bit parts of W
+    constexpr int NT = kBf && MODE != kOutputs ? 4 : 2;  // 16-bit parts of W
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_align1k(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + oBar), *empty = full + NS;
     uint64_t *r_done = empty + NS, *r_free = r_done + 1, *p_ready = r_done + 2, *w_ready = r_done + 3,
              *ds_done = r_done + 4, *ds_free = r_done + 5, *qs_done = r_done + 6, *s_ready = r_done + 7,
-             *pv_done = r_done + 8, *o_done = r_done + 9, *o_free = r_done + 10, *drain = r_done + 11;
+             *o_done = r_done + 8, *o_free = r_done + 9, *drain = r_done + 10, *ds_half = r_done + 11;
     uint32_t *slot = reinterpret_cast<uint32_t *>(r_done + 12);
     // (through a shuffle: known to be the same in every lane)
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -193,16 +201,16 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             mbar_init(&full[s], 2);                          // the copies' bytes, the decay sums
             mbar_init(&empty[s], kOut ? 2 + 4 + 4 : 1 + 4);  // MMA warps, state warps, output warps
         }
+        mbar_init(ds_half, 1);
         mbar_init(ds_done, 1);
-        mbar_init(pv_done, 1);
         mbar_init(r_done, 1);
-        mbar_init(r_free, 2);
-        mbar_init(p_ready, 2);
+        mbar_init(r_free, 3);
+        mbar_init(p_ready, 3);
         mbar_init(w_ready, 8);
         mbar_init(ds_free, 4);
         mbar_init(qs_done, 1);
         mbar_init(s_ready, 4);
-        mbar_init(o_done, 2);
+        mbar_init(o_done, 1);
         mbar_init(o_free, 4);
         mbar_init(drain, kOut ? 2 : 1);
         fence_mbar_init();
@@ -361,7 +369,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     } else if (warp < 8 || warp >= 20) {
         // ============================== W ================================
         // Two warps for each 32 features, 16 of them each.
-        regs_dec<72>();
+        regs_dec<64>();
         const int wq = warp & 3, hh = warp >= 20 ? 1 : 0;
         const uint32_t lane_base = tm + ((uint32_t)(wq * 32 + 16 * hh) << 16);
         float *winv = reinterpret_cast<float *>(sm + oWInv) + wq * 32 + 16 * hh + (lane >> 2);
@@ -375,7 +383,6 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             ok = n >= 0;
             if (n <= 0) break;
             uint8_t *st = sm + (it % NS) * kStage;
-            const float *w = gate_of(it) + gW + 2 * (lane & 3);
             if (n < C) {
                 // K and V rows past the row's end: zeros, whatever was loaded
 #pragma unroll 1
@@ -393,15 +400,15 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             // 16 tokens (j): features g and g + 8, tokens 2 t, 2 t + 1 of each eight,
             // which is the layout of the TMEM store
             auto values = [&](int j, uint32_t (&v)[4]) { ldsm_x4_trans(v, st + v_off + j * 2048); };
-            auto scaled = [&](int j, float2 (&x)[4]) {
+            float sc[2] = {1.f, 1.f}, inv[2];
+            auto scaled = [&](int j, float2 (&x)[4]) {  // fp16: in fp32
                 uint32_t v[4];
                 values(j, v);
-                const float2 w0 = *reinterpret_cast<const float2 *>(w + 16 * j);
-                const float2 w1 = *reinterpret_cast<const float2 *>(w + 16 * j + 8);
+                const float *w = gate_of(it) + gW + 2 * (lane & 3) + 16 * j;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = __fmul2_rn(e < 2 ? w0 : w1, H::unpack2(v[e]));
+                for (int e = 0; e < 4; ++e)
+                    x[e] = __fmul2_rn(*reinterpret_cast<const float2 *>(w + 8 * (e >> 1)), H::unpack2(v[e]));
             };
-            float sc[2] = {1.f, 1.f}, inv[2];
             if constexpr (!kBf) {
                 // the largest magnitude of each feature gives its scale; the four
                 // lanes of a group hold a feature's tokens
@@ -420,51 +427,52 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     half_scale(m[e], sc[e], inv[e]);
                 }
             }
-            // All of W is formed in registers while the last chunk's product still
-            // reads TMEM: the stores alone stand between that product and the next.
-            uint32_t part[NT][16];
+            // Each half of the chunk is formed while the last chunk's product still
+            // reads that half of TMEM.
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                uint32_t part[NT][8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (kBf && NT == 2) {
-                    // w = wh + wl to 16 bits: wh v = p + r exactly in two bf16 numbers,
-                    // and wl v joins the second, in packed bf16 arithmetic
-                    uint32_t v[4];
-                    values(j, v);
+                for (int jj = 0; jj < 2; ++jj) {
+                    const int j = 2 * half + jj;
+                    if constexpr (kBf) {
+                        // packed bf16 arithmetic: with w = w0 + w1 + w2 to 24 bits, a
+                        // product of bf16 numbers is exactly its rounding plus a rest
+                        uint32_t v[4];
+                        values(j, v);
+                        const uint4 *w = reinterpret_cast<const uint4 *>(gate_of(it) + gW) + (lane & 3) + 8 * j;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint2 ww = *reinterpret_cast<const uint2 *>(w + 16 * j + 8 * (e >> 1));
-                        part[0][4 * j + e] = bf2_mul(ww.x, v[e]);
-                        part[1][4 * j + e] = bf2_fma(ww.y, v[e], bf2_fma(ww.x, v[e], part[0][4 * j + e] ^ 0x80008000u));
-                    }
-                } else {
-                    float2 x[4];
-                    scaled(j, x);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float2 r = x[e];
-                        if constexpr (kBf) {
-                            // the upper 16 bits are a bf16 by truncation; what is left is exact
-#pragma unroll
-                            for (int m = 0; m < NT - 1; ++m) {
-                                const uint32_t a = __float_as_uint(r.x), b = __float_as_uint(r.y);
-                                part[m][4 * j + e] = __byte_perm(a, b, 0x7632);
-                                r = __fadd2_rn(r, make_float2(__uint_as_float((a & 0xffff0000u) ^ 0x80000000u),
-                                                              __uint_as_float((b & 0xffff0000u) ^ 0x80000000u)));
+                        for (int e = 0; e < 4; ++e) {
+                            const uint4 ww = w[4 * (e >> 1)];
+                            const uint32_t a = bf2_mul(ww.x, v[e]), r = bf2_rest(ww.x, v[e], a);
+                            part[0][4 * jj + e] = a;
+                            if constexpr (NT == 2) {
+                                part[1][4 * jj + e] = bf2_fma(ww.y, v[e], r);
+                            } else {
+                                const uint32_t b = bf2_mul(ww.y, v[e]);
+                                part[1][4 * jj + e] = r;
+                                part[2][4 * jj + e] = b;
+                                part[3][4 * jj + e] = bf2_fma(ww.z, v[e], bf2_rest(ww.y, v[e], b));
                             }
-                            part[NT - 1][4 * j + e] = H::pack2(r.x, r.y);
-                        } else {
-                            r = __fmul2_rn(make_float2(sc[e & 1], sc[e & 1]), r);
-                            part[0][4 * j + e] = H::pack2(r.x, r.y);
-                            const float2 h = H::unpack2(part[0][4 * j + e]);
-                            part[1][4 * j + e] = H::pack2(r.x - h.x, r.y - h.y);
+                        }
+                    } else {
+                        float2 x[4];
+                        scaled(j, x);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 r = __fmul2_rn(make_float2(sc[e & 1], sc[e & 1]), x[e]);
+                            part[0][4 * jj + e] = H::pack2(r.x, r.y);
+                            const float2 h = H::unpack2(part[0][4 * jj + e]);
+                            part[1][4 * jj + e] = H::pack2(r.x - h.x, r.y - h.y);
                         }
                     }
                 }
-            }
-            if (it > 0 && !(ok = wait(ds_done, it - 1))) break;
-            fence_after_sync();
+                if (it > 0 && !(ok = wait(half == 0 ? ds_half : ds_done, it - 1))) break;
+                fence_after_sync();
 #pragma unroll
-            for (int m = 0; m < NT; ++m) tmem_st_16x32(lane_base + tW + 32 * m, part[m]);
+                for (int m = 0; m < NT; ++m) tmem_st_16x16(lane_base + tW + 32 * m + 16 * half, part[m]);
+            }
+            if (!ok) break;
             // (the last product was issued after the state warps had read the
             // scales of the one before it)
             if constexpr (!kBf)
@@ -558,7 +566,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             if (lane == 0) bulk_wait_all();
         }
     } else if (warp < 16) {
-        regs_dec<64>();
+        regs_dec<72>();
         const uint32_t leader = elect_leader();
         if (warp == 12) {
             // ============================ tiles ==========================
@@ -596,54 +604,38 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 for (int j = it > NS ? it - NS : 0; j < it; ++j)
                     mbar_wait(&full[j % NS], (uint32_t)(j / NS) & 1u, kDefaultWaitNs / 8);
         } else if (warp == 13) {
-            // ======================= MMAs of the state ===================
-            const uint32_t id_o2 = idesc_f16(128, 64, false, false, kBf);
+            // ================= MMAs of the state's update ================
             const uint32_t id_ds = idesc_f16(128, dk, false, true, kBf);
-            const int ks = dk / 16;  // K = 16 steps over dk
-            // (loops are kept rolled: an MMA takes longer than its turn)
 #pragma unroll 1
             for (int it = 0;; ++it) {
                 const int n = chunk(it);
                 ok = n >= 0;
                 if (n <= 0) break;
                 const uint32_t st = smem_u32(sm) + (it % NS) * kStage;
-                // dS = W^T K, 16 tokens of every part of W at a time
+                // dS = W^T K, every part of 16 tokens of W at a time
                 if (!(ok = wait(w_ready, it)) || (it > 0 && !(ok = wait(ds_free, it - 1)))) break;
                 fence_after_sync();
-                uint64_t kn = desc_sw128(st, kBlock, 1024);
-#pragma unroll 1
+                const uint64_t kn = desc_sw128(st, kBlock, 1024);
+#pragma unroll
                 for (int j = 0; j < 4; ++j) {
 #pragma unroll
                     for (int m = 0; m < NT; ++m)
-                        mma_f16_ta_warp(leader, tm + tDS, tm + tW + 32 * m + 8 * j, kn, id_ds, m + j > 0);
-                    kn = desc_add(kn, 2048);
+                        mma_f16_ta_warp(leader, tm + tDS, tm + tW + 32 * m + 8 * j, desc_add(kn, j * 2048), id_ds, m + j > 0);
+                    if (j == 1) mma_commit_warp(leader, ds_half);
                 }
                 mma_commit_warp(leader, ds_done);
-                if constexpr (kOut) {
-                    // O2^T = S Q^T
-                    if (!(ok = wait(s_ready, it)) || (it > 0 && !(ok = wait(o_free, it - 1)))) break;
-                    fence_after_sync();
-                    uint64_t qd = desc_sw128(st + 8192, 16, 1024);
-#pragma unroll 1
-                    for (int k = 0; k < ks; ++k) {
-                        mma_f16_ta_warp(leader, tm + tO2, tm + tS + 8 * k, qd, id_o2, k > 0);
-                        qd = desc_add(qd, k == 3 ? kBlock - 96 : 32);
-                    }
-                    mma_commit_warp(leader, qs_done);
-                    mma_commit_warp(leader, o_done);
-                }
                 mma_commit_warp(leader, &empty[it % NS]);
             }
             mma_commit_warp(leader, drain);  // nothing may be in flight when TMEM is given back
             mbar_wait(drain, 0, kDefaultWaitNs);
         } else if constexpr (kOut) {
-            // ============================= P =============================
-            const int diag = 32 * (warp - 14);  // the rows' diagonal block of 32 columns
-            const int i = diag + lane;          // token of the chunk
+            // ============ P: the rows' diagonal blocks of 32 columns ==========
+            const int diag = 32 * (warp - 14);
+            const int i = diag + lane;  // token of the chunk
             const uint32_t lane_base = tm + ((uint32_t)(64 + diag) << 16);
             float *pinv = reinterpret_cast<float *>(sm + oPInv);
             const float2 scale2 = make_float2(p.scale, p.scale);
-            if (diag == 0)  // right of the first rows' diagonal block: zeros, once
+            if (diag == 0)  // right of the first rows' block: zeros, once
 #pragma unroll 1
                 for (int q = 4; q < 8; ++q)
                     *reinterpret_cast<uint4 *>(sm + oP + sw128_chunk(i, q)) = make_uint4(0u, 0u, 0u, 0u);
@@ -653,6 +645,11 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 ok = n >= 0;
                 if (n <= 0 || !(ok = wait(r_done, it))) break;
                 fence_after_sync();
+                uint32_t x[32];
+                tmem_ld32_async(lane_base + tR + diag, x);
+                tmem_wait_ld();
+                fence_before_sync();
+                arrive(r_free);
                 if (n < C) {  // V rows past the row's end: zeros, whatever was loaded
                     uint8_t *v = sm + (it % NS) * kStage + kStageV;
 #pragma unroll 1
@@ -662,97 +659,73 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                         *reinterpret_cast<uint4 *>(v + 8192 + off) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
-                const float *gate = gate_of(it);
-                const float bi = gate[gSum + i];
-                // 2^{b_i - b_31} of the columns left of the diagonal block: with
-                // 2^{b_31 - b_j} two factors of at most 1 where no decay is above 1
-                const float l = p.scale * ex2_approx(bi - gate[gSum + 31]);
-                const float2 l2 = make_float2(l, l);
-                // 16 columns from diag + 16 hh on, and the 16 from 16 hh on
-                auto columns = [&](int hh, uint32_t (&x)[16], uint32_t (&y)[16]) {
-                    tmem_ld16_async(lane_base + tR + diag + 16 * hh, x);
-                    if (diag > 0) tmem_ld16_async(lane_base + tR + 16 * hh, y);
-                    tmem_wait_ld();
-                };
-                auto decayed = [&](int hh, uint32_t (&x)[16], uint32_t (&y)[16], float &m) {
+                const float *b = gate_of(it) + gSum + diag;
+                const float bi = b[lane];
+                float m = 0.f, sc = 1.f, inv = 1.f;
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float2 b2 = *reinterpret_cast<const float2 *>(gate + gSum + diag + 16 * hh + j);
-                        float2 v = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-                        v = __fmul2_rn(__fmul2_rn(v, scale2), make_float2(ex2_approx(bi - b2.x), ex2_approx(bi - b2.y)));
-                        v.x = 16 * hh + j <= lane ? v.x : 0.f;
-                        v.y = 16 * hh + j + 1 <= lane ? v.y : 0.f;
-                        if constexpr (!kBf) m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
+                for (int j = 0; j < 32; j += 2) {
+                    const float2 b2 = *reinterpret_cast<const float2 *>(b + j);
+                    float2 v = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                    v = __fmul2_rn(__fmul2_rn(v, scale2), make_float2(ex2_approx(bi - b2.x), ex2_approx(bi - b2.y)));
+                    v.x = j <= lane ? v.x : 0.f;
+                    v.y = j + 1 <= lane ? v.y : 0.f;
+                    if constexpr (kBf) {
+                        x[j / 2] = H::pack2(v.x, v.y);
+                    } else {
+                        m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
                         x[j] = __float_as_uint(v.x);
                         x[j + 1] = __float_as_uint(v.y);
                     }
-                    if (diag > 0)
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const float2 c2 = *reinterpret_cast<const float2 *>(gate + gLeft + 16 * hh + j);
-                            const float2 v =
-                                __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), c2), l2);
-                            if constexpr (!kBf) m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
-                            y[j] = __float_as_uint(v.x);
-                            y[j + 1] = __float_as_uint(v.y);
-                        }
-                };
-                float sc = 1.f, inv = 1.f, m = 0.f;
+                }
+                // the products with the last chunk's P are done (and so are the reads
+                // of the scales of the one before)
+                if (it > 0 && !(ok = wait(o_done, it - 1))) break;
                 if constexpr (!kBf) {
-#pragma unroll 1
-                    for (int hh = 0; hh < 2; ++hh) {
-                        uint32_t x[16], y[16];
-                        columns(hh, x, y);
-                        decayed(hh, x, y, m);
+                    if (diag > 0) {  // one scale a row: with the maximum of its left part
+                        float *pmax = reinterpret_cast<float *>(sm + oPMax);
+                        pmax[lane] = m;
+                        named_bar(kBarP, 64);
+                        m = fmaxf(m, pmax[32 + lane]);
                     }
                     half_scale(m, sc, inv);
-                }
-                auto store = [&](int q, const uint32_t *z) {  // eight columns from 8 q on
-                    uint32_t v[4];
+                    pinv[(it & 1) * 64 + i] = inv;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float a = __uint_as_float(z[2 * e]), b = __uint_as_float(z[2 * e + 1]);
-                        v[e] = kBf ? H::pack2(a, b) : H::pack2(sc * a, sc * b);
-                    }
-                    *reinterpret_cast<uint4 *>(sm + oP + sw128_chunk(i, q)) = make_uint4(v[0], v[1], v[2], v[3]);
-                };
-#pragma unroll 1
-                for (int hh = 0; hh < 2; ++hh) {
-                    uint32_t x[16], y[16];
-                    columns(hh, x, y);
-                    if (hh == 1) {
-                        fence_before_sync();
-                        arrive(r_free);
-                    }
-                    decayed(hh, x, y, m);
-                    if (hh == 0) {
-                        // the products with the last chunk's P are done (and so are
-                        // the reads of the scales of the one before)
-                        if (it > 0 && !(ok = wait(pv_done, it - 1))) break;
-                        if constexpr (!kBf) pinv[(it & 1) * 64 + i] = inv;
-                    }
-                    store(diag / 8 + 2 * hh, x);
-                    store(diag / 8 + 2 * hh + 1, x + 8);
-                    if (diag > 0) {
-                        store(2 * hh, y);
-                        store(2 * hh + 1, y + 8);
-                    }
+                    for (int j = 0; j < 32; j += 2)
+                        x[j / 2] = H::pack2(sc * __uint_as_float(x[j]), sc * __uint_as_float(x[j + 1]));
                 }
-                if (!ok) break;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<uint4 *>(sm + oP + sw128_chunk(i, diag / 8 + q)) =
+                        make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
                 fence_proxy_async();
                 arrive(p_ready);
             }
         }
     } else {
-        regs_dec<40>();
+        regs_dec<48>();
         const uint32_t leader = elect_leader();
         if (warp == 16) {
-            // ====================== MMAs of the scores ===================
+            // ===================== MMAs of the outputs ===================
             if constexpr (kOut) {
                 const uint32_t id_r = idesc_f16(128, 64, false, false, kBf);
                 const uint32_t id_o1 = idesc_f16(128, 64, true, false, kBf);
-                const int ks = dk / 16;
                 const uint32_t s0 = smem_u32(sm);
+                // K = 16 steps over dk, each with constant offsets: an MMA whose
+                // descriptor is computed in a loop costs its issuer twice the time
+                auto over_dk = [&](auto step) {
+                    step(0);
+                    step(1);
+                    if (dk >= 64) {
+                        step(2);
+                        step(3);
+                    }
+                    if (dk == 128) {
+                        step(4);
+                        step(5);
+                        step(6);
+                        step(7);
+                    }
+                };
 #pragma unroll 1
                 for (int it = 0;; ++it) {
                     const int n = chunk(it);
@@ -761,28 +734,32 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                         // R = [K;Q] K^T
                         if (it > 0 && !(ok = wait(r_free, it - 1))) break;
                         fence_after_sync();
-                        uint64_t d = desc_sw128(s0 + (it % NS) * kStage, 16, 1024);
-#pragma unroll 1
-                        for (int k = 0; k < ks; ++k) {
+                        const uint64_t kq = desc_sw128(s0 + (it % NS) * kStage, 16, 1024);
+                        over_dk([&](int k) {
+                            const uint64_t d = desc_add(kq, (k >> 2) * kBlock + (k & 3) * 32);
                             mma_f16_warp(leader, tm + tR, d, d, id_r, k > 0);
-                            d = desc_add(d, k == 3 ? kBlock - 96 : 32);
-                        }
+                        });
                         mma_commit_warp(leader, r_done);
                     }
                     if (it > 0 && ok) {
-                        // O1^T = V^T P^T of the chunk before
+                        // of the chunk before: O2^T = S Q^T,
                         const int pt = it - 1;
-                        if (!(ok = wait(p_ready, pt)) || (pt > 0 && !(ok = wait(o_free, pt - 1)))) break;
+                        if (!(ok = wait(s_ready, pt)) || (pt > 0 && !(ok = wait(o_free, pt - 1)))) break;
                         fence_after_sync();
-                        uint64_t vd = desc_sw128(s0 + (pt % NS) * kStage + kStageV, 8192, 1024);
-                        uint64_t pd = desc_sw128(s0 + oP, 16, 1024);
-#pragma unroll 1
-                        for (int j = 0; j < 4; ++j) {
-                            mma_f16_warp(leader, tm + tO1, vd, pd, id_o1, j > 0);
-                            vd = desc_add(vd, 2048);
-                            pd = desc_add(pd, 32);
-                        }
-                        mma_commit_warp(leader, pv_done);
+                        const uint64_t qd = desc_sw128(s0 + (pt % NS) * kStage + 8192, 16, 1024);
+                        over_dk([&](int k) {
+                            mma_f16_ta_warp(leader, tm + tO2, tm + tS + 8 * k,
+                                            desc_add(qd, (k >> 2) * kBlock + (k & 3) * 32), id_r, k > 0);
+                        });
+                        mma_commit_warp(leader, qs_done);
+                        // and O1^T = V^T P^T
+                        if (!(ok = wait(p_ready, pt))) break;
+                        fence_after_sync();
+                        const uint64_t vd = desc_sw128(s0 + (pt % NS) * kStage + kStageV, 8192, 1024);
+                        const uint64_t pd = desc_sw128(s0 + oP, 16, 1024);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_f16_warp(leader, tm + tO1, desc_add(vd, j * 2048), desc_add(pd, j * 32), id_o1, j > 0);
                         mma_commit_warp(leader, o_done);
                         mma_commit_warp(leader, &empty[pt % NS]);
                     }
@@ -791,9 +768,70 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 mma_commit_warp(leader, drain);
                 mbar_wait(drain, 0, kDefaultWaitNs);
             }
+        } else if (warp == 19) {
+            if constexpr (kOut) {
+                // ======== P: the columns left of the second diagonal block ========
+                // 2^{b_i - b_31} 2^{b_31 - b_j}: two factors of at most 1 where no
+                // decay is above 1.
+                const int i = 32 + lane;  // token of the chunk
+                const uint32_t lane_base = tm + (96u << 16);
+#pragma unroll 1
+                for (int it = 0;; ++it) {
+                    const int n = chunk(it);
+                    ok = n >= 0;
+                    if (n <= 0 || !(ok = wait(r_done, it))) break;
+                    fence_after_sync();
+                    const float *gate = gate_of(it);
+                    const float l = p.scale * ex2_approx(gate[gSum + i] - gate[gSum + 31]);
+                    float2 l2 = make_float2(l, l);
+                    if constexpr (!kBf) {
+                        float m = 0.f, sc, inv;
+#pragma unroll 1
+                        for (int hh = 0; hh < 2; ++hh) {
+                            uint32_t y[16];
+                            tmem_ld16_async(lane_base + tR + 16 * hh, y);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                m = fmaxf(m, fabsf(__uint_as_float(y[j]) * gate[gLeft + 16 * hh + j] * l));
+                        }
+                        float *pmax = reinterpret_cast<float *>(sm + oPMax);
+                        // (one buffer: the diagonal part's warp reads it before its
+                        // p_ready, and the next R comes after both)
+                        pmax[32 + lane] = m;
+                        named_bar(kBarP, 64);
+                        half_scale(fmaxf(m, pmax[lane]), sc, inv);
+                        l2 = make_float2(l * sc, l * sc);
+                    }
+                    if (it > 0 && !(ok = wait(o_done, it - 1))) break;
+#pragma unroll 1
+                    for (int hh = 0; hh < 2; ++hh) {
+                        uint32_t y[16];
+                        tmem_ld16_async(lane_base + tR + 16 * hh, y);
+                        tmem_wait_ld();
+                        if (hh == 1) {
+                            fence_before_sync();
+                            arrive(r_free);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 c2 = *reinterpret_cast<const float2 *>(gate + gLeft + 16 * hh + j);
+                            const float2 v =
+                                __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), c2), l2);
+                            y[j / 2] = H::pack2(v.x, v.y);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            *reinterpret_cast<uint4 *>(sm + oP + sw128_chunk(i, 2 * hh + q)) =
+                                make_uint4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+                    }
+                    fence_proxy_async();
+                    arrive(p_ready);
+                }
+            }
         } else {
             // ========================= decay sums ========================
-            // Three warps take the chunks in turn: a chunk's decays are loaded while
+            // Two warps take the chunks in turn: a chunk's decays are loaded while
             // the warp's last one is worked on, and take longer than a chunk does.
             const bool per_head = (p.conv & GDN_ALPHA_PER_HEAD) != 0;
             unsigned u = blockIdx.x - gridDim.x;  // (wraps to blockIdx.x at the first step)
@@ -805,7 +843,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             bool end = false;                 // the next one would be the first past the last
             bool over = false;                // no more chunks
 #pragma unroll 1
-            for (int it = warp - 20;; it += 3) {
+            for (int it = warp - 19;; it += 2) {
                 const int t0_ = t0, n_ = n, h_ = h;
                 const bool end_ = end;
                 float a[2] = {raw[0], raw[1]};
@@ -822,7 +860,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     }
                     end = over && steps == 1;
                 }
-                steps = 3;
+                steps = 2;
                 if (!over) {
                     t0 = (int)(x.tok0 + (long)c * C);
                     n = min(C, x.len - c * C);
@@ -873,10 +911,13 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 *reinterpret_cast<float2 *>(gate + gScaled + 2 * lane) =
                     make_float2(p.scale * ex2_approx(ex + a[0]), p.scale * ex2_approx(up));
                 const float2 w2 = make_float2(ex2_approx(suf + a[1]), ex2_approx(suf));
-                if constexpr (kBf && NT == 2) {
-                    const uint32_t wh = H::pack2(w2.x, w2.y);
-                    const float2 u = H::unpack2(wh);
-                    *reinterpret_cast<uint2 *>(gate + gW + 2 * lane) = make_uint2(wh, H::pack2(w2.x - u.x, w2.y - u.y));
+                if constexpr (kBf) {
+                    const uint32_t wa = H::pack2(w2.x, w2.y);
+                    float2 r = H::unpack2(wa);
+                    r = make_float2(w2.x - r.x, w2.y - r.y);
+                    const uint32_t wb = H::pack2(r.x, r.y);
+                    const float2 y = H::unpack2(wb);
+                    *reinterpret_cast<uint4 *>(gate + gW + 4 * lane) = make_uint4(wa, wb, H::pack2(r.x - y.x, r.y - y.y), 0u);
                 } else {
                     *reinterpret_cast<float2 *>(gate + gW + 2 * lane) = w2;
                 }
