@@ -108,9 +108,18 @@ def _p(t) -> Optional[int]:
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (2.8 us less a
+# call on the GB300's host, where a whole decode call takes some ten); the public
+# call where this PyTorch has no such function.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -335,8 +344,8 @@ def gdn_linear_prefill(q, k, v, alpha, *, B: int, T: Optional[int] = None, cu_se
         final_state = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=v.device)
     n0 = initial_state.shape[0] if initial_state is not None else 0
     if workspace is None:
-        need = gdn_linear_prefill_workspace_size(B, T, Hk, Hv, dk, dv, q.dtype,
-                                                 varlen=cu_seqlens is not None)
+        need = lib().gdn_linear_prefill_workspace_size(B, T, Hk, Hv, dk, dv, _DT[q.dtype],
+                                                       int(cu_seqlens is not None))
         if need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
@@ -381,6 +390,8 @@ def _rows(t, width_dims: int):
     width_dims dimensions) are contiguous."""
     if not t.is_cuda:
         raise ValueError("libgdn takes device tensors")
+    if t.is_contiguous():
+        return t.data_ptr(), t.shape[1] * (t.shape[2] if width_dims == 2 else 1)
     want = 1
     for d in range(t.dim() - 1, t.dim() - 1 - width_dims, -1):
         if t.shape[d] != 1 and t.stride(d) != want:
@@ -394,24 +405,32 @@ def gdn_gated_norm(x, z=None, weight=None, *, eps: float = 1e-6, gate: int = GDN
     """Norm of each head of x [N, H, d], fused with its gate z: rmsnorm(x) *
     weight * act(z), or with GDN_GATE_FIRST rmsnorm(x * act(z)) * weight.  x, z
     and out may be slices of wider rows.  Without z the gate is none."""
-    N, H, d = x.shape
+    shape, dtype = x.shape, x.dtype
+    N, H, d = shape
     if z is None:
         gate &= ~0xF
-    elif z.shape != x.shape or z.dtype != x.dtype:
-        raise ValueError("z must have the shape and the dtype of x")
-    if weight is not None and weight.shape != (d,):
-        raise ValueError("weight must have one element for each of a head")
+        zp, zs = None, H * d
+    else:
+        if z.shape != shape or z.dtype != dtype:
+            raise ValueError("z must have the shape and the dtype of x")
+        zp, zs = _rows(z, 2)
+    wp, wt = None, GDN_F32
+    if weight is not None:
+        if weight.dim() != 1 or weight.shape[0] != d:
+            raise ValueError("weight must have one element for each of a head")
+        wp, wt = _p(weight), _DT[weight.dtype]
     if out is None:
-        out = torch.empty((N, H, d), dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != x.dtype:
-        raise ValueError("out must have the shape and the dtype of x")
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+        op, os_ = out.data_ptr(), H * d
+    else:
+        if out.shape != shape or out.dtype != dtype:
+            raise ValueError("out must have the shape and the dtype of x")
+        op, os_ = _rows(out, 2)
     xp, xs = _rows(x, 2)
-    zp, zs = _rows(z, 2) if z is not None else (None, H * d)
-    op, os_ = _rows(out, 2)
-    st = lib().gdn_gated_norm(xp, zp, _p(weight), op, N, H, d, xs, zs, os_, eps, gate,
-                              _DT[x.dtype], _DT[weight.dtype] if weight is not None else GDN_F32,
+    st = lib().gdn_gated_norm(xp, zp, wp, op, N, H, d, xs, zs, os_, eps, gate, _DT[dtype], wt,
                               _stream(stream))
-    _check(st, "gdn_gated_norm")
+    if st:
+        _check(st, "gdn_gated_norm")
     return out
 
 
@@ -423,34 +442,59 @@ def gdn_residual_norm(y, residual=None, *, post_weight=None, gate=None,
     [rmsnorm(y) * post_weight], and rmsnorm(x') * pre_weight.  y and gate are
     [N, D] (rows may be slices).  Returns (x', out); residual_out may be
     residual itself."""
-    N, D = y.shape
-    if residual is not None and residual.shape != y.shape:
-        raise ValueError("residual must have the shape of y")
-    if gate is not None and (gate.shape != y.shape or gate.dtype != y.dtype):
-        raise ValueError("gate must have the shape and the dtype of y")
-    for w in (post_weight, pre_weight):
-        if w is not None and w.shape != (D,):
+    shape, dtype = y.shape, y.dtype
+    N, D = shape
+    flags = GDN_NORM_UNIT_OFFSET if unit_offset else 0
+    xp, rdt = None, residual_dtype or dtype
+    if residual is not None:
+        if residual.shape != shape:
+            raise ValueError("residual must have the shape of y")
+        xp, rdt = _p(residual), residual.dtype
+    gp, gs = None, D
+    if gate is not None:
+        if gate.shape != shape or gate.dtype != dtype:
+            raise ValueError("gate must have the shape and the dtype of y")
+        gp, gs = _rows(gate, 1)
+        flags |= gate_act
+    w1 = w2 = None
+    wt = GDN_F32
+    if post_weight is not None:
+        if post_weight.dim() != 1 or post_weight.shape[0] != D:
             raise ValueError("a norm's weight must have one element for each of a row")
-    if post_weight is not None and pre_weight is not None and post_weight.dtype != pre_weight.dtype:
-        raise ValueError("the two weights must have one dtype")
-    rdt = residual.dtype if residual is not None else (residual_dtype or y.dtype)
+        w1, wt = _p(post_weight), _DT[post_weight.dtype]
+    if pre_weight is not None:
+        if pre_weight.dim() != 1 or pre_weight.shape[0] != D:
+            raise ValueError("a norm's weight must have one element for each of a row")
+        if w1 is not None and _DT[pre_weight.dtype] != wt:
+            raise ValueError("the two weights must have one dtype")
+        w2, wt = _p(pre_weight), _DT[pre_weight.dtype]
     if residual_out is None:
-        residual_out = torch.empty((N, D), dtype=rdt, device=y.device)
+        residual_out = torch.empty(shape, dtype=rdt, device=y.device)
+    elif residual_out.shape != shape or residual_out.dtype != rdt:
+        raise ValueError("residual_out must have the shape of y and the residual's dtype")
     if out is None:
-        out = torch.empty((N, D), dtype=y.dtype, device=y.device)
-    if (residual_out.shape != y.shape or residual_out.dtype != rdt or out.shape != y.shape
-            or out.dtype != y.dtype):
-        raise ValueError("outputs must have the shape of y and their input's dtype")
+        out = torch.empty(shape, dtype=dtype, device=y.device)
+    elif out.shape != shape or out.dtype != dtype:
+        raise ValueError("out must have the shape and the dtype of y")
     yp, ys = _rows(y, 1)
-    gp, gs = _rows(gate, 1) if gate is not None else (None, D)
-    w = post_weight if post_weight is not None else pre_weight
-    flags = (gate_act if gate is not None else GDN_GATE_NONE) | (GDN_NORM_UNIT_OFFSET if unit_offset else 0)
-    st = lib().gdn_residual_norm(yp, _p(residual), gp, _p(post_weight), _p(pre_weight),
-                                 _p(residual_out), _p(out), N, D, ys, gs, res_scale, eps, flags,
-                                 _DT[y.dtype], _DT[rdt],
-                                 _DT[w.dtype] if w is not None else GDN_F32, _stream(stream))
-    _check(st, "gdn_residual_norm")
+    st = lib().gdn_residual_norm(yp, xp, gp, w1, w2, _p(residual_out), _p(out), N, D, ys, gs,
+                                 res_scale, eps, flags, _DT[dtype], _DT[rdt], wt, _stream(stream))
+    if st:
+        _check(st, "gdn_residual_norm")
     return residual_out, out
+
+
+def _positions(t, K: int):
+    """Pointer and position stride (elements) of probabilities [B, K, V] whose
+    rows are contiguous and evenly spaced (a slice of a padded vocabulary)."""
+    if t.is_contiguous():
+        return _p(t), t.shape[2]
+    if not t.is_cuda:
+        raise ValueError("libgdn takes device tensors")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (t.shape[0] > 1 and s0 != K * s1):
+        raise ValueError("probabilities must be contiguous rows, evenly spaced")
+    return t.data_ptr(), s1
 
 
 def gdn_accept_drafts(target_probs, draft_probs, draft_tokens, uniform, *, draft_count=None,
@@ -461,24 +505,32 @@ def gdn_accept_drafts(target_probs, draft_probs, draft_tokens, uniform, *, draft
     token, then -1; emitted_count is the accepted_count of a replay."""
     B, K1, V = target_probs.shape
     K = K1 - 1
+    dtype, i32 = target_probs.dtype, torch.int32
     if draft_tokens.shape != (B, K) or uniform.shape != (B, K1):
         raise ValueError("draft_tokens must be [B, K] and uniform [B, K + 1]")
-    if draft_probs is not None and (draft_probs.shape != (B, K, V)
-                                    or draft_probs.dtype != target_probs.dtype):
-        raise ValueError("draft_probs must be [B, K, V] in target_probs' dtype")
+    if draft_tokens.dtype != i32 or uniform.dtype != torch.float32:
+        raise ValueError("draft_tokens are int32, uniform is float32")
+    qp, qs = None, V
+    if draft_probs is not None:
+        if draft_probs.shape != (B, K, V) or draft_probs.dtype != dtype:
+            raise ValueError("draft_probs must be [B, K, V] in target_probs' dtype")
+        qp, qs = _positions(draft_probs, K)
+    if draft_count is not None and (draft_count.shape != (B,) or draft_count.dtype != i32):
+        raise ValueError("draft_count is int32 [B]")
     if tokens is None:
-        tokens = torch.empty((B, K1), dtype=torch.int32, device=target_probs.device)
+        tokens = torch.empty((B, K1), dtype=i32, device=target_probs.device)
+    elif tokens.shape != (B, K1) or tokens.dtype != i32:
+        raise ValueError("tokens is int32 [B, K + 1]")
     if emitted_count is None:
-        emitted_count = torch.empty((B,), dtype=torch.int32, device=target_probs.device)
-    for t in (draft_tokens, draft_count, tokens, emitted_count):
-        if t is not None and t.dtype != torch.int32:
-            raise ValueError("tokens and counts are int32")
-    if uniform.dtype != torch.float32:
-        raise ValueError("uniform is float32")
-    st = lib().gdn_accept_drafts(
-        _p(target_probs), _p(draft_probs), _p(draft_tokens), _p(uniform), _p(draft_count),
-        _p(tokens), _p(emitted_count), B, K, V, V, V, _DT[target_probs.dtype], _stream(stream))
-    _check(st, "gdn_accept_drafts")
+        emitted_count = torch.empty((B,), dtype=i32, device=target_probs.device)
+    elif emitted_count.shape != (B,) or emitted_count.dtype != i32:
+        raise ValueError("emitted_count is int32 [B]")
+    pp, ps = _positions(target_probs, K1)
+    st = lib().gdn_accept_drafts(pp, qp, _p(draft_tokens), _p(uniform), _p(draft_count),
+                                 _p(tokens), _p(emitted_count), B, K, V, ps, qs, _DT[dtype],
+                                 _stream(stream))
+    if st:
+        _check(st, "gdn_accept_drafts")
     return tokens, emitted_count
 
 
