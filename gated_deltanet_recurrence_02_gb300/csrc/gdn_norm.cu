@@ -13,6 +13,8 @@
 // row is spread over a group of threads (part of a warp, or a whole CTA), each
 // holding ITEMS 16-byte vectors of it.  Sums of squares are fp32; h is formed
 // from the unrounded x'.
+#include <atomic>
+
 #include "gdn_internal.cuh"
 
 namespace gdn {
@@ -37,21 +39,52 @@ __device__ __forceinline__ void load_vec(const T *p, float (&x)[VEC]) {
         for (int j = 0; j < VEC; ++j) x[j] = ld_f(&u.v[j]);
     }
 }
+// VEC elements as they are stored, loaded ahead of their use.
+template <typename T, int VEC>
+struct Raw {
+    static constexpr int kPacks = sizeof(T) * VEC > 16 ? (int)(sizeof(T) * VEC / 16) : 1;
+    Pack<T, VEC / kPacks> v[kPacks];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int k = 0; k < kPacks; ++k) v[k] = reinterpret_cast<const Pack<T, VEC / kPacks> *>(p)[k];
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int k = 0; k < kPacks; ++k)
+#pragma unroll
+            for (int j = 0; j < VEC / kPacks; ++j) v[k].v[j] = T(0.f);
+    }
+    __device__ __forceinline__ void get(float (&x)[VEC]) const {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) x[j] = at(j);
+    }
+    __device__ __forceinline__ float at(int j) const { return ld_f(&v[j / (VEC / kPacks)].v[j % (VEC / kPacks)]); }
+};
+__device__ __forceinline__ void st_pair(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
+__device__ __forceinline__ void st_pair(__half *p, float a, float b) {
+    *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(a, b);
+}
+__device__ __forceinline__ void st_pair(__nv_bfloat16 *p, float a, float b) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(a, b);
+}
 template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T *p, const float (&x)[VEC]) {
-    if constexpr (sizeof(T) * VEC > 16) {
-#pragma unroll
-        for (int j = 0; j < VEC; j += 4)
-            *reinterpret_cast<float4 *>(p + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+    if constexpr (VEC == 1) {
+        st_out(p, x[0]);
     } else {
-        Pack<T, VEC> u;
+        constexpr int P = 16 / (int)sizeof(T);  // elements of a 16-byte store
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) st_out(&u.v[j], x[j]);
-        *reinterpret_cast<Pack<T, VEC> *>(p) = u;
+        for (int j = 0; j < VEC; j += P) {
+            Pack<T, P> u;
+#pragma unroll
+            for (int e = 0; e < P; e += 2) st_pair(&u.v[e], x[j + e], x[j + e + 1]);
+            *reinterpret_cast<Pack<T, P> *>(p + j) = u;
+        }
     }
 }
 
-// VEC weights from element i on, of runtime type; ones without weights.
+// VEC weights from element i on, of runtime type (vectors: 16-byte aligned);
+// ones without weights.
 template <int VEC>
 __device__ __forceinline__ void load_weight(const void *w, int i, int dt, float offset, float (&x)[VEC]) {
     if (w == nullptr) {
@@ -59,23 +92,52 @@ __device__ __forceinline__ void load_weight(const void *w, int i, int dt, float 
         for (int j = 0; j < VEC; ++j) x[j] = 1.f;
         return;
     }
+    if (dt == GDN_F32) load_vec<float, VEC>(reinterpret_cast<const float *>(w) + i, x);
+    else if (dt == GDN_F16) load_vec<__half, VEC>(reinterpret_cast<const __half *>(w) + i, x);
+    else load_vec<__nv_bfloat16, VEC>(reinterpret_cast<const __nv_bfloat16 *>(w) + i, x);
+    if (offset != 0.f)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) x[j] = ld_gate(w, i + j, dt) + offset;
+        for (int j = 0; j < VEC; ++j) x[j] += offset;
 }
 
-// silu(z) or sigmoid(z).  With 16-bit storage the fast exponential and divide
-// are far below the rounding of the result.
-template <typename T>
-__device__ __forceinline__ float activation(float z, int act) {
-    float s;
-    if constexpr (sizeof(T) == 2) s = __fdividef(1.f, 1.f + __expf(-z));
-    else s = 1.f / (1.f + expf(-z));
-    return act == GDN_GATE_SILU ? z * s : s;
+// 1 / (1 + e^-z) by the base-2 exponential and the reciprocal of the PTX ISA
+// (relative errors 2^-22 and 2^-23), in place.  For 16-bit values the rounding of
+// z log2 e is as far below their own as those; fp32 takes its rest along.
+template <typename T, int VEC>
+__device__ __forceinline__ void sigmoid_of(float (&z)[VEC]) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        const float t = -1.4426950408889634f * z[j];
+        float e, s;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+        if constexpr (sizeof(T) == 4) {
+            const float rest = fmaf(-1.4426950408889634f, z[j], -t);
+            const float more = e * (0.6931471805599453f * rest);
+            e = t < 126.f ? e + more : e;  // (no rest beside an infinite e)
+        }
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+        z[j] = s;
+    }
+}
+// act(z), in place; the branches are the same for every thread.
+template <typename T, int VEC>
+__device__ __forceinline__ void activate(float (&z)[VEC], int act) {
+    float s[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s[j] = z[j];
+    sigmoid_of<T, VEC>(s);
+    if (act == GDN_GATE_SILU) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) z[j] *= s[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) z[j] = s[j];
+    }
 }
 
 // Sum over the row's group of threads: `lanes` (a power of two) threads of a
-// warp, or, with lanes > 32, all threads of the CTA (red: one float a warp and
-// the total; safe to call again after the next __syncthreads-ordered call).
+// warp, or, with lanes > 32, all threads of the CTA.  red: a float for each
+// warp, another buffer in every second call.
 __device__ __forceinline__ float row_sum(float x, int lanes, float *red) {
     for (int o = (lanes < 32 ? lanes : 32) / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     if (lanes <= 32) return x;
@@ -95,51 +157,78 @@ constexpr int kMaxThreads = VEC > 1 ? 512 : 1024;
 
 template <typename T, int VEC, int ITEMS>
 __global__ void __launch_bounds__(kMaxThreads<VEC>) gated_norm_kernel(const GatedNormParams p, int lanes) {
-    __shared__ float red[32];
+    __shared__ float red[2][32];
     const int per_cta = blockDim.x / lanes;
-    const int64_t rows = p.N * p.H;
-    const int64_t r = (int64_t)blockIdx.x * per_cta + threadIdx.x / lanes;
+    const unsigned rows = (unsigned)(p.N * p.H), H = (unsigned)p.H;
     const int t = threadIdx.x % lanes;
-    const bool live = r < rows;  // a dead row's threads still take part in the shuffles
-    const int64_t n = live ? r / p.H : 0;
-    const int h = (int)(live ? r - n * p.H : 0);
-    const T *x = reinterpret_cast<const T *>(p.x) + n * p.xs + (int64_t)h * p.d;
-    const T *z = reinterpret_cast<const T *>(p.z) + n * p.zs + (int64_t)h * p.d;
-    T *y = reinterpret_cast<T *>(p.out) + n * p.os + (int64_t)h * p.d;
     const int act = p.gate & 0xF;
     const bool first = (p.gate & GDN_GATE_FIRST) != 0;
     const float offset = (p.gate & GDN_NORM_UNIT_OFFSET) ? 1.f : 0.f;
-    float a[ITEMS][VEC], g[ITEMS][VEC];
+    const float inv_d = 1.f / (float)p.d;
+    // the thread's columns, and so its weights, are the same in every row
+    float w[ITEMS][VEC];
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
         const int i = (k * lanes + t) * VEC;
-        const bool in = live && i < p.d;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) a[k][j] = 0.f, g[k][j] = 0.f;
-        if (in) load_vec<T, VEC>(x + i, a[k]);
-        if (in && act != GDN_GATE_NONE) load_vec<T, VEC>(z + i, g[k]);
+        if (i < p.d) load_weight<VEC>(p.w, i, p.dt_w, offset, w[k]);
     }
-    float ss = 0.f;
+    Raw<T, VEC> nx[ITEMS], nz[ITEMS];  // the next row, on its way while this one is worked on
+    auto fetch = [&](unsigned r) {
+        const unsigned n = r / H, h = r - n * H;
+        const T *x = reinterpret_cast<const T *>(p.x) + (int64_t)n * p.xs + (int64_t)h * p.d;
+        const T *z = reinterpret_cast<const T *>(p.z) + (int64_t)n * p.zs + (int64_t)h * p.d;
 #pragma unroll
-    for (int k = 0; k < ITEMS; ++k)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            g[k][j] = act != GDN_GATE_NONE ? activation<T>(g[k][j], act) : 1.f;
-            if (first) a[k][j] *= g[k][j];
-            // elements past the row are zeros, and stay zeros through a gate
-            ss = fmaf(a[k][j], a[k][j], ss);
+        for (int k = 0; k < ITEMS; ++k) {
+            const int i = (k * lanes + t) * VEC;
+            if (i < p.d) {
+                nx[k].load(x + i);
+                if (act != GDN_GATE_NONE) nz[k].load(z + i);
+            }
         }
-    ss = row_sum(ss, lanes, red);
-    const float rs = 1.f / sqrtf(ss / (float)p.d + p.eps);
+    };
+    // (every thread of a CTA takes as many turns: the sums are taken together)
+    const unsigned r0 = blockIdx.x * per_cta, step = gridDim.x * per_cta, mine = threadIdx.x / lanes;
 #pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-        const int i = (k * lanes + t) * VEC;
-        if (live && i < p.d) {
-            float w[VEC];
-            load_weight<VEC>(p.w, i, p.dt_w, offset, w);
+    for (int k = 0; k < ITEMS; ++k) nx[k].clear(), nz[k].clear();
+    if (r0 + mine < rows) fetch(r0 + mine);
+    int turn = 0;
+    for (unsigned base = r0; base < rows; base += step, ++turn) {
+        const unsigned r = base + mine;
+        const bool live = r < rows;
+        float a[ITEMS][VEC], g[ITEMS][VEC];
+        float ss = 0.f;
+        // (columns past the row and rows past the last hold zeros or old values)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) a[k][j] *= rs * w[j] * (first ? 1.f : g[k][j]);
-            store_vec<T, VEC>(y + i, a[k]);
+        for (int k = 0; k < ITEMS; ++k) {
+            nx[k].get(a[k]);
+            if (act != GDN_GATE_NONE) {
+                nz[k].get(g[k]);
+                activate<T, VEC>(g[k], act);
+                if (first)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) a[k][j] *= g[k][j];
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) ss = fmaf(a[k][j], a[k][j], ss);
+        }
+        if (r + step < rows) fetch(r + step);
+        ss = row_sum(ss, lanes, red[turn & 1]);
+        const float rs = rsqrtf(fmaf(ss, inv_d, p.eps));
+        if (live) {
+            const unsigned n = r / H, h = r - n * H;
+            T *y = reinterpret_cast<T *>(p.out) + (int64_t)n * p.os + (int64_t)h * p.d;
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) {
+                const int i = (k * lanes + t) * VEC;
+                if (i < p.d) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) a[k][j] *= rs * w[k][j];
+                    if (act != GDN_GATE_NONE && !first)
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) a[k][j] *= g[k][j];
+                    store_vec<T, VEC>(y + i, a[k]);
+                }
+            }
         }
     }
 }
@@ -147,68 +236,93 @@ __global__ void __launch_bounds__(kMaxThreads<VEC>) gated_norm_kernel(const Gate
 template <typename T, typename TR, int VEC, int ITEMS>
 __global__ void __launch_bounds__(kMaxThreads<VEC>) residual_norm_kernel(const ResidualNormParams p, int lanes) {
     __shared__ float red[2][32];
-    const int per_cta = blockDim.x / lanes;
-    const int64_t r = (int64_t)blockIdx.x * per_cta + threadIdx.x / lanes;
-    const int t = threadIdx.x % lanes;
-    const bool live = r < p.N;
-    const int64_t n = live ? r : 0;
-    const T *y = reinterpret_cast<const T *>(p.y) + n * p.ys;
-    const T *z = reinterpret_cast<const T *>(p.z) + n * p.zs;
-    const TR *x = reinterpret_cast<const TR *>(p.x) + n * p.D;
+    const int per_cta = blockDim.x / lanes, t = threadIdx.x % lanes;
     const int act = p.flags & 0xF;
     const float offset = (p.flags & GDN_NORM_UNIT_OFFSET) ? 1.f : 0.f;
-    float u[ITEMS][VEC], g[ITEMS][VEC], a[ITEMS][VEC];
+    const float inv_d = 1.f / (float)p.D;
+    // the next row, on its way while this one is worked on
+    Raw<T, VEC> ny[ITEMS], nz[ITEMS];
+    Raw<TR, VEC> nx[ITEMS];
+    auto fetch = [&](int64_t n) {
+        const T *y = reinterpret_cast<const T *>(p.y) + n * p.ys;
+        const T *z = reinterpret_cast<const T *>(p.z) + n * p.zs;
+        const TR *x = reinterpret_cast<const TR *>(p.x) + n * p.D;
 #pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-        const int i = (k * lanes + t) * VEC;
-        const bool in = live && i < p.D;
+        for (int k = 0; k < ITEMS; ++k) {
+            const int i = (k * lanes + t) * VEC;
+            if (i < p.D) {
+                ny[k].load(y + i);
+                if (act != GDN_GATE_NONE) nz[k].load(z + i);
+                if (p.x != nullptr) nx[k].load(x + i);
+            }
+        }
+    };
+    // (every thread of a CTA takes as many turns: the sums are taken together)
+    const int64_t step = (int64_t)gridDim.x * per_cta, mine = threadIdx.x / lanes;
+    int64_t base = (int64_t)blockIdx.x * per_cta;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) u[k][j] = 0.f, g[k][j] = 0.f, a[k][j] = 0.f;
-        if (in) load_vec<T, VEC>(y + i, u[k]);
-        if (in && act != GDN_GATE_NONE) load_vec<T, VEC>(z + i, g[k]);
-        if (in && p.x != nullptr) load_vec<TR, VEC>(x + i, a[k]);
-    }
-    float rs = 1.f;
-    if (p.w_post != nullptr) {
-        float ss = 0.f;
+    for (int k = 0; k < ITEMS; ++k) ny[k].clear(), nz[k].clear(), nx[k].clear();
+    if (base + mine < p.N) fetch(base + mine);
+    for (; base < p.N; base += step) {
+        const int64_t n = base + mine;
+        const bool live = n < p.N;
+        float u[ITEMS][VEC], a[ITEMS][VEC], ss = 0.f;
+        // (columns past the row and rows past the last hold zeros or old values)
 #pragma unroll
-        for (int k = 0; k < ITEMS; ++k)
+        for (int k = 0; k < ITEMS; ++k) {
+            ny[k].get(u[k]);
+            nx[k].get(a[k]);
+            if (p.w_post != nullptr)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) ss = fmaf(u[k][j], u[k][j], ss);
-        rs = 1.f / sqrtf(row_sum(ss, lanes, red[0]) / (float)p.D + p.eps);
-    }
-    float ss = 0.f;
+                for (int j = 0; j < VEC; ++j) ss = fmaf(u[k][j], u[k][j], ss);
+            if (act != GDN_GATE_NONE) {
+                float g[VEC];
+                nz[k].get(g);
+                activate<T, VEC>(g, act);
 #pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-        const int i = (k * lanes + t) * VEC;
-        if (live && i < p.D) {
-            if (p.w_post != nullptr) {
+                for (int j = 0; j < VEC; ++j) u[k][j] *= g[j];
+            }
+        }
+        if (n + step < p.N) fetch(n + step);
+        float rs = p.scale;
+        if (p.w_post != nullptr) rs *= rsqrtf(fmaf(row_sum(ss, lanes, red[0]), inv_d, p.eps));
+        ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const int i = (k * lanes + t) * VEC;
+            if (live && i < p.D) {
+                if (p.w_post != nullptr) {
+                    float w[VEC];
+                    load_weight<VEC>(p.w_post, i, p.dt_w, offset, w);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) u[k][j] *= w[j];
+                }
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    a[k][j] = fmaf(rs, u[k][j], a[k][j]);
+                    ss = fmaf(a[k][j], a[k][j], ss);
+                }
+                if (p.x_out != nullptr) store_vec<TR, VEC>(reinterpret_cast<TR *>(p.x_out) + n * p.D + i, a[k]);
+            }
+        }
+        if (p.out == nullptr) {
+            if (lanes > 32) __syncthreads();  // the next turn writes red[0] again
+            continue;
+        }
+        rs = rsqrtf(fmaf(row_sum(ss, lanes, red[1]), inv_d, p.eps));
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const int i = (k * lanes + t) * VEC;
+            if (live && i < p.D) {
                 float w[VEC];
-                load_weight<VEC>(p.w_post, i, p.dt_w, offset, w);
+                load_weight<VEC>(p.w_pre, i, p.dt_w, offset, w);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) u[k][j] *= rs * w[j];
+                for (int j = 0; j < VEC; ++j) a[k][j] *= rs * w[j];
+                store_vec<T, VEC>(reinterpret_cast<T *>(p.out) + n * p.D + i, a[k]);
             }
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                if (act != GDN_GATE_NONE) u[k][j] *= activation<T>(g[k][j], act);
-                a[k][j] = fmaf(p.scale, u[k][j], a[k][j]);
-                ss = fmaf(a[k][j], a[k][j], ss);
-            }
-            if (p.x_out != nullptr) store_vec<TR, VEC>(reinterpret_cast<TR *>(p.x_out) + n * p.D + i, a[k]);
         }
-    }
-    if (p.out == nullptr) return;
-    rs = 1.f / sqrtf(row_sum(ss, lanes, red[1]) / (float)p.D + p.eps);
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-        const int i = (k * lanes + t) * VEC;
-        if (live && i < p.D) {
-            float w[VEC];
-            load_weight<VEC>(p.w_pre, i, p.dt_w, offset, w);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) a[k][j] *= rs * w[j];
-            store_vec<T, VEC>(reinterpret_cast<T *>(p.out) + n * p.D + i, a[k]);
-        }
+        // without the first sum no barrier stands between this one and the next turn's
+        if (p.w_post == nullptr && lanes > 32) __syncthreads();
     }
 }
 
@@ -252,20 +366,36 @@ cudaError_t with_items(int items, F f) {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// CTAs of `threads` threads that run at once, asked once for each kernel and size.
+template <auto Kern>
+unsigned resident(int threads) {
+    static std::atomic<int> cache[33];
+    int c = cache[threads / 32].load(std::memory_order_relaxed);
+    if (c == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&c, Kern, threads, 0) != cudaSuccess || c < 1) c = 1;
+        cache[threads / 32].store(c, std::memory_order_relaxed);
+    }
+    return (unsigned)(c * sm_count_of_current_device());
+}
+template <auto Kern, typename P>
+cudaError_t launch_rows(const P &p, const Spread &s, int64_t rows, cudaStream_t stream) {
+    const int64_t per = s.threads / s.lanes, ctas = (rows + per - 1) / per;
+    const unsigned most = resident<Kern>(s.threads);
+    Kern<<<ctas < most ? (unsigned)ctas : most, s.threads, 0, stream>>>(p, s.lanes);
+    return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t launch_gated_t(const GatedNormParams &p, cudaStream_t stream) {
     constexpr int V = 16 / (int)sizeof(T);
     // 16-byte vectors where every row of x, z and out starts on 16 bytes
     const bool vec = p.d % V == 0 && p.xs % V == 0 && p.os % V == 0 && (p.z == nullptr || p.zs % V == 0) &&
-                     aligned16(p.x) && aligned16(p.z) && aligned16(p.out);
+                     aligned16(p.x) && aligned16(p.z) && aligned16(p.out) && aligned16(p.w);
     const Spread s = spread(p.d, vec ? V : 1);
-    const int64_t rows = p.N * p.H, per = s.threads / s.lanes;
-    const unsigned grid = (unsigned)((rows + per - 1) / per);
     return with_items(s.items, [&](auto items) {
         constexpr int I = decltype(items)::value;
-        if (vec) gated_norm_kernel<T, V, (I > 8 ? 8 : I)><<<grid, s.threads, 0, stream>>>(p, s.lanes);
-        else gated_norm_kernel<T, 1, I><<<grid, s.threads, 0, stream>>>(p, s.lanes);
-        return cudaGetLastError();
+        return vec ? launch_rows<gated_norm_kernel<T, V, (I > 32 / V ? 32 / V : I)>>(p, s, p.N * p.H, stream)
+                   : launch_rows<gated_norm_kernel<T, 1, I>>(p, s, p.N * p.H, stream);
     });
 }
 
@@ -273,15 +403,13 @@ template <typename T, typename TR>
 cudaError_t launch_residual_t(const ResidualNormParams &p, cudaStream_t stream) {
     constexpr int V = 16 / (int)sizeof(T);
     const bool vec = p.D % V == 0 && p.ys % V == 0 && (p.z == nullptr || p.zs % V == 0) && aligned16(p.y) &&
-                     aligned16(p.z) && aligned16(p.x) && aligned16(p.x_out) && aligned16(p.out);
+                     aligned16(p.z) && aligned16(p.x) && aligned16(p.x_out) && aligned16(p.out) &&
+                     aligned16(p.w_post) && aligned16(p.w_pre);
     const Spread s = spread(p.D, vec ? V : 1);
-    const int64_t per = s.threads / s.lanes;
-    const unsigned grid = (unsigned)((p.N + per - 1) / per);
     return with_items(s.items, [&](auto items) {
         constexpr int I = decltype(items)::value;
-        if (vec) residual_norm_kernel<T, TR, V, (I > 8 ? 8 : I)><<<grid, s.threads, 0, stream>>>(p, s.lanes);
-        else residual_norm_kernel<T, TR, 1, I><<<grid, s.threads, 0, stream>>>(p, s.lanes);
-        return cudaGetLastError();
+        return vec ? launch_rows<residual_norm_kernel<T, TR, V, (I > 32 / V ? 32 / V : I)>>(p, s, p.N, stream)
+                   : launch_rows<residual_norm_kernel<T, TR, 1, I>>(p, s, p.N, stream);
     });
 }
 
