@@ -150,6 +150,45 @@ __device__ __forceinline__ float row_sum(float x, int lanes, float *red) {
     return s;
 }
 
+// Rows on their way.  With vectors, each thread copies its own 16-byte pieces of
+// its next rows to shared memory, `depth` rows deep (cp.async: no other thread
+// reads them, so no barrier stands between copy and use); without, the next row
+// waits in registers.  NP: pieces of a row a thread.
+template <int NP>
+struct Ring {
+    uint4 *mine;
+    __device__ __forceinline__ Ring(uint4 *base) : mine(base + threadIdx.x) {}
+    __device__ __forceinline__ uint4 *at(int slot, int piece) const { return mine + (slot * NP + piece) * blockDim.x; }
+    __device__ __forceinline__ void copy(int slot, int piece, const void *src) const {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         static_cast<uint32_t>(__cvta_generic_to_shared(at(slot, piece)))),
+                     "l"(src)
+                     : "memory");
+    }
+    __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // all but the last `depth` - 1 rows copied
+    __device__ __forceinline__ static void wait(int depth) {
+        if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+        else if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+        else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    template <typename R>
+    __device__ __forceinline__ void get(int slot, int piece, R &raw) const {
+#pragma unroll
+        for (int k = 0; k < R::kPacks; ++k) *reinterpret_cast<uint4 *>(&raw.v[k]) = *at(slot, piece + k);
+    }
+    __device__ __forceinline__ void clear(int depth) const {
+        for (int s = 0; s < depth; ++s)
+            for (int k = 0; k < NP; ++k) *at(s, k) = make_uint4(0u, 0u, 0u, 0u);
+    }
+};
+constexpr int kRingBytes = 98304;  // most of a CTA's ring: two CTAs an SM
+__host__ __device__ constexpr int ring_depth(int np, int threads) {
+    const int d = kRingBytes / (np * threads * 16);
+    return d > 4 ? 4 : d < 1 ? 1 : d;
+}
+
 constexpr int kThreads = 256;
 // Largest CTA that spread() asks for: only scalar rows beyond 8192 elements take more than 512 threads.
 template <int VEC>
@@ -172,8 +211,12 @@ __global__ void __launch_bounds__(kMaxThreads<VEC>) gated_norm_kernel(const Gate
         const int i = (k * lanes + t) * VEC;
         if (i < p.d) load_weight<VEC>(p.w, i, p.dt_w, offset, w[k]);
     }
-    Raw<T, VEC> nx[ITEMS], nz[ITEMS];  // the next row, on its way while this one is worked on
-    auto fetch = [&](unsigned r) {
+    constexpr int NP = 2 * ITEMS;
+    extern __shared__ uint4 ring_smem[];
+    const Ring<NP> ring(ring_smem);
+    const int depth = VEC > 1 ? ring_depth(NP, blockDim.x) : 1;
+    Raw<T, VEC> nx[ITEMS], nz[ITEMS];
+    auto fetch = [&](unsigned r, int slot) {
         const unsigned n = r / H, h = r - n * H;
         const T *x = reinterpret_cast<const T *>(p.x) + (int64_t)n * p.xs + (int64_t)h * p.d;
         const T *z = reinterpret_cast<const T *>(p.z) + (int64_t)n * p.zs + (int64_t)h * p.d;
@@ -181,8 +224,13 @@ __global__ void __launch_bounds__(kMaxThreads<VEC>) gated_norm_kernel(const Gate
         for (int k = 0; k < ITEMS; ++k) {
             const int i = (k * lanes + t) * VEC;
             if (i < p.d) {
-                nx[k].load(x + i);
-                if (act != GDN_GATE_NONE) nz[k].load(z + i);
+                if constexpr (VEC > 1) {
+                    ring.copy(slot, 2 * k, x + i);
+                    if (act != GDN_GATE_NONE) ring.copy(slot, 2 * k + 1, z + i);
+                } else {
+                    nx[k].load(x + i);
+                    if (act != GDN_GATE_NONE) nz[k].load(z + i);
+                }
             }
         }
     };
@@ -190,11 +238,31 @@ __global__ void __launch_bounds__(kMaxThreads<VEC>) gated_norm_kernel(const Gate
     const unsigned r0 = blockIdx.x * per_cta, step = gridDim.x * per_cta, mine = threadIdx.x / lanes;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) nx[k].clear(), nz[k].clear();
-    if (r0 + mine < rows) fetch(r0 + mine);
-    int turn = 0;
+    if constexpr (VEC > 1) {
+        ring.clear(depth);
+        for (int k = 0; k < depth - 1; ++k) {
+            if (r0 + mine + k * step < rows) fetch(r0 + mine + k * step, k);
+            ring.commit();
+        }
+    } else if (r0 + mine < rows) {
+        fetch(r0 + mine, 0);
+    }
+    int turn = 0, slot = 0;
     for (unsigned base = r0; base < rows; base += step, ++turn) {
         const unsigned r = base + mine;
         const bool live = r < rows;
+        if constexpr (VEC > 1) {
+            const unsigned ahead = (depth - 1) * step;
+            if (r + ahead < rows) fetch(r + ahead, slot == 0 ? depth - 1 : slot - 1);
+            ring.commit();
+            ring.wait(depth);
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) {
+                ring.get(slot, 2 * k, nx[k]);
+                if (act != GDN_GATE_NONE) ring.get(slot, 2 * k + 1, nz[k]);
+            }
+            slot = slot + 1 == depth ? 0 : slot + 1;
+        }
         float a[ITEMS][VEC], g[ITEMS][VEC];
         float ss = 0.f;
         // (columns past the row and rows past the last hold zeros or old values)
@@ -211,7 +279,8 @@ __global__ void __launch_bounds__(kMaxThreads<VEC>) gated_norm_kernel(const Gate
 #pragma unroll
             for (int j = 0; j < VEC; ++j) ss = fmaf(a[k][j], a[k][j], ss);
         }
-        if (r + step < rows) fetch(r + step);
+        if constexpr (VEC == 1)
+            if (r + step < rows) fetch(r + step, 0);
         ss = row_sum(ss, lanes, red[turn & 1]);
         const float rs = rsqrtf(fmaf(ss, inv_d, p.eps));
         if (live) {
@@ -240,10 +309,13 @@ __global__ void __launch_bounds__(kMaxThreads<VEC>) residual_norm_kernel(const R
     const int act = p.flags & 0xF;
     const float offset = (p.flags & GDN_NORM_UNIT_OFFSET) ? 1.f : 0.f;
     const float inv_d = 1.f / (float)p.D;
-    // the next row, on its way while this one is worked on
+    constexpr int XP = Raw<TR, VEC>::kPacks, NP = (2 + XP) * ITEMS;
+    extern __shared__ uint4 ring_smem[];
+    const Ring<NP> ring(ring_smem);
+    const int depth = VEC > 1 ? ring_depth(NP, blockDim.x) : 1;
     Raw<T, VEC> ny[ITEMS], nz[ITEMS];
     Raw<TR, VEC> nx[ITEMS];
-    auto fetch = [&](int64_t n) {
+    auto fetch = [&](int64_t n, int slot) {
         const T *y = reinterpret_cast<const T *>(p.y) + n * p.ys;
         const T *z = reinterpret_cast<const T *>(p.z) + n * p.zs;
         const TR *x = reinterpret_cast<const TR *>(p.x) + n * p.D;
@@ -251,9 +323,17 @@ __global__ void __launch_bounds__(kMaxThreads<VEC>) residual_norm_kernel(const R
         for (int k = 0; k < ITEMS; ++k) {
             const int i = (k * lanes + t) * VEC;
             if (i < p.D) {
-                ny[k].load(y + i);
-                if (act != GDN_GATE_NONE) nz[k].load(z + i);
-                if (p.x != nullptr) nx[k].load(x + i);
+                if constexpr (VEC > 1) {
+                    ring.copy(slot, (2 + XP) * k, y + i);
+                    if (act != GDN_GATE_NONE) ring.copy(slot, (2 + XP) * k + 1, z + i);
+                    if (p.x != nullptr)
+#pragma unroll
+                        for (int e = 0; e < XP; ++e) ring.copy(slot, (2 + XP) * k + 2 + e, x + i + e * (VEC / XP));
+                } else {
+                    ny[k].load(y + i);
+                    if (act != GDN_GATE_NONE) nz[k].load(z + i);
+                    if (p.x != nullptr) nx[k].load(x + i);
+                }
             }
         }
     };
@@ -262,10 +342,32 @@ __global__ void __launch_bounds__(kMaxThreads<VEC>) residual_norm_kernel(const R
     int64_t base = (int64_t)blockIdx.x * per_cta;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) ny[k].clear(), nz[k].clear(), nx[k].clear();
-    if (base + mine < p.N) fetch(base + mine);
+    if constexpr (VEC > 1) {
+        ring.clear(depth);
+        for (int k = 0; k < depth - 1; ++k) {
+            if (base + mine + k * step < p.N) fetch(base + mine + k * step, k);
+            ring.commit();
+        }
+    } else if (base + mine < p.N) {
+        fetch(base + mine, 0);
+    }
+    int slot = 0;
     for (; base < p.N; base += step) {
         const int64_t n = base + mine;
         const bool live = n < p.N;
+        if constexpr (VEC > 1) {
+            const int64_t ahead = (depth - 1) * step;
+            if (n + ahead < p.N) fetch(n + ahead, slot == 0 ? depth - 1 : slot - 1);
+            ring.commit();
+            ring.wait(depth);
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) {
+                ring.get(slot, (2 + XP) * k, ny[k]);
+                if (act != GDN_GATE_NONE) ring.get(slot, (2 + XP) * k + 1, nz[k]);
+                if (p.x != nullptr) ring.get(slot, (2 + XP) * k + 2, nx[k]);
+            }
+            slot = slot + 1 == depth ? 0 : slot + 1;
+        }
         float u[ITEMS][VEC], a[ITEMS][VEC], ss = 0.f;
         // (columns past the row and rows past the last hold zeros or old values)
 #pragma unroll
@@ -283,7 +385,8 @@ __global__ void __launch_bounds__(kMaxThreads<VEC>) residual_norm_kernel(const R
                 for (int j = 0; j < VEC; ++j) u[k][j] *= g[j];
             }
         }
-        if (n + step < p.N) fetch(n + step);
+        if constexpr (VEC == 1)
+            if (n + step < p.N) fetch(n + step, 0);
         float rs = p.scale;
         if (p.w_post != nullptr) rs *= rsqrtf(fmaf(row_sum(ss, lanes, red[0]), inv_d, p.eps));
         ss = 0.f;
@@ -342,7 +445,7 @@ Spread spread(int width, int vec) {
         while (lanes * items < nv) items *= 2;
         return {lanes, kThreads, items};
     }
-    int items = 2;
+    int items = 1;
     while ((nv + items - 1) / items > 512 && items < 16) items *= 2;
     const int threads = ((nv + items - 1) / items + 31) / 32 * 32;
     // one warp is a group of its own; more are a CTA
@@ -366,22 +469,26 @@ cudaError_t with_items(int items, F f) {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// CTAs of `threads` threads that run at once, asked once for each kernel and size.
-template <auto Kern>
-unsigned resident(int threads) {
+// CTAs of `threads` threads that run at once, asked once for each kernel and size
+// (0: the question failed).  NP: the pieces of its ring, 0 without one.
+template <auto Kern, int NP>
+unsigned resident(int threads, int bytes) {
     static std::atomic<int> cache[33];
     int c = cache[threads / 32].load(std::memory_order_relaxed);
     if (c == 0) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&c, Kern, threads, 0) != cudaSuccess || c < 1) c = 1;
+        if (NP > 0 && set_smem_once<Kern>(2 * kRingBytes) != cudaSuccess) return 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&c, Kern, threads, bytes) != cudaSuccess || c < 1) return 0;
         cache[threads / 32].store(c, std::memory_order_relaxed);
     }
     return (unsigned)(c * sm_count_of_current_device());
 }
-template <auto Kern, typename P>
+template <auto Kern, int NP, typename P>
 cudaError_t launch_rows(const P &p, const Spread &s, int64_t rows, cudaStream_t stream) {
     const int64_t per = s.threads / s.lanes, ctas = (rows + per - 1) / per;
-    const unsigned most = resident<Kern>(s.threads);
-    Kern<<<ctas < most ? (unsigned)ctas : most, s.threads, 0, stream>>>(p, s.lanes);
+    const int bytes = NP > 0 ? ring_depth(NP, s.threads) * NP * s.threads * 16 : 0;
+    const unsigned most = resident<Kern, NP>(s.threads, bytes);
+    if (most == 0) return cudaErrorInvalidConfiguration;
+    Kern<<<ctas < most ? (unsigned)ctas : most, s.threads, bytes, stream>>>(p, s.lanes);
     return cudaGetLastError();
 }
 
@@ -394,8 +501,9 @@ cudaError_t launch_gated_t(const GatedNormParams &p, cudaStream_t stream) {
     const Spread s = spread(p.d, vec ? V : 1);
     return with_items(s.items, [&](auto items) {
         constexpr int I = decltype(items)::value;
-        return vec ? launch_rows<gated_norm_kernel<T, V, (I > 32 / V ? 32 / V : I)>>(p, s, p.N * p.H, stream)
-                   : launch_rows<gated_norm_kernel<T, 1, I>>(p, s, p.N * p.H, stream);
+        constexpr int IV = I > 32 / V ? 32 / V : I;  // (a row has 32 elements a thread at most)
+        return vec ? launch_rows<gated_norm_kernel<T, V, IV>, 2 * IV>(p, s, p.N * p.H, stream)
+                   : launch_rows<gated_norm_kernel<T, 1, I>, 0>(p, s, p.N * p.H, stream);
     });
 }
 
@@ -408,8 +516,10 @@ cudaError_t launch_residual_t(const ResidualNormParams &p, cudaStream_t stream) 
     const Spread s = spread(p.D, vec ? V : 1);
     return with_items(s.items, [&](auto items) {
         constexpr int I = decltype(items)::value;
-        return vec ? launch_rows<residual_norm_kernel<T, TR, V, (I > 32 / V ? 32 / V : I)>>(p, s, p.N, stream)
-                   : launch_rows<residual_norm_kernel<T, TR, 1, I>>(p, s, p.N, stream);
+        constexpr int IV = I > 32 / V ? 32 / V : I;  // (a row has 32 elements a thread at most)
+        constexpr int NP = (2 + (sizeof(TR) > sizeof(T) ? 2 : 1)) * IV;
+        return vec ? launch_rows<residual_norm_kernel<T, TR, V, IV>, NP>(p, s, p.N, stream)
+                   : launch_rows<residual_norm_kernel<T, TR, 1, I>, 0>(p, s, p.N, stream);
     });
 }
 
