@@ -136,68 +136,62 @@ __device__ __forceinline__ void activate(float (&z)[VEC], int act) {
 }
 
 // Sum over the row's group of threads: `lanes` (a power of two) threads of a
-// warp, or, with lanes > 32, all threads of the CTA.  red: a float for each
-// warp, another buffer in every second call.
+// warp, or, with lanes > 32, all THREADS of the CTA.  red: a float for each warp,
+// another buffer in every second call.
+template <int THREADS>
 __device__ __forceinline__ float row_sum(float x, int lanes, float *red) {
     for (int o = (lanes < 32 ? lanes : 32) / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     if (lanes <= 32) return x;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    if (lane == 0) red[warp] = x;
+    constexpr int W = THREADS / 32;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
     __syncthreads();
-    float s = lane < nw ? red[lane] : 0.f;
+    float s = red[threadIdx.x & (W - 1)];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int o = W / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
 }
 
 // Rows on their way.  With vectors, each thread copies its own 16-byte pieces of
-// its next rows to shared memory, `depth` rows deep (cp.async: no other thread
+// its next rows to shared memory, DEPTH rows deep (cp.async: no other thread
 // reads them, so no barrier stands between copy and use); without, the next row
 // waits in registers.  NP: pieces of a row a thread.
-template <int NP>
+template <int NP, int THREADS>
 struct Ring {
-    uint4 *mine;
-    __device__ __forceinline__ Ring(uint4 *base) : mine(base + threadIdx.x) {}
-    __device__ __forceinline__ uint4 *at(int slot, int piece) const { return mine + (slot * NP + piece) * blockDim.x; }
+    static constexpr int kRow = NP * THREADS * 16;
+    // (most of a CTA's ring: two CTAs an SM)
+    static constexpr int DEPTH = 98304 / kRow > 4 ? 4 : 98304 / kRow < 1 ? 1 : 98304 / kRow;
+    static constexpr int kBytes = DEPTH * kRow;
+    uint32_t mine;
+    __device__ __forceinline__ Ring(const uint4 *base)
+        : mine(static_cast<uint32_t>(__cvta_generic_to_shared(base + threadIdx.x))) {}
     __device__ __forceinline__ void copy(int slot, int piece, const void *src) const {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                         static_cast<uint32_t>(__cvta_generic_to_shared(at(slot, piece)))),
-                     "l"(src)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(mine + slot * kRow + piece * THREADS * 16), "l"(src)
                      : "memory");
     }
     __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-    // all but the last `depth` - 1 rows copied
-    __device__ __forceinline__ static void wait(int depth) {
-        if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
-        else if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
-        else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else asm volatile("cp.async.wait_group 0;" ::: "memory");
-    }
+    // all but the last DEPTH - 1 rows copied
+    __device__ __forceinline__ static void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory"); }
     template <typename R>
     __device__ __forceinline__ void get(int slot, int piece, R &raw) const {
 #pragma unroll
-        for (int k = 0; k < R::kPacks; ++k) *reinterpret_cast<uint4 *>(&raw.v[k]) = *at(slot, piece + k);
+        for (int k = 0; k < R::kPacks; ++k) {
+            uint4 &u = *reinterpret_cast<uint4 *>(&raw.v[k]);
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                         : "r"(mine + slot * kRow + (piece + k) * THREADS * 16)
+                         : "memory");
+        }
     }
-    __device__ __forceinline__ void clear(int depth) const {
-        for (int s = 0; s < depth; ++s)
-            for (int k = 0; k < NP; ++k) *at(s, k) = make_uint4(0u, 0u, 0u, 0u);
-    }
+    __device__ __forceinline__ static int next(int slot) { return slot + 1 == DEPTH ? 0 : slot + 1; }
 };
-constexpr int kRingBytes = 98304;  // most of a CTA's ring: two CTAs an SM
-__host__ __device__ constexpr int ring_depth(int np, int threads) {
-    const int d = kRingBytes / (np * threads * 16);
-    return d > 4 ? 4 : d < 1 ? 1 : d;
-}
 
-constexpr int kThreads = 256;
-// Largest CTA that spread() asks for: only scalar rows beyond 8192 elements take more than 512 threads.
-template <int VEC>
-constexpr int kMaxThreads = VEC > 1 ? 512 : 1024;
-
-template <typename T, int VEC, int ITEMS>
-__global__ void __launch_bounds__(kMaxThreads<VEC>) gated_norm_kernel(const GatedNormParams p, int lanes) {
+template <typename T, int VEC, int ITEMS, int THREADS>
+__global__ void __launch_bounds__(THREADS, VEC * ITEMS <= 8 ? 1024 / THREADS : 1) gated_norm_kernel(const GatedNormParams p, int lanes) {
     __shared__ float red[2][32];
-    const int per_cta = blockDim.x / lanes;
+    extern __shared__ uint4 ring_smem[];
+    using R = Ring<2 * ITEMS, THREADS>;
+    const R ring(ring_smem);
+    const int per_cta = THREADS / lanes;
     const unsigned rows = (unsigned)(p.N * p.H), H = (unsigned)p.H;
     const int t = threadIdx.x % lanes;
     const int act = p.gate & 0xF;
@@ -206,66 +200,63 @@ __global__ void __launch_bounds__(kMaxThreads<VEC>) gated_norm_kernel(const Gate
     const float inv_d = 1.f / (float)p.d;
     // the thread's columns, and so its weights, are the same in every row
     float w[ITEMS][VEC];
+    Raw<T, VEC> nx[ITEMS], nz[ITEMS];
+    bool in[ITEMS];
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
         const int i = (k * lanes + t) * VEC;
-        if (i < p.d) load_weight<VEC>(p.w, i, p.dt_w, offset, w[k]);
+        in[k] = i < p.d;
+        nx[k].clear();
+        nz[k].clear();
+        if (in[k]) load_weight<VEC>(p.w, i, p.dt_w, offset, w[k]);
     }
-    constexpr int NP = 2 * ITEMS;
-    extern __shared__ uint4 ring_smem[];
-    const Ring<NP> ring(ring_smem);
-    const int depth = VEC > 1 ? ring_depth(NP, blockDim.x) : 1;
-    Raw<T, VEC> nx[ITEMS], nz[ITEMS];
     auto fetch = [&](unsigned r, int slot) {
         const unsigned n = r / H, h = r - n * H;
-        const T *x = reinterpret_cast<const T *>(p.x) + (int64_t)n * p.xs + (int64_t)h * p.d;
-        const T *z = reinterpret_cast<const T *>(p.z) + (int64_t)n * p.zs + (int64_t)h * p.d;
+        const T *x = reinterpret_cast<const T *>(p.x) + (int64_t)n * p.xs + h * p.d + t * VEC;
+        const T *z = reinterpret_cast<const T *>(p.z) + (int64_t)n * p.zs + h * p.d + t * VEC;
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            const int i = (k * lanes + t) * VEC;
-            if (i < p.d) {
+            if (in[k]) {
                 if constexpr (VEC > 1) {
-                    ring.copy(slot, 2 * k, x + i);
-                    if (act != GDN_GATE_NONE) ring.copy(slot, 2 * k + 1, z + i);
+                    ring.copy(slot, 2 * k, x + k * lanes * VEC);
+                    if (act != GDN_GATE_NONE) ring.copy(slot, 2 * k + 1, z + k * lanes * VEC);
                 } else {
-                    nx[k].load(x + i);
-                    if (act != GDN_GATE_NONE) nz[k].load(z + i);
+                    nx[k].load(x + k * lanes);
+                    if (act != GDN_GATE_NONE) nz[k].load(z + k * lanes);
                 }
             }
         }
     };
     // (every thread of a CTA takes as many turns: the sums are taken together)
-    const unsigned r0 = blockIdx.x * per_cta, step = gridDim.x * per_cta, mine = threadIdx.x / lanes;
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k) nx[k].clear(), nz[k].clear();
+    const unsigned step = gridDim.x * per_cta, mine = threadIdx.x / lanes;
+    unsigned base = blockIdx.x * per_cta;
+    int parity = 0, slot = 0;
     if constexpr (VEC > 1) {
-        ring.clear(depth);
-        for (int k = 0; k < depth - 1; ++k) {
-            if (r0 + mine + k * step < rows) fetch(r0 + mine + k * step, k);
+        for (int k = 0; k < R::DEPTH - 1; ++k) {
+            if (base + mine + k * step < rows) fetch(base + mine + k * step, k);
             ring.commit();
         }
-    } else if (r0 + mine < rows) {
-        fetch(r0 + mine, 0);
+    } else if (base + mine < rows) {
+        fetch(base + mine, 0);
     }
-    int turn = 0, slot = 0;
-    for (unsigned base = r0; base < rows; base += step, ++turn) {
+    for (; base < rows; base += step, parity ^= 1) {
         const unsigned r = base + mine;
-        const bool live = r < rows;
         if constexpr (VEC > 1) {
-            const unsigned ahead = (depth - 1) * step;
-            if (r + ahead < rows) fetch(r + ahead, slot == 0 ? depth - 1 : slot - 1);
+            const unsigned ahead = r + (R::DEPTH - 1) * step;
+            if (ahead < rows) fetch(ahead, slot == 0 ? R::DEPTH - 1 : slot - 1);
             ring.commit();
-            ring.wait(depth);
+            ring.wait();
 #pragma unroll
-            for (int k = 0; k < ITEMS; ++k) {
-                ring.get(slot, 2 * k, nx[k]);
-                if (act != GDN_GATE_NONE) ring.get(slot, 2 * k + 1, nz[k]);
-            }
-            slot = slot + 1 == depth ? 0 : slot + 1;
+            for (int k = 0; k < ITEMS; ++k)
+                if (in[k]) {
+                    ring.get(slot, 2 * k, nx[k]);
+                    if (act != GDN_GATE_NONE) ring.get(slot, 2 * k + 1, nz[k]);
+                }
+            slot = R::next(slot);
         }
         float a[ITEMS][VEC], g[ITEMS][VEC];
         float ss = 0.f;
-        // (columns past the row and rows past the last hold zeros or old values)
+        // (columns past the row are zeros; rows past the last are not stored)
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
             nx[k].get(a[k]);
@@ -281,54 +272,84 @@ __global__ void __launch_bounds__(kMaxThreads<VEC>) gated_norm_kernel(const Gate
         }
         if constexpr (VEC == 1)
             if (r + step < rows) fetch(r + step, 0);
-        ss = row_sum(ss, lanes, red[turn & 1]);
+        ss = row_sum<THREADS>(ss, lanes, red[parity]);
         const float rs = rsqrtf(fmaf(ss, inv_d, p.eps));
-        if (live) {
+        if (r < rows) {
             const unsigned n = r / H, h = r - n * H;
-            T *y = reinterpret_cast<T *>(p.out) + (int64_t)n * p.os + (int64_t)h * p.d;
+            T *y = reinterpret_cast<T *>(p.out) + (int64_t)n * p.os + h * p.d + t * VEC;
 #pragma unroll
             for (int k = 0; k < ITEMS; ++k) {
-                const int i = (k * lanes + t) * VEC;
-                if (i < p.d) {
+                if (in[k]) {
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) a[k][j] *= rs * w[k][j];
                     if (act != GDN_GATE_NONE && !first)
 #pragma unroll
                         for (int j = 0; j < VEC; ++j) a[k][j] *= g[k][j];
-                    store_vec<T, VEC>(y + i, a[k]);
+                    store_vec<T, VEC>(y + k * lanes * VEC, a[k]);
                 }
             }
         }
     }
 }
 
-template <typename T, typename TR, int VEC, int ITEMS>
-__global__ void __launch_bounds__(kMaxThreads<VEC>) residual_norm_kernel(const ResidualNormParams p, int lanes) {
+// A weight's vector for the thread's columns: kept in registers where they are few
+// enough, else read again (from L1) for every row.
+template <int VEC, int ITEMS>
+struct Weights {
+    static constexpr bool kKept = VEC * ITEMS <= 8;
+    float w[kKept ? ITEMS : 1][VEC];
+    __device__ __forceinline__ void keep(const void *p, int i, int dt, float offset, int k) {
+        if constexpr (kKept) load_weight<VEC>(p, i, dt, offset, w[k]);
+    }
+    __device__ __forceinline__ const float (&at(const void *p, int i, int dt, float offset, int k))[VEC] {
+        if constexpr (kKept) return w[k];
+        load_weight<VEC>(p, i, dt, offset, w[0]);
+        return w[0];
+    }
+};
+
+template <typename T, typename TR, int VEC, int ITEMS, int THREADS>
+__global__ void __launch_bounds__(THREADS, VEC * ITEMS <= 8 ? 1024 / THREADS : 1) residual_norm_kernel(const ResidualNormParams p, int lanes) {
     __shared__ float red[2][32];
-    const int per_cta = blockDim.x / lanes, t = threadIdx.x % lanes;
+    extern __shared__ uint4 ring_smem[];
+    constexpr int XP = Raw<TR, VEC>::kPacks, NP = 2 + XP;
+    using R = Ring<NP * ITEMS, THREADS>;
+    const R ring(ring_smem);
+    const int per_cta = THREADS / lanes, t = threadIdx.x % lanes;
     const int act = p.flags & 0xF;
     const float offset = (p.flags & GDN_NORM_UNIT_OFFSET) ? 1.f : 0.f;
     const float inv_d = 1.f / (float)p.D;
-    constexpr int XP = Raw<TR, VEC>::kPacks, NP = (2 + XP) * ITEMS;
-    extern __shared__ uint4 ring_smem[];
-    const Ring<NP> ring(ring_smem);
-    const int depth = VEC > 1 ? ring_depth(NP, blockDim.x) : 1;
+    const bool post = p.w_post != nullptr;
     Raw<T, VEC> ny[ITEMS], nz[ITEMS];
     Raw<TR, VEC> nx[ITEMS];
+    Weights<VEC, ITEMS> w_post, w_pre;
+    bool in[ITEMS];
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int i = (k * lanes + t) * VEC;
+        in[k] = i < p.D;
+        ny[k].clear();
+        nz[k].clear();
+        nx[k].clear();
+        if (in[k]) {
+            if (post) w_post.keep(p.w_post, i, p.dt_w, offset, k);
+            w_pre.keep(p.w_pre, i, p.dt_w, offset, k);
+        }
+    }
     auto fetch = [&](int64_t n, int slot) {
-        const T *y = reinterpret_cast<const T *>(p.y) + n * p.ys;
-        const T *z = reinterpret_cast<const T *>(p.z) + n * p.zs;
-        const TR *x = reinterpret_cast<const TR *>(p.x) + n * p.D;
+        const T *y = reinterpret_cast<const T *>(p.y) + n * p.ys + t * VEC;
+        const T *z = reinterpret_cast<const T *>(p.z) + n * p.zs + t * VEC;
+        const TR *x = reinterpret_cast<const TR *>(p.x) + n * p.D + t * VEC;
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            const int i = (k * lanes + t) * VEC;
-            if (i < p.D) {
+            if (in[k]) {
+                const int i = k * lanes * VEC;
                 if constexpr (VEC > 1) {
-                    ring.copy(slot, (2 + XP) * k, y + i);
-                    if (act != GDN_GATE_NONE) ring.copy(slot, (2 + XP) * k + 1, z + i);
+                    ring.copy(slot, NP * k, y + i);
+                    if (act != GDN_GATE_NONE) ring.copy(slot, NP * k + 1, z + i);
                     if (p.x != nullptr)
 #pragma unroll
-                        for (int e = 0; e < XP; ++e) ring.copy(slot, (2 + XP) * k + 2 + e, x + i + e * (VEC / XP));
+                        for (int e = 0; e < XP; ++e) ring.copy(slot, NP * k + 2 + e, x + i + e * (VEC / XP));
                 } else {
                     ny[k].load(y + i);
                     if (act != GDN_GATE_NONE) nz[k].load(z + i);
@@ -338,43 +359,39 @@ __global__ void __launch_bounds__(kMaxThreads<VEC>) residual_norm_kernel(const R
         }
     };
     // (every thread of a CTA takes as many turns: the sums are taken together)
-    const int64_t step = (int64_t)gridDim.x * per_cta, mine = threadIdx.x / lanes;
-    int64_t base = (int64_t)blockIdx.x * per_cta;
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k) ny[k].clear(), nz[k].clear(), nx[k].clear();
+    const int64_t step = (int64_t)gridDim.x * per_cta;
+    int64_t n = (int64_t)blockIdx.x * per_cta + threadIdx.x / lanes, base = (int64_t)blockIdx.x * per_cta;
+    int slot = 0;
     if constexpr (VEC > 1) {
-        ring.clear(depth);
-        for (int k = 0; k < depth - 1; ++k) {
-            if (base + mine + k * step < p.N) fetch(base + mine + k * step, k);
+        for (int k = 0; k < R::DEPTH - 1; ++k) {
+            if (n + k * step < p.N) fetch(n + k * step, k);
             ring.commit();
         }
-    } else if (base + mine < p.N) {
-        fetch(base + mine, 0);
+    } else if (n < p.N) {
+        fetch(n, 0);
     }
-    int slot = 0;
-    for (; base < p.N; base += step) {
-        const int64_t n = base + mine;
-        const bool live = n < p.N;
+    for (; base < p.N; base += step, n += step) {
         if constexpr (VEC > 1) {
-            const int64_t ahead = (depth - 1) * step;
-            if (n + ahead < p.N) fetch(n + ahead, slot == 0 ? depth - 1 : slot - 1);
+            const int64_t ahead = n + (R::DEPTH - 1) * step;
+            if (ahead < p.N) fetch(ahead, slot == 0 ? R::DEPTH - 1 : slot - 1);
             ring.commit();
-            ring.wait(depth);
+            ring.wait();
 #pragma unroll
-            for (int k = 0; k < ITEMS; ++k) {
-                ring.get(slot, (2 + XP) * k, ny[k]);
-                if (act != GDN_GATE_NONE) ring.get(slot, (2 + XP) * k + 1, nz[k]);
-                if (p.x != nullptr) ring.get(slot, (2 + XP) * k + 2, nx[k]);
-            }
-            slot = slot + 1 == depth ? 0 : slot + 1;
+            for (int k = 0; k < ITEMS; ++k)
+                if (in[k]) {
+                    ring.get(slot, NP * k, ny[k]);
+                    if (act != GDN_GATE_NONE) ring.get(slot, NP * k + 1, nz[k]);
+                    if (p.x != nullptr) ring.get(slot, NP * k + 2, nx[k]);
+                }
+            slot = R::next(slot);
         }
         float u[ITEMS][VEC], a[ITEMS][VEC], ss = 0.f;
-        // (columns past the row and rows past the last hold zeros or old values)
+        // (columns past the row are zeros; rows past the last are not stored)
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
             ny[k].get(u[k]);
             nx[k].get(a[k]);
-            if (p.w_post != nullptr)
+            if (post)
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) ss = fmaf(u[k][j], u[k][j], ss);
             if (act != GDN_GATE_NONE) {
@@ -388,15 +405,17 @@ __global__ void __launch_bounds__(kMaxThreads<VEC>) residual_norm_kernel(const R
         if constexpr (VEC == 1)
             if (n + step < p.N) fetch(n + step, 0);
         float rs = p.scale;
-        if (p.w_post != nullptr) rs *= rsqrtf(fmaf(row_sum(ss, lanes, red[0]), inv_d, p.eps));
+        if (post) rs *= rsqrtf(fmaf(row_sum<THREADS>(ss, lanes, red[0]), inv_d, p.eps));
         ss = 0.f;
+        const bool live = n < p.N;
+        TR *x_out = reinterpret_cast<TR *>(p.x_out) + n * p.D + t * VEC;
+        T *out = reinterpret_cast<T *>(p.out) + n * p.D + t * VEC;
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            const int i = (k * lanes + t) * VEC;
-            if (live && i < p.D) {
-                if (p.w_post != nullptr) {
-                    float w[VEC];
-                    load_weight<VEC>(p.w_post, i, p.dt_w, offset, w);
+            const int i = k * lanes * VEC;
+            if (live && in[k]) {
+                if (post) {
+                    const float(&w)[VEC] = w_post.at(p.w_post, i + t * VEC, p.dt_w, offset, k);
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) u[k][j] *= w[j];
                 }
@@ -405,34 +424,31 @@ __global__ void __launch_bounds__(kMaxThreads<VEC>) residual_norm_kernel(const R
                     a[k][j] = fmaf(rs, u[k][j], a[k][j]);
                     ss = fmaf(a[k][j], a[k][j], ss);
                 }
-                if (p.x_out != nullptr) store_vec<TR, VEC>(reinterpret_cast<TR *>(p.x_out) + n * p.D + i, a[k]);
+                if (p.x_out != nullptr) store_vec<TR, VEC>(x_out + i, a[k]);
             }
         }
-        if (p.out == nullptr) {
-            if (lanes > 32) __syncthreads();  // the next turn writes red[0] again
-            continue;
-        }
-        rs = rsqrtf(fmaf(row_sum(ss, lanes, red[1]), inv_d, p.eps));
+        if (p.out != nullptr) {
+            rs = rsqrtf(fmaf(row_sum<THREADS>(ss, lanes, red[1]), inv_d, p.eps));
 #pragma unroll
-        for (int k = 0; k < ITEMS; ++k) {
-            const int i = (k * lanes + t) * VEC;
-            if (live && i < p.D) {
-                float w[VEC];
-                load_weight<VEC>(p.w_pre, i, p.dt_w, offset, w);
+            for (int k = 0; k < ITEMS; ++k) {
+                const int i = k * lanes * VEC;
+                if (live && in[k]) {
+                    const float(&w)[VEC] = w_pre.at(p.w_pre, i + t * VEC, p.dt_w, offset, k);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) a[k][j] *= rs * w[j];
-                store_vec<T, VEC>(reinterpret_cast<T *>(p.out) + n * p.D + i, a[k]);
+                    for (int j = 0; j < VEC; ++j) a[k][j] *= rs * w[j];
+                    store_vec<T, VEC>(out + i, a[k]);
+                }
             }
         }
-        // without the first sum no barrier stands between this one and the next turn's
-        if (p.w_post == nullptr && lanes > 32) __syncthreads();
+        // with only one of the two sums no barrier stands between this one and the
+        // next turn's
+        if (lanes > 32 && (!post || p.out == nullptr)) __syncthreads();
     }
 }
 
-// How a row of `width` elements is spread: `lanes` threads of ITEMS vectors
-// each, `threads` a CTA.  Rows of up to 32 vectors take the smallest power of
-// two of lanes of one vector each, so several rows share a warp; longer rows
-// take a warp of up to four vectors a lane, then a whole CTA.
+// How a row of `width` elements is spread over threads of ITEMS vectors each.
+// Rows of up to 32 vectors take the smallest power of two of lanes of one vector
+// each, so several rows share a warp; up to 128 a warp; longer ones a whole CTA.
 struct Spread {
     int lanes, threads, items;
 };
@@ -443,53 +459,63 @@ Spread spread(int width, int vec) {
         while (lanes < 32 && lanes < nv) lanes *= 2;
         int items = 1;
         while (lanes * items < nv) items *= 2;
-        return {lanes, kThreads, items};
+        return {lanes, 256, items};
     }
+    if (nv <= 256) return {256, 256, 1};
     int items = 1;
-    while ((nv + items - 1) / items > 512 && items < 16) items *= 2;
-    const int threads = ((nv + items - 1) / items + 31) / 32 * 32;
-    // one warp is a group of its own; more are a CTA
+    while (512 * items < nv && items < 16) items *= 2;
+    const int threads = 512 * items < nv ? 1024 : 512;
     return {threads, threads, items};
-}
-
-template <int N>
-struct Int {
-    static constexpr int value = N;
-};
-template <typename F>
-cudaError_t with_items(int items, F f) {
-    switch (items) {
-        case 1: return f(Int<1>{});
-        case 2: return f(Int<2>{});
-        case 4: return f(Int<4>{});
-        case 8: return f(Int<8>{});
-        default: return f(Int<16>{});
-    }
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// CTAs of `threads` threads that run at once, asked once for each kernel and size
-// (0: the question failed).  NP: the pieces of its ring, 0 without one.
-template <auto Kern, int NP>
+// CTAs that run at once, asked once a device; 0 if the question failed.
+template <auto Kern>
 unsigned resident(int threads, int bytes) {
-    static std::atomic<int> cache[33];
-    int c = cache[threads / 32].load(std::memory_order_relaxed);
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int c = cache[dev].load(std::memory_order_relaxed);
     if (c == 0) {
-        if (NP > 0 && set_smem_once<Kern>(2 * kRingBytes) != cudaSuccess) return 0;
+        if (bytes > 0 && set_smem_once<Kern>(bytes) != cudaSuccess) return 0;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&c, Kern, threads, bytes) != cudaSuccess || c < 1) return 0;
-        cache[threads / 32].store(c, std::memory_order_relaxed);
+        c *= sm_count_of_current_device();
+        cache[dev].store(c, std::memory_order_relaxed);
     }
-    return (unsigned)(c * sm_count_of_current_device());
+    return (unsigned)c;
 }
-template <auto Kern, int NP, typename P>
+template <auto Kern, int BYTES, typename P>
 cudaError_t launch_rows(const P &p, const Spread &s, int64_t rows, cudaStream_t stream) {
     const int64_t per = s.threads / s.lanes, ctas = (rows + per - 1) / per;
-    const int bytes = NP > 0 ? ring_depth(NP, s.threads) * NP * s.threads * 16 : 0;
-    const unsigned most = resident<Kern, NP>(s.threads, bytes);
+    const unsigned most = resident<Kern>(s.threads, BYTES);
     if (most == 0) return cudaErrorInvalidConfiguration;
-    Kern<<<ctas < most ? (unsigned)ctas : most, s.threads, bytes, stream>>>(p, s.lanes);
+    Kern<<<ctas < most ? (unsigned)ctas : most, s.threads, BYTES, stream>>>(p, s.lanes);
     return cudaGetLastError();
+}
+
+template <int I, int TH>
+struct Shape {
+    static constexpr int items = I, threads = TH;
+};
+// Calls f with the spread's items and threads as constants.  A row of vectors has
+// at most 32 elements a thread, so never more than `most` vectors.
+template <int MOST, typename F>
+cudaError_t with_shape(const Spread &s, F f) {
+    if (s.threads == 256) {
+        if (s.items == 1) return f(Shape<1, 256>{});
+        if (s.items == 2) return f(Shape<2, 256>{});
+        return f(Shape<4, 256>{});
+    }
+    if constexpr (MOST > 8)
+        if (s.threads == 1024) return f(Shape<16, 1024>{});
+    if (s.items == 1) return f(Shape<1, 512>{});
+    if (s.items == 2) return f(Shape<2, 512>{});
+    if constexpr (MOST > 4)
+        if (s.items == 8) return f(Shape<8, 512>{});
+    if constexpr (MOST > 8)
+        if (s.items == 16) return f(Shape<16, 512>{});
+    return f(Shape<4, 512>{});
 }
 
 template <typename T>
@@ -499,11 +525,15 @@ cudaError_t launch_gated_t(const GatedNormParams &p, cudaStream_t stream) {
     const bool vec = p.d % V == 0 && p.xs % V == 0 && p.os % V == 0 && (p.z == nullptr || p.zs % V == 0) &&
                      aligned16(p.x) && aligned16(p.z) && aligned16(p.out) && aligned16(p.w);
     const Spread s = spread(p.d, vec ? V : 1);
-    return with_items(s.items, [&](auto items) {
-        constexpr int I = decltype(items)::value;
-        constexpr int IV = I > 32 / V ? 32 / V : I;  // (a row has 32 elements a thread at most)
-        return vec ? launch_rows<gated_norm_kernel<T, V, IV>, 2 * IV>(p, s, p.N * p.H, stream)
-                   : launch_rows<gated_norm_kernel<T, 1, I>, 0>(p, s, p.N * p.H, stream);
+    if (vec)
+        return with_shape<32 / V>(s, [&](auto shape) {
+            using S = decltype(shape);
+            return launch_rows<gated_norm_kernel<T, V, S::items, S::threads>, Ring<2 * S::items, S::threads>::kBytes>(
+                p, s, p.N * p.H, stream);
+        });
+    return with_shape<16>(s, [&](auto shape) {
+        using S = decltype(shape);
+        return launch_rows<gated_norm_kernel<T, 1, S::items, S::threads>, 0>(p, s, p.N * p.H, stream);
     });
 }
 
@@ -514,12 +544,16 @@ cudaError_t launch_residual_t(const ResidualNormParams &p, cudaStream_t stream) 
                      aligned16(p.z) && aligned16(p.x) && aligned16(p.x_out) && aligned16(p.out) &&
                      aligned16(p.w_post) && aligned16(p.w_pre);
     const Spread s = spread(p.D, vec ? V : 1);
-    return with_items(s.items, [&](auto items) {
-        constexpr int I = decltype(items)::value;
-        constexpr int IV = I > 32 / V ? 32 / V : I;  // (a row has 32 elements a thread at most)
-        constexpr int NP = (2 + (sizeof(TR) > sizeof(T) ? 2 : 1)) * IV;
-        return vec ? launch_rows<residual_norm_kernel<T, TR, V, IV>, NP>(p, s, p.N, stream)
-                   : launch_rows<residual_norm_kernel<T, TR, 1, I>, 0>(p, s, p.N, stream);
+    if (vec)
+        return with_shape<32 / V>(s, [&](auto shape) {
+            using S = decltype(shape);
+            constexpr int NP = (2 + (sizeof(TR) > sizeof(T) ? 2 : 1)) * S::items;
+            return launch_rows<residual_norm_kernel<T, TR, V, S::items, S::threads>, Ring<NP, S::threads>::kBytes>(
+                p, s, p.N, stream);
+        });
+    return with_shape<16>(s, [&](auto shape) {
+        using S = decltype(shape);
+        return launch_rows<residual_norm_kernel<T, TR, 1, S::items, S::threads>, 0>(p, s, p.N, stream);
     });
 }
 
