@@ -31,42 +31,76 @@ namespace cg = cooperative_groups;
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCluster = 8;
-constexpr int kUnroll = 8;
 
-// A weight in units of 2^-40; not above 1 and 0 for NaN.
-__device__ __forceinline__ long long units(float x) {
-    return x > 0.f ? __float2ll_rz(fminf(x, 1.f) * 1099511627776.f) : 0ll;
+// Weights in whole units of 2^-40, floor(w 2^40) for w clamped to [0, 1] (NaN: 0).
+// A conversion to a 64-bit integer runs at a fraction of the load rate, so the two
+// halves of 20 bits are read off sums with 2^23 that are rounded down: floor(w 2^20)
+// are the low bits of the first, the rest of w goes into the second exactly, and
+// each half is summed in 32 bits over a few weights before it joins the total.
+struct Units {
+    uint32_t hi = 0, lo = 0;
+    __device__ __forceinline__ void add(float w) {
+        w = __saturatef(w);
+        const float a = __fmaf_rz(w, 1048576.f, 8388608.f);
+        const float rest = fmaf(w, 1048576.f, 8388608.f - a);
+        const float b = __fmaf_rz(rest, 1048576.f, 8388608.f);
+        hi += __float_as_uint(a) - 0x4B000000u;
+        lo += __float_as_uint(b) - 0x4B000000u;
+    }
+    __device__ __forceinline__ long long total() const { return ((long long)hi << 20) + lo; }
+};
+__device__ __forceinline__ long long units(float w) {
+    Units u;
+    u.add(w);
+    return u.total();
 }
+
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Pack {
+    T v[VEC];
+};
 
 template <typename T>
 struct Row {
     const T *p, *q;   // q: nullptr if nothing is taken off
     int drop;         // token whose weight is 0 (the rejected one of a certain draft), or -1
-    __device__ __forceinline__ long long at(int j) const {
+    __device__ __forceinline__ float weight(int j) const {
         const float t = ld_f(p + j);
-        const long long w = units(q != nullptr ? t - ld_f(q + j) : t);
-        return j == drop ? 0ll : w;
+        return q != nullptr ? t - ld_f(q + j) : t;
     }
+    __device__ __forceinline__ long long at(int j) const { return j == drop ? 0ll : units(weight(j)); }
 };
 
-template <typename T>
+// Sum over tokens lo .. hi - 1 by a warp, VEC tokens a load.  hi - lo need not be a
+// multiple; with VEC > 1 lo is one, and rows are aligned to VEC tokens.
+template <typename T, int VEC, bool Q>
 __device__ __forceinline__ long long segment_sum(const Row<T> &row, int lo, int hi, int lane) {
+    constexpr int N = VEC > 1 ? 4 : 8;  // loads of a row in flight
     long long s = 0;
-    int j = lo + lane;
-    for (; j + (kUnroll - 1) * 32 < hi; j += kUnroll * 32) {
-        long long w[kUnroll];
+    int j = lo + lane * VEC;
+    for (; j + ((N - 1) * 32 + 1) * VEC <= hi; j += N * 32 * VEC) {
+        Pack<T, VEC> a[N], b[N];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) w[i] = row.at(j + i * 32);
+        for (int i = 0; i < N; ++i) {
+            a[i] = *reinterpret_cast<const Pack<T, VEC> *>(row.p + j + i * 32 * VEC);
+            if constexpr (Q) b[i] = *reinterpret_cast<const Pack<T, VEC> *>(row.q + j + i * 32 * VEC);
+        }
+        Units u;
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) s += w[i];
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) u.add(Q ? ld_f(&a[i].v[e]) - ld_f(&b[i].v[e]) : ld_f(&a[i].v[e]));
+        s += u.total();
     }
-    for (; j < hi; j += 32) s += row.at(j);
+    for (; j < hi; j += 32 * VEC)
+        for (int e = 0; e < VEC && j + e < hi; ++e) s += units(row.weight(j + e));
+    if (lo <= row.drop && row.drop < hi && lane == 0) s -= units(row.weight(row.drop));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
 }
 
-template <typename T>
+template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams p) {
     __shared__ long long seg[kWarps];                 // this CTA's segment sums, read by the cluster
     __shared__ long long all[kMaxCluster * kWarps];   // the cluster's, in token order
@@ -114,13 +148,14 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams p) 
     row.q = (n < c && Q != nullptr) ? Q + ((int64_t)b * K + n) * p.qs : nullptr;
     row.drop = (n < c && Q == nullptr) ? x[n] : -1;
     const int nseg = cs * kWarps;
-    const int len = (V + nseg - 1) / nseg;
+    const int len = ((V + nseg - 1) / nseg + VEC - 1) / VEC * VEC;
     const int mine = rank * kWarps + warp;
-    const int lo = min((int64_t)mine * len, (int64_t)V), hi = min(lo + len, V);
+    const int lo = (int)min((int64_t)mine * len, (int64_t)V), hi = min(lo + len, V);
 
     long long total = 0;
     for (int pass = 0; pass < 2; ++pass) {
-        const long long s = segment_sum(row, lo, hi, lane);
+        const long long s = row.q != nullptr ? segment_sum<T, VEC, true>(row, lo, hi, lane)
+                                             : segment_sum<T, VEC, false>(row, lo, hi, lane);
         if (lane == 0) seg[warp] = s;
         cluster.sync();
         for (int i = threadIdx.x; i < nseg; i += kThreads) all[i] = cluster.map_shared_rank(seg, i / kWarps)[i % kWarps];
@@ -166,7 +201,7 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams p) 
     }
     if (hit / kWarps != rank) return;
     // its tokens, a run of consecutive ones for each thread
-    const int s_lo = min((int64_t)hit * len, (int64_t)V), s_hi = min(s_lo + len, V);
+    const int s_lo = (int)min((int64_t)hit * len, (int64_t)V), s_hi = min(s_lo + len, V);
     const int per = (len + kThreads - 1) / kThreads;
     const int t_lo = min(s_lo + (int)threadIdx.x * per, s_hi), t_hi = min(t_lo + per, s_hi);
     long long s = 0;
@@ -210,7 +245,11 @@ cudaError_t launch_t(const AcceptParams &p, cudaStream_t stream) {
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, accept_kernel<T>, p);
+    constexpr int W = 16 / (int)sizeof(T);
+    const bool vec = p.ps % W == 0 && (p.q == nullptr || p.qs % W == 0) &&
+                     ((reinterpret_cast<uintptr_t>(p.p) | reinterpret_cast<uintptr_t>(p.q)) & 15) == 0;
+    const cudaError_t e = vec ? cudaLaunchKernelEx(&cfg, accept_kernel<T, W>, p)
+                              : cudaLaunchKernelEx(&cfg, accept_kernel<T, 1>, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

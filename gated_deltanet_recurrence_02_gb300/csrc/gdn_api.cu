@@ -439,6 +439,8 @@ int gdn_residual_norm(const void *y, const void *residual, const void *gate, con
     p.N = N; p.D = D; p.ys = y_stride; p.zs = gate_stride;
     p.scale = res_scale; p.eps = eps; p.flags = flags;
     p.dt_x = dtype_x; p.dt_res = dtype_res; p.dt_w = dtype_w;
+    p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+    if (error_word(&p.err) != cudaSuccess) return GDN_ERR_CUDA;
     return launch_residual_norm(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -117,6 +117,8 @@ struct ResidualNormParams {
     float scale, eps;
     int flags;  // GDN_GATE_* | GDN_NORM_UNIT_OFFSET
     int dt_x, dt_res, dt_w;
+    uint64_t wait_ns;
+    uint32_t *err;
 };
 
 struct AcceptParams {

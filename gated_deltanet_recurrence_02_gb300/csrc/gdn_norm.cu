@@ -16,6 +16,7 @@
 #include <atomic>
 
 #include "gdn_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace gdn {
 namespace {
@@ -446,15 +447,150 @@ __global__ void __launch_bounds__(THREADS, VEC * ITEMS <= 8 ? 1024 / THREADS : 1
     }
 }
 
+// fp32 vectors of eight elements: one 32-byte store where the row allows it (two
+// 16-byte ones of neighbouring threads would each touch every sector).
+__device__ __forceinline__ void store8(float *p, const float (&x)[8], bool wide) {
+    if (wide)
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+                     "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                     : "memory");
+    else
+        store_vec<float, 8>(p, x);
+}
+
+// residual_norm of rows longer than a warp's 128 vectors: a CTA a row, its next rows
+// on their way to shared memory by bulk copies, `stages` deep.  A bulk copy costs
+// one thread a few instructions a row, where per-thread copies cost every thread
+// more than the norm's own arithmetic.  Rows are multiples of 16 bytes.
+template <typename T, typename TR, int ITEMS, int THREADS>
+__global__ void __launch_bounds__(THREADS, ITEMS == 1 ? 1024 / THREADS : 1)
+residual_row_kernel(const ResidualNormParams p, int stages) {
+    constexpr int VEC = 16 / (int)sizeof(T);
+    __shared__ float red[2][32];
+    __shared__ uint64_t full[4];
+    extern __shared__ uint4 ring_smem[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>(ring_smem);
+    const int t = threadIdx.x, D = p.D;
+    const int act = p.flags & 0xF;
+    const float offset = (p.flags & GDN_NORM_UNIT_OFFSET) ? 1.f : 0.f;
+    const float inv_d = 1.f / (float)D;
+    const bool post = p.w_post != nullptr;
+    const bool wide = (reinterpret_cast<uintptr_t>(p.x_out) & 31) == 0;
+    // a stage: y, then the gate and the residual where there are any
+    const uint32_t yb = (uint32_t)D * sizeof(T), zb = act != GDN_GATE_NONE ? yb : 0u;
+    const uint32_t xb = p.x != nullptr ? (uint32_t)D * sizeof(TR) : 0u, bytes = yb + zb + xb;
+    if (t == 0) {
+        for (int s = 0; s < stages; ++s) tc::mbar_init(&full[s], 1);
+        tc::fence_mbar_init();
+    }
+    Weights<VEC, ITEMS> w_post, w_pre;
+    bool in[ITEMS];
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int i = (k * THREADS + t) * VEC;
+        in[k] = i < D;
+        if (in[k]) {
+            if (post) w_post.keep(p.w_post, i, p.dt_w, offset, k);
+            w_pre.keep(p.w_pre, i, p.dt_w, offset, k);
+        }
+    }
+    __syncthreads();
+    auto issue = [&](int64_t n, int s) {  // one thread
+        uint8_t *st = sm + s * bytes;
+        tc::mbar_arrive_expect_tx(&full[s], bytes);
+        tc::bulk_load(st, reinterpret_cast<const T *>(p.y) + n * p.ys, yb, &full[s]);
+        if (zb) tc::bulk_load(st + yb, reinterpret_cast<const T *>(p.z) + n * p.zs, zb, &full[s]);
+        if (xb) tc::bulk_load(st + yb + zb, reinterpret_cast<const TR *>(p.x) + n * D, xb, &full[s]);
+    };
+    const int64_t step = gridDim.x;
+    int64_t n = blockIdx.x;
+    if (t == 0)
+        for (int s = 0; s < stages; ++s)
+            if (n + s * step < p.N) issue(n + s * step, s);
+    int s = 0, phase = 0;
+    bool dead = false;  // a copy did not come in time: the rows after it are not waited for
+    for (; n < p.N; n += step) {
+        if (!dead) dead = !tc::mbar_wait(&full[s], phase, p.wait_ns);
+        const uint8_t *st = sm + s * bytes;
+        float u[ITEMS][VEC], a[ITEMS][VEC], ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const int i = (k * THREADS + t) * VEC;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) u[k][j] = 0.f, a[k][j] = 0.f;
+            if (!in[k]) continue;
+            load_vec<T, VEC>(reinterpret_cast<const T *>(st) + i, u[k]);
+            if (xb) load_vec<TR, VEC>(reinterpret_cast<const TR *>(st + yb + zb) + i, a[k]);
+            if (post)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) ss = fmaf(u[k][j], u[k][j], ss);
+            if (zb) {
+                float g[VEC];
+                load_vec<T, VEC>(reinterpret_cast<const T *>(st + yb) + i, g);
+                activate<T, VEC>(g, act);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) u[k][j] *= g[j];
+            }
+        }
+        float rs = p.scale;
+        if (post) rs *= rsqrtf(fmaf(row_sum<THREADS>(ss, THREADS, red[0]), inv_d, p.eps));
+        else __syncthreads();
+        // every thread has read the stage
+        if (t == 0 && n + stages * step < p.N && !dead) issue(n + stages * step, s);
+        ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const int i = (k * THREADS + t) * VEC;
+            if (!in[k]) continue;
+            if (post) {
+                const float(&w)[VEC] = w_post.at(p.w_post, i, p.dt_w, offset, k);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) u[k][j] *= w[j];
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                a[k][j] = fmaf(rs, u[k][j], a[k][j]);
+                ss = fmaf(a[k][j], a[k][j], ss);
+            }
+            if (p.x_out != nullptr) {
+                TR *dst = reinterpret_cast<TR *>(p.x_out) + n * D + i;
+                if constexpr (sizeof(TR) * VEC == 32) store8(dst, a[k], wide);
+                else store_vec<TR, VEC>(dst, a[k]);
+            }
+        }
+        if (p.out != nullptr) {
+            rs = rsqrtf(fmaf(row_sum<THREADS>(ss, THREADS, red[1]), inv_d, p.eps));
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) {
+                const int i = (k * THREADS + t) * VEC;
+                if (!in[k]) continue;
+                const float(&w)[VEC] = w_pre.at(p.w_pre, i, p.dt_w, offset, k);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) a[k][j] *= rs * w[j];
+                store_vec<T, VEC>(reinterpret_cast<T *>(p.out) + n * D + i, a[k]);
+            }
+        } else if (post) {
+            __syncthreads();  // red[0] is written again in the next turn
+        }
+        if (++s == stages) s = 0, phase ^= 1;
+    }
+    if (dead && t == 0) {
+        atomicOr(p.err, (uint32_t)GDN_DEVERR_TIMEOUT);
+        // the copies in flight must land before the CTA ends
+        for (int k = 0; k < stages; ++k) tc::mbar_wait(&full[k], phase ^ (k < s), kDefaultWaitNs / 8);
+    }
+}
+
 // How a row of `width` elements is spread over threads of ITEMS vectors each.
 // Rows of up to 32 vectors take the smallest power of two of lanes of one vector
-// each, so several rows share a warp; up to 128 a warp; longer ones a whole CTA.
+// each, so several rows share a warp; up to 128 (single elements: 256) a warp;
+// longer ones a whole CTA.
 struct Spread {
     int lanes, threads, items;
 };
 Spread spread(int width, int vec) {
     const int nv = (width + vec - 1) / vec;
-    if (nv <= 128) {
+    if (nv <= (vec > 1 ? 128 : 256)) {
         int lanes = 1;
         while (lanes < 32 && lanes < nv) lanes *= 2;
         int items = 1;
@@ -494,6 +630,8 @@ cudaError_t launch_rows(const P &p, const Spread &s, int64_t rows, cudaStream_t 
     return cudaGetLastError();
 }
 
+constexpr int kRowSmem = 204800;  // a multiprocessor's shared memory for rows
+
 template <int I, int TH>
 struct Shape {
     static constexpr int items = I, threads = TH;
@@ -505,6 +643,8 @@ cudaError_t with_shape(const Spread &s, F f) {
     if (s.threads == 256) {
         if (s.items == 1) return f(Shape<1, 256>{});
         if (s.items == 2) return f(Shape<2, 256>{});
+        if constexpr (MOST > 8)
+            if (s.items == 8) return f(Shape<8, 256>{});
         return f(Shape<4, 256>{});
     }
     if constexpr (MOST > 8)
@@ -544,12 +684,30 @@ cudaError_t launch_residual_t(const ResidualNormParams &p, cudaStream_t stream) 
                      aligned16(p.z) && aligned16(p.x) && aligned16(p.x_out) && aligned16(p.out) &&
                      aligned16(p.w_post) && aligned16(p.w_pre);
     const Spread s = spread(p.D, vec ? V : 1);
+    if (vec && s.lanes > 32)
+        return with_shape<32 / V>(s, [&](auto shape) {
+            using S = decltype(shape);
+            constexpr auto kern = residual_row_kernel<T, TR, S::items, S::threads>;
+            // two CTAs an SM where two rows fit each
+            const int row = p.D * (int)(sizeof(T) * (p.z != nullptr ? 2 : 1) + (p.x != nullptr ? sizeof(TR) : 0));
+            const int most = row <= kRowSmem / 4 ? kRowSmem / 2 : kRowSmem;
+            const int stages = most / row > 4 ? 4 : most / row < 1 ? 1 : most / row;
+            const cudaError_t e = set_smem_once<kern>(kRowSmem);
+            if (e != cudaSuccess) return e;
+            const int64_t ctas = (int64_t)sm_count_of_current_device() * (most < kRowSmem ? 1024 / S::threads : 1);
+            kern<<<(unsigned)(p.N < ctas ? p.N : ctas), S::threads, stages * row, stream>>>(p, stages);
+            return cudaGetLastError();
+        });
     if (vec)
         return with_shape<32 / V>(s, [&](auto shape) {
             using S = decltype(shape);
-            constexpr int NP = (2 + (sizeof(TR) > sizeof(T) ? 2 : 1)) * S::items;
-            return launch_rows<residual_norm_kernel<T, TR, V, S::items, S::threads>, Ring<NP, S::threads>::kBytes>(
-                p, s, p.N, stream);
+            if constexpr (S::threads > 256) {
+                return cudaErrorInvalidConfiguration;  // (a CTA's row: above)
+            } else {
+                constexpr int NP = (2 + (sizeof(TR) > sizeof(T) ? 2 : 1)) * S::items;
+                return launch_rows<residual_norm_kernel<T, TR, V, S::items, S::threads>, Ring<NP, S::threads>::kBytes>(
+                    p, s, p.N, stream);
+            }
         });
     return with_shape<16>(s, [&](auto shape) {
         using S = decltype(shape);
