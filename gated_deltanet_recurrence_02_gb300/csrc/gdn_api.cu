@@ -307,7 +307,8 @@ size_t gdn_linear_prefill_workspace_size(int B, int T, int Hk, int Hv, int dk, i
                                          int varlen) {
     if (B < 0 || T < 0 || Hk <= 0 || Hv <= 0 || dk <= 0 || dv <= 0 || dtype_bytes(dtype_qkv) == 0)
         return (size_t)-1;
-    return linear_tc_supported(dk, dv, dtype_qkv) ? linear_tc_workspace_bytes(B, T, Hv, dk, dv, varlen != 0) : 0;
+    return linear_tc_supported(dk, dv, dtype_qkv) ? linear_tc_workspace_bytes(B, T, Hv, dk, dv, varlen != 0)
+                                                  : linear_f32_workspace_bytes(B, T, Hv, dk, dv, varlen != 0);
 }
 
 int gdn_linear_prefill(const void *q, const void *k, const void *v, const void *alpha,
@@ -347,10 +348,6 @@ int gdn_linear_prefill(const void *q, const void *k, const void *v, const void *
     st = check_alias(spans, (int)(sizeof(spans) / sizeof(spans[0])), 5, 7);
     if (st != GDN_OK) return st;
     if (B == 0) return GDN_OK;
-    if (!linear_tc_supported(dk, dv, dtq))
-        return gdn_linear_recurrent(q, k, v, alpha, cu_seqlens, initial_state, initial_state_indices,
-                                    num_initial_states, final_state, out, B, T, Hq, Hk, Hv, dk, dv, scale,
-                                    dtype_qkv, dtype_gate, 0, nullptr, nullptr, nullptr, stream);
     PrefillParams p{};
     p.q = q; p.k = k; p.v = v; p.alpha = alpha;
     p.cu_seqlens = cu_seqlens;
@@ -361,7 +358,9 @@ int gdn_linear_prefill(const void *q, const void *k, const void *v, const void *
     p.ws = workspace; p.ws_bytes = workspace_bytes;
     p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     if (error_word(&p.err) != cudaSuccess) return GDN_ERR_CUDA;
-    return launch_linear_tc(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    const cudaStream_t on = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = linear_tc_supported(dk, dv, dtq) ? launch_linear_tc(p, on) : launch_linear_f32(p, on);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 int gdn_gated_norm(const void *x, const void *z, const void *weight, void *out, int64_t N, int H, int d,

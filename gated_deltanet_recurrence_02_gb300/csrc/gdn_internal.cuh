@@ -181,6 +181,9 @@ size_t prefill_tc_workspace_bytes(int B, int T, int Hk, int Hv, bool varlen);
 cudaError_t launch_linear_tc(const PrefillParams &p, cudaStream_t stream);
 bool linear_tc_supported(int dk, int dv, int dt_qkv);
 size_t linear_tc_workspace_bytes(int B, int T, int Hv, int dk, int dv, bool varlen);
+// The same for fp32 inputs, on the CUDA cores.
+cudaError_t launch_linear_f32(const PrefillParams &p, cudaStream_t stream);
+size_t linear_f32_workspace_bytes(int B, int T, int Hv, int dk, int dv, bool varlen);
 cudaError_t launch_gated_norm(const GatedNormParams &p, cudaStream_t stream);
 cudaError_t launch_residual_norm(const ResidualNormParams &p, cudaStream_t stream);
 cudaError_t launch_accept(const AcceptParams &p, cudaStream_t stream);
