@@ -82,8 +82,8 @@ constexpr int gW = 128;                            // 2^{s_t}: fp32 [64], or for
 constexpr int gLast = 256;                         // 2^{b_63}
 constexpr int gN = 257, gTok = 258, gHead = 259;   // ints: the chunk's tokens (0: no more chunks), first token, head
 constexpr int gLeft = 264;                         // [32] 2^{b_31 - b_t}
-constexpr uint32_t oWInv = oGate + NS * kGate;     // [2][128] 1 / scale of a lane of W
-constexpr uint32_t oSInv = oWInv + 1024;           // [2][128] 1 / scale of a lane of the image
+constexpr uint32_t oWInv = oGate + NS * kGate;     // [4][128] 1 / scale of a lane of W
+constexpr uint32_t oSInv = oWInv + 2048;           // [2][128] 1 / scale of a lane of the image
 constexpr uint32_t oPInv = oSInv + 1024;           // [2][64]  1 / scale of a row of P
 constexpr uint32_t oPMax = oPInv + 512;            // [64] maxima of both parts of the later rows of P
 constexpr uint32_t oBar = oPMax + 256;
@@ -185,13 +185,18 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     constexpr bool kBf = H::kBf16;
     constexpr bool kOut = MODE != kStateOnly;
     constexpr int NT = kBf && MODE != kOutputs ? 4 : 2;  // 16-bit parts of W
+    // Buffers of W and of dS in TMEM: two where the columns allow it, so that a
+    // product need not wait for what reads or replaces the last one's.
+    constexpr int WB = MODE == kStateOnly || NT == 2 ? 2 : 1, DB = MODE == kStateOnly ? 2 : 1;
+    constexpr uint32_t cDS = MODE == kStateOnly ? 0 : tDS, cW = MODE == kStateOnly ? 256 : tW;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_align1k(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + oBar), *empty = full + NS;
-    uint64_t *r_done = empty + NS, *r_free = r_done + 1, *p_ready = r_done + 2, *w_ready = r_done + 3,
-             *ds_done = r_done + 4, *ds_free = r_done + 5, *qs_done = r_done + 6, *s_ready = r_done + 7,
-             *o_done = r_done + 8, *o_free = r_done + 9, *drain = r_done + 10, *ds_half = r_done + 11;
-    uint32_t *slot = reinterpret_cast<uint32_t *>(r_done + 12);
+    uint64_t *r_done = empty + NS, *r_free = r_done + 1, *p_ready = r_done + 2, *qs_done = r_done + 3,
+             *s_ready = r_done + 4, *o_done = r_done + 5, *o_free = r_done + 6, *drain = r_done + 7;
+    // of even and of odd chunks, where a wait may lie more than one chunk back
+    uint64_t *w_ready = r_done + 8, *ds_half = r_done + 10, *ds_done = r_done + 12, *ds_free = r_done + 14;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(r_done + 16);
     // (through a shuffle: known to be the same in every lane)
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int dk = p.dk, dv = p.dv, Hv = p.Hv;
@@ -201,13 +206,15 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             mbar_init(&full[s], 2);                          // the copies' bytes, the decay sums
             mbar_init(&empty[s], kOut ? 2 + 4 + 4 : 1 + 4);  // MMA warps, state warps, output warps
         }
-        mbar_init(ds_half, 1);
-        mbar_init(ds_done, 1);
         mbar_init(r_done, 1);
         mbar_init(r_free, 3);
         mbar_init(p_ready, 3);
-        mbar_init(w_ready, 8);
-        mbar_init(ds_free, 4);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&w_ready[s], 8);
+            mbar_init(&ds_half[s], 1);
+            mbar_init(&ds_done[s], 1);
+            mbar_init(&ds_free[s], 4);
+        }
         mbar_init(qs_done, 1);
         mbar_init(s_ready, 4);
         mbar_init(o_done, 1);
@@ -233,6 +240,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     auto wait = [&](uint64_t *bar, int it) {
         return __all_sync(0xffffffffu, mbar_wait_until(bar, (uint32_t)it & 1u, deadline)) != 0;
     };
+    auto wait2 = [&](uint64_t *bars, int it) { return wait(&bars[it & 1], it >> 1); };
     auto gate_of = [&](int it) { return reinterpret_cast<float *>(sm + oGate + (it % NS) * kGate); };
     // The chunk's tiles and sums are there; its tokens n, or 0 past the last one
     // (and -1 where the wait ran out).
@@ -320,16 +328,16 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     arrive(s_ready);
                 }
                 // S <- 2^b_63 S + dS
-                if (!(ok = chunk(it) > 0) || !(ok = wait(ds_done, it))) break;
+                if (!(ok = chunk(it) > 0) || !(ok = wait2(ds_done, it))) break;
                 fence_after_sync();
                 const float gam = gate_of(it)[gLast];
-                const float wi = kBf ? 1.f : winv[(it & 1) * 128 + i];
+                const float wi = kBf ? 1.f : winv[(it & 3) * 128 + i];
                 const float2 gam2 = make_float2(gam, gam), wi2 = make_float2(wi, wi);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     if (g * 32 < dk) {
                         uint32_t v[32];
-                        tmem_ld32_async(lane_base + tDS + 32 * g, v);
+                        tmem_ld32_async(lane_base + cDS + 128 * (it % DB) + 32 * g, v);
                         tmem_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
@@ -341,7 +349,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 }
                 kept *= gam;
                 fence_before_sync();
-                arrive(ds_free);
+                arrive(&ds_free[it & 1]);
                 arrive(&empty[it % NS]);
             }
             if (!ok) break;
@@ -467,21 +475,21 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                         }
                     }
                 }
-                if (it > 0 && !(ok = wait(half == 0 ? ds_half : ds_done, it - 1))) break;
+                if (it >= WB && !(ok = wait2(half == 0 ? ds_half : ds_done, it - WB))) break;
                 fence_after_sync();
 #pragma unroll
-                for (int m = 0; m < NT; ++m) tmem_st_16x16(lane_base + tW + 32 * m + 16 * half, part[m]);
+                for (int m = 0; m < NT; ++m) tmem_st_16x16(lane_base + cW + 32 * NT * (it % WB) + 32 * m + 16 * half, part[m]);
             }
             if (!ok) break;
-            // (the last product was issued after the state warps had read the
-            // scales of the one before it)
+            // (four buffers: the state warps read their scale before the product two
+            // chunks on, whose end was waited for two chunks after that at the latest)
             if constexpr (!kBf)
                 if ((lane & 3) == 0)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) winv[(it & 1) * 128 + 8 * e] = inv[e];
+                    for (int e = 0; e < 2; ++e) winv[(it & 3) * 128 + 8 * e] = inv[e];
             tmem_wait_st();
             fence_before_sync();
-            arrive(w_ready);
+            arrive(&w_ready[it & 1]);
         }
     } else if (warp < 12) {
         // ============================ outputs ============================
@@ -613,17 +621,18 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 if (n <= 0) break;
                 const uint32_t st = smem_u32(sm) + (it % NS) * kStage;
                 // dS = W^T K, every part of 16 tokens of W at a time
-                if (!(ok = wait(w_ready, it)) || (it > 0 && !(ok = wait(ds_free, it - 1)))) break;
+                if (!(ok = wait2(w_ready, it)) || (it >= DB && !(ok = wait2(ds_free, it - DB)))) break;
                 fence_after_sync();
                 const uint64_t kn = desc_sw128(st, kBlock, 1024);
+                const uint32_t ds = tm + cDS + 128 * (it % DB), w = tm + cW + 32 * NT * (it % WB);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
 #pragma unroll
                     for (int m = 0; m < NT; ++m)
-                        mma_f16_ta_warp(leader, tm + tDS, tm + tW + 32 * m + 8 * j, desc_add(kn, j * 2048), id_ds, m + j > 0);
-                    if (j == 1) mma_commit_warp(leader, ds_half);
+                        mma_f16_ta_warp(leader, ds, w + 32 * m + 8 * j, desc_add(kn, j * 2048), id_ds, m + j > 0);
+                    if (j == 1) mma_commit_warp(leader, &ds_half[it & 1]);
                 }
-                mma_commit_warp(leader, ds_done);
+                mma_commit_warp(leader, &ds_done[it & 1]);
                 mma_commit_warp(leader, &empty[it % NS]);
             }
             mma_commit_warp(leader, drain);  // nothing may be in flight when TMEM is given back
