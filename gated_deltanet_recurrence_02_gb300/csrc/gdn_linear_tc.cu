@@ -74,20 +74,22 @@ constexpr uint32_t kStageV = 2 * kBlock;
 constexpr uint32_t kStage = kStageV + 16384;
 constexpr uint32_t oP = NS * kStage;
 constexpr uint32_t oOut = oP + 8192;               // [4 warps][64 tokens][32 features] on their way out
-constexpr uint32_t oGate = oOut + 16384;           // per stage (kGate bytes), the words below
-constexpr uint32_t kGate = 1280;
+constexpr uint32_t oGate = oOut + 16384;           // kGates slots of kGate bytes, the words below
+constexpr int kGates = 8;
+constexpr uint32_t kGate = 1040;
 constexpr int gSum = 0;                            // [64] b_t (decays of at least 2^-40 each)
 constexpr int gScaled = 64;                        // [64] scale 2^{b_t}
-constexpr int gW = 128;                            // 2^{s_t}: fp32 [64], or for bf16 [32 pairs][its three parts, 0]
+constexpr int gW = 128;                            // 2^{s_t}: fp32 [64], or for bf16 [32 pairs][two parts]
+constexpr int gW2 = 192;                           // and the third part [32 pairs]
+constexpr int gLeft = 224;                         // [32] 2^{b_31 - b_t}
 constexpr int gLast = 256;                         // 2^{b_63}
 constexpr int gN = 257, gTok = 258, gHead = 259;   // ints: the chunk's tokens (0: no more chunks), first token, head
-constexpr int gLeft = 264;                         // [32] 2^{b_31 - b_t}
-constexpr uint32_t oWInv = oGate + NS * kGate;     // [4][128] 1 / scale of a lane of W
-constexpr uint32_t oSInv = oWInv + 2048;           // [2][128] 1 / scale of a lane of the image
-constexpr uint32_t oPInv = oSInv + 1024;           // [2][64]  1 / scale of a row of P
+constexpr uint32_t oWExp = oGate + kGates * kGate; // [4][128] int8: the exponent of a lane's scale of W
+constexpr uint32_t oSExp = oWExp + 512;            // [2][128] int8: of a lane's scale of the image
+constexpr uint32_t oPInv = oSExp + 256;           // [2][64]  1 / scale of a row of P
 constexpr uint32_t oPMax = oPInv + 512;            // [64] maxima of both parts of the later rows of P
 constexpr uint32_t oBar = oPMax + 256;
-constexpr uint32_t kSmem = oBar + 256 + 1024;      // + alignment slack
+constexpr uint32_t kSmem = oBar + 384 + 1024;      // + alignment slack
 
 // TMEM columns
 constexpr uint32_t tR = 0, tO1 = 64, tO2 = 128, tDS = 192, tS = 320, tW = 384;
@@ -149,15 +151,13 @@ __device__ __forceinline__ uint32_t bf2_rest(uint32_t a, uint32_t b, uint32_t c)
     return d;
 }
 
-// A power of two that brings a largest magnitude m into [2^13, 2^14), and its
-// inverse (fp16 holds 2^-14 .. 2^15 in full precision).
-__device__ __forceinline__ void half_scale(float m, float &s, float &inv) {
-    int e = 13 + 127 - (int)(__float_as_uint(m) >> 23);
-    e = e > 126 ? 126 : (e < -126 ? -126 : e);
-    if (!(m > 0.f)) e = 0;
-    s = __uint_as_float((uint32_t)(127 + e) << 23);
-    inv = __uint_as_float((uint32_t)(127 - e) << 23);
+// The exponent of the power of two that brings a largest magnitude m into
+// [2^13, 2^14) (fp16 holds 2^-14 .. 2^15 in full precision).
+__device__ __forceinline__ int half_exp(float m) {
+    const int e = 13 + 127 - (int)(__float_as_uint(m) >> 23);
+    return !(m > 0.f) ? 0 : e > 126 ? 126 : e < -126 ? -126 : e;
 }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // One unit: a segment of a (row, value head).
 struct Unit {
@@ -192,7 +192,8 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_align1k(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + oBar), *empty = full + NS;
-    uint64_t *r_done = empty + NS, *r_free = r_done + 1, *p_ready = r_done + 2, *qs_done = r_done + 3,
+    uint64_t *g_full = empty + NS, *g_empty = g_full + kGates;
+    uint64_t *r_done = g_empty + kGates, *r_free = r_done + 1, *p_ready = r_done + 2, *qs_done = r_done + 3,
              *s_ready = r_done + 4, *o_done = r_done + 5, *o_free = r_done + 6, *drain = r_done + 7;
     // of even and of odd chunks, where a wait may lie more than one chunk back
     uint64_t *w_ready = r_done + 8, *ds_half = r_done + 10, *ds_done = r_done + 12, *ds_free = r_done + 14;
@@ -203,8 +204,12 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&full[s], 2);                          // the copies' bytes, the decay sums
-            mbar_init(&empty[s], kOut ? 2 + 4 + 4 : 1 + 4);  // MMA warps, state warps, output warps
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kOut ? 2 : 1);  // the warps that issue MMAs
+        }
+        for (int s = 0; s < kGates; ++s) {
+            mbar_init(&g_full[s], 1);
+            mbar_init(&g_empty[s], kOut ? 4 + 4 : 4);  // the last readers: state warps, output warps
         }
         mbar_init(r_done, 1);
         mbar_init(r_free, 3);
@@ -241,14 +246,15 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
         return __all_sync(0xffffffffu, mbar_wait_until(bar, (uint32_t)it & 1u, deadline)) != 0;
     };
     auto wait2 = [&](uint64_t *bars, int it) { return wait(&bars[it & 1], it >> 1); };
-    auto gate_of = [&](int it) { return reinterpret_cast<float *>(sm + oGate + (it % NS) * kGate); };
-    // The chunk's tiles and sums are there; its tokens n, or 0 past the last one
-    // (and -1 where the wait ran out).
+    auto gate_of = [&](int it) { return reinterpret_cast<float *>(sm + oGate + (it % kGates) * kGate); };
+    // The chunk's decay sums are there; its tokens n, or 0 past the last one (and -1
+    // where the wait ran out).
     auto chunk = [&](int it) {
-        if (!wait(&full[it % NS], it / NS)) return -1;
+        if (!wait(&g_full[it % kGates], it / kGates)) return -1;
         deadline = limit();
         return reinterpret_cast<const int *>(gate_of(it))[gN];
     };
+    auto tiles = [&](int it) { return wait(&full[it % NS], it / NS); };
     auto arrive = [&](uint64_t *bar) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
@@ -259,8 +265,8 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
         regs_inc<168>();
         const int i = warp * 32 + lane;  // value feature
         const uint32_t lane_base = tm + ((uint32_t)(warp * 32) << 16);
-        const float *winv = reinterpret_cast<const float *>(sm + oWInv);
-        float *sinv = reinterpret_cast<float *>(sm + oSInv);
+        const int8_t *wexp = reinterpret_cast<const int8_t *>(sm + oWExp);
+        int8_t *sexp = reinterpret_cast<int8_t *>(sm + oSExp);
         float2 S[64];  // columns 2 j, 2 j + 1
         int it = 0;
         const size_t mat = (size_t)dv * dk;
@@ -300,18 +306,20 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             for (int c = x.c0; c < x.c1; ++c, ++it) {
                 if constexpr (kOut) {
                     // this chunk's start state as an MMA operand
-                    float sc = 1.f, inv = 1.f;
+                    float sc = 1.f;
+                    int se = 0;
                     if constexpr (!kBf) {
                         float m = 0.f;
 #pragma unroll
                         for (int j = 0; j < 64; ++j) m = fmaxf(m, fmaxf(fabsf(S[j].x), fabsf(S[j].y)));
-                        half_scale(m, sc, inv);
+                        se = half_exp(m);
+                        sc = pow2(se);
                     }
                     if (it > 0 && !(ok = wait(qs_done, it - 1))) break;
                     fence_after_sync();
                     // (the outputs two chunks back have read their scales: that
                     // product was issued after them)
-                    if constexpr (!kBf) sinv[(it & 1) * 128 + i] = inv;
+                    if constexpr (!kBf) sexp[(it & 1) * 128 + i] = (int8_t)se;
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         if (g * 32 < dk) {
@@ -331,7 +339,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 if (!(ok = chunk(it) > 0) || !(ok = wait2(ds_done, it))) break;
                 fence_after_sync();
                 const float gam = gate_of(it)[gLast];
-                const float wi = kBf ? 1.f : winv[(it & 3) * 128 + i];
+                const float wi = kBf ? 1.f : pow2(-wexp[(it & 3) * 128 + i]);
                 const float2 gam2 = make_float2(gam, gam), wi2 = make_float2(wi, wi);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
@@ -350,7 +358,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 kept *= gam;
                 fence_before_sync();
                 arrive(&ds_free[it & 1]);
-                arrive(&empty[it % NS]);
+                arrive(&g_empty[it % kGates]);
             }
             if (!ok) break;
             float *dst = nullptr;
@@ -380,7 +388,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
         regs_dec<64>();
         const int wq = warp & 3, hh = warp >= 20 ? 1 : 0;
         const uint32_t lane_base = tm + ((uint32_t)(wq * 32 + 16 * hh) << 16);
-        float *winv = reinterpret_cast<float *>(sm + oWInv) + wq * 32 + 16 * hh + (lane >> 2);
+        int8_t *wexp = reinterpret_cast<int8_t *>(sm + oWExp) + wq * 32 + 16 * hh + (lane >> 2);
         // ldmatrix: this lane's row of the four 8 x 8 matrices (tokens 0-7 and
         // 8-15 of 16, features 0-7 and 8-15 of 16)
         const int row = (lane & 7) + ((lane >> 4) << 3), cg = (wq & 1) * 4 + 2 * hh + ((lane >> 3) & 1);
@@ -390,6 +398,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             const int n = chunk(it);
             ok = n >= 0;
             if (n <= 0) break;
+            if (!(ok = tiles(it))) break;
             uint8_t *st = sm + (it % NS) * kStage;
             if (n < C) {
                 // K and V rows past the row's end: zeros, whatever was loaded
@@ -408,7 +417,8 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             // 16 tokens (j): features g and g + 8, tokens 2 t, 2 t + 1 of each eight,
             // which is the layout of the TMEM store
             auto values = [&](int j, uint32_t (&v)[4]) { ldsm_x4_trans(v, st + v_off + j * 2048); };
-            float sc[2] = {1.f, 1.f}, inv[2];
+            float sc[2] = {1.f, 1.f};
+            int we[2];
             auto scaled = [&](int j, float2 (&x)[4]) {  // fp16: in fp32
                 uint32_t v[4];
                 values(j, v);
@@ -432,7 +442,8 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 for (int e = 0; e < 2; ++e) {
                     m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], 1));
                     m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], 2));
-                    half_scale(m[e], sc[e], inv[e]);
+                    we[e] = half_exp(m[e]);
+                    sc[e] = pow2(we[e]);
                 }
             }
             // Each half of the chunk is formed while the last chunk's product still
@@ -448,10 +459,11 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                         // product of bf16 numbers is exactly its rounding plus a rest
                         uint32_t v[4];
                         values(j, v);
-                        const uint4 *w = reinterpret_cast<const uint4 *>(gate_of(it) + gW) + (lane & 3) + 8 * j;
+                        const uint2 *w = reinterpret_cast<const uint2 *>(gate_of(it) + gW) + (lane & 3) + 8 * j;
+                        const uint32_t *w2 = reinterpret_cast<const uint32_t *>(gate_of(it) + gW2) + (lane & 3) + 8 * j;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const uint4 ww = w[4 * (e >> 1)];
+                            const uint2 ww = w[4 * (e >> 1)];
                             const uint32_t a = bf2_mul(ww.x, v[e]), r = bf2_rest(ww.x, v[e], a);
                             part[0][4 * jj + e] = a;
                             if constexpr (NT == 2) {
@@ -460,7 +472,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                                 const uint32_t b = bf2_mul(ww.y, v[e]);
                                 part[1][4 * jj + e] = r;
                                 part[2][4 * jj + e] = b;
-                                part[3][4 * jj + e] = bf2_fma(ww.z, v[e], bf2_rest(ww.y, v[e], b));
+                                part[3][4 * jj + e] = bf2_fma(w2[4 * (e >> 1)], v[e], bf2_rest(ww.y, v[e], b));
                             }
                         }
                     } else {
@@ -486,7 +498,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             if constexpr (!kBf)
                 if ((lane & 3) == 0)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) winv[(it & 3) * 128 + 8 * e] = inv[e];
+                    for (int e = 0; e < 2; ++e) wexp[(it & 3) * 128 + 8 * e] = (int8_t)we[e];
             tmem_wait_st();
             fence_before_sync();
             arrive(&w_ready[it & 1]);
@@ -497,7 +509,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
         if constexpr (kOut) {
             const int wq = warp - 8;
             const uint32_t lane_base = tm + ((uint32_t)(wq * 32) << 16);
-            const float *sinv = reinterpret_cast<const float *>(sm + oSInv) + wq * 32 + (lane >> 2);
+            const int8_t *sexp = reinterpret_cast<const int8_t *>(sm + oSExp) + wq * 32 + (lane >> 2);
             const float *pinv = reinterpret_cast<const float *>(sm + oPInv) + 2 * (lane & 3);
             uint8_t *buf = sm + oOut + wq * 4096;  // [64 tokens][32 features], 64-byte swizzle
             // stmatrix: this lane's row (token) of the four 8 x 8 matrices (features
@@ -534,7 +546,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                                 make_float2(__uint_as_float(o2[4 * r + 2 * m]), __uint_as_float(o2[4 * r + 2 * m + 1]));
                             float2 e = e2;
                             if constexpr (!kBf) {
-                                const float si = sinv[(it & 1) * 128 + 16 * hh + 8 * m];
+                                const float si = pow2(-sexp[(it & 1) * 128 + 16 * hh + 8 * m]);
                                 e = __fmul2_rn(e, make_float2(si, si));
                                 a = __fmul2_rn(a, p2);
                             }
@@ -551,7 +563,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 }
                 fence_before_sync();
                 arrive(o_free);
-                arrive(&empty[it % NS]);
+                arrive(&g_empty[it % kGates]);
                 if (wq * 32 >= dv) continue;
                 if (n == C) {
                     fence_proxy_async();
@@ -603,10 +615,6 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     }
                 }
             }
-            if (ok) {  // the end of the chunks
-                if (it >= NS) ok = wait(&empty[it % NS], it / NS - 1);
-                if (ok) arrive(&full[it % NS]);
-            }
             // the copies in flight must land before the CTA ends
             if (!ok)
                 for (int j = it > NS ? it - NS : 0; j < it; ++j)
@@ -619,6 +627,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 const int n = chunk(it);
                 ok = n >= 0;
                 if (n <= 0) break;
+                if (!(ok = tiles(it))) break;
                 const uint32_t st = smem_u32(sm) + (it % NS) * kStage;
                 // dS = W^T K, every part of 16 tokens of W at a time
                 if (!(ok = wait2(w_ready, it)) || (it >= DB && !(ok = wait2(ds_free, it - DB)))) break;
@@ -670,7 +679,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 }
                 const float *b = gate_of(it) + gSum + diag;
                 const float bi = b[lane];
-                float m = 0.f, sc = 1.f, inv = 1.f;
+                float m = 0.f;
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
                     const float2 b2 = *reinterpret_cast<const float2 *>(b + j);
@@ -696,8 +705,9 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                         named_bar(kBarP, 64);
                         m = fmaxf(m, pmax[32 + lane]);
                     }
-                    half_scale(m, sc, inv);
-                    pinv[(it & 1) * 64 + i] = inv;
+                    const int pe = half_exp(m);
+                    const float sc = pow2(pe);
+                    pinv[(it & 1) * 64 + i] = pow2(-pe);
 #pragma unroll
                     for (int j = 0; j < 32; j += 2)
                         x[j / 2] = H::pack2(sc * __uint_as_float(x[j]), sc * __uint_as_float(x[j + 1]));
@@ -741,7 +751,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     ok = n >= 0;
                     if (n > 0) {
                         // R = [K;Q] K^T
-                        if (it > 0 && !(ok = wait(r_free, it - 1))) break;
+                        if (!(ok = tiles(it)) || (it > 0 && !(ok = wait(r_free, it - 1)))) break;
                         fence_after_sync();
                         const uint64_t kq = desc_sw128(s0 + (it % NS) * kStage, 16, 1024);
                         over_dk([&](int k) {
@@ -794,7 +804,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     const float l = p.scale * ex2_approx(gate[gSum + i] - gate[gSum + 31]);
                     float2 l2 = make_float2(l, l);
                     if constexpr (!kBf) {
-                        float m = 0.f, sc, inv;
+                        float m = 0.f;
 #pragma unroll 1
                         for (int hh = 0; hh < 2; ++hh) {
                             uint32_t y[16];
@@ -809,7 +819,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                         // p_ready, and the next R comes after both)
                         pmax[32 + lane] = m;
                         named_bar(kBarP, 64);
-                        half_scale(fmaxf(m, pmax[lane]), sc, inv);
+                        const float sc = pow2(half_exp(fmaxf(m, pmax[lane])));
                         l2 = make_float2(l * sc, l * sc);
                     }
                     if (it > 0 && !(ok = wait(o_done, it - 1))) break;
@@ -881,8 +891,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 }
                 if (it < 0) continue;
                 if (n_ == 0 && !end_) break;
-                const int s = it % NS;
-                if (it >= NS && !(ok = wait(&empty[s], it / NS - 1))) break;
+                if (it >= kGates && !(ok = wait(&g_empty[it % kGates], it / kGates - 1))) break;
                 deadline = limit();
                 float *gate = gate_of(it);
                 if (lane == 0) {
@@ -926,7 +935,8 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     r = make_float2(w2.x - r.x, w2.y - r.y);
                     const uint32_t wb = H::pack2(r.x, r.y);
                     const float2 y = H::unpack2(wb);
-                    *reinterpret_cast<uint4 *>(gate + gW + 4 * lane) = make_uint4(wa, wb, H::pack2(r.x - y.x, r.y - y.y), 0u);
+                    *reinterpret_cast<uint2 *>(gate + gW + 2 * lane) = make_uint2(wa, wb);
+                    reinterpret_cast<uint32_t *>(gate)[gW2 + lane] = H::pack2(r.x - y.x, r.y - y.y);
                 } else {
                     *reinterpret_cast<float2 *>(gate + gW + 2 * lane) = w2;
                 }
@@ -934,7 +944,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     *reinterpret_cast<float2 *>(gate + gLeft + 2 * lane) =
                         make_float2(ex2_approx(b31 - b2.x), ex2_approx(b31 - b2.y));
                 if (lane == 31) gate[gLast] = ex2_approx(up);
-                arrive(&full[s]);
+                arrive(&g_full[it % kGates]);
                 if (n_ == 0) break;  // past the last chunk
             }
         }
