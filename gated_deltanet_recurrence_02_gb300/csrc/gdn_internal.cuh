@@ -244,6 +244,21 @@ __device__ __forceinline__ float4 ld4(const __nv_bfloat16 *p) {
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
+// Eight consecutive fp32 values as one 32-byte access (p 32-byte aligned).  Where
+// lanes are rows apart, 16-byte accesses use half of each sector that they move,
+// and meet its other half only if L1 still has it.
+__device__ __forceinline__ void ld8_wide(const float *p, float2 &a, float2 &b, float2 &c, float2 &d) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(a.x), "=f"(a.y), "=f"(b.x), "=f"(b.y), "=f"(c.x), "=f"(c.y), "=f"(d.x), "=f"(d.y)
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void st8_wide(float *p, float2 a, float2 b, float2 c, float2 d) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(a.x), "f"(a.y), "f"(b.x),
+                 "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y)
+                 : "memory");
+}
+
 // Store fp32 as the output type, round-to-nearest-even.
 __device__ __forceinline__ void st_out(float *p, float x) { *p = x; }
 __device__ __forceinline__ void st_out(__half *p, float x) { *p = __float2half_rn(x); }

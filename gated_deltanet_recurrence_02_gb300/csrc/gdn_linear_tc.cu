@@ -37,8 +37,10 @@
 //               costs its issuer some 55 cycles, and half of them run for 32)
 //   warps 17-18 the chunks' decay sums
 // Few rows are cut into segments of whole chunks, so that every SM has one: a
-// first pass (kStateOnly) forms each segment's end state from its start on,
-// and the second takes each segment's start state from those.
+// first pass (kStateOnly) forms each segment's end state from zeros, a small kernel
+// joins them along the row, and the second pass takes each segment's start state from
+// those.  (Joining them in the second pass, by the state warps, took as long as its
+// chunks: a thread is a row of the state there, and has few registers left.)
 //
 // Ragged chunks: tokens past the row's end get decay 1 and W = 0, and their K
 // and V rows are zeroed in shared memory, so that nothing of the next row (NaN
@@ -235,6 +237,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     __syncthreads();
     fence_after_sync();
     const uint32_t tm = __shfl_sync(0xffffffffu, *slot, 0);
+    if constexpr (MODE == kStateOnly) grid_launch_dependents();
     bool ok = true;
     // Waits run out p.wait_ns after the warp's last chunk came (a limit below a
     // microsecond at the first check that finds a phase incomplete).
@@ -268,118 +271,124 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
         const int8_t *wexp = reinterpret_cast<const int8_t *>(sm + oWExp);
         int8_t *sexp = reinterpret_cast<int8_t *>(sm + oSExp);
         float2 S[64];  // columns 2 j, 2 j + 1
+        if constexpr (MODE == kOutputs) grid_dependency_wait();  // the fold's states
         int it = 0;
         const size_t mat = (size_t)dv * dk;
-        auto clear = [&]() {
-#pragma unroll
-            for (int j = 0; j < 64; ++j) S[j] = make_float2(0.f, 0.f);
-        };
-        auto add_row = [&](const float *src, float keep) {  // S <- keep S + row i
-            const float2 k2 = make_float2(keep, keep);
-#pragma unroll
-            for (int q = 0; q < 32; ++q) {
-                if (q * 4 < dk) {
-                    const float4 f = *reinterpret_cast<const float4 *>(src + (size_t)i * dk + q * 4);
-                    S[2 * q] = __ffma2_rn(k2, S[2 * q], make_float2(f.x, f.y));
-                    S[2 * q + 1] = __ffma2_rn(k2, S[2 * q + 1], make_float2(f.z, f.w));
-                }
-            }
-        };
-        // S <- the state after the row's segments s < n (nothing yet if 0)
-        auto fold = [&](size_t seg0, int n) {
-#pragma unroll 1
-            for (int s = 0; s < n; ++s) add_row(p.seg_state + (seg0 + s) * mat, p.seg_decay[seg0 + s]);
-        };
 #pragma unroll 1
         for (unsigned u = blockIdx.x; ok && u < p.n_units; u += gridDim.x) {
             const Unit x = unit_at(p, u);
             const size_t seg0 = ((size_t)x.b * Hv + x.h) * p.G;
-            clear();
-            if (x.g == 0) {
-                const float *s0 = initial_state_ptr(p.s0, p.s0_idx, p.n_s0, x.b, x.h, Hv, dv, dk, p.err);
-                if (s0 != nullptr && i < dv) add_row(s0, 0.f);
-            } else if (MODE == kOutputs && i < dv) {
-                fold(seg0, x.g);
-            }
-            float kept = 1.f;  // the segment's decay
+            float *final = p.s_final != nullptr ? p.s_final + ((size_t)x.b * Hv + x.h) * mat : nullptr;
+            // A last state in the place of the initial one: the unit of the row's first
+            // segment copies it there in a second turn without chunks, when each thread
+            // has read its row of the initial state.  (Else the fold has written it.)
+            const int turns = MODE == kOutputs && x.g == 0 && final != nullptr && p.s_final == p.s0 ? 2 : 1;
 #pragma unroll 1
-            for (int c = x.c0; c < x.c1; ++c, ++it) {
-                if constexpr (kOut) {
-                    // this chunk's start state as an MMA operand
-                    float sc = 1.f;
-                    int se = 0;
-                    if constexpr (!kBf) {
-                        float m = 0.f;
+            for (int turn = 0; ok && turn < turns; ++turn) {
+                // the start: the initial state, or the state after the segment before
+                const float *src = nullptr;
+                if (x.g == 0 && turn == 0)
+                    src = initial_state_ptr(p.s0, p.s0_idx, p.n_s0, x.b, x.h, Hv, dv, dk, p.err);
+                else if (MODE == kOutputs)
+                    src = p.seg_state + (seg0 + (turn == 0 ? x.g : p.G) - 1) * mat;
 #pragma unroll
-                        for (int j = 0; j < 64; ++j) m = fmaxf(m, fmaxf(fabsf(S[j].x), fabsf(S[j].y)));
-                        se = half_exp(m);
-                        sc = pow2(se);
+                for (int j = 0; j < 64; ++j) S[j] = make_float2(0.f, 0.f);
+                if (src != nullptr && i < dv) {
+                    src += (size_t)i * dk;
+                    // (a lane is a row: 32-byte loads, as ld8_wide explains)
+                    if ((reinterpret_cast<uintptr_t>(src) & 31) == 0) {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            if (q * 8 < dk) ld8_wide(src + q * 8, S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 32; ++q)
+                            if (q * 4 < dk) {
+                                const float4 f = *reinterpret_cast<const float4 *>(src + q * 4);
+                                S[2 * q] = make_float2(f.x, f.y);
+                                S[2 * q + 1] = make_float2(f.z, f.w);
+                            }
                     }
-                    if (it > 0 && !(ok = wait(qs_done, it - 1))) break;
+                }
+                float kept = 1.f;  // the segment's decay
+#pragma unroll 1
+                for (int c = turn == 0 ? x.c0 : x.c1; c < x.c1; ++c, ++it) {
+                    if constexpr (kOut) {
+                        // this chunk's start state as an MMA operand
+                        float sc = 1.f;
+                        int se = 0;
+                        if constexpr (!kBf) {
+                            float m = 0.f;
+#pragma unroll
+                            for (int j = 0; j < 64; ++j) m = fmaxf(m, fmaxf(fabsf(S[j].x), fabsf(S[j].y)));
+                            se = half_exp(m);
+                            sc = pow2(se);
+                        }
+                        if (it > 0 && !(ok = wait(qs_done, it - 1))) break;
+                        fence_after_sync();
+                        // (the outputs two chunks back have read their scales: that
+                        // product was issued after them)
+                        if constexpr (!kBf) sexp[(it & 1) * 128 + i] = (int8_t)se;
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            if (g * 32 < dk) {
+                                uint32_t v[16];
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    v[j] = kBf ? H::pack2(S[16 * g + j].x, S[16 * g + j].y)
+                                               : H::pack2(sc * S[16 * g + j].x, sc * S[16 * g + j].y);
+                                tmem_st16(lane_base + tS + 16 * g, v);
+                            }
+                        }
+                        tmem_wait_st();
+                        fence_before_sync();
+                        arrive(s_ready);
+                    }
+                    // S <- 2^b_63 S + dS
+                    if (!(ok = chunk(it) > 0) || !(ok = wait2(ds_done, it))) break;
                     fence_after_sync();
-                    // (the outputs two chunks back have read their scales: that
-                    // product was issued after them)
-                    if constexpr (!kBf) sexp[(it & 1) * 128 + i] = (int8_t)se;
+                    const float gam = gate_of(it)[gLast];
+                    const float wi = kBf ? 1.f : pow2(-wexp[(it & 3) * 128 + i]);
+                    const float2 gam2 = make_float2(gam, gam), wi2 = make_float2(wi, wi);
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         if (g * 32 < dk) {
-                            uint32_t v[16];
+                            uint32_t v[32];
+                            tmem_ld32_async(lane_base + cDS + 128 * (it % DB) + 32 * g, v);
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                v[j] = kBf ? H::pack2(S[16 * g + j].x, S[16 * g + j].y)
-                                           : H::pack2(sc * S[16 * g + j].x, sc * S[16 * g + j].y);
-                            tmem_st16(lane_base + tS + 16 * g, v);
+                            for (int j = 0; j < 16; ++j) {
+                                float2 d = make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                                if constexpr (!kBf) d = __fmul2_rn(wi2, d);
+                                S[16 * g + j] = __ffma2_rn(gam2, S[16 * g + j], d);
+                            }
                         }
                     }
-                    tmem_wait_st();
+                    kept *= gam;
                     fence_before_sync();
-                    arrive(s_ready);
+                    arrive(&ds_free[it & 1]);
+                    arrive(&g_empty[it % kGates]);
                 }
-                // S <- 2^b_63 S + dS
-                if (!(ok = chunk(it) > 0) || !(ok = wait2(ds_done, it))) break;
-                fence_after_sync();
-                const float gam = gate_of(it)[gLast];
-                const float wi = kBf ? 1.f : pow2(-wexp[(it & 3) * 128 + i]);
-                const float2 gam2 = make_float2(gam, gam), wi2 = make_float2(wi, wi);
+                if (!ok) break;
+                float *dst = MODE == kWhole || turn == 1 ? final : nullptr;
+                if (MODE == kStateOnly) {
+                    dst = p.seg_state + (seg0 + x.g) * mat;
+                    if (i == 0) p.seg_decay[seg0 + x.g] = kept;
+                }
+                if (dst != nullptr && i < dv) {
+                    dst += (size_t)i * dk;
+                    if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    if (g * 32 < dk) {
-                        uint32_t v[32];
-                        tmem_ld32_async(lane_base + cDS + 128 * (it % DB) + 32 * g, v);
-                        tmem_wait_ld();
+                        for (int q = 0; q < 16; ++q)
+                            if (q * 8 < dk) st8_wide(dst + q * 8, S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
+                    } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float2 d = make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-                            if constexpr (!kBf) d = __fmul2_rn(wi2, d);
-                            S[16 * g + j] = __ffma2_rn(gam2, S[16 * g + j], d);
-                        }
+                        for (int q = 0; q < 32; ++q)
+                            if (q * 4 < dk)
+                                *reinterpret_cast<float4 *>(dst + q * 4) =
+                                    make_float4(S[2 * q].x, S[2 * q].y, S[2 * q + 1].x, S[2 * q + 1].y);
                     }
                 }
-                kept *= gam;
-                fence_before_sync();
-                arrive(&ds_free[it & 1]);
-                arrive(&g_empty[it % kGates]);
-            }
-            if (!ok) break;
-            float *dst = nullptr;
-            if (MODE == kStateOnly) {
-                dst = p.seg_state + (seg0 + x.g) * mat;
-                if (i == 0) p.seg_decay[seg0 + x.g] = kept;
-            } else if (p.s_final != nullptr && x.g == 0) {
-                // with segments, the row's last state from theirs (this thread
-                // has read its row of the initial state: final may replace it)
-                dst = p.s_final + ((size_t)x.b * Hv + x.h) * mat;
-                if (MODE == kOutputs && i < dv) {
-                    clear();
-                    fold(seg0, p.G);
-                }
-            }
-            if (dst != nullptr && i < dv) {
-#pragma unroll
-                for (int q = 0; q < 32; ++q)
-                    if (q * 4 < dk)
-                        *reinterpret_cast<float4 *>(dst + (size_t)i * dk + q * 4) =
-                            make_float4(S[2 * q].x, S[2 * q].y, S[2 * q + 1].x, S[2 * q + 1].y);
             }
         }
     } else if (warp < 8 || warp >= 20) {
@@ -956,6 +965,28 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     if (warp == 0) tmem_dealloc(tm, kTmemCols);
 }
 
+// Between the two passes: every segment's end state from the ones from zeros, in
+// place, E_g <- decay_g E_{g-1} + E_g, and the row's last one to final (unless that
+// is the initial state, which the second pass still reads).  Four columns a thread.
+__global__ void __launch_bounds__(256) fold_kernel(const LinearParams p, float *final) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const size_t mat = (size_t)p.dv * p.dk, per = mat / 4;
+    const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x;
+    const size_t bh = e / per, at = (e - bh * per) * 4;
+    if (bh >= (size_t)p.B * p.Hv) return;
+    float *m = p.seg_state + bh * p.G * mat + at;
+    float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int g = 0; g < p.G_run; ++g) {
+        const float d = p.seg_decay[bh * p.G + g];
+        const float4 x = *reinterpret_cast<const float4 *>(m + g * mat);
+        run = g == 0 ? x : make_float4(fmaf(d, run.x, x.x), fmaf(d, run.y, x.y), fmaf(d, run.z, x.z), fmaf(d, run.w, x.w));
+        *reinterpret_cast<float4 *>(m + g * mat) = run;
+    }
+    if (final != nullptr) *reinterpret_cast<float4 *>(final + bh * mat + at) = run;
+}
+
 // Segments a row: 1 as soon as the rows and heads alone give every SM a unit;
 // else as many as fit one wave, with two chunks each at least.
 int segments(int B, int T, int Hv, bool varlen) {
@@ -968,6 +999,24 @@ int segments(int B, int T, int Hv, bool varlen) {
     return g < 2 ? 1 : (int)g;
 }
 
+// A launch that may start while the one before it in the stream still runs.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), unsigned grid, int threads, uint32_t smem, cudaStream_t stream, bool early,
+                         const A &...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <typename E, int MODE>
 cudaError_t launch_mode(LinearParams p, int g_run, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                         const CUtensorMap &mo, cudaStream_t stream) {
@@ -978,8 +1027,10 @@ cudaError_t launch_mode(LinearParams p, int g_run, const CUtensorMap &mq, const 
     p.n_units = (unsigned)units;
     cudaError_t e = set_smem_once<linear_kernel<E, MODE>>((int)kSmem);
     if (e != cudaSuccess) return e;
-    linear_kernel<E, MODE><<<(unsigned)(units < sms ? units : sms), kThreads, kSmem, stream>>>(p, mq, mk, mv, mo);
-    return cudaGetLastError();
+    // the second pass starts as SMs come free, and waits for the fold only where it
+    // reads the states
+    return launch_after(linear_kernel<E, MODE>, (unsigned)(units < sms ? units : sms), kThreads, kSmem, stream,
+                        MODE == kOutputs, p, mq, mk, mv, mo);
 }
 
 template <typename E>
@@ -997,7 +1048,14 @@ cudaError_t launch_e(const LinearParams &p, long total_T, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     if (p.G == 1) return launch_mode<E, kWhole>(p, 1, mq, mk, mv, mo, stream);
     // the last segment's end state is only needed for the final state
-    cudaError_t e = launch_mode<E, kStateOnly>(p, p.s_final != nullptr ? p.G : p.G - 1, mq, mk, mv, mo, stream);
+    const int g_run = p.s_final != nullptr ? p.G : p.G - 1;
+    cudaError_t e = launch_mode<E, kStateOnly>(p, g_run, mq, mk, mv, mo, stream);
+    if (e != cudaSuccess) return e;
+    LinearParams f = p;
+    f.G_run = g_run;
+    const size_t threads = (size_t)p.B * p.Hv * p.dv * p.dk / 4;
+    e = launch_after(fold_kernel, (unsigned)((threads + 255) / 256), 256, 0, stream, true, f,
+                     p.s_final != p.s0 ? p.s_final : nullptr);
     if (e != cudaSuccess) return e;
     return launch_mode<E, kOutputs>(p, p.G, mq, mk, mv, mo, stream);
 }

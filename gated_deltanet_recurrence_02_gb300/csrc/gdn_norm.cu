@@ -447,17 +447,6 @@ __global__ void __launch_bounds__(THREADS, VEC * ITEMS <= 8 ? 1024 / THREADS : 1
     }
 }
 
-// fp32 vectors of eight elements: one 32-byte store where the row allows it (two
-// 16-byte ones of neighbouring threads would each touch every sector).
-__device__ __forceinline__ void store8(float *p, const float (&x)[8], bool wide) {
-    if (wide)
-        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
-                     "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
-                     : "memory");
-    else
-        store_vec<float, 8>(p, x);
-}
-
 // residual_norm of rows longer than a warp's 128 vectors: a CTA a row, its next rows
 // on their way to shared memory by bulk copies, `stages` deep.  A bulk copy costs
 // one thread a few instructions a row, where per-thread copies cost every thread
@@ -554,8 +543,15 @@ residual_row_kernel(const ResidualNormParams p, int stages) {
             }
             if (p.x_out != nullptr) {
                 TR *dst = reinterpret_cast<TR *>(p.x_out) + n * D + i;
-                if constexpr (sizeof(TR) * VEC == 32) store8(dst, a[k], wide);
-                else store_vec<TR, VEC>(dst, a[k]);
+                if constexpr (sizeof(TR) * VEC == 32) {
+                    if (wide)
+                        st8_wide(dst, make_float2(a[k][0], a[k][1]), make_float2(a[k][2], a[k][3]),
+                                 make_float2(a[k][4], a[k][5]), make_float2(a[k][6], a[k][7]));
+                    else
+                        store_vec<TR, VEC>(dst, a[k]);
+                } else {
+                    store_vec<TR, VEC>(dst, a[k]);
+                }
             }
         }
         if (p.out != nullptr) {
