@@ -28,7 +28,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCluster = 8;
 
@@ -101,7 +101,7 @@ __device__ __forceinline__ long long segment_sum(const Row<T> &row, int lo, int 
 }
 
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams p) {
+__global__ void __launch_bounds__(kThreads, 6) accept_kernel(const AcceptParams p) {
     __shared__ long long seg[kWarps];                 // this CTA's segment sums, read by the cluster
     __shared__ long long all[kMaxCluster * kWarps];   // the cluster's, in token order
     __shared__ long long part[kWarps];
@@ -229,10 +229,12 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams p) 
 
 template <typename T>
 cudaError_t launch_t(const AcceptParams &p, cudaStream_t stream) {
-    // CTAs a row: more while the grid leaves multiprocessors without work for
-    // four CTAs and each warp still sums a few hundred tokens
+    // CTAs a row: more while the grid stays below eight a multiprocessor (six run at
+    // once; fewer, larger ones leave some multiprocessors a CTA more than others:
+    // 128 requests of 100003 tokens took 37 us as 512 CTAs of 512 threads) and each
+    // warp still sums a few hundred tokens
     int cs = 1;
-    const long slots = 4l * sm_count_of_current_device();
+    const long slots = 8l * sm_count_of_current_device();
     while (cs < kMaxCluster && (long)p.B * cs * 2 <= slots && p.V / (2 * cs * kWarps) >= 128) cs *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p.B * cs));
