@@ -239,8 +239,8 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     const uint32_t tm = __shfl_sync(0xffffffffu, *slot, 0);
     if constexpr (MODE == kStateOnly) grid_launch_dependents();
     bool ok = true;
-    // Waits run out p.wait_ns after the warp's last chunk came (a limit below a
-    // microsecond at the first check that finds a phase incomplete).
+    // Waits run out p.wait_ns after the warp's last chunk came.  A limit below a
+    // microsecond gives up at the first check that finds a chunk not there.
     auto limit = [&]() { return p.wait_ns < 1000 ? 0ull : globaltimer_ns() + p.wait_ns; };
     uint64_t deadline = limit();
     // A wait of a whole warp: the outcome is the same in every lane, so that
@@ -253,6 +253,9 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     // The chunk's decay sums are there; its tokens n, or 0 past the last one (and -1
     // where the wait ran out).
     auto chunk = [&](int it) {
+        if (p.wait_ns < 1000 &&
+            !__all_sync(0xffffffffu, mbar_test_wait(&g_full[it % kGates], (uint32_t)(it / kGates) & 1u)))
+            return -1;
         if (!wait(&g_full[it % kGates], it / kGates)) return -1;
         deadline = limit();
         return reinterpret_cast<const int *>(gate_of(it))[gN];

@@ -115,7 +115,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
     }
 }
 // The same until a time of the global timer, for kernels with many waits in
-// their instruction cache (0: gives up at the first incomplete check).
+// their instruction cache: one instruction where the phase is complete.
 __device__ __forceinline__ bool mbar_wait_until(uint64_t *bar, uint32_t parity, uint64_t deadline_ns) {
 #pragma unroll 1
     do {

@@ -137,3 +137,20 @@ def test_frequencies_are_the_targets():
     f = torch.bincount(t[:, 0].long(), minlength=V).double() / B
     # five standard deviations of a frequency
     assert bool(((f - p1.double()).abs() < 5 * torch.sqrt(p1.double() * (1 - p1.double()) / B)).all()), f
+
+
+def test_padded_vocabulary_and_offsets_past_32_bits():
+    """Rows of a wider buffer; and probabilities of more than 2^31 elements."""
+    p, q, x, u = inputs(5, 3, 900, seed=8)
+    wide_p, wide_q = torch.full((5, 4, 1024), 9.0, device="cuda"), torch.full((5, 3, 1024), 9.0, device="cuda")
+    wide_p[..., :900], wide_q[..., :900] = p, q
+    t, n = gdn.gdn_accept_drafts(p, q, x, u)
+    t2, n2 = gdn.gdn_accept_drafts(wide_p[..., :900], wide_q[..., :900], x, u)
+    assert torch.equal(t, t2) and torch.equal(n, n2)
+    B, V = 600, 1 << 20
+    big = torch.zeros(B, 4, V, device="cuda")          # 2.5e9 elements
+    at = torch.randint(0, V, (B, 4), device="cuda")
+    big.scatter_(2, at[..., None], 1.0)
+    drafts = at[:, :3].to(torch.int32)
+    t, n = gdn.gdn_accept_drafts(big, None, drafts.contiguous(), torch.full((B, 4), 0.5, device="cuda"))
+    assert (n == 4).all() and torch.equal(t.long(), at)

@@ -230,3 +230,53 @@ def test_prefill_equals_recurrent_continued():
     for o, s in ((torch.cat([a, b]), Sb), (c, Sc)):
         assert float((o - whole).norm() / whole.norm()) < 1e-5
         assert float((s - S).norm() / S.norm()) < 1e-5
+
+
+def test_segmented_prefill_in_a_graph_and_in_place():
+    """A row long enough for both passes, captured; the last state in the place of the initial one."""
+    x = make_inputs(19, lengths=[1500], Hk=1, Hv=2, dk=128, dv=128, dtype_qkv="bf16", dtype_gate="f32")
+    g = [t.cuda() for t in (x.q, x.k, x.v, x.alpha)]
+    S0 = x.initial_state.cuda()
+    assert gdn.gdn_linear_prefill_workspace_size(1, 1500, 1, 2, 128, 128, torch.bfloat16) > 0
+    out, last = gdn.gdn_linear_prefill(*g, B=1, T=1500, initial_state=S0)
+    S = S0.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o2, _ = gdn.gdn_linear_prefill(*g, B=1, T=1500, initial_state=S, final_state=S)
+    for _ in range(2):
+        S.copy_(S0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o2, out) and torch.equal(S, last)
+
+
+@pytest.mark.parametrize("offset", [4, 8])
+def test_states_on_16_byte_boundaries(offset):
+    """States that start on 16 but not on 32 bytes."""
+    x = make_inputs(20, lengths=[130], Hk=1, Hv=2, dk=64, dv=128, dtype_qkv="bf16", dtype_gate="f32")
+    g = [t.cuda() for t in (x.q, x.k, x.v, x.alpha)]
+    S0 = x.initial_state.cuda()
+    buf = torch.zeros(2, S0.numel() + 16, device="cuda")
+    a, b = (t[offset:offset + S0.numel()].view(S0.shape) for t in (buf[0], buf[1]))
+    a.copy_(S0)
+    o1, s1 = gdn.gdn_linear_prefill(*g, B=1, T=130, initial_state=S0)
+    o2, s2 = gdn.gdn_linear_prefill(*g, B=1, T=130, initial_state=a, final_state=b)
+    assert torch.equal(o1, o2) and torch.equal(s1, s2)
+
+
+@pytest.mark.parametrize("rows", [[90] * 3, [900]])
+def test_wait_that_runs_out_is_reported(rows):
+    """With a limit that gives up at the first incomplete check the call ends with the
+    timeout bit, and the next call, with the limit restored, is right."""
+    x = make_inputs(21, lengths=rows, Hk=1, Hv=2, dk=128, dv=128, dtype_qkv="bf16", dtype_gate="f32")
+    gdn.gdn_set_wait_limit_ns(1)
+    try:
+        call(x, x.alpha, gdn.gdn_linear_prefill, state=x.initial_state)
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.gdn_device_errors()
+        assert e.value.status == 6
+    finally:
+        gdn.gdn_set_wait_limit_ns(0)
+    out, last, _ = call(x, x.alpha, gdn.gdn_linear_prefill, state=x.initial_state)
+    check(x, x.alpha, out, last, "bf16", state=x.initial_state)
+    assert gdn.gdn_device_errors() == 0

@@ -118,3 +118,33 @@ def test_residual_without_residual_offset_and_slices():
     near(a, want)
     near(h, rms(want, 1e-6) * (1 + w.double()))
     assert gdn.gdn_residual_norm(y[:0], None)[1].shape == (0, 256)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements in one call, the last rows checked."""
+    N, H, d = 140000, 128, 128
+    x = torch.empty(N, H, d, device="cuda", dtype=torch.bfloat16).fill_(2.0)
+    x[-1] = torch.randn(H, d, device="cuda")
+    y = gdn.gdn_gated_norm(x, x, None)
+    xd = x[-1].double()
+    near(y[-1], rms(xd, 1e-6) * xd * torch.sigmoid(xd))
+    assert torch.allclose(y[:3].float(), torch.full((3, H, d), 1.7616, device="cuda"), atol=0.01)
+    del y
+    a, h = gdn.gdn_residual_norm(x.view(N, H * d), None)
+    near(h[-1:], rms(x[-1].double().view(1, -1), 1e-6))
+    assert torch.equal(a[-1], x[-1].view(-1))
+
+
+def test_row_copies_that_run_out_are_reported():
+    y = torch.randn(400, 4096, device="cuda").bfloat16()
+    gdn.gdn_set_wait_limit_ns(1)
+    try:
+        gdn.gdn_residual_norm(y, y)
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.gdn_device_errors()
+        assert e.value.status == 6
+    finally:
+        gdn.gdn_set_wait_limit_ns(0)
+    _, h = gdn.gdn_residual_norm(y, None)
+    near(h, rms(y.double(), 1e-6))
+    assert gdn.gdn_device_errors() == 0
