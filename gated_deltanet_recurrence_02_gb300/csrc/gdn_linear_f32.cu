@@ -2,18 +2,21 @@
 // for fp32 inputs: S <- alpha S + v k^T, o = S (scale q), token by token on the
 // CUDA cores, so every product and sum is fp32 and no decay is ever divided out.
 //
-// One CTA (128 threads) holds 32 rows (value features) of one (row, value head)
-// state in registers: each lane dk/8 columns of two rows as fp32 pairs.  Tokens
+// One CTA (128 threads) holds 16 R rows (value features) of one (row, value head)
+// state in registers: each lane dk/8 columns of R rows as fp32 pairs.  Tokens
 // come to shared memory kTokens at a time by cp.async, two blocks ahead; a block
 // is then worked through without a barrier.  The readout's sums over the eight
-// lanes of a row are taken for four tokens at once (a reduce-scatter of eight
-// values costs 7 shuffles, eight separate butterflies 24).
+// lanes of a row are taken for four tokens at once (a reduce-scatter of 4 R = 16
+// values costs 14 shuffles, sixteen separate butterflies 48).
 //
-// Bound by fp32 arithmetic: 2 dk dv multiply-adds a token and head against the
-// 4 (2 dk + 2 dv) bytes that they need, so the CUDA cores take about four times
-// what HBM does.  The tensor cores take fp32 products only as three tf32 ones,
-// and the chunked form they would need adds the scores; at dk = dv = 128 that
-// is no gain over this.
+// Bound by fp32 arithmetic: 3 dk dv multiplications and fused multiply-adds a token and
+// head (the decayed state, the update, the readout), 172 us for 4100 tokens of 32 heads
+// with dk = dv = 128 on all SMs and two thirds of that again for the segments' first
+// pass, against 30 us of HBM time.  Measured there: 435 us (four state rows a lane;
+// 554 us with two, which loads k and q twice as often from shared memory).  The chunked
+// form on the tensor cores would need each operand as sums of tf32 numbers and three
+// products for each (about 40 us of tensor time at that size): not built; 16-bit inputs
+// are the ones that prompts come in.
 //
 // Few rows are cut into segments, as on the tensor-core path: a first pass forms
 // each segment's end state from zeros (the first one from the initial state), the
@@ -24,7 +27,6 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRows = 32;    // state rows a CTA
 constexpr int kTokens = 16;  // a block
 constexpr int kBlocks = 3;   // blocks in shared memory
 
@@ -33,9 +35,9 @@ struct F32Params : PrefillParams {
     float *seg_state, *seg_decay;
 };
 
-template <int DK>
+template <int DK, int R>
 struct Block {
-    float k[kTokens][DK], q[kTokens][DK], v[kTokens][kRows], alpha[kTokens];
+    float k[kTokens][DK], q[kTokens][DK], v[kTokens][16 * R], alpha[kTokens];
 };
 
 __device__ __forceinline__ void copy16(void *dst, const void *src) {
@@ -44,11 +46,13 @@ __device__ __forceinline__ void copy16(void *dst, const void *src) {
                  : "memory");
 }
 
-template <int DK, bool kStateOnly>
+// R: rows a lane; a CTA holds 16 R.
+template <int DK, int R, bool kStateOnly>
 __global__ void __launch_bounds__(kThreads) linear_f32_kernel(const F32Params p) {
     constexpr int F2 = DK / 16;  // pairs of a lane's columns of one row
+    constexpr int kRows = 16 * R;
     extern __shared__ float4 smem4[];
-    Block<DK> *blocks = reinterpret_cast<Block<DK> *>(smem4);
+    Block<DK, R> *blocks = reinterpret_cast<Block<DK, R> *>(smem4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = lane >> 3, l8 = lane & 7;
     const int Hv = p.Hv, Hk = p.Hk, dv = p.dv;
     const int tiles = dv / kRows;
@@ -65,35 +69,33 @@ __global__ void __launch_bounds__(kThreads) linear_f32_kernel(const F32Params p)
     const int per = ((len + p.G - 1) / p.G + kTokens - 1) / kTokens * kTokens;
     const int t_lo = min((int)min((long)g * per, (long)len), len), t_hi = min(t_lo + per, len);
 
-    // the lane's two rows (of the state and of v) and columns 4 (f 8 + l8) + ..
-    int row[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) row[r] = warp * 8 + r * 4 + grp;
-    float2 S[2][F2];
+    // the lane's R rows (of the state and of v) from row0 on, and columns 4 (f 8 + l8) + ..
+    const int row0 = (warp * 4 + grp) * R;
+    float2 S[R][F2];
     const size_t mat = (size_t)dv * DK, seg0 = ((size_t)b * Hv + h) * p.G;
     auto add_rows = [&](const float *m, float keep) {  // S <- keep S + the matrix's rows
         const float2 k2 = make_float2(keep, keep);
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int f = 0; f < F2 / 2; ++f) {
                 const float4 x =
-                    *reinterpret_cast<const float4 *>(m + (size_t)(tile * kRows + row[r]) * DK + (f * 8 + l8) * 4);
+                    *reinterpret_cast<const float4 *>(m + (size_t)(tile * kRows + row0 + r) * DK + (f * 8 + l8) * 4);
                 S[r][2 * f] = __ffma2_rn(k2, S[r][2 * f], make_float2(x.x, x.y));
                 S[r][2 * f + 1] = __ffma2_rn(k2, S[r][2 * f + 1], make_float2(x.z, x.w));
             }
     };
     auto store_rows = [&](float *m) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int f = 0; f < F2 / 2; ++f)
-                __stcs(reinterpret_cast<float4 *>(m + (size_t)(tile * kRows + row[r]) * DK + (f * 8 + l8) * 4),
+                __stcs(reinterpret_cast<float4 *>(m + (size_t)(tile * kRows + row0 + r) * DK + (f * 8 + l8) * 4),
                        make_float4(S[r][2 * f].x, S[r][2 * f].y, S[r][2 * f + 1].x, S[r][2 * f + 1].y));
     };
     auto clear = [&]() {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int f = 0; f < F2; ++f) S[r][f] = make_float2(0.f, 0.f);
     };
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) linear_f32_kernel(const F32Params p)
             a_next = conv_alpha(ld_gate(p.alpha, (p.conv & GDN_ALPHA_PER_HEAD) ? h : (tok0 + t) * Hv + h, p.dt_gate), p.conv);
     };
     auto fetch = [&](int blk) {
-        Block<DK> &x = blocks[blk % kBlocks];
+        Block<DK, R> &x = blocks[blk % kBlocks];
         const int t = t_lo + blk * kTokens, n = min(kTokens, t_hi - t);
         for (int i = tid; i < n * (DK / 4); i += kThreads) {
             const int tt = i / (DK / 4), c = i % (DK / 4) * 4;
@@ -147,10 +149,10 @@ __global__ void __launch_bounds__(kThreads) linear_f32_kernel(const F32Params p)
         if (blk + 2 < n_blocks) fetch(blk + 2);
         asm volatile("cp.async.commit_group;" ::: "memory");
         if (blk + 3 < n_blocks) fetch_alpha(blk + 3);
-        const Block<DK> &x = blocks[blk % kBlocks];
+        const Block<DK, R> &x = blocks[blk % kBlocks];
         const int t = t_lo + blk * kTokens, n = min(kTokens, t_hi - t);
         for (int i0 = 0; i0 < n; i0 += 4) {
-            float part[8];  // [row][token] of this lane's columns
+            float part[4 * R];  // [row][token] of this lane's columns
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int i = i0 + j;
@@ -158,19 +160,20 @@ __global__ void __launch_bounds__(kThreads) linear_f32_kernel(const F32Params p)
                     const float a = x.alpha[i];
                     const float2 a2 = make_float2(a, a);
                     if constexpr (kStateOnly) kept *= a;
-                    float2 v2[2], acc[2];
+                    float2 v2[R], acc[R];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float v = x.v[i][row[r]];
-                        v2[r] = make_float2(v, v);
-                        acc[r] = make_float2(0.f, 0.f);
+                    for (int r = 0; r < R; r += 2) {
+                        const float2 v = *reinterpret_cast<const float2 *>(&x.v[i][row0 + r]);
+                        v2[r] = make_float2(v.x, v.x);
+                        v2[r + 1] = make_float2(v.y, v.y);
+                        acc[r] = acc[r + 1] = make_float2(0.f, 0.f);
                     }
 #pragma unroll
                     for (int f = 0; f < F2 / 2; ++f) {
                         const float4 k4 = *reinterpret_cast<const float4 *>(&x.k[i][(f * 8 + l8) * 4]);
                         const float2 k2[2] = {make_float2(k4.x, k4.y), make_float2(k4.z, k4.w)};
 #pragma unroll
-                        for (int r = 0; r < 2; ++r)
+                        for (int r = 0; r < R; ++r)
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
                                 S[r][2 * f + e] = __ffma2_rn(a2, S[r][2 * f + e], __fmul2_rn(v2[r], k2[e]));
@@ -178,31 +181,35 @@ __global__ void __launch_bounds__(kThreads) linear_f32_kernel(const F32Params p)
                             const float4 q4 = *reinterpret_cast<const float4 *>(&x.q[i][(f * 8 + l8) * 4]);
                             const float2 q2[2] = {make_float2(q4.x, q4.y), make_float2(q4.z, q4.w)};
 #pragma unroll
-                            for (int r = 0; r < 2; ++r)
+                            for (int r = 0; r < R; ++r)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) acc[r] = __ffma2_rn(S[r][2 * f + e], q2[e], acc[r]);
                         }
                     }
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) part[r * 4 + j] = acc[r].x + acc[r].y;
+                    for (int r = 0; r < R; ++r) part[r * 4 + j] = acc[r].x + acc[r].y;
                 } else {
-                    part[j] = part[4 + j] = 0.f;
+                    #pragma unroll
+                    for (int r = 0; r < R; ++r) part[r * 4 + j] = 0.f;
                 }
             }
             if constexpr (!kStateOnly) {
-                // reduce-scatter over the row's eight lanes: lane l8 ends with the sum of
-                // value l8 = [row l8 / 4][token l8 % 4]
+                // reduce-scatter over the rows' eight lanes: lane l8 ends with the sums of
+                // the values [row][token] from l8 R / 2 on
 #pragma unroll
-                for (int o = 4; o > 0; o >>= 1) {
+                for (int o = 4, m = 2 * R; o > 0; o >>= 1, m >>= 1) {
                     const bool up = (l8 & o) != 0;
 #pragma unroll
-                    for (int e = 0; e < o; ++e) {
-                        const float give = up ? part[e] : part[e + o], keep = up ? part[e + o] : part[e];
+                    for (int e = 0; e < m; ++e) {
+                        const float give = up ? part[e] : part[e + m], keep = up ? part[e + m] : part[e];
                         part[e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
                     }
                 }
-                const int i = i0 + (l8 & 3);
-                if (i < n) ob[(long)(t + i) * v_step + (l8 < 4 ? row[0] : row[1])] = p.scale * part[0];
+#pragma unroll
+                for (int e = 0; e < R / 2; ++e) {
+                    const int at = l8 * (R / 2) + e, i = i0 + (at & 3);
+                    if (i < n) ob[(long)(t + i) * v_step + row0 + (at >> 2)] = p.scale * part[e];
+                }
             }
         }
     }
@@ -218,36 +225,41 @@ __global__ void __launch_bounds__(kThreads) linear_f32_kernel(const F32Params p)
     }
 }
 
-// Segments a row: 1 once the rows, heads and tiles alone fill two CTAs on every SM
-// (the first pass costs a third of the work again); else as many as fill four, of
-// 64 tokens at least.
+// Rows a lane: four where a CTA's 64 divide dv (half the key and query loads from
+// shared memory, which bound two rows), else two.
+int rows_of(int dv) { return dv % 64 == 0 ? 64 : 32; }
+
+// Segments a row: as many as fill three CTAs on every SM, of 64 tokens at least, where
+// that makes four or more.  The first pass costs two thirds of the work again, and three
+// CTAs on an SM take 2.2 times as long as one: at dk = dv = 128, 32 heads and 4100 tokens
+// took 832 us as one segment, 535 as 4, 435 as 7; two rows of 2048: 420 us, 498 as 3.
 int segments(int B, int T, int Hv, int dv, bool varlen) {
-    const long slots = 4l * sm_count_of_current_device(), units = (long)B * Hv * (dv / kRows);
-    if (units == 0 || units * 2 > slots) return 1;
+    const long slots = 3l * sm_count_of_current_device(), units = (long)B * Hv * (dv / rows_of(dv));
+    if (units == 0) return 1;
     const long longest = varlen ? (T + B - 1) / B : T;  // packed rows: their mean
     long g = slots / units;
     if (g > longest / 64) g = longest / 64;
-    return g < 2 ? 1 : (int)g;
+    return g < 4 ? 1 : (int)g;
 }
 
-template <int DK>
+template <int DK, int R>
 cudaError_t launch_dk(F32Params p, cudaStream_t stream) {
-    constexpr int bytes = kBlocks * (int)sizeof(Block<DK>);
-    const long units = (long)p.B * p.Hv * (p.dv / kRows);
+    constexpr int bytes = kBlocks * (int)sizeof(Block<DK, R>);
+    const long units = (long)p.B * p.Hv * (p.dv / (16 * R));
     if (units * p.G > 0x7fffffffL) return cudaErrorInvalidValue;
-    cudaError_t e = set_smem_once<linear_f32_kernel<DK, false>>(bytes);
+    cudaError_t e = set_smem_once<linear_f32_kernel<DK, R, false>>(bytes);
     if (e != cudaSuccess) return e;
     if (p.G > 1) {
-        e = set_smem_once<linear_f32_kernel<DK, true>>(bytes);
+        e = set_smem_once<linear_f32_kernel<DK, R, true>>(bytes);
         if (e != cudaSuccess) return e;
         // the last segment's end state is only needed for the final state
         p.G_run = p.s_final != nullptr ? p.G : p.G - 1;
-        linear_f32_kernel<DK, true><<<(unsigned)(units * p.G_run), kThreads, bytes, stream>>>(p);
+        linear_f32_kernel<DK, R, true><<<(unsigned)(units * p.G_run), kThreads, bytes, stream>>>(p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     p.G_run = p.G;
-    linear_f32_kernel<DK, false><<<(unsigned)(units * p.G), kThreads, bytes, stream>>>(p);
+    linear_f32_kernel<DK, R, false><<<(unsigned)(units * p.G), kThreads, bytes, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -266,10 +278,11 @@ cudaError_t launch_linear_f32(const PrefillParams &pp, cudaStream_t stream) {
         p.seg_state = reinterpret_cast<float *>(p.ws);
         p.seg_decay = p.seg_state + (size_t)p.B * p.Hv * p.G * p.dv * p.dk;
     }
+    const bool four = rows_of(p.dv) == 64;
     switch (p.dk) {
-        case 32: return launch_dk<32>(p, stream);
-        case 64: return launch_dk<64>(p, stream);
-        default: return launch_dk<128>(p, stream);
+        case 32: return four ? launch_dk<32, 4>(p, stream) : launch_dk<32, 2>(p, stream);
+        case 64: return four ? launch_dk<64, 4>(p, stream) : launch_dk<64, 2>(p, stream);
+        default: return four ? launch_dk<128, 4>(p, stream) : launch_dk<128, 2>(p, stream);
     }
 }
 
