@@ -14,28 +14,47 @@
 // (TMEM) and the outputs of one value feature belong to one lane; values and
 // outputs are transposed by ldmatrix and stmatrix on their way.
 //
-// Precision.  The state stays in fp32 registers.  W is given to the MMAs as a
-// sum of 16-bit parts: bf16 values split by truncation into three parts hold
-// all 24 bits of w v (two parts, 2^-17, where the state is only read by 16-bit
-// outputs); fp16 ones into two (22 bits).  P and the state's MMA image are
-// rounded to the inputs' type once each, which is the outputs' own rounding
-// again.  With fp16, W and the image are scaled per lane, and P per token, by
-// powers of two, so neither small nor large states leave fp16's range.
+// Precision.  The state stays in fp32 registers; sums of decays are fp32.  Roundings
+// to 16 bits, and why each is enough:
+//   W    is given to the MMAs as a sum of 16-bit parts.  bf16: w v in fp32, cut into
+//        three parts of 8 bits, which is exact: the state is as good as one updated in
+//        fp32.  Where only outputs read the state (the second pass over segments) two
+//        parts, 2^-17, are below the outputs' rounding.  fp16: two parts, 22 bits,
+//        scaled as below.
+//   P, the state's image as an MMA operand: once each to the inputs' type, which is
+//        the outputs' own rounding again.
+// With fp16, W and the image are scaled per lane, and P per token, by powers of two, so
+// neither small nor large states leave fp16's range.
 //
-// What bounds it: each chunk and head moves 64 KB and takes 1408 tensor cycles
-// a SM (256 R, 128 O1, 256 O2, 768 dS) against about 2100 of its share of HBM
-// bandwidth, so the loads bound a full grid as long as the tensor pipe never
-// waits for the threads.  One persistent CTA a SM, warp-specialised, four
-// stages of tiles in flight; every hand-off between the roles is an mbarrier:
+// What bounds it.  A chunk and head of dk = dv = 128 moves 48 KB where two value heads
+// share their keys and queries (2100 cycles of an SM's share of HBM bandwidth), and its
+// products take about 1630 cycles of the tensor pipe (390 R, 195 O1, 260 O2, 780 dS:
+// an M = 128, K = 16 MMA runs for 49 cycles at N = 64 with A in shared memory, 33 with A
+// in TMEM, 65 at N = 128).  Measured: 64 packed rows of 500 to 1500 tokens, 32 heads,
+// bf16: 365-406 us (4.2-4.7 TB/s, 0.62-0.70 of the measured copy bandwidth), 2300-2400
+// cycles a chunk: between the end of one dS and the start of the next stand the state
+// warps' read of it and, with one buffer of W, the store of the next W's first half.
+// One row of 4100 tokens: 57 us, two passes of 25 and 31 us (a chunk takes a CTA some
+// 2400 cycles alone too, and 17 of them one after another are most of a pass).  12 rows
+// of 200 to 1000 tokens, 6 heads, d = 64, fp16: 36 us, the same chain.
+//
+// One persistent CTA a SM, warp-specialised, four stages of tiles in flight; every
+// hand-off between the roles is an mbarrier:
 //   warps 0-3   state: dS -> fp32 registers -> the next chunk's image
 //   warps 4-7, 20-23  W: values (ldmatrix, transposed), scaled and split, -> TMEM
 //   warps 8-11  outputs: O1 + 2^{b} O2, transposed through shared memory (stmatrix), TMA stores
 //   warp 12     tiles (TMA)
 //   warp 13     issues dS
 //   warps 14, 15, 19  P
-//   warp 16     issues R, one chunk ahead, O2 and O1 (two issuing warps: an MMA
-//               costs its issuer some 55 cycles, and half of them run for 32)
-//   warps 17-18 the chunks' decay sums
+//   warp 16     issues R, one chunk ahead, O2 and O1 (two issuing warps: an MMA costs
+//               its issuer some 40 cycles, and half of them run for 33 to 49)
+//   warps 17-18 the chunks' decay sums, up to eight chunks ahead
+// What made the difference, at 64 packed rows: MMAs issued by a whole converged warp
+// with descriptors at constant offsets, TMEM moved in fragment layouts and outputs by
+// TMA, 1345 -> 433 us; code small enough for the instruction cache (each role's loops
+// rolled where they can be), 433 -> 390 us; W formed in registers by two warpgroups and
+// P on three warps, 390 -> 370 us.
+//
 // Few rows are cut into segments of whole chunks, so that every SM has one: a
 // first pass (kStateOnly) forms each segment's end state from zeros, a small kernel
 // joins them along the row, and the second pass takes each segment's start state from
@@ -78,14 +97,13 @@ constexpr uint32_t oP = NS * kStage;
 constexpr uint32_t oOut = oP + 8192;               // [4 warps][64 tokens][32 features] on their way out
 constexpr uint32_t oGate = oOut + 16384;           // kGates slots of kGate bytes, the words below
 constexpr int kGates = 8;
-constexpr uint32_t kGate = 1040;
+constexpr uint32_t kGate = 912;
 constexpr int gSum = 0;                            // [64] b_t (decays of at least 2^-40 each)
 constexpr int gScaled = 64;                        // [64] scale 2^{b_t}
-constexpr int gW = 128;                            // 2^{s_t}: fp32 [64], or for bf16 [32 pairs][two parts]
-constexpr int gW2 = 192;                           // and the third part [32 pairs]
-constexpr int gLeft = 224;                         // [32] 2^{b_31 - b_t}
-constexpr int gLast = 256;                         // 2^{b_63}
-constexpr int gN = 257, gTok = 258, gHead = 259;   // ints: the chunk's tokens (0: no more chunks), first token, head
+constexpr int gW = 128;                            // 2^{s_t}: fp32 [64], or bf16 [32 pairs][two parts]
+constexpr int gLeft = 192;                         // [32] 2^{b_31 - b_t}
+constexpr int gLast = 224;                         // 2^{b_63}
+constexpr int gN = 225, gTok = 226, gHead = 227;   // ints: the chunk's tokens (0: no more chunks), first token, head
 constexpr uint32_t oWExp = oGate + kGates * kGate; // [4][128] int8: the exponent of a lane's scale of W
 constexpr uint32_t oSExp = oWExp + 512;            // [2][128] int8: of a lane's scale of the image
 constexpr uint32_t oPInv = oSExp + 256;           // [2][64]  1 / scale of a row of P
@@ -186,7 +204,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     using H = Half16<E>;
     constexpr bool kBf = H::kBf16;
     constexpr bool kOut = MODE != kStateOnly;
-    constexpr int NT = kBf && MODE != kOutputs ? 4 : 2;  // 16-bit parts of W
+    constexpr int NT = kBf && MODE != kOutputs ? 3 : 2;  // 16-bit parts of W
     // Buffers of W and of dS in TMEM: two where the columns allow it, so that a
     // product need not wait for what reads or replaces the last one's.
     constexpr int WB = MODE == kStateOnly || NT == 2 ? 2 : 1, DB = MODE == kStateOnly ? 2 : 1;
@@ -466,25 +484,34 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
 #pragma unroll
                 for (int jj = 0; jj < 2; ++jj) {
                     const int j = 2 * half + jj;
-                    if constexpr (kBf) {
-                        // packed bf16 arithmetic: with w = w0 + w1 + w2 to 24 bits, a
-                        // product of bf16 numbers is exactly its rounding plus a rest
+                    if constexpr (kBf && NT == 2) {
+                        // packed bf16 arithmetic: with w = w0 + w1 to 16 bits, w0 v is
+                        // exactly its rounding plus a rest
                         uint32_t v[4];
                         values(j, v);
                         const uint2 *w = reinterpret_cast<const uint2 *>(gate_of(it) + gW) + (lane & 3) + 8 * j;
-                        const uint32_t *w2 = reinterpret_cast<const uint32_t *>(gate_of(it) + gW2) + (lane & 3) + 8 * j;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const uint2 ww = w[4 * (e >> 1)];
-                            const uint32_t a = bf2_mul(ww.x, v[e]), r = bf2_rest(ww.x, v[e], a);
+                            const uint32_t a = bf2_mul(ww.x, v[e]);
                             part[0][4 * jj + e] = a;
-                            if constexpr (NT == 2) {
-                                part[1][4 * jj + e] = bf2_fma(ww.y, v[e], r);
-                            } else {
-                                const uint32_t b = bf2_mul(ww.y, v[e]);
-                                part[1][4 * jj + e] = r;
-                                part[2][4 * jj + e] = b;
-                                part[3][4 * jj + e] = bf2_fma(w2[4 * (e >> 1)], v[e], bf2_rest(ww.y, v[e], b));
+                            part[1][4 * jj + e] = bf2_fma(ww.y, v[e], bf2_rest(ww.x, v[e], a));
+                        }
+                    } else if constexpr (kBf) {
+                        // w v in fp32, cut into its bits 0-7, 8-15 and 16-23
+                        float2 x[4];
+                        scaled(j, x);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                            for (int m = 0; m < 3; ++m) {
+                                const uint32_t a = __float_as_uint(x[e].x), b = __float_as_uint(x[e].y);
+                                part[m][4 * jj + e] = __byte_perm(a, b, 0x7632);
+                                if (m < 2)
+                                    x[e] = __ffma2_rn(make_float2(-1.f, -1.f),
+                                                      make_float2(__uint_as_float(a & 0xffff0000u),
+                                                                  __uint_as_float(b & 0xffff0000u)),
+                                                      x[e]);
                             }
                         }
                     } else {
@@ -609,6 +636,14 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             for (; ok && u < p.n_units; u += gridDim.x) {
                 const Unit x = unit_at(p, u);
                 const int hk = x.h / G;
+                // The unit's initial state to L2, up to four chunks before the state warps
+                // read it: 64 packed rows with states 410 -> 392 us.  (Not for units of a
+                // chunk or two, whose tiles it would hold up: 128 rows of 64 tokens 172 us,
+                // 185 with it.)
+                if (x.g == 0 && x.c1 - x.c0 > 2 && u != blockIdx.x) {
+                    const float *s0 = initial_state_ptr(p.s0, p.s0_idx, p.n_s0, x.b, x.h, Hv, dv, dk, p.err);
+                    if (s0 != nullptr && leader) bulk_prefetch_l2(s0, (uint32_t)(dv * dk) * 4);
+                }
 #pragma unroll 1
                 for (int c = x.c0; c < x.c1; ++c, ++it) {
                     const int s = it % NS, t0 = (int)(x.tok0 + (long)c * C);
@@ -941,14 +976,10 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 *reinterpret_cast<float2 *>(gate + gScaled + 2 * lane) =
                     make_float2(p.scale * ex2_approx(ex + a[0]), p.scale * ex2_approx(up));
                 const float2 w2 = make_float2(ex2_approx(suf + a[1]), ex2_approx(suf));
-                if constexpr (kBf) {
+                if constexpr (kBf && NT == 2) {
                     const uint32_t wa = H::pack2(w2.x, w2.y);
-                    float2 r = H::unpack2(wa);
-                    r = make_float2(w2.x - r.x, w2.y - r.y);
-                    const uint32_t wb = H::pack2(r.x, r.y);
-                    const float2 y = H::unpack2(wb);
-                    *reinterpret_cast<uint2 *>(gate + gW + 2 * lane) = make_uint2(wa, wb);
-                    reinterpret_cast<uint32_t *>(gate)[gW2 + lane] = H::pack2(r.x - y.x, r.y - y.y);
+                    const float2 r = H::unpack2(wa);
+                    *reinterpret_cast<uint2 *>(gate + gW + 2 * lane) = make_uint2(wa, H::pack2(w2.x - r.x, w2.y - r.y));
                 } else {
                     *reinterpret_cast<float2 *>(gate + gW + 2 * lane) = w2;
                 }
@@ -990,16 +1021,28 @@ __global__ void __launch_bounds__(256) fold_kernel(const LinearParams p, float *
     if (final != nullptr) *reinterpret_cast<float4 *>(final + bh * mat + at) = run;
 }
 
-// Segments a row: 1 as soon as the rows and heads alone give every SM a unit;
-// else as many as fit one wave, with two chunks each at least.
+// Segments a row.  One pass takes its chunks one after another; two passes over G
+// segments take each chunk of a segment twice (measured: 1.5 times one pass's time), as
+// much as 8 chunks for the second launch, the fold and the states' way between them, and
+// a third of a chunk a segment in the fold.  The least of these, with no more segments
+// than one wave of SMs: 32 heads, 4100 tokens (65 chunks): 93 us as one segment, 84, 67
+// and 61 us as 2, 3 and 4; 8 heads: 91 us, 51 as 4, 39 as 8, 43 as 19; but 64 heads,
+// 2048 tokens: 54 us, 59 as 2, and 32 heads, 512 tokens: 23 us, 28 as 4.
 int segments(int B, int T, int Hv, bool varlen) {
     const long sms = sm_count_of_current_device(), units = (long)B * Hv;
-    if (units == 0 || units * 2 > sms) return 1;
+    if (units == 0) return 1;
     const long longest = varlen ? (T + B - 1) / B : T;  // packed rows: their mean
     const long chunks = (longest + C - 1) / C;
-    long g = sms / units;
-    if (g > chunks / 2) g = chunks / 2;
-    return g < 2 ? 1 : (int)g;
+    long best = 6 * chunks;
+    int G = 1;
+    for (long g = 2; g <= sms / units && g <= chunks; ++g) {
+        const long cost = 9 * ((chunks + g - 1) / g) + 48 + 2 * g;
+        if (cost < best) {
+            best = cost;
+            G = (int)g;
+        }
+    }
+    return G;
 }
 
 // A launch that may start while the one before it in the stream still runs.

@@ -259,20 +259,10 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// The same with A in TMEM: lane = row of A, each 32-bit column two 16-bit
-// elements along K (one K = 16 step is eight columns), K-major.
-__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// The three above by a whole converged warp of which the lane with `leader` set
-// (always the same one) issues.  Operands that are the same in every lane then
-// stay in uniform registers; issued from a branch on the lane, each MMA waits
-// for its descriptors to be moved there (a measured ~140 cycles apiece).
+// The same by a whole converged warp of which the lane with `leader` set (always the
+// same one) issues.  Operands that are the same in every lane then stay in uniform
+// registers; issued from a branch on the lane, each MMA waits for its descriptors to be
+// moved there (a measured ~140 cycles apiece).
 __device__ __forceinline__ void mma_f16_warp(uint32_t leader, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                              uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -281,6 +271,8 @@ __device__ __forceinline__ void mma_f16_warp(uint32_t leader, uint32_t d_tmem, u
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
+// With A in TMEM: lane = row of A, each 32-bit column two 16-bit elements along K (one
+// K = 16 step is eight columns), K-major.
 __device__ __forceinline__ void mma_f16_ta_warp(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                                 uint32_t idesc, uint32_t accumulate) {
     asm volatile(

@@ -321,11 +321,13 @@ GDN_API int gdn_replay_verify(const void *q, const void *k, const void *v,
  * the delta-rule calls; beta does not exist.  Extra convention bit:
  *  GDN_ALPHA_PER_HEAD  in dtype_gate: alpha is [Hv], one decay for each head
  *                      (else [total_T, Hv], one for each token and head).
- * GDN_ALPHA_LOG applies to both forms; no other bit is taken.  alpha = 0 is
- * allowed (the state is dropped).  Inputs that are not finite reach the
- * tokens after them in the same row and, in the chunked form, the up to 127
- * tokens before them that share their chunk; they touch no other row, and
- * values of one head touch no other head.
+ * GDN_ALPHA_LOG applies to both forms; no other bit is taken.  Precondition:
+ * every alpha in [0, 1]; 0 drops the state.  (The recurrent form multiplies by
+ * whatever it is given; the chunked one for 16-bit inputs takes logarithms, so a
+ * negative alpha gives NaN there.)  Inputs that are not finite reach the tokens
+ * after them in the same row and, in the chunked form, the up to 63 tokens
+ * before them that share their chunk; they touch no other row, and values of
+ * one head touch no other head.
  */
 #define GDN_ALPHA_PER_HEAD 0x800
 
