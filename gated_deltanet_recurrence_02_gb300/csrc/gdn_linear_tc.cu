@@ -31,12 +31,16 @@
 // products take about 1630 cycles of the tensor pipe (390 R, 195 O1, 260 O2, 780 dS:
 // an M = 128, K = 16 MMA runs for 49 cycles at N = 64 with A in shared memory, 33 with A
 // in TMEM, 65 at N = 128).  Measured: 64 packed rows of 500 to 1500 tokens, 32 heads,
-// bf16: 365-406 us (4.2-4.7 TB/s, 0.62-0.70 of the measured copy bandwidth), 2300-2400
-// cycles a chunk: between the end of one dS and the start of the next stand the state
-// warps' read of it and, with one buffer of W, the store of the next W's first half.
-// One row of 4100 tokens: 57 us, two passes of 25 and 31 us (a chunk takes a CTA some
-// 2400 cycles alone too, and 17 of them one after another are most of a pass).  12 rows
-// of 200 to 1000 tokens, 6 heads, d = 64, fp16: 36 us, the same chain.
+// bf16: 337 us without initial states, 365 with (5.0 TB/s, 0.75 of the measured copy
+// bandwidth), some 2100 cycles a chunk: between the end of one dS and the start of the
+// next stand the state warps' read of it and, with one buffer of W, the store of the next
+// W's first half, and every role's instructions compete for the issue slots and the
+// instruction cache.  (A ring of W in blocks of 16 tokens, stored while the last product
+// runs, gained nothing; nor did freeing the outputs' columns before their last part.)
+// One row of 4100 tokens: 57 us, two passes of 25 and 31 us (a chunk takes a CTA as long
+// alone, and 17 of them one after another are most of a pass).  12 rows of 200 to 1000
+// tokens, 6 heads, d = 64, fp16: 33 us, the same chain.  128 rows of 16 tokens with their
+// states: 160 us (0.54): a unit's state is read, used and written by the same four warps.
 //
 // One persistent CTA a SM, warp-specialised, four stages of tiles in flight; every
 // hand-off between the roles is an mbarrier:
@@ -53,7 +57,8 @@
 // with descriptors at constant offsets, TMEM moved in fragment layouts and outputs by
 // TMA, 1345 -> 433 us; code small enough for the instruction cache (each role's loops
 // rolled where they can be), 433 -> 390 us; W formed in registers by two warpgroups and
-// P on three warps, 390 -> 370 us.
+// P on three warps, 390 -> 370 us; three parts of W for four, states prefetched, and W's
+// loop rolled, 370 -> 337 us.
 //
 // Few rows are cut into segments of whole chunks, so that every SM has one: a
 // first pass (kStateOnly) forms each segment's end state from zeros, a small kernel
@@ -67,6 +72,7 @@
 //
 // Every wait is bounded; on timeout the CTA raises GDN_DEVERR_TIMEOUT, waits
 // (bounded) for its copies and MMAs in flight, releases its TMEM and exits.
+#include <algorithm>
 #include <cstring>
 
 #include "gdn_internal.cuh"
@@ -126,6 +132,7 @@ enum Mode {
 struct LinearParams : PrefillParams {
     int G;             // segments a row
     int G_run;         // segments of this pass
+    uint32_t limit;    // of waits, ns: wait_ns, 4 s at most
     unsigned n_units;  // B Hv G_run
     float *seg_state;  // [B, Hv, G, dv, dk]
     float *seg_decay;  // [B, Hv, G]
@@ -257,25 +264,22 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     const uint32_t tm = __shfl_sync(0xffffffffu, *slot, 0);
     if constexpr (MODE == kStateOnly) grid_launch_dependents();
     bool ok = true;
-    // Waits run out p.wait_ns after the warp's last chunk came.  A limit below a
-    // microsecond gives up at the first check that finds a chunk not there.
-    auto limit = [&]() { return p.wait_ns < 1000 ? 0ull : globaltimer_ns() + p.wait_ns; };
-    uint64_t deadline = limit();
+    // Waits run out p.limit nanoseconds after the warp's last chunk came.  (The roles'
+    // loops share the instruction cache, and every wait's instructions count there:
+    // 64 packed rows took 400 us with 3 KB more of them, 337 with 4 KB less.)
+    uint32_t since = globaltimer_lo();
     // A wait of a whole warp: the outcome is the same in every lane, so that
     // the warp-wide TMEM accesses behind it stay converged.
     auto wait = [&](uint64_t *bar, int it) {
-        return __all_sync(0xffffffffu, mbar_wait_until(bar, (uint32_t)it & 1u, deadline)) != 0;
+        return __all_sync(0xffffffffu, mbar_wait_since(bar, (uint32_t)it & 1u, since, p.limit)) != 0;
     };
     auto wait2 = [&](uint64_t *bars, int it) { return wait(&bars[it & 1], it >> 1); };
     auto gate_of = [&](int it) { return reinterpret_cast<float *>(sm + oGate + (it % kGates) * kGate); };
     // The chunk's decay sums are there; its tokens n, or 0 past the last one (and -1
     // where the wait ran out).
     auto chunk = [&](int it) {
-        if (p.wait_ns < 1000 &&
-            !__all_sync(0xffffffffu, mbar_test_wait(&g_full[it % kGates], (uint32_t)(it / kGates) & 1u)))
-            return -1;
         if (!wait(&g_full[it % kGates], it / kGates)) return -1;
-        deadline = limit();
+        since = globaltimer_lo();
         return reinterpret_cast<const int *>(gate_of(it))[gN];
     };
     auto tiles = [&](int it) { return wait(&full[it % NS], it / NS); };
@@ -295,6 +299,9 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
         if constexpr (MODE == kOutputs) grid_dependency_wait();  // the fold's states
         int it = 0;
         const size_t mat = (size_t)dv * dk;
+        // (a limit below a microsecond gives up where the first chunk is not there yet;
+        // the other roles then wait for the state in vain)
+        if (p.limit < 1000) ok = __all_sync(0xffffffffu, mbar_test_wait(&g_full[0], 0)) != 0;
 #pragma unroll 1
         for (unsigned u = blockIdx.x; ok && u < p.n_units; u += gridDim.x) {
             const Unit x = unit_at(p, u);
@@ -476,60 +483,56 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     sc[e] = pow2(we[e]);
                 }
             }
-            // Each half of the chunk is formed while the last chunk's product still
-            // reads that half of TMEM.
+            // 16 tokens at a time.  Each half of the chunk is formed while the last
+            // chunk's product still reads that half of TMEM.
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                uint32_t part[NT][8];
+            for (int j = 0; j < 4; ++j) {
+                uint32_t part[NT][4];
+                if constexpr (kBf && NT == 2) {
+                    // packed bf16 arithmetic: with w = w0 + w1 to 16 bits, w0 v is
+                    // exactly its rounding plus a rest
+                    uint32_t v[4];
+                    values(j, v);
+                    const uint2 *w = reinterpret_cast<const uint2 *>(gate_of(it) + gW) + (lane & 3) + 8 * j;
 #pragma unroll
-                for (int jj = 0; jj < 2; ++jj) {
-                    const int j = 2 * half + jj;
-                    if constexpr (kBf && NT == 2) {
-                        // packed bf16 arithmetic: with w = w0 + w1 to 16 bits, w0 v is
-                        // exactly its rounding plus a rest
-                        uint32_t v[4];
-                        values(j, v);
-                        const uint2 *w = reinterpret_cast<const uint2 *>(gate_of(it) + gW) + (lane & 3) + 8 * j;
+                    for (int e = 0; e < 4; ++e) {
+                        const uint2 ww = w[4 * (e >> 1)];
+                        const uint32_t a = bf2_mul(ww.x, v[e]);
+                        part[0][e] = a;
+                        part[1][e] = bf2_fma(ww.y, v[e], bf2_rest(ww.x, v[e], a));
+                    }
+                } else if constexpr (kBf) {
+                    // w v in fp32, cut into its bits 0-7, 8-15 and 16-23
+                    float2 x[4];
+                    scaled(j, x);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint2 ww = w[4 * (e >> 1)];
-                            const uint32_t a = bf2_mul(ww.x, v[e]);
-                            part[0][4 * jj + e] = a;
-                            part[1][4 * jj + e] = bf2_fma(ww.y, v[e], bf2_rest(ww.x, v[e], a));
-                        }
-                    } else if constexpr (kBf) {
-                        // w v in fp32, cut into its bits 0-7, 8-15 and 16-23
-                        float2 x[4];
-                        scaled(j, x);
+                    for (int e = 0; e < 4; ++e) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-#pragma unroll
-                            for (int m = 0; m < 3; ++m) {
-                                const uint32_t a = __float_as_uint(x[e].x), b = __float_as_uint(x[e].y);
-                                part[m][4 * jj + e] = __byte_perm(a, b, 0x7632);
-                                if (m < 2)
-                                    x[e] = __ffma2_rn(make_float2(-1.f, -1.f),
-                                                      make_float2(__uint_as_float(a & 0xffff0000u),
-                                                                  __uint_as_float(b & 0xffff0000u)),
-                                                      x[e]);
-                            }
-                        }
-                    } else {
-                        float2 x[4];
-                        scaled(j, x);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 r = __fmul2_rn(make_float2(sc[e & 1], sc[e & 1]), x[e]);
-                            part[0][4 * jj + e] = H::pack2(r.x, r.y);
-                            const float2 h = H::unpack2(part[0][4 * jj + e]);
-                            part[1][4 * jj + e] = H::pack2(r.x - h.x, r.y - h.y);
+                        for (int m = 0; m < 3; ++m) {
+                            const uint32_t a = __float_as_uint(x[e].x), b = __float_as_uint(x[e].y);
+                            part[m][e] = __byte_perm(a, b, 0x7632);
+                            if (m < 2)
+                                x[e] = __ffma2_rn(make_float2(-1.f, -1.f),
+                                                  make_float2(__uint_as_float(a & 0xffff0000u),
+                                                              __uint_as_float(b & 0xffff0000u)),
+                                                  x[e]);
                         }
                     }
+                } else {
+                    float2 x[4];
+                    scaled(j, x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 r = __fmul2_rn(make_float2(sc[e & 1], sc[e & 1]), x[e]);
+                        part[0][e] = H::pack2(r.x, r.y);
+                        const float2 h = H::unpack2(part[0][e]);
+                        part[1][e] = H::pack2(r.x - h.x, r.y - h.y);
+                    }
                 }
-                if (it >= WB && !(ok = wait2(half == 0 ? ds_half : ds_done, it - WB))) break;
+                if (it >= WB && (j & 1) == 0 && !(ok = wait2(j == 0 ? ds_half : ds_done, it - WB))) break;
                 fence_after_sync();
 #pragma unroll
-                for (int m = 0; m < NT; ++m) tmem_st_16x16(lane_base + cW + 32 * NT * (it % WB) + 32 * m + 16 * half, part[m]);
+                for (int m = 0; m < NT; ++m) tmem_st_16x8(lane_base + cW + 32 * NT * (it % WB) + 32 * m + 8 * j, part[m]);
             }
             if (!ok) break;
             // (four buffers: the state warps read their scale before the product two
@@ -648,7 +651,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 for (int c = x.c0; c < x.c1; ++c, ++it) {
                     const int s = it % NS, t0 = (int)(x.tok0 + (long)c * C);
                     if (it >= NS && !(ok = wait(&empty[s], it / NS - 1))) break;
-                    deadline = limit();
+                    since = globaltimer_lo();
                     uint8_t *st = sm + s * kStage;
                     if (leader) mbar_arrive_expect_tx(&full[s], bytes);
                     __syncwarp();
@@ -939,7 +942,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 if (it < 0) continue;
                 if (n_ == 0 && !end_) break;
                 if (it >= kGates && !(ok = wait(&g_empty[it % kGates], it / kGates - 1))) break;
-                deadline = limit();
+                since = globaltimer_lo();
                 float *gate = gate_of(it);
                 if (lane == 0) {
                     reinterpret_cast<int *>(gate)[gN] = n_;
@@ -959,7 +962,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     held[e] = a[e] < -40.f ? -40.f : a[e];
                 }
                 float up = a[0] + a[1], down = up, hup = held[0] + held[1];
-#pragma unroll
+#pragma unroll 1
                 for (int o = 1; o < 32; o <<= 1) {
                     const float y0 = __shfl_up_sync(0xffffffffu, up, o), y1 = __shfl_down_sync(0xffffffffu, down, o);
                     const float y2 = __shfl_up_sync(0xffffffffu, hup, o);
@@ -1126,6 +1129,7 @@ cudaError_t launch_linear_tc(const PrefillParams &pp, cudaStream_t stream) {
     const bool varlen = p.cu_seqlens != nullptr;
     const long total_T = varlen ? (long)p.T : (long)p.B * p.T;
     p.G = segments(p.B, p.T, p.Hv, varlen);
+    p.limit = (uint32_t)std::min<uint64_t>(p.wait_ns, 4000000000ull);
     if (p.G > 1) {
         p.seg_state = reinterpret_cast<float *>(p.ws);
         p.seg_decay = reinterpret_cast<float *>(static_cast<uint8_t *>(p.ws) + state_bytes(p.B, p.Hv, p.G, p.dk, p.dv));

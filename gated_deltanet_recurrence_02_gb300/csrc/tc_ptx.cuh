@@ -114,13 +114,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
         if (globaltimer_ns() - t0 > limit_ns) return false;
     }
 }
-// The same until a time of the global timer, for kernels with many waits in
-// their instruction cache: one instruction where the phase is complete.
-__device__ __forceinline__ bool mbar_wait_until(uint64_t *bar, uint32_t parity, uint64_t deadline_ns) {
+// The low word of the global timer, for differences of less than 4 s.
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(t));
+    return t;
+}
+// The same for kernels with many waits in their instruction cache: as few
+// instructions as a bounded wait takes.  Gives up limit_ns after t0.
+__device__ __forceinline__ bool mbar_wait_since(uint64_t *bar, uint32_t parity, uint32_t t0, uint32_t limit_ns) {
 #pragma unroll 1
     do {
         if (mbar_try_wait(bar, parity)) return true;
-    } while (globaltimer_ns() < deadline_ns);
+    } while (globaltimer_lo() - t0 <= limit_ns);
     return false;
 }
 
@@ -372,12 +378,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
-// 16 lanes x 16 columns in the layout of the warp-level MMA's fragments (g =
+// 16 lanes x 8 columns in the layout of the warp-level MMA's fragments (g =
 // lane / 4, t = lane % 4): v[2 r] = (lane g, column 4 r + t), v[2 r + 1] =
-// (lane g + 8, column 4 r + t), r < 4.
-__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t (&v)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+// (lane g + 8, column 4 r + t), r < 2.
+__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3])
                  : "memory");
 }
 // 16 lanes x 32 columns of 32 bits as accumulator fragments: v[4 r], v[4 r + 1]
