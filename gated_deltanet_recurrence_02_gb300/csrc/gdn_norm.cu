@@ -8,11 +8,21 @@
 //     x' = x + s act(g) u
 //     h  = x' / sqrt(mean x'^2 + eps) * w_pre
 //
-// Both are bound by HBM: every input element is read once, kept in registers
-// in fp32 across the reductions, and every output element written once.  A
-// row is spread over a group of threads (part of a warp, or a whole CTA), each
-// holding ITEMS 16-byte vectors of it.  Sums of squares are fp32; h is formed
-// from the unrounded x'.
+// Both are bound by HBM where rows are vectors: every input element is read once, kept
+// in registers in fp32 across the reductions, and every output element written once.  A
+// row is spread over a group of threads (part of a warp, or a whole CTA), each holding
+// ITEMS 16-byte vectors of it.  Sums of squares are fp32; h is formed from the unrounded
+// x'; each output is rounded once.  What a single wave of CTAs over the rows leaves on
+// the table is its start and end; bf16 elements also cost their conversions and the
+// gate's exponential (one pass of loads, all of them in flight, then 12 to 20
+// instructions an element).  Measured:
+//   gated, 4100 x 32 x 128 bf16   22.5 us (4.5 TB/s, 0.66 of the measured copy bandwidth);
+//     fp32 36 us (5.6 TB/s); 26.5 with the next row in registers instead of the ring below
+//   residual, 4100 x 4096 bf16, fp32 residual, gate, both norms   44 us (5.3 TB/s, 0.78);
+//     52 with the ring of per-thread copies that shorter rows use; 2050 x 8192: 48 us (72)
+// Rows that are not aligned to 16 bytes (odd widths, odd strides) are read and written an
+// element a lane, at 8 to 9 cycles an access whatever its width: 4100 x 2047 bf16 41 us
+// (floor 12), 2000 x 32 x 129 25 us (7).
 #include <atomic>
 
 #include "gdn_internal.cuh"
@@ -186,8 +196,14 @@ struct Ring {
     __device__ __forceinline__ static int next(int slot) { return slot + 1 == DEPTH ? 0 : slot + 1; }
 };
 
+// CTAs an SM at least, which is a limit of registers: 64 a thread, and more where a row
+// takes them (4100 x 4095 bf16, eight elements a thread: 90 us with 64 and spills, 70).
+constexpr int ctas_of(int vec, int items, int threads) {
+    return vec * items > 8 ? 1 : (vec == 1 && items > 5 ? 768 : 1024) / threads;
+}
+
 template <typename T, int VEC, int ITEMS, int THREADS>
-__global__ void __launch_bounds__(THREADS, VEC * ITEMS <= 8 ? 1024 / THREADS : 1) gated_norm_kernel(const GatedNormParams p, int lanes) {
+__global__ void __launch_bounds__(THREADS, ctas_of(VEC, ITEMS, THREADS)) gated_norm_kernel(const GatedNormParams p, int lanes) {
     __shared__ float red[2][32];
     extern __shared__ uint4 ring_smem[];
     using R = Ring<2 * ITEMS, THREADS>;
@@ -310,7 +326,7 @@ struct Weights {
 };
 
 template <typename T, typename TR, int VEC, int ITEMS, int THREADS>
-__global__ void __launch_bounds__(THREADS, VEC * ITEMS <= 8 ? 1024 / THREADS : 1) residual_norm_kernel(const ResidualNormParams p, int lanes) {
+__global__ void __launch_bounds__(THREADS, ctas_of(VEC, ITEMS, THREADS)) residual_norm_kernel(const ResidualNormParams p, int lanes) {
     __shared__ float red[2][32];
     extern __shared__ uint4 ring_smem[];
     constexpr int XP = Raw<TR, VEC>::kPacks, NP = 2 + XP;
@@ -579,25 +595,22 @@ residual_row_kernel(const ResidualNormParams p, int stages) {
 
 // How a row of `width` elements is spread over threads of ITEMS vectors each.
 // Rows of up to 32 vectors take the smallest power of two of lanes of one vector
-// each, so several rows share a warp; up to 128 (single elements: 256) a warp;
-// longer ones a whole CTA.
+// each, so several rows share a warp; up to 128 (single elements: 512, where a CTA's
+// two barriers a row made 4100 x 4 rows of 257 take 43 us, now 25) a warp; longer
+// ones a whole CTA.
 struct Spread {
     int lanes, threads, items;
 };
 Spread spread(int width, int vec) {
     const int nv = (width + vec - 1) / vec;
-    if (nv <= (vec > 1 ? 128 : 256)) {
+    if (nv <= (vec > 1 ? 128 : 512)) {
         int lanes = 1;
         while (lanes < 32 && lanes < nv) lanes *= 2;
-        int items = 1;
-        while (lanes * items < nv) items *= 2;
-        return {lanes, 256, items};
+        return {lanes, 256, (nv + lanes - 1) / lanes};
     }
-    if (nv <= 256) return {256, 256, 1};
-    int items = 1;
-    while (512 * items < nv && items < 16) items *= 2;
-    const int threads = 512 * items < nv ? 1024 : 512;
-    return {threads, threads, items};
+    if (vec > 1 && nv <= 256) return {256, 256, 1};
+    const int threads = nv > 16 * 512 ? 1024 : 512;
+    return {threads, threads, (nv + threads - 1) / threads};
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -632,26 +645,25 @@ template <int I, int TH>
 struct Shape {
     static constexpr int items = I, threads = TH;
 };
-// Calls f with the spread's items and threads as constants.  A row of vectors has
-// at most 32 elements a thread, so never more than `most` vectors.
+// Calls f with the spread's threads and the least items of those built that hold its
+// row as constants.  A row of vectors has at most 32 elements a thread, so never more
+// than MOST vectors, in powers of two; single elements come in finer steps, as their
+// loads and stores are what such rows cost (2000 x 32 x 129 bf16: 25 us as five a lane,
+// 35 as eight).
+template <int MOST, int THREADS, int I, typename F>
+cudaError_t with_items(int items, F f) {
+    constexpr int next = MOST > 8 && (I == 2 || I == 4) ? I + 1 : I == 3 ? 4 : I == 5 ? 6 : I == 6 ? 8 : MOST > 8 && I == 8 ? 12 : I == 12 ? 16 : 2 * I;
+    if constexpr (next <= MOST && (THREADS == 512 || MOST > 8 || next <= 4)) {
+        if (items > I) return with_items<MOST, THREADS, next>(items, f);
+    }
+    return f(Shape<I, THREADS>{});
+}
 template <int MOST, typename F>
 cudaError_t with_shape(const Spread &s, F f) {
-    if (s.threads == 256) {
-        if (s.items == 1) return f(Shape<1, 256>{});
-        if (s.items == 2) return f(Shape<2, 256>{});
-        if constexpr (MOST > 8)
-            if (s.items == 8) return f(Shape<8, 256>{});
-        return f(Shape<4, 256>{});
-    }
+    if (s.threads == 256) return with_items<MOST, 256, 1>(s.items, f);
     if constexpr (MOST > 8)
         if (s.threads == 1024) return f(Shape<16, 1024>{});
-    if (s.items == 1) return f(Shape<1, 512>{});
-    if (s.items == 2) return f(Shape<2, 512>{});
-    if constexpr (MOST > 4)
-        if (s.items == 8) return f(Shape<8, 512>{});
-    if constexpr (MOST > 8)
-        if (s.items == 16) return f(Shape<16, 512>{});
-    return f(Shape<4, 512>{});
+    return with_items<MOST, 512, 1>(s.items, f);
 }
 
 template <typename T>
