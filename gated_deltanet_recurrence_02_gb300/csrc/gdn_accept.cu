@@ -13,12 +13,15 @@
 // random number of its own: given a rejection, the tests' ones are no longer
 // uniform.
 //
-// Of B (2K + 1) rows of V probabilities only two rows a request are read, by
-// a cluster of CTAs: each warp sums a contiguous segment, the warps' sums are
-// shared through distributed shared memory, and the CTA that owns the segment
-// with the goal scans it again (from L2) for the token.  Bound by HBM for many
-// requests and by the chain of dependent reads (drafts, their probabilities,
-// the rows, the segment) for few.
+// Of B (2K + 1) rows of V probabilities only two rows a request are read, by a cluster
+// of CTAs: each warp sums a contiguous segment, the warps' sums are shared through
+// distributed shared memory, and the CTA that owns the segment with the goal scans it
+// again (from L2) for the token.  For many requests bound by HBM and by what surrounds
+// the one read of the rows, a chain of dependent accesses: the drafts, their
+// probabilities, the rows, the cluster's sums, the segment.  128 requests of 100003 fp32
+// probabilities, 4 drafts: 33 us (15 us of HBM time; 47 us with element loads and
+// conversions to 64-bit integers, 38 with CTAs of 512 threads); 1 request of 32000 bf16
+// ones without draft probabilities: 6 us, the chain.
 #include <cooperative_groups.h>
 
 #include "gdn_internal.cuh"

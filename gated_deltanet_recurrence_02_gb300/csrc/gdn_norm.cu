@@ -13,16 +13,17 @@
 // row is spread over a group of threads (part of a warp, or a whole CTA), each holding
 // ITEMS 16-byte vectors of it.  Sums of squares are fp32; h is formed from the unrounded
 // x'; each output is rounded once.  What a single wave of CTAs over the rows leaves on
-// the table is its start and end; bf16 elements also cost their conversions and the
-// gate's exponential (one pass of loads, all of them in flight, then 12 to 20
-// instructions an element).  Measured:
-//   gated, 4100 x 32 x 128 bf16   22.5 us (4.5 TB/s, 0.66 of the measured copy bandwidth);
-//     fp32 36 us (5.6 TB/s); 26.5 with the next row in registers instead of the ring below
-//   residual, 4100 x 4096 bf16, fp32 residual, gate, both norms   44 us (5.3 TB/s, 0.78);
-//     52 with the ring of per-thread copies that shorter rows use; 2050 x 8192: 48 us (72)
+// the table is its start and end; 16-bit elements cost their conversions and the gate's
+// exponential and reciprocal besides, so the gated norm's time follows its instructions.
+// Measured:
+//   gated, 4100 x 32 x 128 bf16   20.9 us (4.8 TB/s, 0.71 of the measured copy bandwidth;
+//     22.7 with a division a row and one element an instruction, 26.5 with the next row
+//     in registers instead of the ring below); fp32 36 to 37 us (5.4 TB/s)
+//   residual, 4100 x 4096 bf16, fp32 residual, gate, both norms   44 us (5.3 TB/s, 0.78;
+//     52 with the ring of per-thread copies that shorter rows use); 2050 x 8192: 48 us
+//     (72)
 // Rows that are not aligned to 16 bytes (odd widths, odd strides) are read and written an
-// element a lane, at 8 to 9 cycles an access whatever its width: 4100 x 2047 bf16 41 us
-// (floor 12), 2000 x 32 x 129 25 us (7).
+// element a lane: 4100 x 2047 bf16 41 us (floor 12), 2000 x 32 x 129 24 us (7).
 #include <atomic>
 
 #include "gdn_internal.cuh"
@@ -111,35 +112,81 @@ __device__ __forceinline__ void load_weight(const void *w, int i, int dt, float 
         for (int j = 0; j < VEC; ++j) x[j] += offset;
 }
 
-// 1 / (1 + e^-z) by the base-2 exponential and the reciprocal of the PTX ISA
-// (relative errors 2^-22 and 2^-23), in place.  For 16-bit values the rounding of
-// z log2 e is as far below their own as those; fp32 takes its rest along.
-template <typename T, int VEC>
-__device__ __forceinline__ void sigmoid_of(float (&z)[VEC]) {
+// Elementwise arithmetic on a vector, by fp32 pairs (one instruction for two elements:
+// 16-bit norms are bound by their instructions before HBM).
+__device__ __forceinline__ float2 pair(const float *x) { return make_float2(x[0], x[1]); }
+__device__ __forceinline__ void put(float *x, float2 v) { x[0] = v.x, x[1] = v.y; }
+template <int VEC>
+__device__ __forceinline__ void mul(float (&a)[VEC], const float (&b)[VEC]) {
+    if constexpr (VEC == 1) {
+        a[0] *= b[0];
+    } else {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        const float t = -1.4426950408889634f * z[j];
-        float e, s;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-        if constexpr (sizeof(T) == 4) {
-            const float rest = fmaf(-1.4426950408889634f, z[j], -t);
-            const float more = e * (0.6931471805599453f * rest);
-            e = t < 126.f ? e + more : e;  // (no rest beside an infinite e)
-        }
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
-        z[j] = s;
+        for (int j = 0; j < VEC; j += 2) put(a + j, __fmul2_rn(pair(a + j), pair(b + j)));
     }
 }
-// act(z), in place; the branches are the same for every thread.
+template <int VEC>
+__device__ __forceinline__ void mul(float (&a)[VEC], float b) {
+    if constexpr (VEC == 1) {
+        a[0] *= b;
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2) put(a + j, __fmul2_rn(pair(a + j), make_float2(b, b)));
+    }
+}
+// a <- b c + a
+template <int VEC>
+__device__ __forceinline__ void add_mul(float (&a)[VEC], float b, const float (&c)[VEC]) {
+    if constexpr (VEC == 1) {
+        a[0] = fmaf(b, c[0], a[0]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2)
+            put(a + j, __ffma2_rn(make_float2(b, b), pair(c + j), pair(a + j)));
+    }
+}
+// The sum of squares, in two halves.
+template <int VEC>
+__device__ __forceinline__ void add_squares(float2 &ss, const float (&a)[VEC]) {
+    if constexpr (VEC == 1) {
+        ss.x = fmaf(a[0], a[0], ss.x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2) ss = __ffma2_rn(pair(a + j), pair(a + j), ss);
+    }
+}
+
+// 1 / (1 + e^-z) by the base-2 exponential and the reciprocal of the PTX ISA
+// (relative errors 2^-22 and 2^-23).  For 16-bit values the rounding of z log2 e is as
+// far below their own as those; fp32 takes its rest along.  act(z), in place; the
+// branches are the same for every thread.
 template <typename T, int VEC>
 __device__ __forceinline__ void activate(float (&z)[VEC], int act) {
     float s[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) s[j] = z[j];
-    sigmoid_of<T, VEC>(s);
-    if (act == GDN_GATE_SILU) {
+    mul(s, -1.4426950408889634f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) z[j] *= s[j];
+    for (int j = 0; j < VEC; ++j) {
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(s[j]));
+        if constexpr (sizeof(T) == 4) {
+            const float rest = fmaf(-1.4426950408889634f, z[j], -s[j]);
+            const float more = e * (0.6931471805599453f * rest);
+            e = s[j] < 126.f ? e + more : e;  // (no rest beside an infinite e)
+        }
+        s[j] = e;
+    }
+    if constexpr (VEC == 1) {
+        s[0] += 1.f;
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2) put(s + j, __fadd2_rn(pair(s + j), make_float2(1.f, 1.f)));
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s[j]));
+    if (act == GDN_GATE_SILU) {
+        mul(z, s);
     } else {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) z[j] = s[j];
@@ -227,10 +274,28 @@ __global__ void __launch_bounds__(THREADS, ctas_of(VEC, ITEMS, THREADS)) gated_n
         nz[k].clear();
         if (in[k]) load_weight<VEC>(p.w, i, p.dt_w, offset, w[k]);
     }
-    auto fetch = [&](unsigned r, int slot) {
-        const unsigned n = r / H, h = r - n * H;
-        const T *x = reinterpret_cast<const T *>(p.x) + (int64_t)n * p.xs + h * p.d + t * VEC;
-        const T *z = reinterpret_cast<const T *>(p.z) + (int64_t)n * p.zs + h * p.d + t * VEC;
+    // (every thread of a CTA takes as many turns: the sums are taken together)
+    const unsigned step = gridDim.x * per_cta;
+    unsigned base = blockIdx.x * per_cta;
+    const unsigned step_n = step / H, step_h = step - step_n * H;
+    struct Row {  // head h of token n
+        unsigned r, n, h;
+    };
+    auto advance = [&](Row &x) {
+        x.r += step;
+        x.n += step_n;
+        x.h += step_h;
+        if (x.h >= H) x.h -= H, ++x.n;
+    };
+    Row out;  // the next one to finish, and to fetch
+    out.r = base + threadIdx.x / lanes;
+    out.n = out.r / H;
+    out.h = out.r - out.n * H;
+    Row in_row = out;
+    auto fetch = [&](int slot) {  // unless it is past the last
+        if (in_row.r >= rows) return;
+        const T *x = reinterpret_cast<const T *>(p.x) + (int64_t)in_row.n * p.xs + in_row.h * p.d + t * VEC;
+        const T *z = reinterpret_cast<const T *>(p.z) + (int64_t)in_row.n * p.zs + in_row.h * p.d + t * VEC;
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
             if (in[k]) {
@@ -244,23 +309,16 @@ __global__ void __launch_bounds__(THREADS, ctas_of(VEC, ITEMS, THREADS)) gated_n
             }
         }
     };
-    // (every thread of a CTA takes as many turns: the sums are taken together)
-    const unsigned step = gridDim.x * per_cta, mine = threadIdx.x / lanes;
-    unsigned base = blockIdx.x * per_cta;
     int parity = 0, slot = 0;
-    if constexpr (VEC > 1) {
-        for (int k = 0; k < R::DEPTH - 1; ++k) {
-            if (base + mine + k * step < rows) fetch(base + mine + k * step, k);
-            ring.commit();
-        }
-    } else if (base + mine < rows) {
-        fetch(base + mine, 0);
+    for (int k = 0; k < (VEC > 1 ? R::DEPTH - 1 : 1); ++k) {
+        fetch(k);
+        advance(in_row);
+        if constexpr (VEC > 1) ring.commit();
     }
-    for (; base < rows; base += step, parity ^= 1) {
-        const unsigned r = base + mine;
+    for (; base < rows; base += step, parity ^= 1, advance(out)) {
         if constexpr (VEC > 1) {
-            const unsigned ahead = r + (R::DEPTH - 1) * step;
-            if (ahead < rows) fetch(ahead, slot == 0 ? R::DEPTH - 1 : slot - 1);
+            fetch(slot == 0 ? R::DEPTH - 1 : slot - 1);
+            advance(in_row);
             ring.commit();
             ring.wait();
 #pragma unroll
@@ -272,7 +330,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of(VEC, ITEMS, THREADS)) gated_n
             slot = R::next(slot);
         }
         float a[ITEMS][VEC], g[ITEMS][VEC];
-        float ss = 0.f;
+        float2 ss2 = make_float2(0.f, 0.f);
         // (columns past the row are zeros; rows past the last are not stored)
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
@@ -280,28 +338,24 @@ __global__ void __launch_bounds__(THREADS, ctas_of(VEC, ITEMS, THREADS)) gated_n
             if (act != GDN_GATE_NONE) {
                 nz[k].get(g[k]);
                 activate<T, VEC>(g[k], act);
-                if (first)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) a[k][j] *= g[k][j];
+                if (first) mul(a[k], g[k]);
             }
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) ss = fmaf(a[k][j], a[k][j], ss);
+            add_squares(ss2, a[k]);
         }
-        if constexpr (VEC == 1)
-            if (r + step < rows) fetch(r + step, 0);
-        ss = row_sum<THREADS>(ss, lanes, red[parity]);
+        if constexpr (VEC == 1) {
+            fetch(0);
+            advance(in_row);
+        }
+        const float ss = row_sum<THREADS>(ss2.x + ss2.y, lanes, red[parity]);
         const float rs = rsqrtf(fmaf(ss, inv_d, p.eps));
-        if (r < rows) {
-            const unsigned n = r / H, h = r - n * H;
-            T *y = reinterpret_cast<T *>(p.out) + (int64_t)n * p.os + h * p.d + t * VEC;
+        if (out.r < rows) {
+            T *y = reinterpret_cast<T *>(p.out) + (int64_t)out.n * p.os + out.h * p.d + t * VEC;
 #pragma unroll
             for (int k = 0; k < ITEMS; ++k) {
                 if (in[k]) {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) a[k][j] *= rs * w[k][j];
-                    if (act != GDN_GATE_NONE && !first)
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) a[k][j] *= g[k][j];
+                    mul(a[k], rs);
+                    mul(a[k], w[k]);
+                    if (act != GDN_GATE_NONE && !first) mul(a[k], g[k]);
                     store_vec<T, VEC>(y + k * lanes * VEC, a[k]);
                 }
             }
@@ -402,28 +456,26 @@ __global__ void __launch_bounds__(THREADS, ctas_of(VEC, ITEMS, THREADS)) residua
                 }
             slot = R::next(slot);
         }
-        float u[ITEMS][VEC], a[ITEMS][VEC], ss = 0.f;
+        float u[ITEMS][VEC], a[ITEMS][VEC];
+        float2 ss = make_float2(0.f, 0.f);
         // (columns past the row are zeros; rows past the last are not stored)
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
             ny[k].get(u[k]);
             nx[k].get(a[k]);
-            if (post)
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) ss = fmaf(u[k][j], u[k][j], ss);
+            if (post) add_squares(ss, u[k]);
             if (act != GDN_GATE_NONE) {
                 float g[VEC];
                 nz[k].get(g);
                 activate<T, VEC>(g, act);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) u[k][j] *= g[j];
+                mul(u[k], g);
             }
         }
         if constexpr (VEC == 1)
             if (n + step < p.N) fetch(n + step, 0);
         float rs = p.scale;
-        if (post) rs *= rsqrtf(fmaf(row_sum<THREADS>(ss, lanes, red[0]), inv_d, p.eps));
-        ss = 0.f;
+        if (post) rs *= rsqrtf(fmaf(row_sum<THREADS>(ss.x + ss.y, lanes, red[0]), inv_d, p.eps));
+        ss = make_float2(0.f, 0.f);
         const bool live = n < p.N;
         TR *x_out = reinterpret_cast<TR *>(p.x_out) + n * p.D + t * VEC;
         T *out = reinterpret_cast<T *>(p.out) + n * p.D + t * VEC;
@@ -433,26 +485,22 @@ __global__ void __launch_bounds__(THREADS, ctas_of(VEC, ITEMS, THREADS)) residua
             if (live && in[k]) {
                 if (post) {
                     const float(&w)[VEC] = w_post.at(p.w_post, i + t * VEC, p.dt_w, offset, k);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) u[k][j] *= w[j];
+                    mul(u[k], w);
                 }
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    a[k][j] = fmaf(rs, u[k][j], a[k][j]);
-                    ss = fmaf(a[k][j], a[k][j], ss);
-                }
+                add_mul(a[k], rs, u[k]);
+                add_squares(ss, a[k]);
                 if (p.x_out != nullptr) store_vec<TR, VEC>(x_out + i, a[k]);
             }
         }
         if (p.out != nullptr) {
-            rs = rsqrtf(fmaf(row_sum<THREADS>(ss, lanes, red[1]), inv_d, p.eps));
+            rs = rsqrtf(fmaf(row_sum<THREADS>(ss.x + ss.y, lanes, red[1]), inv_d, p.eps));
 #pragma unroll
             for (int k = 0; k < ITEMS; ++k) {
                 const int i = k * lanes * VEC;
                 if (live && in[k]) {
                     const float(&w)[VEC] = w_pre.at(p.w_pre, i + t * VEC, p.dt_w, offset, k);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) a[k][j] *= rs * w[j];
+                    mul(a[k], rs);
+                    mul(a[k], w);
                     store_vec<T, VEC>(out + i, a[k]);
                 }
             }
@@ -517,7 +565,8 @@ residual_row_kernel(const ResidualNormParams p, int stages) {
     for (; n < p.N; n += step) {
         if (!dead) dead = !tc::mbar_wait(&full[s], phase, p.wait_ns);
         const uint8_t *st = sm + s * bytes;
-        float u[ITEMS][VEC], a[ITEMS][VEC], ss = 0.f;
+        float u[ITEMS][VEC], a[ITEMS][VEC];
+        float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
             const int i = (k * THREADS + t) * VEC;
@@ -526,37 +575,30 @@ residual_row_kernel(const ResidualNormParams p, int stages) {
             if (!in[k]) continue;
             load_vec<T, VEC>(reinterpret_cast<const T *>(st) + i, u[k]);
             if (xb) load_vec<TR, VEC>(reinterpret_cast<const TR *>(st + yb + zb) + i, a[k]);
-            if (post)
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) ss = fmaf(u[k][j], u[k][j], ss);
+            if (post) add_squares(ss, u[k]);
             if (zb) {
                 float g[VEC];
                 load_vec<T, VEC>(reinterpret_cast<const T *>(st + yb) + i, g);
                 activate<T, VEC>(g, act);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) u[k][j] *= g[j];
+                mul(u[k], g);
             }
         }
         float rs = p.scale;
-        if (post) rs *= rsqrtf(fmaf(row_sum<THREADS>(ss, THREADS, red[0]), inv_d, p.eps));
+        if (post) rs *= rsqrtf(fmaf(row_sum<THREADS>(ss.x + ss.y, THREADS, red[0]), inv_d, p.eps));
         else __syncthreads();
         // every thread has read the stage
         if (t == 0 && n + stages * step < p.N && !dead) issue(n + stages * step, s);
-        ss = 0.f;
+        ss = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
             const int i = (k * THREADS + t) * VEC;
             if (!in[k]) continue;
             if (post) {
                 const float(&w)[VEC] = w_post.at(p.w_post, i, p.dt_w, offset, k);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) u[k][j] *= w[j];
+                mul(u[k], w);
             }
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                a[k][j] = fmaf(rs, u[k][j], a[k][j]);
-                ss = fmaf(a[k][j], a[k][j], ss);
-            }
+            add_mul(a[k], rs, u[k]);
+            add_squares(ss, a[k]);
             if (p.x_out != nullptr) {
                 TR *dst = reinterpret_cast<TR *>(p.x_out) + n * D + i;
                 if constexpr (sizeof(TR) * VEC == 32) {
@@ -571,14 +613,14 @@ residual_row_kernel(const ResidualNormParams p, int stages) {
             }
         }
         if (p.out != nullptr) {
-            rs = rsqrtf(fmaf(row_sum<THREADS>(ss, THREADS, red[1]), inv_d, p.eps));
+            rs = rsqrtf(fmaf(row_sum<THREADS>(ss.x + ss.y, THREADS, red[1]), inv_d, p.eps));
 #pragma unroll
             for (int k = 0; k < ITEMS; ++k) {
                 const int i = (k * THREADS + t) * VEC;
                 if (!in[k]) continue;
                 const float(&w)[VEC] = w_pre.at(p.w_pre, i, p.dt_w, offset, k);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) a[k][j] *= rs * w[j];
+                mul(a[k], rs);
+                mul(a[k], w);
                 store_vec<T, VEC>(reinterpret_cast<T *>(p.out) + n * D + i, a[k]);
             }
         } else if (post) {
