@@ -19,9 +19,9 @@
 // again (from L2) for the token.  For many requests bound by HBM and by what surrounds
 // the one read of the rows, a chain of dependent accesses: the drafts, their
 // probabilities, the rows, the cluster's sums, the segment.  128 requests of 100003 fp32
-// probabilities, 4 drafts: 33 us (15 us of HBM time; 47 us with element loads and
-// conversions to 64-bit integers, 38 with CTAs of 512 threads); 1 request of 32000 bf16
-// ones without draft probabilities: 6 us, the chain.
+// probabilities, 4 drafts: 25 us (15 us of HBM time, 0.6 of the copy bandwidth; 47 us with
+// conversions to 64-bit integers); 1 request of 32000 bf16 ones without draft
+// probabilities: 8.8 us, the chain.
 #include <cooperative_groups.h>
 
 #include "gdn_internal.cuh"
@@ -34,6 +34,7 @@ namespace cg = cooperative_groups;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCluster = 8;
+constexpr int kCtas = 8;  // on a multiprocessor at once, which takes 32 registers a thread
 
 // Weights in whole units of 2^-40, floor(w 2^40) for w clamped to [0, 1] (NaN: 0).
 // A conversion to a 64-bit integer runs at a fraction of the load rate, so the two
@@ -78,7 +79,7 @@ struct Row {
 // multiple; with VEC > 1 lo is one, and rows are aligned to VEC tokens.
 template <typename T, int VEC, bool Q>
 __device__ __forceinline__ long long segment_sum(const Row<T> &row, int lo, int hi, int lane) {
-    constexpr int N = VEC > 1 ? 4 : 8;  // loads of a row in flight
+    constexpr int N = (VEC > 1 ? 4 : 8) / (Q ? 2 : 1);  // loads of a row in flight
     long long s = 0;
     int j = lo + lane * VEC;
     for (; j + ((N - 1) * 32 + 1) * VEC <= hi; j += N * 32 * VEC) {
@@ -104,7 +105,7 @@ __device__ __forceinline__ long long segment_sum(const Row<T> &row, int lo, int 
 }
 
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads, 6) accept_kernel(const AcceptParams p) {
+__global__ void __launch_bounds__(kThreads, kCtas) accept_kernel(const AcceptParams p) {
     __shared__ long long seg[kWarps];                 // this CTA's segment sums, read by the cluster
     __shared__ long long all[kMaxCluster * kWarps];   // the cluster's, in token order
     __shared__ long long part[kWarps];
@@ -232,12 +233,12 @@ __global__ void __launch_bounds__(kThreads, 6) accept_kernel(const AcceptParams 
 
 template <typename T>
 cudaError_t launch_t(const AcceptParams &p, cudaStream_t stream) {
-    // CTAs a row: more while the grid stays below eight a multiprocessor (six run at
-    // once; fewer, larger ones leave some multiprocessors a CTA more than others:
-    // 128 requests of 100003 tokens took 37 us as 512 CTAs of 512 threads) and each
-    // warp still sums a few hundred tokens
+    // CTAs a row: more while all of them run at once and each warp still sums a few
+    // hundred tokens (128 requests of 100003 fp32 tokens: 25 us as 1024 CTAs of 256 threads;
+    // 34 with room for six of them on a multiprocessor, a second wave; 37 as 512 CTAs of
+    // 512 threads, of which some multiprocessors had one more than others)
     int cs = 1;
-    const long slots = 8l * sm_count_of_current_device();
+    const long slots = (long)kCtas * sm_count_of_current_device();
     while (cs < kMaxCluster && (long)p.B * cs * 2 <= slots && p.V / (2 * cs * kWarps) >= 128) cs *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p.B * cs));
