@@ -21,7 +21,7 @@
 //     in registers instead of the ring below); fp32 36 to 37 us (5.4 TB/s)
 //   residual, 4100 x 4096 bf16, fp32 residual, gate, both norms   44 us (5.3 TB/s, 0.78;
 //     52 with the ring of per-thread copies that shorter rows use); 2050 x 8192: 48 us
-//     (72)
+//     (72); 10000 x 1024 bf16, bf16 residual: 22.5 us (4.5 TB/s)
 // Rows that are not aligned to 16 bytes (odd widths, odd strides) are read and written an
 // element a lane: 4100 x 2047 bf16 41 us (floor 12), 2000 x 32 x 129 24 us (7).
 #include <atomic>
@@ -198,7 +198,9 @@ __device__ __forceinline__ void activate(float (&z)[VEC], int act) {
 // another buffer in every second call.
 template <int THREADS>
 __device__ __forceinline__ float row_sum(float x, int lanes, float *red) {
-    for (int o = (lanes < 32 ? lanes : 32) / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < lanes) x += __shfl_xor_sync(0xffffffffu, x, o);
     if (lanes <= 32) return x;
     constexpr int W = THREADS / 32;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
@@ -364,7 +366,9 @@ __global__ void __launch_bounds__(THREADS, ctas_of(VEC, ITEMS, THREADS)) gated_n
 }
 
 // A weight's vector for the thread's columns: kept in registers where they are few
-// enough, else read again (from L1) for every row.
+// enough, else read again for every row: from shared memory, in fp32, where the CTA's
+// rows are short (`share`; 10000 x 1024 bf16: 22.5 us, 26.6 with loads and conversions
+// from L1), else from L1.
 template <int VEC, int ITEMS>
 struct Weights {
     static constexpr bool kKept = VEC * ITEMS <= 8;
@@ -375,6 +379,23 @@ struct Weights {
     __device__ __forceinline__ const float (&at(const void *p, int i, int dt, float offset, int k))[VEC] {
         if constexpr (kKept) return w[k];
         load_weight<VEC>(p, i, dt, offset, w[0]);
+        return w[0];
+    }
+    // All D weights by the whole CTA, element 4 e of vector v at [128 e + v].
+    template <int THREADS>
+    __device__ __forceinline__ static void share(float4 *s, const void *p, int D, int dt, float offset) {
+        for (int i = threadIdx.x; i < D / 4; i += THREADS) {
+            float x[4];
+            load_weight<4>(p, 4 * i, dt, offset, x);
+            s[i % (VEC / 4) * 128 + i / (VEC / 4)] = make_float4(x[0], x[1], x[2], x[3]);
+        }
+    }
+    __device__ __forceinline__ const float (&at(const float4 *s, int v))[VEC] {
+#pragma unroll
+        for (int e = 0; e < VEC / 4; ++e) {
+            const float4 f = s[128 * e + v];
+            w[0][4 * e] = f.x, w[0][4 * e + 1] = f.y, w[0][4 * e + 2] = f.z, w[0][4 * e + 3] = f.w;
+        }
         return w[0];
     }
 };
@@ -393,7 +414,15 @@ __global__ void __launch_bounds__(THREADS, ctas_of(VEC, ITEMS, THREADS)) residua
     const bool post = p.w_post != nullptr;
     Raw<T, VEC> ny[ITEMS], nz[ITEMS];
     Raw<TR, VEC> nx[ITEMS];
-    Weights<VEC, ITEMS> w_post, w_pre;
+    using W = Weights<VEC, ITEMS>;
+    W w_post, w_pre;
+    constexpr bool kShared = VEC > 1 && !W::kKept;
+    __shared__ float4 shared_w[kShared ? 2 : 1][kShared ? 256 : 1];
+    if constexpr (kShared) {
+        if (post) W::template share<THREADS>(shared_w[0], p.w_post, p.D, p.dt_w, offset);
+        W::template share<THREADS>(shared_w[1], p.w_pre, p.D, p.dt_w, offset);
+        __syncthreads();
+    }
     bool in[ITEMS];
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
@@ -484,7 +513,8 @@ __global__ void __launch_bounds__(THREADS, ctas_of(VEC, ITEMS, THREADS)) residua
             const int i = k * lanes * VEC;
             if (live && in[k]) {
                 if (post) {
-                    const float(&w)[VEC] = w_post.at(p.w_post, i + t * VEC, p.dt_w, offset, k);
+                    const float(&w)[VEC] = kShared ? w_post.at(shared_w[0], k * lanes + t)
+                                                   : w_post.at(p.w_post, i + t * VEC, p.dt_w, offset, k);
                     mul(u[k], w);
                 }
                 add_mul(a[k], rs, u[k]);
@@ -498,7 +528,8 @@ __global__ void __launch_bounds__(THREADS, ctas_of(VEC, ITEMS, THREADS)) residua
             for (int k = 0; k < ITEMS; ++k) {
                 const int i = k * lanes * VEC;
                 if (live && in[k]) {
-                    const float(&w)[VEC] = w_pre.at(p.w_pre, i + t * VEC, p.dt_w, offset, k);
+                    const float(&w)[VEC] = kShared ? w_pre.at(shared_w[1], k * lanes + t)
+                                                   : w_pre.at(p.w_pre, i + t * VEC, p.dt_w, offset, k);
                     mul(a[k], rs);
                     mul(a[k], w);
                     store_vec<T, VEC>(out + i, a[k]);
