@@ -16,9 +16,9 @@
 // the table is its start and end; 16-bit elements cost their conversions and the gate's
 // exponential and reciprocal besides, so the gated norm's time follows its instructions.
 // Measured:
-//   gated, 4100 x 32 x 128 bf16   20.9 us (4.8 TB/s, 0.71 of the measured copy bandwidth;
-//     22.7 with a division a row and one element an instruction, 26.5 with the next row
-//     in registers instead of the ring below); fp32 36 to 37 us (5.4 TB/s)
+//   gated, 4100 x 32 x 128 bf16   19.6 to 20.7 us (4.9 TB/s, 0.72 to 0.76 of the measured
+//     copy bandwidth; 22.7 with a division a row and one element an instruction, 26.5
+//     with the next row in registers instead of the ring below); fp32 36 us (5.5 TB/s)
 //   residual, 4100 x 4096 bf16, fp32 residual, gate, both norms   44 us (5.3 TB/s, 0.78;
 //     52 with the ring of per-thread copies that shorter rows use); 2050 x 8192: 48 us
 //     (72); 10000 x 1024 bf16, bf16 residual: 22.5 us (4.5 TB/s)
