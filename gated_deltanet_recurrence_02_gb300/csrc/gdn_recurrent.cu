@@ -39,8 +39,8 @@
 // alpha is a gate of each (token, head) or, with GDN_ALPHA_PER_HEAD, of each
 // head.  A capture holds decay, key and v, which the replay of the delta rule
 // rebuilds the state from unchanged.  It moves the same bytes as the delta
-// rule and is bound by them: 256 rows of 32 heads, dk = dv = 128, one token with
-// its capture, 173 us (0.92 of the measured copy bandwidth).
+// rule and is bound by them: 256 rows of 32 heads, dk = dv = 128, one token,
+// 173 us (0.92 of the measured copy bandwidth).
 #include "gdn_internal.cuh"
 #include "tc_ptx.cuh"
 
