@@ -332,7 +332,8 @@ GDN_API int gdn_replay_verify(const void *q, const void *k, const void *v,
 #define GDN_ALPHA_PER_HEAD 0x800
 
 /*
- * gdn_linear_prefill -- chunked form, for prompts of any length.
+ * gdn_linear_prefill -- chunked form, for prompts of any length (T of at most
+ * four runs in the recurrent form, which is faster there).
  *  final_state may be NULL (not written), or exactly initial_state when
  *  initial_state_indices is NULL.  workspace: device buffer of
  *  gdn_linear_prefill_workspace_size() bytes (same B, T, sizes and dtype_qkv;
