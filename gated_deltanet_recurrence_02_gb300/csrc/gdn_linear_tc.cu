@@ -120,8 +120,7 @@ constexpr uint32_t kSmem = oBar + 384 + 1024;      // + alignment slack
 // TMEM columns
 constexpr uint32_t tR = 0, tO1 = 64, tO2 = 128, tDS = 192, tS = 320, tW = 384;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kBarW = 1;  // named barriers: the W warps, and the two of the later rows of P
-constexpr uint32_t kBarP = 2;
+constexpr uint32_t kBarP = 1;  // named barrier: the two warps of the later rows of P
 
 enum Mode {
     kWhole,      // a unit is a whole row: outputs and final state
@@ -438,18 +437,23 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             if (!(ok = tiles(it))) break;
             uint8_t *st = sm + (it % NS) * kStage;
             if (n < C) {
-                // K and V rows past the row's end: zeros, whatever was loaded
+                // Rows past the row's end: zeros, whatever was loaded.  Of V this warp's own
+                // 16 features, which no other warp reads for W; of K an eighth, which the
+                // product reads behind all eight warps' w_ready.  (So no barrier stands
+                // here, which a warp whose wait ran out would leave the others in.)
+                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
                 for (int e = (wq + 4 * hh) * 32 + lane; e < (C - n) * 8; e += 256) {
                     const int off = (n + (e >> 3)) * 128 + (e & 7) * 16;
-                    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
                     *reinterpret_cast<uint4 *>(st + off) = z;
                     *reinterpret_cast<uint4 *>(st + kBlock + off) = z;
-                    *reinterpret_cast<uint4 *>(st + kStageV + off) = z;
-                    *reinterpret_cast<uint4 *>(st + kStageV + 8192 + off) = z;
                 }
+#pragma unroll 1
+                for (int e = lane; e < (C - n) * 2; e += 32)
+                    *reinterpret_cast<uint4 *>(st + kStageV + (wq >> 1) * 8192 +
+                                               sw128_chunk(n + (e >> 1), (wq & 1) * 4 + 2 * hh + (e & 1))) = z;
                 fence_proxy_async();
-                named_bar(kBarW, 256);
+                __syncwarp();
             }
             // 16 tokens (j): features g and g + 8, tokens 2 t, 2 t + 1 of each eight,
             // which is the layout of the TMEM store
