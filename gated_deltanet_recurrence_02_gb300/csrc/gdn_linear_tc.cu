@@ -113,14 +113,13 @@ constexpr int gN = 225, gTok = 226, gHead = 227;   // ints: the chunk's tokens (
 constexpr uint32_t oWExp = oGate + kGates * kGate; // [4][128] int8: the exponent of a lane's scale of W
 constexpr uint32_t oSExp = oWExp + 512;            // [2][128] int8: of a lane's scale of the image
 constexpr uint32_t oPInv = oSExp + 256;           // [2][64]  1 / scale of a row of P
-constexpr uint32_t oPMax = oPInv + 512;            // [64] maxima of both parts of the later rows of P
-constexpr uint32_t oBar = oPMax + 256;
+constexpr uint32_t oPMax = oPInv + 512;            // [2][64] maxima of both parts of the later rows of P
+constexpr uint32_t oBar = oPMax + 512;
 constexpr uint32_t kSmem = oBar + 384 + 1024;      // + alignment slack
 
 // TMEM columns
 constexpr uint32_t tR = 0, tO1 = 64, tO2 = 128, tDS = 192, tS = 320, tW = 384;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kBarP = 1;  // named barrier: the two warps of the later rows of P
 
 enum Mode {
     kWhole,      // a unit is a whole row: outputs and final state
@@ -223,7 +222,8 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
              *s_ready = r_done + 4, *o_done = r_done + 5, *o_free = r_done + 6, *drain = r_done + 7;
     // of even and of odd chunks, where a wait may lie more than one chunk back
     uint64_t *w_ready = r_done + 8, *ds_half = r_done + 10, *ds_done = r_done + 12, *ds_free = r_done + 14;
-    uint32_t *slot = reinterpret_cast<uint32_t *>(r_done + 16);
+    uint64_t *max_there = r_done + 16;  // both parts' maxima of the later rows of P
+    uint32_t *slot = reinterpret_cast<uint32_t *>(r_done + 17);
     // (through a shuffle: known to be the same in every lane)
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int dk = p.dk, dv = p.dv, Hv = p.Hv;
@@ -240,6 +240,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
         mbar_init(r_done, 1);
         mbar_init(r_free, 3);
         mbar_init(p_ready, 3);
+        mbar_init(max_there, 2);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&w_ready[s], 8);
             mbar_init(&ds_half[s], 1);
@@ -754,9 +755,10 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 if (it > 0 && !(ok = wait(o_done, it - 1))) break;
                 if constexpr (!kBf) {
                     if (diag > 0) {  // one scale a row: with the maximum of its left part
-                        float *pmax = reinterpret_cast<float *>(sm + oPMax);
+                        float *pmax = reinterpret_cast<float *>(sm + oPMax) + (it & 1) * 64;
                         pmax[lane] = m;
-                        named_bar(kBarP, 64);
+                        arrive(max_there);
+                        if (!(ok = wait(max_there, it))) break;
                         m = fmaxf(m, pmax[32 + lane]);
                     }
                     const int pe = half_exp(m);
@@ -868,11 +870,12 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                             for (int j = 0; j < 16; ++j)
                                 m = fmaxf(m, fabsf(__uint_as_float(y[j]) * gate[gLeft + 16 * hh + j] * l));
                         }
-                        float *pmax = reinterpret_cast<float *>(sm + oPMax);
-                        // (one buffer: the diagonal part's warp reads it before its
-                        // p_ready, and the next R comes after both)
+                        // (two buffers: the next chunk's maxima may be there before the
+                        // other warp has read these, the one after next's are not)
+                        float *pmax = reinterpret_cast<float *>(sm + oPMax) + (it & 1) * 64;
                         pmax[32 + lane] = m;
-                        named_bar(kBarP, 64);
+                        arrive(max_there);
+                        if (!(ok = wait(max_there, it))) break;
                         const float sc = pow2(half_exp(fmaxf(m, pmax[lane])));
                         l2 = make_float2(l * sc, l * sc);
                     }

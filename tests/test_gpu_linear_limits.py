@@ -52,6 +52,14 @@ def test_ragged_rows_bf16(lengths):
     runs_out(x, "bf16")
 
 
+@pytest.mark.parametrize("lengths", [[64] * 12, [90, 1, 65, 130, 63, 7], [1000, 333]],
+                         ids=["chunks", "rows", "segments"])
+def test_fp16(lengths):
+    """Two warps share the scales of P's later rows."""
+    x = make_inputs(53, lengths=lengths, Hk=1, Hv=2, dk=128, dv=64, dtype_qkv="f16", dtype_gate="f32")
+    runs_out(x, "f16")
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("dk,dv", [(128, 128), (64, 32), (32, 64)])
 @pytest.mark.parametrize("n", [5, 63, 97])
