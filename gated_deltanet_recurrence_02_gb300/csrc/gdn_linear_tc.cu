@@ -670,10 +670,11 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     }
                 }
             }
-            // the copies in flight must land before the CTA ends
-            if (!ok)
-                for (int j = it > NS ? it - NS : 0; j < it; ++j)
-                    mbar_wait(&full[j % NS], (uint32_t)(j / NS) & 1u, kDefaultWaitNs / 8);
+            // The copies in flight must land before the CTA ends: the warps that read
+            // the last tiles may have given up although this one did not.
+#pragma unroll 1
+            for (int j = it > NS ? it - NS : 0; j < it; ++j)
+                mbar_wait(&full[j % NS], (uint32_t)(j / NS) & 1u, kDefaultWaitNs / 8);
         } else if (warp == 13) {
             // ================= MMAs of the state's update ================
             const uint32_t id_ds = idesc_f16(128, dk, false, true, kBf);

@@ -61,6 +61,25 @@ def test_fp16(lengths):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_few_chunks(dtype):
+    """CTAs whose tiles are all on their way at once, and calls that follow at once."""
+    x = make_inputs(54, lengths=[64, 40, 200, 129] * 40, Hk=2, Hv=4, dk=128, dv=128, dtype_qkv=dtype, dtype_gate="f32")
+    g = [t.cuda() for t in (x.q, x.k, x.v, x.alpha)]
+    how = dict(B=x.B, cu_seqlens=x.cu_seqlens.cuda(), initial_state=x.initial_state.cuda())
+    whole, last = gdn.gdn_linear_prefill(*g, **how)
+    assert errors() == 0
+    for _ in range(5):
+        gdn.gdn_set_wait_limit_ns(1)
+        try:
+            gdn.gdn_linear_prefill(*g, **how)
+        finally:
+            gdn.gdn_set_wait_limit_ns(0)
+        out, end = gdn.gdn_linear_prefill(*g, **how)  # on the same SMs, right behind it
+        assert errors() == gdn.GDN_DEVERR_TIMEOUT
+        assert torch.equal(out, whole) and torch.equal(end, last)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("dk,dv", [(128, 128), (64, 32), (32, 64)])
 @pytest.mark.parametrize("n", [5, 63, 97])
 def test_the_next_row_stays_out(dtype, dk, dv, n):
