@@ -550,6 +550,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
             fence_before_sync();
             arrive(&w_ready[it & 1]);
         }
+        if (!ok) tmem_wait_st();  // given up between two halves: TMEM is freed behind the stores
     } else if (warp < 12) {
         // ============================ outputs ============================
         regs_dec<64>();
