@@ -195,16 +195,18 @@ __device__ __forceinline__ void activate(float (&z)[VEC], int act) {
 
 // Sum over the row's group of threads: `lanes` (a power of two) threads of a
 // warp, or, with lanes > 32, all THREADS of the CTA.  red: a float for each warp,
-// another buffer in every second call.
+// another buffer in every second call.  `any` (a whole CTA's rows only) becomes whether
+// it was set in any thread.
 template <int THREADS>
-__device__ __forceinline__ float row_sum(float x, int lanes, float *red) {
+__device__ __forceinline__ float row_sum(float x, int lanes, float *red, bool *any = nullptr) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         if (o < lanes) x += __shfl_xor_sync(0xffffffffu, x, o);
     if (lanes <= 32) return x;
     constexpr int W = THREADS / 32;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-    __syncthreads();
+    if (any != nullptr) *any = __syncthreads_or(*any) != 0;
+    else __syncthreads();
     float s = red[threadIdx.x & (W - 1)];
 #pragma unroll
     for (int o = W / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -592,9 +594,9 @@ residual_row_kernel(const ResidualNormParams p, int stages) {
         for (int s = 0; s < stages; ++s)
             if (n + s * step < p.N) issue(n + s * step, s);
     int s = 0, phase = 0;
-    bool dead = false;  // a copy did not come in time: the rows after it are not waited for
+    bool late = false;  // a copy did not come in time, as any thread saw it
     for (; n < p.N; n += step) {
-        if (!dead) dead = !tc::mbar_wait(&full[s], phase, p.wait_ns);
+        late = !tc::mbar_wait(&full[s], phase, p.wait_ns);
         const uint8_t *st = sm + s * bytes;
         float u[ITEMS][VEC], a[ITEMS][VEC];
         float2 ss = make_float2(0.f, 0.f);
@@ -615,10 +617,11 @@ residual_row_kernel(const ResidualNormParams p, int stages) {
             }
         }
         float rs = p.scale;
-        if (post) rs *= rsqrtf(fmaf(row_sum<THREADS>(ss.x + ss.y, THREADS, red[0]), inv_d, p.eps));
-        else __syncthreads();
+        if (post) rs *= rsqrtf(fmaf(row_sum<THREADS>(ss.x + ss.y, THREADS, red[0], &late), inv_d, p.eps));
+        else late = __syncthreads_or(late) != 0;
+        if (late) break;  // the whole CTA, before any of the row is written
         // every thread has read the stage
-        if (t == 0 && n + stages * step < p.N && !dead) issue(n + stages * step, s);
+        if (t == 0 && n + stages * step < p.N) issue(n + stages * step, s);
         ss = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
@@ -659,10 +662,13 @@ residual_row_kernel(const ResidualNormParams p, int stages) {
         }
         if (++s == stages) s = 0, phase ^= 1;
     }
-    if (dead && t == 0) {
+    if (late && t == 0) {
         atomicOr(p.err, (uint32_t)GDN_DEVERR_TIMEOUT);
-        // the copies in flight must land before the CTA ends
-        for (int k = 0; k < stages; ++k) tc::mbar_wait(&full[k], phase ^ (k < s), kDefaultWaitNs / 8);
+        // the copies in flight, of this row and of those after it, must land before the CTA ends
+        for (int k = 0; k < stages && n < p.N; ++k, n += step) {
+            tc::mbar_wait(&full[s], phase, kDefaultWaitNs / 8);
+            if (++s == stages) s = 0, phase ^= 1;
+        }
     }
 }
 
