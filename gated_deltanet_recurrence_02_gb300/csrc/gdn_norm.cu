@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of(VEC, ITEMS, THREADS)) gated_n
     const unsigned step = gridDim.x * per_cta;
     unsigned base = blockIdx.x * per_cta;
     const unsigned step_n = step / H, step_h = step - step_n * H;
-    struct Row {  // head h of token n
+    struct Row {  // head h of token n (h d may pass 32 bits)
         unsigned r, n, h;
     };
     auto advance = [&](Row &x) {
@@ -298,8 +298,8 @@ __global__ void __launch_bounds__(THREADS, ctas_of(VEC, ITEMS, THREADS)) gated_n
     Row in_row = out;
     auto fetch = [&](int slot) {  // unless it is past the last
         if (in_row.r >= rows) return;
-        const T *x = reinterpret_cast<const T *>(p.x) + (int64_t)in_row.n * p.xs + in_row.h * p.d + t * VEC;
-        const T *z = reinterpret_cast<const T *>(p.z) + (int64_t)in_row.n * p.zs + in_row.h * p.d + t * VEC;
+        const T *x = reinterpret_cast<const T *>(p.x) + (int64_t)in_row.n * p.xs + (uint64_t)in_row.h * (unsigned)p.d + t * VEC;
+        const T *z = reinterpret_cast<const T *>(p.z) + (int64_t)in_row.n * p.zs + (uint64_t)in_row.h * (unsigned)p.d + t * VEC;
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
             if (in[k]) {
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of(VEC, ITEMS, THREADS)) gated_n
         const float ss = row_sum<THREADS>(ss2.x + ss2.y, lanes, red[parity]);
         const float rs = rsqrtf(fmaf(ss, inv_d, p.eps));
         if (out.r < rows) {
-            T *y = reinterpret_cast<T *>(p.out) + (int64_t)out.n * p.os + out.h * p.d + t * VEC;
+            T *y = reinterpret_cast<T *>(p.out) + (int64_t)out.n * p.os + (uint64_t)out.h * (unsigned)p.d + t * VEC;
 #pragma unroll
             for (int k = 0; k < ITEMS; ++k) {
                 if (in[k]) {
