@@ -104,7 +104,7 @@ constexpr uint32_t oOut = oP + 8192;               // [4 warps][64 tokens][32 fe
 constexpr uint32_t oGate = oOut + 16384;           // kGates slots of kGate bytes, the words below
 constexpr int kGates = 8;
 constexpr uint32_t kGate = 912;
-constexpr int gSum = 0;                            // [64] b_t (decays of at least 2^-40 each)
+constexpr int gSum = 0;                            // [64] b_t, or b_t - b_31 from token 32 on (decays of at least 2^-127 each)
 constexpr int gScaled = 64;                        // [64] scale 2^{b_t}
 constexpr int gW = 128;                            // 2^{s_t}: fp32 [64], or bf16 [32 pairs][two parts]
 constexpr int gLeft = 192;                         // [32] 2^{b_31 - b_t}
@@ -859,7 +859,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                     if (n <= 0 || !(ok = wait(r_done, it))) break;
                     fence_after_sync();
                     const float *gate = gate_of(it);
-                    const float l = p.scale * ex2_approx(gate[gSum + i] - gate[gSum + 31]);
+                    const float l = p.scale * ex2_approx(gate[gSum + i]);
                     float2 l2 = make_float2(l, l);
                     if constexpr (!kBf) {
                         float m = 0.f;
@@ -961,26 +961,30 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
                 // Inclusive sums over the lanes from both ends; the exclusive ones
                 // are the neighbours' (a difference would lose what a strong decay
                 // has in front of it, and be no number after a decay of 0).  For
-                // P's differences a decay below 2^-40 (0 among them) counts as 2^-40,
-                // far below the scores' own rounding: the sums stay finite, and small
-                // enough for their differences to be exact to 2^-12.
+                // P's differences the sums start anew at token 32, and a decay below
+                // 2^-127 (0 among them) counts as 2^-127: P's exponential of a difference
+                // across it is 0 all the same, and the sums stay finite.  They are exact
+                // to 2^-17 for decays that sum to less than 2^6 in a half, to 2^-13 a sum
+                // for the strongest ones.
                 float held[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     a[e] = 2 * lane + e >= n_ ? 0.f : (p.conv & GDN_ALPHA_LOG) ? a[e] * kLog2e : log2f(a[e]);
-                    held[e] = a[e] < -40.f ? -40.f : a[e];
+                    held[e] = a[e] < -127.f ? -127.f : a[e];
                 }
                 float up = a[0] + a[1], down = up, hup = held[0] + held[1];
 #pragma unroll 1
                 for (int o = 1; o < 32; o <<= 1) {
                     const float y0 = __shfl_up_sync(0xffffffffu, up, o), y1 = __shfl_down_sync(0xffffffffu, down, o);
                     const float y2 = __shfl_up_sync(0xffffffffu, hup, o);
-                    if (lane >= o) up += y0, hup += y2;
+                    if (lane >= o) up += y0;
+                    if ((lane & 15) >= o) hup += y2;
                     if (lane + o < 32) down += y1;
                 }
                 float ex = __shfl_up_sync(0xffffffffu, up, 1), eh = __shfl_up_sync(0xffffffffu, hup, 1);
                 float suf = __shfl_down_sync(0xffffffffu, down, 1);
-                if (lane == 0) ex = eh = 0.f;
+                if (lane == 0) ex = 0.f;
+                if ((lane & 15) == 0) eh = 0.f;
                 if (lane == 31) suf = 0.f;
                 const float b31 = __shfl_sync(0xffffffffu, hup, 15);
                 const float2 b2 = make_float2(eh + held[0], hup);

@@ -324,7 +324,8 @@ GDN_API int gdn_replay_verify(const void *q, const void *k, const void *v,
  * GDN_ALPHA_LOG applies to both forms; no other bit is taken.  Precondition:
  * every alpha in [0, 1]; 0 drops the state.  (The recurrent form multiplies by
  * whatever it is given; the chunked one for 16-bit inputs takes logarithms, so a
- * negative alpha gives NaN there.)  Inputs that are not finite reach the tokens
+ * negative alpha gives NaN there, and takes a product of decays within a chunk of
+ * 64 tokens that is below 2^-126 as 0.)  Inputs that are not finite reach the tokens
  * after them in the same row and, in the chunked form, the up to 63 tokens
  * before them that share their chunk; they touch no other row, and values of
  * one head touch no other head.
