@@ -173,18 +173,21 @@ __device__ __forceinline__ void activate(float (&z)[VEC], int act) {
         if constexpr (sizeof(T) == 4) {
             const float rest = fmaf(-1.4426950408889634f, z[j], -s[j]);
             const float more = e * (0.6931471805599453f * rest);
-            e = s[j] < 126.f ? e + more : e;  // (no rest beside an infinite e)
+            e = fabsf(s[j]) < 126.f ? e + more : e;  // (no rest beside an infinite e or z)
         }
         s[j] = e;
     }
+    // (a quarter of 1 + e^-z: its reciprocal is a normal number wherever e^-z is finite)
     if constexpr (VEC == 1) {
-        s[0] += 1.f;
+        s[0] = fmaf(s[0], 0.25f, 0.25f);
     } else {
 #pragma unroll
-        for (int j = 0; j < VEC; j += 2) put(s + j, __fadd2_rn(pair(s + j), make_float2(1.f, 1.f)));
+        for (int j = 0; j < VEC; j += 2)
+            put(s + j, __ffma2_rn(pair(s + j), make_float2(0.25f, 0.25f), make_float2(0.25f, 0.25f)));
     }
 #pragma unroll
     for (int j = 0; j < VEC; ++j) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s[j]));
+    mul(s, 0.25f);
     if (act == GDN_GATE_SILU) {
         mul(z, s);
     } else {
