@@ -330,6 +330,37 @@ def gdn_linear_prefill_workspace_size(B, T, Hk, Hv, dk, dv, dtype_qkv, varlen=Fa
                                                        int(bool(varlen))))
 
 
+def _is(t, shape, dtype) -> bool:
+    """Whether an optional buffer is absent, a raw pointer, or a tensor of this kind."""
+    return t is None or isinstance(t, int) or (t.shape == shape and t.dtype == dtype)
+
+
+def _linear_check(q, k, v, alpha, cu_seqlens, initial_state, initial_state_indices, final_state,
+                  out, B, T, conventions):
+    """Shapes and dtypes of a linear-attention call: the library sees addresses only, and
+    would read and write past the end of a smaller tensor."""
+    total, Hk, dk = q.shape
+    _, Hv, dv = v.shape
+    if k.shape != q.shape or v.shape[0] != total or not (q.dtype == k.dtype == v.dtype):
+        raise ValueError("q and k are [total_T, Hk, dk], v [total_T, Hv, dv], of one dtype")
+    if alpha.shape != ((Hv,) if conventions & GDN_ALPHA_PER_HEAD else (total, Hv)):
+        raise ValueError("alpha is [Hv] with GDN_ALPHA_PER_HEAD and [total_T, Hv] without")
+    if cu_seqlens is None:
+        if B * T > total:
+            raise ValueError("q, k and v hold B rows of T tokens")
+    elif not _is(cu_seqlens, (B + 1,), torch.int32):
+        raise ValueError("cu_seqlens is int32 [B + 1]")
+    if initial_state is not None and (initial_state.dtype != torch.float32
+                                      or initial_state.shape[1:] != (Hv, dv, dk)):
+        raise ValueError("initial_state is float32 [states, Hv, dv, dk]")
+    if not _is(initial_state_indices, (B,), torch.int32):
+        raise ValueError("initial_state_indices is int32 [B]")
+    if not _is(final_state, (B, Hv, dv, dk), torch.float32):
+        raise ValueError("final_state is float32 [B, Hv, dv, dk]")
+    if not _is(out, v.shape, v.dtype):
+        raise ValueError("out must have the shape and the dtype of v")
+
+
 def gdn_linear_prefill(q, k, v, alpha, *, B: int, T: Optional[int] = None, cu_seqlens=None,
                        initial_state=None, initial_state_indices=None, final_state=None,
                        out=None, scale: float = 1.0, workspace=None,
@@ -338,6 +369,8 @@ def gdn_linear_prefill(q, k, v, alpha, *, B: int, T: Optional[int] = None, cu_se
     [total_T, Hv], or [Hv] with GDN_ALPHA_PER_HEAD in conventions.  Returns
     (out, final_state)."""
     T, Hk, dk, Hv, dv = _dims(q, v, B, T, cu_seqlens)
+    _linear_check(q, k, v, alpha, cu_seqlens, initial_state, initial_state_indices, final_state,
+                  out, B, T, conventions)
     if out is None:
         out = torch.empty_like(v)
     if final_state is None and want_final_state:
@@ -367,14 +400,24 @@ def gdn_linear_recurrent(q, k, v, alpha, *, B: int, T: Optional[int] = None, cu_
     Returns (out, final_state, state_update).  final_state may be
     initial_state itself (in place)."""
     T, Hk, dk, Hv, dv = _dims(q, v, B, T, cu_seqlens)
+    _linear_check(q, k, v, alpha, cu_seqlens, initial_state, initial_state_indices, final_state,
+                  out, B, T, conventions)
     if out is None:
         out = torch.empty_like(v)
     if final_state is None and want_final_state:
         final_state = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=v.device)
     cap = int(state_update_capacity)
-    if cap > 0 and state_update is None:
-        state_update = torch.empty((B, cap, slot_width(Hk, Hv, dk, dv)),
-                                   dtype=torch.float32, device=v.device)
+    if cap > 0:
+        slots = (B, cap, slot_width(Hk, Hv, dk, dv))
+        if state_update is None:
+            state_update = torch.empty(slots, dtype=torch.float32, device=v.device)
+        elif not _is(state_update, slots, torch.float32):
+            raise ValueError("state_update is float32 [B, capacity, slot_width]")
+        if not _is(capture_count, (B,), torch.int32):
+            raise ValueError("capture_count is int32 [B]")
+        if not (state_update_active is None or isinstance(state_update_active, int)
+                or (state_update_active.dtype == torch.int32 and state_update_active.numel() >= 1)):
+            raise ValueError("state_update_active is an int32 on the device")
     n0 = initial_state.shape[0] if initial_state is not None else 0
     st = lib().gdn_linear_recurrent(
         _p(q), _p(k), _p(v), _p(alpha), _p(cu_seqlens), _p(initial_state),
