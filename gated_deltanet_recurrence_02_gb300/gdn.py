@@ -125,6 +125,25 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream, scratch: bool = False):
+    """Memory for a call on `stream`.  Where that is not the current stream it comes from
+    that stream's pool, as for torch operations under torch.cuda.stream: from the current
+    one's it could still be in use there, and would be handed out again there as soon as
+    the caller drops it, with the call still to run.  What the caller receives (all but
+    scratch) is marked as used on the current stream, where it will be read."""
+    if stream is None or _stream(stream) == _stream(None):
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if not scratch:
+        t.record_stream(current)
+    return t
+
+
 def _codes(q, alpha, conventions: int):
     """dtype_qkv and dtype_gate arguments: storage types plus the input
     convention bits (GDN_QK_L2NORM goes with q/k, the gate bits with alpha/beta)."""
@@ -165,14 +184,14 @@ def gdn_prefill_chunked(q, k, v, alpha, beta, *, B: int, T: Optional[int] = None
     """Chunked prefill.  Returns (out, final_state)."""
     T, Hk, dk, Hv, dv = _dims(q, v, B, T, cu_seqlens)
     if out is None:
-        out = torch.empty_like(v)
+        out = _empty(v.shape, v.dtype, v.device, stream)
     if final_state is None and want_final_state:
-        final_state = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=v.device)
+        final_state = _empty((B, Hv, dv, dk), torch.float32, v.device, stream)
     n0 = initial_state.shape[0] if initial_state is not None else 0
     need = gdn_prefill_workspace_size(B, T, Hk, Hv, dk, dv, chunk, q.dtype,
                                       varlen=cu_seqlens is not None)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+        workspace = _empty(need, torch.uint8, v.device, stream, scratch=True)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = lib().gdn_prefill_chunked(
         _p(q), _p(k), _p(v), _p(alpha), _p(beta), _p(cu_seqlens), _p(initial_state),
@@ -194,17 +213,17 @@ def gdn_prefill_chunked_checkpoints(q, k, v, alpha, beta, *, B: int, checkpoint_
     chunks.  Returns (out, final_state, checkpoints [B, capacity, Hv, dv, dk])."""
     T, Hk, dk, Hv, dv = _dims(q, v, B, T, cu_seqlens)
     if out is None:
-        out = torch.empty_like(v)
+        out = _empty(v.shape, v.dtype, v.device, stream)
     if final_state is None and want_final_state:
-        final_state = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=v.device)
+        final_state = _empty((B, Hv, dv, dk), torch.float32, v.device, stream)
     cap = int(checkpoint_capacity)
     if checkpoints is None and cap > 0:
-        checkpoints = torch.empty((B, cap, Hv, dv, dk), dtype=torch.float32, device=v.device)
+        checkpoints = _empty((B, cap, Hv, dv, dk), torch.float32, v.device, stream)
     n0 = initial_state.shape[0] if initial_state is not None else 0
     need = gdn_prefill_workspace_size(B, T, Hk, Hv, dk, dv, chunk, q.dtype,
                                       varlen=cu_seqlens is not None)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+        workspace = _empty(need, torch.uint8, v.device, stream, scratch=True)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = lib().gdn_prefill_chunked_checkpoints(
         _p(q), _p(k), _p(v), _p(alpha), _p(beta), _p(cu_seqlens), _p(initial_state),
@@ -226,18 +245,18 @@ def gdn_prefill_chunked_capture(q, k, v, alpha, beta, *, B: int, state_update_ca
     Returns (out, final_state, state_update)."""
     T, Hk, dk, Hv, dv = _dims(q, v, B, T, cu_seqlens)
     if out is None:
-        out = torch.empty_like(v)
+        out = _empty(v.shape, v.dtype, v.device, stream)
     if final_state is None and want_final_state:
-        final_state = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=v.device)
+        final_state = _empty((B, Hv, dv, dk), torch.float32, v.device, stream)
     cap = int(state_update_capacity)
     if cap > 0 and state_update is None:
-        state_update = torch.empty((B, cap, slot_width(Hk, Hv, dk, dv)),
-                                   dtype=torch.float32, device=v.device)
+        state_update = _empty((B, cap, slot_width(Hk, Hv, dk, dv)), torch.float32, v.device,
+                              stream)
     n0 = initial_state.shape[0] if initial_state is not None else 0
     need = gdn_prefill_workspace_size(B, T, Hk, Hv, dk, dv, chunk, q.dtype,
                                       varlen=cu_seqlens is not None)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+        workspace = _empty(need, torch.uint8, v.device, stream, scratch=True)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = lib().gdn_prefill_chunked_capture(
         _p(q), _p(k), _p(v), _p(alpha), _p(beta), _p(cu_seqlens), _p(initial_state),
@@ -259,13 +278,13 @@ def gdn_recurrent_capture(q, k, v, alpha, beta, *, B: int, T: Optional[int] = No
     state_update).  final_state may be initial_state itself (in place)."""
     T, Hk, dk, Hv, dv = _dims(q, v, B, T, cu_seqlens)
     if out is None:
-        out = torch.empty_like(v)
+        out = _empty(v.shape, v.dtype, v.device, stream)
     if final_state is None and want_final_state:
-        final_state = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=v.device)
+        final_state = _empty((B, Hv, dv, dk), torch.float32, v.device, stream)
     cap = int(state_update_capacity)
     if cap > 0 and state_update is None:
-        state_update = torch.empty((B, cap, slot_width(Hk, Hv, dk, dv)),
-                                   dtype=torch.float32, device=v.device)
+        state_update = _empty((B, cap, slot_width(Hk, Hv, dk, dv)), torch.float32, v.device,
+                              stream)
     n0 = initial_state.shape[0] if initial_state is not None else 0
     st = lib().gdn_recurrent_capture(
         _p(q), _p(k), _p(v), _p(alpha), _p(beta), _p(cu_seqlens), _p(initial_state),
@@ -283,7 +302,7 @@ def gdn_replay_state_updates(state_in, state_update, accepted_count, *,
     Returns state_out (state_in itself is allowed, in place)."""
     B, Hv, dv, dk = state_in.shape
     if state_out is None:
-        state_out = torch.empty_like(state_in)
+        state_out = _empty(state_in.shape, state_in.dtype, state_in.device, stream)
     st = lib().gdn_replay_state_updates(
         _p(state_in), _p(state_out), _p(state_update), int(state_update_capacity),
         _p(accepted_count), B, int(Hk), Hv, dk, dv, _stream(stream))
@@ -305,15 +324,15 @@ def gdn_replay_verify(q, k, v, alpha, beta, *, B: int, T: Optional[int] = None,
     draft_final_state)."""
     T, Hk, dk, Hv, dv = _dims(q, v, B, T, cu_seqlens)
     if out is None:
-        out = torch.empty_like(v)
+        out = _empty(v.shape, v.dtype, v.device, stream)
     if state_out is None:
-        state_out = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=v.device)
+        state_out = _empty((B, Hv, dv, dk), torch.float32, v.device, stream)
     if draft_final_state is None and want_draft_final_state:
-        draft_final_state = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=v.device)
+        draft_final_state = _empty((B, Hv, dv, dk), torch.float32, v.device, stream)
     cap = int(state_update_capacity)
     if cap > 0 and state_update is None:
-        state_update = torch.empty((B, cap, slot_width(Hk, Hv, dk, dv)),
-                                   dtype=torch.float32, device=v.device)
+        state_update = _empty((B, cap, slot_width(Hk, Hv, dk, dv)), torch.float32, v.device,
+                              stream)
     st = lib().gdn_replay_verify(
         _p(q), _p(k), _p(v), _p(alpha), _p(beta), _p(cu_seqlens), _p(state_in),
         _p(state_out), _p(prev_state_update), int(prev_capacity), _p(accepted_count),
@@ -372,15 +391,15 @@ def gdn_linear_prefill(q, k, v, alpha, *, B: int, T: Optional[int] = None, cu_se
     _linear_check(q, k, v, alpha, cu_seqlens, initial_state, initial_state_indices, final_state,
                   out, B, T, conventions)
     if out is None:
-        out = torch.empty_like(v)
+        out = _empty(v.shape, v.dtype, v.device, stream)
     if final_state is None and want_final_state:
-        final_state = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=v.device)
+        final_state = _empty((B, Hv, dv, dk), torch.float32, v.device, stream)
     n0 = initial_state.shape[0] if initial_state is not None else 0
     if workspace is None:
         need = lib().gdn_linear_prefill_workspace_size(B, T, Hk, Hv, dk, dv, _DT[q.dtype],
                                                        int(cu_seqlens is not None))
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+            workspace = _empty(need, torch.uint8, v.device, stream, scratch=True)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = lib().gdn_linear_prefill(
         _p(q), _p(k), _p(v), _p(alpha), _p(cu_seqlens), _p(initial_state),
@@ -403,14 +422,14 @@ def gdn_linear_recurrent(q, k, v, alpha, *, B: int, T: Optional[int] = None, cu_
     _linear_check(q, k, v, alpha, cu_seqlens, initial_state, initial_state_indices, final_state,
                   out, B, T, conventions)
     if out is None:
-        out = torch.empty_like(v)
+        out = _empty(v.shape, v.dtype, v.device, stream)
     if final_state is None and want_final_state:
-        final_state = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=v.device)
+        final_state = _empty((B, Hv, dv, dk), torch.float32, v.device, stream)
     cap = int(state_update_capacity)
     if cap > 0:
         slots = (B, cap, slot_width(Hk, Hv, dk, dv))
         if state_update is None:
-            state_update = torch.empty(slots, dtype=torch.float32, device=v.device)
+            state_update = _empty(slots, torch.float32, v.device, stream)
         elif not _is(state_update, slots, torch.float32):
             raise ValueError("state_update is float32 [B, capacity, slot_width]")
         if not _is(capture_count, (B,), torch.int32):
@@ -463,7 +482,7 @@ def gdn_gated_norm(x, z=None, weight=None, *, eps: float = 1e-6, gate: int = GDN
             raise ValueError("weight must have one element for each of a head")
         wp, wt = _p(weight), _DT[weight.dtype]
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=x.device)
+        out = _empty(shape, dtype, x.device, stream)
         op, os_ = out.data_ptr(), H * d
     else:
         if out.shape != shape or out.dtype != dtype:
@@ -512,11 +531,11 @@ def gdn_residual_norm(y, residual=None, *, post_weight=None, gate=None,
             raise ValueError("the two weights must have one dtype")
         w2, wt = _p(pre_weight), _DT[pre_weight.dtype]
     if residual_out is None:
-        residual_out = torch.empty(shape, dtype=rdt, device=y.device)
+        residual_out = _empty(shape, rdt, y.device, stream)
     elif residual_out.shape != shape or residual_out.dtype != rdt:
         raise ValueError("residual_out must have the shape of y and the residual's dtype")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=y.device)
+        out = _empty(shape, dtype, y.device, stream)
     elif out.shape != shape or out.dtype != dtype:
         raise ValueError("out must have the shape and the dtype of y")
     yp, ys = _rows(y, 1)
@@ -561,11 +580,11 @@ def gdn_accept_drafts(target_probs, draft_probs, draft_tokens, uniform, *, draft
     if draft_count is not None and (draft_count.shape != (B,) or draft_count.dtype != i32):
         raise ValueError("draft_count is int32 [B]")
     if tokens is None:
-        tokens = torch.empty((B, K1), dtype=i32, device=target_probs.device)
+        tokens = _empty((B, K1), i32, target_probs.device, stream)
     elif tokens.shape != (B, K1) or tokens.dtype != i32:
         raise ValueError("tokens is int32 [B, K + 1]")
     if emitted_count is None:
-        emitted_count = torch.empty((B,), dtype=i32, device=target_probs.device)
+        emitted_count = _empty((B,), i32, target_probs.device, stream)
     elif emitted_count.shape != (B,) or emitted_count.dtype != i32:
         raise ValueError("emitted_count is int32 [B]")
     pp, ps = _positions(target_probs, K1)
