@@ -554,6 +554,8 @@ def _positions(t, K: int):
     if not t.is_cuda:
         raise ValueError("libgdn takes device tensors")
     s0, s1, s2 = t.stride()
+    if K == 1 and t.shape[0] > 1:  # (the stride of a dimension of one says nothing)
+        s1 = s0
     if s2 != 1 or (t.shape[0] > 1 and s0 != K * s1):
         raise ValueError("probabilities must be contiguous rows, evenly spaced")
     return t.data_ptr(), s1
