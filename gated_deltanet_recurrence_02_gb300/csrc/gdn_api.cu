@@ -388,7 +388,7 @@ int gdn_gated_norm(const void *x, const void *z, const void *weight, void *out, 
     const size_t ex = dtype_bytes(dtype_x), ew = dtype_bytes(dtype_w);
     if (!aligned(x, ex) || !aligned(z, ex) || !aligned(out, ex) || !aligned(weight, ew)) return GDN_ERR_ALIGN;
     size_t xb, zb, ob;
-    if (!rows_bytes(N, x_stride, row, ex, &xb) || !rows_bytes(N, z_stride, row, ex, &zb) ||
+    if (!rows_bytes(N, x_stride, row, ex, &xb) || !rows_bytes(N, z ? z_stride : row, row, ex, &zb) ||
         !rows_bytes(N, out_stride, row, ex, &ob))
         return GDN_ERR_INVALID_ARG;
     Span spans[] = {
@@ -426,7 +426,7 @@ int gdn_residual_norm(const void *y, const void *residual, const void *gate, con
         !aligned(residual_out, er) || !aligned(post_weight, ew) || !aligned(pre_weight, ew))
         return GDN_ERR_ALIGN;
     size_t yb, gb, rb, ob;
-    if (!rows_bytes(N, y_stride, D, ex, &yb) || !rows_bytes(N, gate_stride, D, ex, &gb) ||
+    if (!rows_bytes(N, y_stride, D, ex, &yb) || !rows_bytes(N, gate ? gate_stride : D, D, ex, &gb) ||
         !rows_bytes(N, D, D, er, &rb) || !rows_bytes(N, D, D, ex, &ob))
         return GDN_ERR_INVALID_ARG;
     Span spans[] = {
