@@ -110,7 +110,7 @@ bool rows_bytes(int64_t n, int64_t stride, int64_t width, size_t elem, size_t *o
         return true;
     }
     size_t body;
-    if (!mul_ok((size_t)(n - 1), (size_t)stride, &body)) return false;
+    if (!mul_ok((size_t)(n - 1), (size_t)stride, &body) || body > SIZE_MAX - (size_t)width) return false;
     return mul_ok(body + (size_t)width, elem, out);
 }
 
