@@ -722,6 +722,7 @@ cudaError_t launch_rows(const P &p, const Spread &s, int64_t rows, cudaStream_t 
 }
 
 constexpr int kRowSmem = 204800;  // a multiprocessor's shared memory for rows
+constexpr int kSmSmem = 228 * 1024;  // all of it (a CTA takes 1 KB and its barriers besides its rows)
 
 template <int I, int TH>
 struct Shape {
@@ -778,13 +779,17 @@ cudaError_t launch_residual_t(const ResidualNormParams &p, cudaStream_t stream) 
         return with_shape<32 / V>(s, [&](auto shape) {
             using S = decltype(shape);
             constexpr auto kern = residual_row_kernel<T, TR, S::items, S::threads>;
-            // two CTAs an SM where two rows fit each
+            // as many CTAs an SM as make 1024 threads, where two rows fit each of two; as
+            // many stages, up to four, as fit each of them, so that all run at once (4100 x
+            // 2048 bf16 with a gate and an fp32 residual: 20.8 us with three stages, 26.7 with
+            // four, where a quarter of the CTAs are a second wave)
             const int row = p.D * (int)(sizeof(T) * (p.z != nullptr ? 2 : 1) + (p.x != nullptr ? sizeof(TR) : 0));
-            const int most = row <= kRowSmem / 4 ? kRowSmem / 2 : kRowSmem;
+            const int per_sm = row <= kRowSmem / 4 ? 1024 / S::threads : 1;
+            const int most = per_sm > 2 ? kSmSmem / per_sm - 2048 : kRowSmem / per_sm;
             const int stages = most / row > 4 ? 4 : most / row < 1 ? 1 : most / row;
             const cudaError_t e = set_smem_once<kern>(kRowSmem);
             if (e != cudaSuccess) return e;
-            const int64_t ctas = (int64_t)sm_count_of_current_device() * (most < kRowSmem ? 1024 / S::threads : 1);
+            const int64_t ctas = (int64_t)sm_count_of_current_device() * per_sm;
             kern<<<(unsigned)(p.N < ctas ? p.N : ctas), S::threads, stages * row, stream>>>(p, stages);
             return cudaGetLastError();
         });
