@@ -350,34 +350,43 @@ def gdn_linear_prefill_workspace_size(B, T, Hk, Hv, dk, dv, dtype_qkv, varlen=Fa
 
 
 def _is(t, shape, dtype) -> bool:
-    """Whether an optional buffer is absent, a raw pointer, or a tensor of this kind."""
-    return t is None or isinstance(t, int) or (t.shape == shape and t.dtype == dtype)
+    """Whether a buffer is a raw pointer, or a tensor of this kind."""
+    return isinstance(t, int) or (t.shape == shape and t.dtype == dtype)
 
 
-def _linear_check(q, k, v, alpha, cu_seqlens, initial_state, initial_state_indices, final_state,
-                  out, B, T, conventions):
-    """Shapes and dtypes of a linear-attention call: the library sees addresses only, and
-    would read and write past the end of a smaller tensor."""
-    total, Hk, dk = q.shape
-    _, Hv, dv = v.shape
-    if k.shape != q.shape or v.shape[0] != total or not (q.dtype == k.dtype == v.dtype):
+def _linear_dims(q, k, v, alpha, cu_seqlens, initial_state, initial_state_indices, final_state,
+                 out, B, T, conventions):
+    """T, Hk, dk, Hv, dv and the number of initial states of a linear-attention call, with
+    its tensors' shapes and dtypes checked: the library sees addresses only, and would read
+    and write past the end of a smaller tensor.  (Each shape is asked for once, as that is
+    what the checks cost.)"""
+    total, Hk, dk = q_shape = q.shape
+    rows, Hv, dv = v_shape = v.shape
+    dtype = q.dtype
+    if k.shape != q_shape or rows != total or k.dtype != dtype or v.dtype != dtype:
         raise ValueError("q and k are [total_T, Hk, dk], v [total_T, Hv, dv], of one dtype")
     if alpha.shape != ((Hv,) if conventions & GDN_ALPHA_PER_HEAD else (total, Hv)):
         raise ValueError("alpha is [Hv] with GDN_ALPHA_PER_HEAD and [total_T, Hv] without")
-    if cu_seqlens is None:
-        if B * T > total:
-            raise ValueError("q, k and v hold B rows of T tokens")
-    elif not _is(cu_seqlens, (B + 1,), torch.int32):
-        raise ValueError("cu_seqlens is int32 [B + 1]")
-    if initial_state is not None and (initial_state.dtype != torch.float32
-                                      or initial_state.shape[1:] != (Hv, dv, dk)):
-        raise ValueError("initial_state is float32 [states, Hv, dv, dk]")
-    if not _is(initial_state_indices, (B,), torch.int32):
-        raise ValueError("initial_state_indices is int32 [B]")
-    if not _is(final_state, (B, Hv, dv, dk), torch.float32):
+    if cu_seqlens is not None:
+        T = total
+        if not _is(cu_seqlens, (B + 1,), torch.int32):
+            raise ValueError("cu_seqlens is int32 [B + 1]")
+    elif T is None:
+        T = total // B if B else 0
+    elif B * T > total:
+        raise ValueError("q, k and v hold B rows of T tokens")
+    states = 0
+    if initial_state is not None:
+        states, *state = initial_state.shape
+        if state != [Hv, dv, dk] or initial_state.dtype != torch.float32:
+            raise ValueError("initial_state is float32 [states, Hv, dv, dk]")
+        if initial_state_indices is not None and not _is(initial_state_indices, (B,), torch.int32):
+            raise ValueError("initial_state_indices is int32 [B]")
+    if final_state is not None and not _is(final_state, (B, Hv, dv, dk), torch.float32):
         raise ValueError("final_state is float32 [B, Hv, dv, dk]")
-    if not _is(out, v.shape, v.dtype):
+    if out is not None and not _is(out, v_shape, dtype):
         raise ValueError("out must have the shape and the dtype of v")
+    return int(T), Hk, dk, Hv, dv, states
 
 
 def gdn_linear_prefill(q, k, v, alpha, *, B: int, T: Optional[int] = None, cu_seqlens=None,
@@ -387,14 +396,12 @@ def gdn_linear_prefill(q, k, v, alpha, *, B: int, T: Optional[int] = None, cu_se
     """Linear attention with a decay for each head, chunked form.  alpha is
     [total_T, Hv], or [Hv] with GDN_ALPHA_PER_HEAD in conventions.  Returns
     (out, final_state)."""
-    T, Hk, dk, Hv, dv = _dims(q, v, B, T, cu_seqlens)
-    _linear_check(q, k, v, alpha, cu_seqlens, initial_state, initial_state_indices, final_state,
-                  out, B, T, conventions)
+    T, Hk, dk, Hv, dv, n0 = _linear_dims(q, k, v, alpha, cu_seqlens, initial_state,
+                                         initial_state_indices, final_state, out, B, T, conventions)
     if out is None:
         out = _empty(v.shape, v.dtype, v.device, stream)
     if final_state is None and want_final_state:
         final_state = _empty((B, Hv, dv, dk), torch.float32, v.device, stream)
-    n0 = initial_state.shape[0] if initial_state is not None else 0
     if workspace is None:
         need = lib().gdn_linear_prefill_workspace_size(B, T, Hk, Hv, dk, dv, _DT[q.dtype],
                                                        int(cu_seqlens is not None))
@@ -418,9 +425,8 @@ def gdn_linear_recurrent(q, k, v, alpha, *, B: int, T: Optional[int] = None, cu_
     """Linear attention token by token, with the compact capture (delta = v).
     Returns (out, final_state, state_update).  final_state may be
     initial_state itself (in place)."""
-    T, Hk, dk, Hv, dv = _dims(q, v, B, T, cu_seqlens)
-    _linear_check(q, k, v, alpha, cu_seqlens, initial_state, initial_state_indices, final_state,
-                  out, B, T, conventions)
+    T, Hk, dk, Hv, dv, n0 = _linear_dims(q, k, v, alpha, cu_seqlens, initial_state,
+                                         initial_state_indices, final_state, out, B, T, conventions)
     if out is None:
         out = _empty(v.shape, v.dtype, v.device, stream)
     if final_state is None and want_final_state:
@@ -432,12 +438,11 @@ def gdn_linear_recurrent(q, k, v, alpha, *, B: int, T: Optional[int] = None, cu_
             state_update = _empty(slots, torch.float32, v.device, stream)
         elif not _is(state_update, slots, torch.float32):
             raise ValueError("state_update is float32 [B, capacity, slot_width]")
-        if not _is(capture_count, (B,), torch.int32):
+        if capture_count is not None and not _is(capture_count, (B,), torch.int32):
             raise ValueError("capture_count is int32 [B]")
         if not (state_update_active is None or isinstance(state_update_active, int)
                 or (state_update_active.dtype == torch.int32 and state_update_active.numel() >= 1)):
             raise ValueError("state_update_active is an int32 on the device")
-    n0 = initial_state.shape[0] if initial_state is not None else 0
     st = lib().gdn_linear_recurrent(
         _p(q), _p(k), _p(v), _p(alpha), _p(cu_seqlens), _p(initial_state),
         _p(initial_state_indices), n0, _p(final_state), _p(out), B, T, Hk, Hk, Hv, dk, dv,
@@ -634,7 +639,6 @@ def gdn_prefill_chunked_noalloc(q, k, v, alpha, beta, *, B: int, T: Optional[int
         fn.argtypes = [vp] * 8 + [i, vp, vp] + [i] * 8 + [f, i, i, vp]
         fn.restype = ctypes.c_int
     T, Hk, dk, Hv, dv = _dims(q, v, B, T, cu_seqlens)
-    n0 = initial_state.shape[0] if initial_state is not None else 0
     st = fn(_p(q), _p(k), _p(v), _p(alpha), _p(beta), _p(cu_seqlens), _p(initial_state),
             _p(initial_state_indices), n0, _p(final_state), _p(out), B, T, Hk, Hk, Hv, dk, dv,
             chunk, scale, *_codes(q, alpha, conventions), _stream(stream))
