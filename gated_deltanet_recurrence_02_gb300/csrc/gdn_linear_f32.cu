@@ -12,7 +12,7 @@
 // Bound by fp32 arithmetic: 3 dk dv multiplications and fused multiply-adds a token and
 // head (the decayed state, the update, the readout), 172 us for 4100 tokens of 32 heads
 // with dk = dv = 128 on all SMs and two thirds of that again for the segments' first
-// pass, against 30 us of HBM time.  Measured there: 435 us (four state rows a lane;
+// pass, against 30 us of HBM time.  Measured there: 431 us (four state rows a lane;
 // 554 us with two, which loads k and q twice as often from shared memory).  The chunked
 // form on the tensor cores would need each operand as sums of tf32 numbers and three
 // products for each (about 40 us of tensor time at that size): not built; 16-bit inputs
@@ -232,7 +232,7 @@ int rows_of(int dv) { return dv % 64 == 0 ? 64 : 32; }
 // Segments a row: as many as fill three CTAs on every SM, of 64 tokens at least, where
 // that makes four or more.  The first pass costs two thirds of the work again, and three
 // CTAs on an SM take 2.2 times as long as one: at dk = dv = 128, 32 heads and 4100 tokens
-// took 832 us as one segment, 535 as 4, 435 as 7; two rows of 2048: 420 us, 498 as 3.
+// took 832 us as one segment, 535 as 4, 431 as 7; two rows of 2048: 420 us, 498 as 3.
 int segments(int B, int T, int Hv, int dv, bool varlen) {
     const long slots = 3l * sm_count_of_current_device(), units = (long)B * Hv * (dv / rows_of(dv));
     if (units == 0) return 1;

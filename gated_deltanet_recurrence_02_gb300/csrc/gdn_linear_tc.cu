@@ -31,7 +31,7 @@
 // products take about 1630 cycles of the tensor pipe (390 R, 195 O1, 260 O2, 780 dS:
 // an M = 128, K = 16 MMA runs for 49 cycles at N = 64 with A in shared memory, 33 with A
 // in TMEM, 65 at N = 128).  Measured: 64 packed rows of 500 to 1500 tokens, 32 heads,
-// bf16: 337 us without initial states, 365 with (5.0 TB/s, 0.75 of the measured copy
+// bf16: 343 us without initial states, 370 with (5.0 TB/s, 0.74 of the measured copy
 // bandwidth), some 2100 cycles a chunk: between the end of one dS and the start of the
 // next stand the state warps' read of it and, with one buffer of W, the store of the next
 // W's first half, and every role's instructions compete for the issue slots and the
@@ -39,8 +39,8 @@
 // runs, gained nothing; nor did freeing the outputs' columns before their last part.)
 // One row of 4100 tokens: 57 us, two passes of 25 and 31 us (a chunk takes a CTA as long
 // alone, and 17 of them one after another are most of a pass).  12 rows of 200 to 1000
-// tokens, 6 heads, d = 64, fp16: 33 us, the same chain.  128 rows of 16 tokens with their
-// states: 160 us (0.54): a unit's state is read, used and written by the same four warps.
+// tokens, 6 heads, d = 64, fp16: 33 to 35 us, the same chain.  128 rows of 16 tokens with their
+// states: 161 us (0.54): a unit's state is read, used and written by the same four warps.
 //
 // One persistent CTA a SM, warp-specialised, four stages of tiles in flight; every
 // hand-off between the roles is an mbarrier:
@@ -58,7 +58,8 @@
 // TMA, 1345 -> 433 us; code small enough for the instruction cache (each role's loops
 // rolled where they can be), 433 -> 390 us; W formed in registers by two warpgroups and
 // P on three warps, 390 -> 370 us; three parts of W for four, states prefetched, and W's
-// loop rolled, 370 -> 337 us.
+// loop rolled, 370 -> 343 us.  (Where a cold loop stands can cost as much: the tile warp's
+// last waits, moved behind the roles or with another form of the wait, 343 -> 357 to 365.)
 //
 // Few rows are cut into segments of whole chunks, so that every SM has one: a
 // first pass (kStateOnly) forms each segment's end state from zeros, a small kernel
@@ -266,7 +267,7 @@ linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap mq, cons
     bool ok = true;
     // Waits run out p.limit nanoseconds after the warp's last chunk came.  (The roles'
     // loops share the instruction cache, and every wait's instructions count there:
-    // 64 packed rows took 400 us with 3 KB more of them, 337 with 4 KB less.)
+    // 64 packed rows took 400 us with 3 KB more of them, 343 with 4 KB less.)
     uint32_t since = globaltimer_lo();
     // A wait of a whole warp: the outcome is the same in every lane, so that
     // the warp-wide TMEM accesses behind it stay converged.

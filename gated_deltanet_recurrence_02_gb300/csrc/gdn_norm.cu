@@ -16,14 +16,15 @@
 // the table is its start and end; 16-bit elements cost their conversions and the gate's
 // exponential and reciprocal besides, so the gated norm's time follows its instructions.
 // Measured:
-//   gated, 4100 x 32 x 128 bf16   19.6 to 20.7 us (4.9 TB/s, 0.72 to 0.76 of the measured
+//   gated, 4100 x 32 x 128 bf16   18.5 to 20.1 us (5.0 to 5.4 TB/s, 0.74 to 0.80 of the measured
 //     copy bandwidth; 22.7 with a division a row and one element an instruction, 26.5
-//     with the next row in registers instead of the ring below); fp32 36 us (5.5 TB/s)
-//   residual, 4100 x 4096 bf16, fp32 residual, gate, both norms   44 us (5.3 TB/s, 0.78;
-//     52 with the ring of per-thread copies that shorter rows use); 2050 x 8192: 48 us
-//     (72); 10000 x 1024 bf16, bf16 residual: 22.5 us (4.5 TB/s)
+//     with the next row in registers instead of the ring below); fp32 35 us (5.8 TB/s)
+//   residual, 4100 x 4096 bf16, fp32 residual, gate, both norms   45 us (5.2 TB/s, 0.77;
+//     52 with the ring of per-thread copies that shorter rows use); 2050 x 8192: 53 us;
+//     4100 x 2048: 21 us (5.6 TB/s); 10000 x 1024 bf16, bf16 residual: 22.5 us (4.5 TB/s)
 // Rows that are not aligned to 16 bytes (odd widths, odd strides) are read and written an
-// element a lane: 4100 x 2047 bf16 41 us (floor 12), 2000 x 32 x 129 24 us (7).
+// element a lane: 4100 x 2047 bf16, fp32 residual, gate
+// 37 us (floor 17), 2000 x 32 x 129 23 us (7).
 #include <atomic>
 
 #include "gdn_internal.cuh"
@@ -250,8 +251,11 @@ struct Ring {
     __device__ __forceinline__ static int next(int slot) { return slot + 1 == DEPTH ? 0 : slot + 1; }
 };
 
-// CTAs an SM at least, which is a limit of registers: 64 a thread, and more where a row
-// takes them (4100 x 4095 bf16, eight elements a thread: 90 us with 64 and spills, 70).
+// CTAs an SM at least, which is a limit of registers: 64 a thread, 80 or 128 where a row
+// has more elements a thread (4100 x 4095 bf16, eight of them: 90 us with 64 and spills,
+// 71).  The widest rows still spill: the gated norm's of more than 16 elements a thread
+// some 340 (16-bit) and 1060 bytes (fp32) a thread, and unaligned rows of more than 8192
+// elements, where 1024 threads leave 64 registers each, 780 to 1090.
 constexpr int ctas_of(int vec, int items, int threads) {
     return vec * items > 8 ? 1 : (vec == 1 && items > 5 ? 768 : 1024) / threads;
 }
@@ -678,7 +682,7 @@ residual_row_kernel(const ResidualNormParams p, int stages) {
 // How a row of `width` elements is spread over threads of ITEMS vectors each.
 // Rows of up to 32 vectors take the smallest power of two of lanes of one vector
 // each, so several rows share a warp; up to 128 (single elements: 512, where a CTA's
-// two barriers a row made 4100 x 4 rows of 257 take 43 us, now 25) a warp; longer
+// two barriers a row made 4100 x 4 rows of 257 take 43 us, now 23) a warp; longer
 // ones a whole CTA.
 struct Spread {
     int lanes, threads, items;
@@ -731,7 +735,7 @@ struct Shape {
 // Calls f with the spread's threads and the least items of those built that hold its
 // row as constants.  A row of vectors has at most 32 elements a thread, so never more
 // than MOST vectors, in powers of two; single elements come in finer steps, as their
-// loads and stores are what such rows cost (2000 x 32 x 129 bf16: 25 us as five a lane,
+// loads and stores are what such rows cost (2000 x 32 x 129 bf16: 23 us as five a lane,
 // 35 as eight).
 template <int MOST, int THREADS, int I, typename F>
 cudaError_t with_items(int items, F f) {
