@@ -423,7 +423,8 @@ GDN_API int gdn_residual_norm(const void *y, const void *residual, const void *g
  * gdn_accept_drafts -- verification of drafted tokens against the target's
  * probabilities, from given random numbers (speculative sampling).  Row b has
  * c_b drafts x_i, i < c_b:
- *     n      = the first i < c_b with  uniform_i * q_i(x_i) >= p_i(x_i),  else c_b
+ *     n      = the first i < c_b without  uniform_i * q_i(x_i) < p_i(x_i)  (a NaN
+ *              rejects),  else c_b
  *     weight = max(p_n - q_n, 0) if n < c_b, else p_n
  *     token  = the first j whose running sum of weights exceeds uniform_K * total
  * Weights are held in whole units of 2^-40 (rounded down, at most 1, NaN as 0),
