@@ -639,6 +639,7 @@ def gdn_prefill_chunked_noalloc(q, k, v, alpha, beta, *, B: int, T: Optional[int
         fn.argtypes = [vp] * 8 + [i, vp, vp] + [i] * 8 + [f, i, i, vp]
         fn.restype = ctypes.c_int
     T, Hk, dk, Hv, dv = _dims(q, v, B, T, cu_seqlens)
+    n0 = initial_state.shape[0] if initial_state is not None else 0
     st = fn(_p(q), _p(k), _p(v), _p(alpha), _p(beta), _p(cu_seqlens), _p(initial_state),
             _p(initial_state_indices), n0, _p(final_state), _p(out), B, T, Hk, Hk, Hv, dk, dv,
             chunk, scale, *_codes(q, alpha, conventions), _stream(stream))
