@@ -114,6 +114,66 @@ bool rows_bytes(int64_t n, int64_t stride, int64_t width, size_t elem, size_t *o
     return mul_ok(body + (size_t)width, elem, out);
 }
 
+// Rows of `width` elements, `stride` apart, of a tensor.
+struct RowSpan {
+    const void *p;
+    int64_t n, stride, width;
+    bool is_output;
+};
+
+// GDN_ERR_ALIAS if an output's rows overlap other rows (all of elements of `elem` bytes),
+// except rows that are exactly the same where `allow_a`, `allow_b` say so.  Rows of one
+// stride may be interleaved.
+int check_row_alias(const RowSpan *s, int n, size_t elem, int allow_a, int allow_b) {
+    for (int i = 0; i < n; ++i)
+        for (int j = i + 1; j < n; ++j) {
+            if ((!s[i].is_output && !s[j].is_output) || s[i].p == nullptr || s[j].p == nullptr) continue;
+            size_t a, b;
+            if (!rows_bytes(s[i].n, s[i].stride, s[i].width, elem, &a) ||
+                !rows_bytes(s[j].n, s[j].stride, s[j].width, elem, &b))
+                return GDN_ERR_INVALID_ARG;
+            if (!overlaps({s[i].p, a, true}, {s[j].p, b, true})) continue;
+            const bool pair = (i == allow_a && j == allow_b) || (i == allow_b && j == allow_a);
+            if (pair && s[i].p == s[j].p && s[i].n == s[j].n && s[i].width == s[j].width &&
+                (s[i].stride == s[j].stride || s[i].n == 1))
+                continue;
+            if (s[i].stride == s[j].stride) {
+                const uint64_t step = (uint64_t)s[i].stride * elem;
+                const uint64_t x = reinterpret_cast<uintptr_t>(s[i].p), y = reinterpret_cast<uintptr_t>(s[j].p);
+                const uint64_t behind = y >= x ? (y - x) % step : (step - (x - y) % step) % step;
+                if (behind >= (uint64_t)s[i].width * elem && behind + (uint64_t)s[j].width * elem <= step) continue;
+            }
+            return GDN_ERR_ALIAS;
+        }
+    return GDN_OK;
+}
+
+// Sizes, strides and alignment of a cache in pages, and the bytes from its first to its
+// last element.
+int check_pages(const void *k, const void *v, const int32_t *table, const int32_t *lens, int B, int Hk, int d,
+                int num_pages, int page_size, int max_pages, int64_t page_stride, int64_t slot_stride,
+                int64_t head_stride, size_t elem, size_t *bytes) {
+    if (num_pages < 0 || page_size <= 0 || max_pages < 0) return GDN_ERR_INVALID_ARG;
+    if ((num_pages > 1 && page_stride < d) || (page_size > 1 && slot_stride < d) || (Hk > 1 && head_stride < d) ||
+        page_stride < 0 || slot_stride < 0 || head_stride < 0)
+        return GDN_ERR_INVALID_ARG;
+    if (!lens || (max_pages > 0 && !table) || (num_pages > 0 && (!k || !v))) return GDN_ERR_INVALID_ARG;
+    if (!aligned(k, elem) || !aligned(v, elem) || !aligned(table, 4) || !aligned(lens, 4)) return GDN_ERR_ALIGN;
+    *bytes = 0;
+    if (num_pages == 0) return GDN_OK;
+    size_t a, b, c, sum = (size_t)d;
+    if (!mul_ok((size_t)(num_pages - 1), (size_t)page_stride, &a) ||
+        !mul_ok((size_t)(page_size - 1), (size_t)slot_stride, &b) ||
+        !mul_ok((size_t)(Hk - 1), (size_t)head_stride, &c))
+        return GDN_ERR_INVALID_ARG;
+    for (size_t x : {a, b, c}) {
+        if (x > (SIZE_MAX >> 4) - sum) return GDN_ERR_INVALID_ARG;
+        sum += x;
+    }
+    *bytes = sum * elem;
+    return GDN_OK;
+}
+
 // Sizes shared by prefill and recurrent calls.
 struct Shapes {
     size_t total_T, qk_bytes, v_bytes, gate_bytes, s0_bytes, sf_bytes;
@@ -488,6 +548,164 @@ int gdn_accept_drafts(const void *target_probs, const void *draft_probs, const i
     p.B = B; p.K = K; p.V = V; p.ps = target_stride; p.qs = draft_stride; p.dt = dtype_probs;
     if (error_word(&p.err) != cudaSuccess) return GDN_ERR_CUDA;
     return launch_accept(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+int gdn_rotary(const void *x, void *out, const int32_t *positions, const int32_t *axes, const float *inv_freq,
+               int64_t N, int H, int d, int R, int A, int64_t x_stride, int64_t out_stride, int flags, int dtype,
+               void *stream) {
+    if (N < 0 || H <= 0 || d <= 0 || R < 0 || R > d || (R & 1) || A <= 0) return GDN_ERR_INVALID_ARG;
+    const size_t e = dtype_bytes(dtype);
+    if ((flags & ~(GDN_ROTARY_PAIRS | GDN_ROTARY_INVERSE)) || e == 0) return GDN_ERR_INVALID_ARG;
+    if (H > kRotaryMaxHeads || d > kRotaryMaxWidth) return GDN_ERR_UNSUPPORTED;
+    const int64_t row = (int64_t)H * d;
+    if (x_stride < row || out_stride < row) return GDN_ERR_INVALID_ARG;
+    if (N > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    if (N == 0) return GDN_OK;
+    if (!x || !out || (R > 0 && (!positions || !inv_freq))) return GDN_ERR_INVALID_ARG;
+    if (!aligned(x, e) || !aligned(out, e) || !aligned(positions, 4) || !aligned(axes, 4) || !aligned(inv_freq, 4))
+        return GDN_ERR_ALIGN;
+    const RowSpan rows[] = {{x, N, x_stride, row, false}, {out, N, out_stride, row, true}};
+    int st = check_row_alias(rows, 2, e, 0, 1);
+    if (st != GDN_OK) return st;
+    size_t ob, pb;
+    if (!rows_bytes(N, out_stride, row, e, &ob) || !mul_ok((size_t)N * 4, (size_t)A, &pb)) return GDN_ERR_INVALID_ARG;
+    const Span spans[] = {
+        {positions, R > 0 ? pb : 0, false},
+        {axes, axes ? (size_t)R * 2 : 0, false},
+        {inv_freq, inv_freq ? (size_t)R * 2 : 0, false},
+        {out, ob, true},
+    };
+    st = check_alias(spans, 4, -1, -1);
+    if (st != GDN_OK) return st;
+    RotaryParams p{};
+    p.q = x; p.q_out = out; p.N = N; p.qs = x_stride; p.os = out_stride;
+    p.pos = positions; p.axes = axes; p.inv_freq = inv_freq;
+    p.Hq = H; p.d = d; p.R = R; p.A = A; p.flags = flags; p.dt = dtype;
+    if (error_word(&p.err) != cudaSuccess) return GDN_ERR_CUDA;
+    return launch_rotary(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+int gdn_paged_append(const void *q, const void *k, const void *v, void *q_out, void *k_pages, void *v_pages,
+                     const int32_t *page_table, const int32_t *kv_lens, const int32_t *cu_seqlens,
+                     const int32_t *positions, const int32_t *axes, const float *inv_freq, int B, int T, int Hq,
+                     int Hk, int d, int R, int A, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                     int64_t q_out_stride, int num_pages, int page_size, int max_pages, int64_t page_stride,
+                     int64_t slot_stride, int64_t head_stride, int flags, int dtype, void *stream) {
+    if (B < 0 || T < 0 || Hq < 0 || Hk <= 0 || d <= 0 || R < 0 || R > d || (R & 1) || A <= 0) return GDN_ERR_INVALID_ARG;
+    const size_t e = dtype_bytes(dtype);
+    if ((flags & ~GDN_ROTARY_PAIRS) || e == 0) return GDN_ERR_INVALID_ARG;
+    if (Hq > kRotaryMaxHeads || Hk > kRotaryMaxHeads || d > kRotaryMaxWidth || B > 65535) return GDN_ERR_UNSUPPORTED;
+    const int64_t N = cu_seqlens ? T : (int64_t)B * T, qrow = (int64_t)Hq * d, krow = (int64_t)Hk * d;
+    if (k_stride < krow || v_stride < krow || (Hq > 0 && (q_stride < qrow || q_out_stride < qrow)))
+        return GDN_ERR_INVALID_ARG;
+    if (N > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    if (B == 0 || N == 0) return GDN_OK;
+    if (!k || !v || (Hq > 0) != (q != nullptr) || (Hq > 0) != (q_out != nullptr) || (R > 0 && !inv_freq))
+        return GDN_ERR_INVALID_ARG;
+    size_t pages;
+    int st = check_pages(k_pages, v_pages, page_table, kv_lens, B, Hk, d, num_pages, page_size, max_pages, page_stride,
+                         slot_stride, head_stride, e, &pages);
+    if (st != GDN_OK) return st;
+    if (!aligned(q, e) || !aligned(k, e) || !aligned(v, e) || !aligned(q_out, e) || !aligned(cu_seqlens, 4) ||
+        !aligned(positions, 4) || !aligned(axes, 4) || !aligned(inv_freq, 4))
+        return GDN_ERR_ALIGN;
+    if (num_pages > 0 && k_pages == v_pages) return GDN_ERR_ALIAS;
+    const RowSpan rows[] = {{q, N, q_stride, qrow, false},
+                            {k, N, k_stride, krow, false},
+                            {v, N, v_stride, krow, false},
+                            {q_out, N, q_out_stride, qrow, true}};
+    st = check_row_alias(rows, 4, e, 0, 3);
+    if (st != GDN_OK) return st;
+    size_t qb, kb, vb, ob, pb, tb;
+    if (!rows_bytes(q ? N : 0, q_stride, qrow, e, &qb) || !rows_bytes(N, k_stride, krow, e, &kb) ||
+        !rows_bytes(N, v_stride, krow, e, &vb) || !rows_bytes(q ? N : 0, q_out_stride, qrow, e, &ob) ||
+        !mul_ok((size_t)N * 4, (size_t)A, &pb) || !mul_ok((size_t)B * 4, (size_t)max_pages, &tb))
+        return GDN_ERR_INVALID_ARG;
+    // (keys' and values' pages may be interleaved, so each is looked at alone)
+    for (int i = 0; i < 3; ++i) {
+        const bool cache = i < 2;
+        const Span spans[] = {
+            {q, cache ? qb : 0, false}, {k, cache ? kb : 0, false}, {v, cache ? vb : 0, false},
+            {q_out, cache ? ob : 0, false},
+            {page_table, tb, false},
+            {kv_lens, (size_t)B * 4, false},
+            {cu_seqlens, cu_seqlens ? (size_t)(B + 1) * 4 : 0, false},
+            {positions, positions && R > 0 ? pb : 0, false},
+            {axes, axes ? (size_t)R * 2 : 0, false},
+            {inv_freq, inv_freq ? (size_t)R * 2 : 0, false},
+            {i == 0 ? k_pages : i == 1 ? v_pages : q_out, cache ? pages : ob, true},
+        };
+        st = check_alias(spans, (int)(sizeof(spans) / sizeof(spans[0])), -1, -1);
+        if (st != GDN_OK) return st;
+    }
+    RotaryParams p{};
+    p.q = q; p.k = k; p.v = v; p.q_out = q_out; p.k_pages = k_pages; p.v_pages = v_pages;
+    p.N = N; p.qs = q_stride; p.ks = k_stride; p.vs = v_stride; p.os = q_out_stride;
+    p.page_stride = page_stride; p.slot_stride = slot_stride; p.head_stride = head_stride;
+    p.pos = positions; p.axes = axes; p.inv_freq = inv_freq;
+    p.page_table = page_table; p.kv_lens = kv_lens; p.cu_seqlens = cu_seqlens;
+    p.B = B; p.T = T; p.Hq = Hq; p.Hk = Hk; p.d = d; p.R = R; p.A = A;
+    p.page_size = page_size; p.num_pages = num_pages; p.max_pages = max_pages;
+    p.flags = flags; p.dt = dtype;
+    if (error_word(&p.err) != cudaSuccess) return GDN_ERR_CUDA;
+    return launch_rotary(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+size_t gdn_paged_attention_workspace_size(int B, int T, int Hq, int Hk, int d, int dtype, int varlen) {
+    if (B < 0 || T < 0 || Hq <= 0 || Hk <= 0 || Hq % Hk != 0 || d <= 0 || dtype_bytes(dtype) == 0) return (size_t)-1;
+    return attention_workspace_bytes(B, T, Hq, Hk, d, dtype, varlen != 0);
+}
+
+int gdn_paged_attention(const void *q, const void *k_pages, const void *v_pages, const int32_t *page_table,
+                        const int32_t *kv_lens, const int32_t *cu_seqlens, void *out, float *lse, int B, int T,
+                        int Hq, int Hk, int d, int64_t q_stride, int num_pages, int page_size, int max_pages,
+                        int64_t page_stride, int64_t slot_stride, int64_t head_stride, float scale, int window,
+                        int flags, int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    if (B < 0 || T < 0 || Hq <= 0 || Hk <= 0 || Hq % Hk != 0 || d <= 0 || window < 0) return GDN_ERR_INVALID_ARG;
+    const size_t e = dtype_bytes(dtype);
+    if ((flags & ~GDN_ATTENTION_FULL) || e == 0 || (window > 0 && (flags & GDN_ATTENTION_FULL))) return GDN_ERR_INVALID_ARG;
+    if (!(d == 32 || d == 64 || d == 128) || B > 65535) return GDN_ERR_UNSUPPORTED;
+    const int64_t N = cu_seqlens ? T : (int64_t)B * T, row = (int64_t)Hq * d;
+    if (q_stride < row) return GDN_ERR_INVALID_ARG;
+    if (N > INT32_MAX / Hq) return GDN_ERR_UNSUPPORTED;
+    if (B == 0 || N == 0) return GDN_OK;
+    if (!q || !out) return GDN_ERR_INVALID_ARG;
+    size_t pages;
+    int st = check_pages(k_pages, v_pages, page_table, kv_lens, B, Hk, d, num_pages, page_size, max_pages, page_stride,
+                         slot_stride, head_stride, e, &pages);
+    if (st != GDN_OK) return st;
+    if (!aligned(q, e) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(cu_seqlens, 4)) return GDN_ERR_ALIGN;
+    const size_t need = attention_workspace_bytes(B, T, Hq, Hk, d, dtype, cu_seqlens != nullptr);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+    if (workspace && !aligned(workspace, 16)) return GDN_ERR_ALIGN;
+    size_t qb, tb;
+    if (!rows_bytes(N, q_stride, row, e, &qb) || !mul_ok((size_t)B * 4, (size_t)max_pages, &tb))
+        return GDN_ERR_INVALID_ARG;
+    const Span spans[] = {
+        {q, qb, false},
+        {k_pages, pages, false},
+        {v_pages, pages, false},
+        {page_table, tb, false},
+        {kv_lens, (size_t)B * 4, false},
+        {cu_seqlens, cu_seqlens ? (size_t)(B + 1) * 4 : 0, false},
+        {out, (size_t)N * row * e, true},
+        {lse, lse ? (size_t)N * Hq * 4 : 0, true},
+        {workspace, need, true},
+    };
+    st = check_alias(spans, (int)(sizeof(spans) / sizeof(spans[0])), -1, -1);
+    if (st != GDN_OK) return st;
+    AttentionParams p{};
+    p.q = q; p.k_pages = k_pages; p.v_pages = v_pages;
+    p.page_table = page_table; p.kv_lens = kv_lens; p.cu_seqlens = cu_seqlens;
+    p.out = out; p.lse = lse;
+    p.B = B; p.T = T; p.Hq = Hq; p.Hk = Hk; p.d = d;
+    p.page_size = page_size; p.num_pages = num_pages; p.max_pages = max_pages;
+    p.qs = q_stride; p.page_stride = page_stride; p.slot_stride = slot_stride; p.head_stride = head_stride;
+    p.scale = scale; p.window = window; p.causal = !(flags & GDN_ATTENTION_FULL); p.dt = dtype;
+    p.ws = workspace;
+    p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+    if (error_word(&p.err) != cudaSuccess) return GDN_ERR_CUDA;
+    return launch_attention(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 int gdn_replay_verify(const void *q, const void *k, const void *v, const void *alpha,

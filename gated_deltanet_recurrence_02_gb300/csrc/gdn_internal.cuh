@@ -133,6 +133,41 @@ struct AcceptParams {
     uint32_t *err;
 };
 
+// Rotation of queries (or any heads: gdn_rotary has only these), and keys and values on
+// their way into a paged cache.  Element (n, h, i) of q is q[n * qs + h * d + i], of k and
+// v with ks and vs; of a page's slot page * page_stride + slot * slot_stride + h *
+// head_stride + i.
+struct RotaryParams {
+    const void *q, *k, *v;
+    void *q_out, *k_pages, *v_pages;
+    int64_t N, qs, ks, vs, os;
+    int64_t page_stride, slot_stride, head_stride;
+    const int32_t *pos, *axes;  // [A, N] (nullptr: cache positions), [R / 2] or nullptr
+    const float *inv_freq;
+    const int32_t *page_table, *kv_lens, *cu_seqlens;
+    int B, T, Hq, Hk, d, R, A, page_size, num_pages, max_pages;
+    int flags, dt;  // GDN_ROTARY_*
+    uint32_t *err;
+};
+
+// Attention over a paged cache (gdn_paged_attention).
+struct AttentionParams {
+    const void *q, *k_pages, *v_pages;
+    const int32_t *page_table, *kv_lens, *cu_seqlens;
+    void *out;
+    float *lse;
+    int B, T, Hq, Hk, d, page_size, num_pages, max_pages;
+    int64_t qs, page_stride, slot_stride, head_stride;
+    float scale;
+    int window;
+    bool causal;
+    int dt;
+    void *ws;
+    uint64_t wait_ns;
+    uint32_t *err;
+};
+
+constexpr int kRotaryMaxHeads = 16384, kRotaryMaxWidth = 1024;
 constexpr int kNormMaxWidth = 16384;
 constexpr int kAcceptMaxVocab = 1 << 22;   // sums of 2^40 units a token stay below 2^62
 constexpr int kAcceptMaxDrafts = 1024;
@@ -187,6 +222,9 @@ size_t linear_f32_workspace_bytes(int B, int T, int Hv, int dk, int dv, bool var
 cudaError_t launch_gated_norm(const GatedNormParams &p, cudaStream_t stream);
 cudaError_t launch_residual_norm(const ResidualNormParams &p, cudaStream_t stream);
 cudaError_t launch_accept(const AcceptParams &p, cudaStream_t stream);
+cudaError_t launch_rotary(const RotaryParams &p, cudaStream_t stream);
+cudaError_t launch_attention(const AttentionParams &p, cudaStream_t stream);
+size_t attention_workspace_bytes(int B, int T, int Hq, int Hk, int d, int dt, bool varlen);
 
 // Raises kernel Kern's dynamic shared-memory limit to `bytes`, once per device
 // (function attributes belong to the device's context): later calls make no

@@ -27,6 +27,9 @@ GDN_ALPHA_PER_HEAD = 0x800
 # gates of the norms
 GDN_GATE_NONE, GDN_GATE_SILU, GDN_GATE_SIGMOID = 0, 1, 2
 GDN_GATE_FIRST, GDN_NORM_UNIT_OFFSET = 0x10, 0x20
+# rotation and cached attention
+GDN_ROTARY_PAIRS, GDN_ROTARY_INVERSE = 0x1, 0x2
+GDN_ATTENTION_FULL = 0x1
 _DT = {torch.float32: GDN_F32, torch.float16: GDN_F16, torch.bfloat16: GDN_BF16}
 
 _lib = None
@@ -82,6 +85,14 @@ def lib() -> ctypes.CDLL:
     L.gdn_residual_norm.restype = i
     L.gdn_accept_drafts.argtypes = [vp] * 7 + [i, i, i, i64, i64, i, vp]
     L.gdn_accept_drafts.restype = i
+    L.gdn_rotary.argtypes = [vp] * 5 + [i64, i, i, i, i, i64, i64, i, i, vp]
+    L.gdn_rotary.restype = i
+    L.gdn_paged_append.argtypes = ([vp] * 12 + [i] * 7 + [i64] * 4 + [i] * 3 + [i64] * 3 + [i, i, vp])
+    L.gdn_paged_append.restype = i
+    L.gdn_paged_attention_workspace_size.argtypes = [i] * 7
+    L.gdn_paged_attention_workspace_size.restype = sz
+    L.gdn_paged_attention.argtypes = ([vp] * 8 + [i] * 5 + [i64] + [i] * 3 + [i64] * 3 + [f, i, i, i, vp, sz, vp])
+    L.gdn_paged_attention.restype = i
     L.gdn_device_errors.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
     L.gdn_device_errors.restype = i
     L.gdn_status_string.argtypes = [i]
@@ -601,6 +612,183 @@ def gdn_accept_drafts(target_probs, draft_probs, draft_tokens, uniform, *, draft
     if st:
         _check(st, "gdn_accept_drafts")
     return tokens, emitted_count
+
+
+def _int32(t, what: str):
+    """Pointer of a contiguous int32 tensor on the device."""
+    if t.dtype != torch.int32:
+        raise ValueError(f"{what} is int32")
+    return _p(t)
+
+
+def _turn_args(inv_freq, positions, axes, N: int, d: int):
+    """Pointers of inv_freq, positions and axes, R and A of a rotation of N tokens."""
+    half = inv_freq.shape[0]
+    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or 2 * half > d:
+        raise ValueError("inv_freq is float32 [R / 2], R of at most a head's size")
+    A = 1
+    pp = ap = None
+    if positions is not None:
+        if positions.dim() == 2:
+            A = positions.shape[0]
+        if positions.shape[-1] != N or positions.dim() > 2 or A < 1:
+            raise ValueError("positions is int32 [N] or [A, N]")
+        pp = _int32(positions, "positions")
+    if axes is not None:
+        if axes.shape != (half,):
+            raise ValueError("axes is int32 [R / 2]")
+        ap = _int32(axes, "axes")
+    return _p(inv_freq), pp, ap, 2 * half, A
+
+
+def gdn_rotary(x, positions, inv_freq, *, axes=None, pairs: bool = False, inverse: bool = False,
+               out=None, stream=None):
+    """Rotary positions on the first R = 2 * inv_freq.numel() elements of each head
+    of x [N, H, d] (rows may be slices).  positions [N], or [A, N] with axes
+    [R / 2] naming each pair's axis.  pairs: elements 2 i and 2 i + 1 turn
+    together, else i and i + R / 2.  inverse turns back, which is the gradient.
+    out may be x."""
+    shape, dtype = x.shape, x.dtype
+    N, H, d = shape
+    fp, pp, ap, R, A = _turn_args(inv_freq, positions, axes, N, d)
+    if out is None:
+        out = _empty(shape, dtype, x.device, stream)
+        op, os_ = out.data_ptr(), H * d
+    else:
+        if out.shape != shape or out.dtype != dtype:
+            raise ValueError("out must have the shape and the dtype of x")
+        op, os_ = _rows(out, 2)
+    xp, xs = _rows(x, 2)
+    flags = (GDN_ROTARY_PAIRS if pairs else 0) | (GDN_ROTARY_INVERSE if inverse else 0)
+    st = lib().gdn_rotary(xp, op, pp, ap, fp, N, H, d, R, A, xs, os_, flags, _DT[dtype], _stream(stream))
+    if st:
+        _check(st, "gdn_rotary")
+    return out
+
+
+def _page_args(k_pages, v_pages, page_table, kv_lens, B: int, dtype):
+    """Shape, pointers and strides of a cache [num_pages, page_size, Hk, d] (any order of the
+    first three dimensions in memory), with its table and its lengths."""
+    pages, page_size, Hk, d = shape = k_pages.shape
+    strides = k_pages.stride()
+    if v_pages.shape != shape or v_pages.stride() != strides:
+        raise ValueError("k_pages and v_pages are [num_pages, page_size, Hk, d] with the same strides")
+    if k_pages.dtype != dtype or v_pages.dtype != dtype:
+        raise ValueError("the pages must have the dtype of the tokens")
+    if strides[3] != 1 and d != 1:
+        raise ValueError("the elements of a slot's head must be contiguous")
+    if not (k_pages.is_cuda and v_pages.is_cuda):
+        raise ValueError("libgdn takes device tensors")
+    if page_table.dim() != 2 or page_table.shape[0] != B or kv_lens.shape != (B,):
+        raise ValueError("page_table is int32 [B, max_pages], kv_lens int32 [B]")
+    return (Hk, d, k_pages.data_ptr(), v_pages.data_ptr(), _int32(page_table, "page_table"),
+            _int32(kv_lens, "kv_lens"), (pages, page_size, page_table.shape[1], *strides[:3]))
+
+
+def _row_count(total: int, B: int, T, cu_seqlens):
+    """T argument and pointer of the rows of `total` tokens."""
+    if cu_seqlens is not None:
+        if cu_seqlens.shape != (B + 1,):
+            raise ValueError("cu_seqlens is int32 [B + 1]")
+        return total, _int32(cu_seqlens, "cu_seqlens")
+    if T is None:
+        T = total // B if B else 0
+    if B * T > total or T < 0:
+        raise ValueError("the tensors hold B rows of T tokens")
+    return T, None
+
+
+def gdn_paged_append(k, v, k_pages, v_pages, page_table, kv_lens, *, B: int, T: Optional[int] = None,
+                     cu_seqlens=None, q=None, q_out=None, inv_freq=None, positions=None, axes=None,
+                     pairs: bool = False, stream=None):
+    """New tokens' keys and values [total_T, Hk, d] into the cache's pages
+    [num_pages, page_size, Hk, d], row b's at the positions that end at kv_lens[b].  With
+    inv_freq the keys, and the queries q [total_T, Hq, d], are rotated on the way, by
+    `positions` or by their positions in the cache (see gdn_rotary).  Returns the
+    rotated queries (q_out, which may be q), or None without q."""
+    N, Hk, d = shape = k.shape
+    dtype = k.dtype
+    if v.shape != shape or v.dtype != dtype:
+        raise ValueError("v must have the shape and the dtype of k")
+    ph, pd, kp, vp, tp, lp, pages = _page_args(k_pages, v_pages, page_table, kv_lens, B, dtype)
+    if (ph, pd) != (Hk, d):
+        raise ValueError("the pages must have the heads of k")
+    T, cp = _row_count(N, B, T, cu_seqlens)
+    fp = pp = ap = None
+    R, A = 0, 1
+    if inv_freq is not None:
+        # (uniform rows may end before the tensor does; positions has their number)
+        fp, pp, ap, R, A = _turn_args(inv_freq, positions, axes, N if cp is not None else B * T, d)
+        if pp is None and ap is not None:
+            ap = None  # the cache position on every axis
+    Hq, qp, qs, op, os_ = 0, None, 0, None, 0
+    if q is not None:
+        if q.shape[0] != N or q.shape[2] != d or q.dtype != dtype:
+            raise ValueError("q is [total_T, Hq, d] in the dtype of k")
+        Hq = q.shape[1]
+        qp, qs = _rows(q, 2)
+        if q_out is None:
+            q_out = _empty(q.shape, dtype, q.device, stream)
+            op, os_ = q_out.data_ptr(), Hq * d
+        else:
+            if q_out.shape != q.shape or q_out.dtype != dtype:
+                raise ValueError("q_out must have the shape and the dtype of q")
+            op, os_ = _rows(q_out, 2)
+    elif q_out is not None:
+        raise ValueError("q_out goes with q")
+    xk, ks = _rows(k, 2)
+    xv, vs = _rows(v, 2)
+    st = lib().gdn_paged_append(qp, xk, xv, op, kp, vp, tp, lp, cp, pp, ap, fp, B, T, Hq, Hk, d, R, A,
+                                qs, ks, vs, os_, *pages, GDN_ROTARY_PAIRS if pairs else 0, _DT[dtype],
+                                _stream(stream))
+    if st:
+        _check(st, "gdn_paged_append")
+    return q_out
+
+
+def gdn_paged_attention_workspace_size(B, T, Hq, Hk, d, dtype, varlen=False) -> int:
+    return int(lib().gdn_paged_attention_workspace_size(B, T, Hq, Hk, d, _DT.get(dtype, dtype),
+                                                        int(bool(varlen))))
+
+
+def gdn_paged_attention(q, k_pages, v_pages, page_table, kv_lens, *, B: int, T: Optional[int] = None,
+                        cu_seqlens=None, scale: Optional[float] = None, causal: bool = True,
+                        window: int = 0, out=None, lse=None, want_lse: bool = False, workspace=None,
+                        stream=None):
+    """Attention of new tokens q [total_T, Hq, d] (rows may be slices) over the
+    cache, row b's last one at position kv_lens[b] - 1: over the keys up to a query's own (with a window, the last `window` of
+    them), or over all keys of the row without `causal`.  scale is d ** -0.5 by
+    default.  Returns (out, lse); lse [total_T, Hq] (None unless wanted) is the log of the sum of
+    weights."""
+    N, Hq, d = shape = q.shape
+    dtype = q.dtype
+    Hk, pd, kp, vp, tp, lp, pages = _page_args(k_pages, v_pages, page_table, kv_lens, B, dtype)
+    if pd != d:
+        raise ValueError("the pages must have the head size of q")
+    T, cp = _row_count(N, B, T, cu_seqlens)
+    if out is None:
+        out = _empty(shape, dtype, q.device, stream)
+    elif out.shape != shape or out.dtype != dtype:
+        raise ValueError("out must have the shape and the dtype of q")
+    if lse is None:
+        if want_lse:
+            lse = _empty((N, Hq), torch.float32, q.device, stream)
+    elif lse.shape != (N, Hq) or lse.dtype != torch.float32:
+        raise ValueError("lse is float32 [total_T, Hq]")
+    L = lib()
+    if workspace is None:
+        need = L.gdn_paged_attention_workspace_size(B, T, Hq, Hk, d, _DT[dtype], int(cp is not None))
+        if 0 < need < 1 << 62:
+            workspace = _empty(need, torch.uint8, q.device, stream, scratch=True)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    qp, qs = _rows(q, 2)
+    st = L.gdn_paged_attention(qp, kp, vp, tp, lp, cp, _p(out), _p(lse), B, T, Hq, Hk, d, qs, *pages,
+                               d ** -0.5 if scale is None else scale, window,
+                               0 if causal else GDN_ATTENTION_FULL, _DT[dtype], _p(workspace), ws_bytes,
+                               _stream(stream))
+    if st:
+        _check(st, "gdn_paged_attention")
+    return out, lse
 
 
 def gdn_set_wait_limit_ns(ns: int) -> None:

@@ -456,6 +456,98 @@ GDN_API int gdn_accept_drafts(const void *target_probs, const void *draft_probs,
                               int dtype_probs, void *stream);
 
 /*
+ * Softmax attention over a cache in pages -- the layers that hybrid backbones keep
+ * between their linear ones.  Keys and values of a row's tokens lie in pages of page_size
+ * slots, which a table assigns:
+ *     position j of row b is in slot j % page_size of page page_table[b][j / page_size]
+ *  k_pages, v_pages   element (page, slot, h, i) at page * page_stride + slot *
+ *              slot_stride + h * head_stride + i (elements; any order of the three), each
+ *              stride at least d and not negative where its dimension is above one.  Both
+ *              have the same strides, and may be interleaved in one buffer.
+ *  page_table  int32 [B, max_pages], device.  Only entries that a row's keys reach are
+ *              read.  One outside [0, num_pages) sets GDN_DEVERR_BAD_INDEX.
+ *  kv_lens     int32 [B], device: keys of the row, its new tokens included.  The row's
+ *              T_b new tokens are at positions kv_lens[b] - T_b ... kv_lens[b] - 1.
+ *              (Negative lengths count as 0; keys past max_pages * page_size do not exist.)
+ * Rows are uniform or packed as above (cu_seqlens); tokens that no row owns are left
+ * alone.  dtype is one of GDN_F32, GDN_F16, GDN_BF16 for everything that is not int32.
+ */
+
+#define GDN_ROTARY_PAIRS 0x1    /* elements 2 i and 2 i + 1 turn together (else i and i + R / 2) */
+#define GDN_ROTARY_INVERSE 0x2  /* turn back: the gradient of the turn */
+
+/*
+ * gdn_rotary -- rotary positions on one or several axes (time, height, width).
+ * Pair i < R / 2 of every head of token n turns by phi = positions[axes[i]][n] * inv_freq[i]:
+ *     (x1, x2) -> (x1 cos phi - x2 sin phi, x2 cos phi + x1 sin phi)
+ * and elements from R on are copied.  Angles are formed in whole turns, off by no more
+ * than 2^-50 of themselves, 2^-31 turns and the fp32 sine's last bit, at any position;
+ * the result is rounded once.
+ *  x, out      element (n, h, i) at [n * stride + h * d + i], aligned to their element
+ *              (vectors of up to 16 bytes where addresses, strides and widths allow).
+ *              out may be exactly x (same stride); else it overlaps no input.
+ *  positions   int32 [A, N], device.
+ *  axes        int32 [R / 2], device, or NULL: the first axis.  One outside [0, A)
+ *              leaves its pair unturned and sets GDN_DEVERR_BAD_INDEX.
+ *  inv_freq    fp32 [R / 2], device, finite (may be NULL when R is 0).
+ *  R           even, 0 .. d.     d: 1 .. 1024.     H: 1 .. 16384.
+ */
+GDN_API int gdn_rotary(const void *x, void *out, const int32_t *positions, const int32_t *axes,
+                       const float *inv_freq, int64_t N, int H, int d, int R, int A, int64_t x_stride,
+                       int64_t out_stride, int flags, int dtype, void *stream);
+
+/*
+ * gdn_paged_append -- the keys and values of new tokens into the cache, with the
+ * rotation on the way: k [total_T, Hk, d] turned as in gdn_rotary, v as it is, and
+ * the queries q [total_T, Hq, d] turned into q_out.
+ *  q, q_out    NULL together with Hq = 0: no queries.  q_out may be exactly q.
+ *  positions   int32 [A, total_T], or NULL: the token's position in the cache on every axis.
+ *  R, inv_freq, axes, A, flags (GDN_ROTARY_PAIRS)   as in gdn_rotary; R = 0: no rotation.
+ *  Rows may be slices of wider ones (strides, elements, as in gdn_rotary); q_out may be
+ *  the q part of the buffer that holds k and v too.
+ * A token whose position is negative, or whose page does not exist (which sets
+ * GDN_DEVERR_BAD_INDEX), is kept nowhere; its query is turned all the same.
+ * Preconditions: the pages that receive tokens belong to one row each, and no two
+ * elements of the pages share an address.
+ *  B <= 65535; total_T < 2^31.
+ */
+GDN_API int gdn_paged_append(const void *q, const void *k, const void *v, void *q_out, void *k_pages,
+                             void *v_pages, const int32_t *page_table, const int32_t *kv_lens,
+                             const int32_t *cu_seqlens, const int32_t *positions, const int32_t *axes,
+                             const float *inv_freq, int B, int T, int Hq, int Hk, int d, int R, int A,
+                             int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t q_out_stride,
+                             int num_pages, int page_size, int max_pages, int64_t page_stride,
+                             int64_t slot_stride, int64_t head_stride, int flags, int dtype, void *stream);
+
+#define GDN_ATTENTION_FULL 0x1  /* every query sees all keys of its row (else those up to its own) */
+
+/*
+ * gdn_paged_attention -- new tokens (one, a few drafts, a chunk of a prompt) over the
+ * cache that holds them and what came before.  Query t of row b, at position
+ * p = kv_lens[b] - T_b + t, with key head h / (Hq / Hk):
+ *     w_j = e^{scale q.k_j},  out = sum_j w_j v_j / sum_j w_j,  lse = log sum_j w_j
+ * over the keys j <= p, with a window only j > p - window, and with GDN_ATTENTION_FULL
+ * over all j < kv_lens[b].  A query without keys gives out 0 and lse -infinity, and so
+ * does one whose scores (scale q.k) all lie below -2^127.
+ *  q           [total_T, Hq, d], rows q_stride elements apart (>= Hq * d).
+ *  out         [total_T, Hq, d], dense.       lse   fp32 [total_T, Hq] or NULL.
+ *  window      0: none.  Not with GDN_ATTENTION_FULL.
+ *  d           32, 64 or 128.       Hq % Hk = 0.       B <= 65535; total_T * Hq < 2^31.
+ *  workspace   gdn_paged_attention_workspace_size() bytes for the same sizes and the
+ *              device of the call, 16-byte aligned; scratch.  Calls that may run at the
+ *              same time need one each.
+ * Slots that hold no key of the row may hold anything.  Keys of a page that does not
+ * exist (GDN_DEVERR_BAD_INDEX) count as zeros, and their values too.
+ */
+GDN_API size_t gdn_paged_attention_workspace_size(int B, int T, int Hq, int Hk, int d, int dtype, int varlen);
+GDN_API int gdn_paged_attention(const void *q, const void *k_pages, const void *v_pages,
+                                const int32_t *page_table, const int32_t *kv_lens, const int32_t *cu_seqlens,
+                                void *out, float *lse, int B, int T, int Hq, int Hk, int d, int64_t q_stride,
+                                int num_pages, int page_size, int max_pages, int64_t page_stride,
+                                int64_t slot_stride, int64_t head_stride, float scale, int window, int flags,
+                                int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * gdn_prefill_chunked_noalloc -- gdn_prefill_chunked for callers that cannot
  * allocate device memory: runtimes with their own memory planner that forbid
  * hidden allocations, or latency-critical paths that must never enter the
@@ -491,7 +583,7 @@ GDN_API int gdn_prefill_chunked_noalloc(const void *q, const void *k, const void
 
 /* Device-side error bits (gdn_device_errors). */
 enum {
-    GDN_DEVERR_BAD_INDEX = 1, /* an initial_state_indices entry was out of range */
+    GDN_DEVERR_BAD_INDEX = 1, /* an index read on the device was out of range */
     GDN_DEVERR_TIMEOUT = 2    /* a kernel abandoned a bounded wait */
 };
 
