@@ -278,6 +278,19 @@ cudaError_t launch_join(const AttentionParams &p, const Plan &s, cudaStream_t st
 // Plans of the two kernels.
 Plan plan_simt(int B, int T, int Hq, int Hk, int d, bool varlen);
 cudaError_t launch_attention_simt(const AttentionParams &p, const Plan &s, cudaStream_t stream);
+// 16-bit tensors that TMA can address, with pages of a multiple of 8 slots and up to 128
+// query heads a key head.
+bool tc_takes(const AttentionParams &p);
+Plan plan_tc(int B, int T, int Hq, int Hk, int d, bool varlen);
+cudaError_t launch_attention_tc(const AttentionParams &p, const Plan &s, cudaStream_t stream);
 
 }  // namespace attn
+
+// Tensor maps of 16-bit tensors, 128-byte swizzle, boxes of 64 features (zeros past d):
+// [tokens][H][d] with `heads` x `tokens` boxes; [pages][heads][slots][d] with boxes of `rows`
+// slots.  Strides in elements.
+bool encode_heads_map(CUtensorMap *m, const void *ptr, bool bf16, int d, int H, long tokens, int64_t head_stride,
+                      int64_t token_stride, int box_heads, int box_tokens);
+bool encode_pages_map(CUtensorMap *m, const void *ptr, bool bf16, int d, int slots, int heads, int pages,
+                      int64_t slot_stride, int64_t head_stride, int64_t page_stride, int rows);
 }  // namespace gdn

@@ -263,15 +263,17 @@ Plan plan_simt(int B, int T, int Hq, int Hk, int d, bool varlen) {
 
 }  // namespace attn
 
+// (for either kernel: strides and pages, which decide, are not among the sizes)
 size_t attention_workspace_bytes(int B, int T, int Hq, int Hk, int d, int dt, bool varlen) {
-    (void)dt;
-    return attn::plan_simt(B, T, Hq, Hk, d, varlen).bytes();
+    const size_t simt = attn::plan_simt(B, T, Hq, Hk, d, varlen).bytes();
+    return dt == GDN_F32 ? simt : std::max(simt, attn::plan_tc(B, T, Hq, Hk, d, varlen).bytes());
 }
 
 cudaError_t launch_attention(const AttentionParams &p, cudaStream_t stream) {
-    attn::Plan s = attn::plan_simt(p.B, p.T, p.Hq, p.Hk, p.d, p.cu_seqlens != nullptr);
+    const bool varlen = p.cu_seqlens != nullptr, tc = attn::tc_takes(p);
+    attn::Plan s = tc ? attn::plan_tc(p.B, p.T, p.Hq, p.Hk, p.d, varlen) : attn::plan_simt(p.B, p.T, p.Hq, p.Hk, p.d, varlen);
     s.ws = static_cast<uint8_t *>(p.ws);
-    return attn::launch_attention_simt(p, s, stream);
+    return tc ? attn::launch_attention_tc(p, s, stream) : attn::launch_attention_simt(p, s, stream);
 }
 
 }  // namespace gdn

@@ -527,8 +527,9 @@ GDN_API int gdn_paged_append(const void *q, const void *k, const void *v, void *
  * p = kv_lens[b] - T_b + t, with key head h / (Hq / Hk):
  *     w_j = e^{scale q.k_j},  out = sum_j w_j v_j / sum_j w_j,  lse = log sum_j w_j
  * over the keys j <= p, with a window only j > p - window, and with GDN_ATTENTION_FULL
- * over all j < kv_lens[b].  A query without keys gives out 0 and lse -infinity, and so
- * does one whose scores (scale q.k) all lie below -2^127.
+ * over all j < kv_lens[b].  A query without keys gives out 0 and lse -infinity.
+ * Precondition: a query's largest score (scale q.k) is below 2^20 in magnitude; others may
+ * be as low as they like.
  *  q           [total_T, Hq, d], rows q_stride elements apart (>= Hq * d).
  *  out         [total_T, Hq, d], dense.       lse   fp32 [total_T, Hq] or NULL.
  *  window      0: none.  Not with GDN_ATTENTION_FULL.

@@ -133,8 +133,8 @@ def test_what_is_not_finite_stays_with_its_row(gdn, dtype, new, Hq):
 
 
 def test_masked_by_the_lowest_value(gdn):
-    """Keys that score the type's lowest value weigh nothing next to others.  Where there are no
-    others, equal scores of half of it (within 2^127) weigh the same."""
+    """Keys that score the type's lowest value weigh nothing next to others; where there are no
+    others, equal scores of -2^19 weigh the same."""
     d, n = 64, 200
     for dt in (torch.bfloat16, torch.float32):
         cache = Cache([n], 1, d, 16, dt)
@@ -147,7 +147,8 @@ def test_masked_by_the_lowest_value(gdn):
         ref = v[150:, 0].double().mean(0)
         u = 2.0 ** -8 if dt == torch.bfloat16 else 2.0 ** -20
         near(out[0, 0], ref, 2 * u * v[150:, 0].double().abs().mean(0) + u * ref.abs())
-        out, _ = gdn.gdn_paged_attention(q, cache.k, cache.v, cache.table, int32([150]), B=1, scale=0.5)
+        out, _ = gdn.gdn_paged_attention(q, cache.k, cache.v, cache.table, int32([150]), B=1,
+                                         scale=2.0 ** 19 / -torch.finfo(dt).min)
         ref = v[:150, 0].double().mean(0)
         near(out[0, 0], ref, 2 * u * v[:150, 0].double().abs().mean(0) + u * ref.abs())
 
