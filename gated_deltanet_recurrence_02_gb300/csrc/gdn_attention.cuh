@@ -1,15 +1,14 @@
 // gdn_attention.cuh -- how the attention kernels cut their work, and join what they cut.
 //
-// A unit is (row b, key head hk, block of query rows): the G = Hq / Hk query heads of a key
-// head and the row's tokens are flattened, rho = t G + g, so that all of them read a tile of
-// keys once; a unit has up to `rows` of them, and as many tiles of `keys` keys as they see.
-// All units' tiles in a row, in the order of b, hk, block, are cut into equal pieces, one a
-// CTA, so that no lengths, however ragged, leave CTAs idle.  Lengths are on the device, so
-// each CTA finds its piece there: a sum over the rows and a walk along the one it starts in.
-// A unit that a cut goes through leaves its parts (unscaled sums, maxima, sums of weights) in
-// the workspace, at most two a CTA: the end of a unit that an earlier CTA began (head) and
-// the start of one that a later CTA goes on with (tail).  The join, a second kernel, adds the
-// parts up in the order of the keys, so the result does not depend on timing.
+// A unit is (row b, group of query heads that share a key head, block of tokens): its query
+// rows are rho = t gs + g, gs heads a token, so that all of them read a tile of keys once.
+// All units' tiles in a row, in the order of b, group, block, are cut into equal pieces, one
+// a CTA, so that no lengths, however ragged, leave CTAs idle.  Lengths are on the device, so
+// each CTA finds its piece there: a sum over the rows and a search along the one it starts
+// in.  A unit that a cut goes through leaves its parts (unscaled sums, maxima, sums of
+// weights) in the workspace, at most two a CTA: the end of a unit that an earlier CTA began
+// (part 0) and the start of one that a later CTA goes on with (part 1).  The join, a second
+// kernel, adds the parts up in the order of the keys, so the result does not depend on timing.
 #pragma once
 
 #include "gdn_internal.cuh"
@@ -19,31 +18,35 @@ namespace gdn {
 namespace attn {
 
 constexpr float kNone = -INFINITY;
+constexpr unsigned kAll = 0xffffffffu;
 
-// What a CTA leaves for the join.
+// What a CTA leaves for the join: the unit that it begins and does not end.
 struct alignas(16) Cut {
-    int tail;          // 1: the CTA's last unit goes on in the next CTA
-    int b, hk, block;  // that unit
-    int head;          // 0: nothing; 1: its first unit began in an earlier CTA and ends here; 2: and goes on
+    long row0;   // out row (token times Hq plus head) of its first query
+    int tokens;  // 0: there is none
+    int heads;   // that the group has (up to gs)
+    int parts;   // CTAs that have a part of it, this one first
     int pad[3];
 };
 
 // The cutting, with the workspace's layout: Cut [ctas], maxima and sums [ctas][2][rows][2],
 // sums [ctas][2][rows][d].
 struct Plan {
-    int rows, keys;  // query rows of a unit, keys of a tile
+    int tokens, gs;      // tokens of a unit, query heads of a group
+    int per_key;         // groups of a key head
     int ctas, d;
     uint8_t *ws;
+    __host__ __device__ int rows() const { return tokens * gs; }
     __host__ __device__ Cut *cut(int c) const { return reinterpret_cast<Cut *>(ws) + c; }
     __host__ __device__ float2 *stats(int c, int part) const {
-        return reinterpret_cast<float2 *>(ws + (size_t)ctas * sizeof(Cut)) + ((size_t)c * 2 + part) * rows;
+        return reinterpret_cast<float2 *>(ws + (size_t)ctas * sizeof(Cut)) + ((size_t)c * 2 + part) * rows();
     }
     __host__ __device__ float *sums(int c, int part) const {
-        return reinterpret_cast<float *>(ws + (size_t)ctas * (sizeof(Cut) + 2 * rows * sizeof(float2))) +
-               ((size_t)c * 2 + part) * rows * d;
+        return reinterpret_cast<float *>(ws + (size_t)ctas * (sizeof(Cut) + 2 * rows() * sizeof(float2))) +
+               ((size_t)c * 2 + part) * rows() * d;
     }
     size_t bytes() const {
-        return (size_t)ctas * (sizeof(Cut) + 2 * (size_t)rows * (sizeof(float2) + d * sizeof(float)));
+        return (size_t)ctas * (sizeof(Cut) + 2 * (size_t)rows() * (sizeof(float2) + d * sizeof(float)));
     }
 };
 
@@ -63,96 +66,138 @@ __device__ __forceinline__ Row row_at(const AttentionParams &p, int b) {
     r.first = len - r.tokens;
     return r;
 }
+__device__ __forceinline__ Row row_of_lane(const Row &r, int lane) {
+    return Row{__shfl_sync(kAll, r.tok0, lane), __shfl_sync(kAll, r.tokens, lane), __shfl_sync(kAll, r.keys, lane),
+               __shfl_sync(kAll, r.first, lane)};
+}
 
-// One unit's query rows and keys.
+// One unit's tokens and keys; tiles of KT keys.
 struct Unit {
-    int rho0, rho1;  // flattened query rows
-    int lo, hi;      // keys that any of them sees
-    int key0, tiles; // the first tile's first key, tiles (one at least)
+    int t0, t1;       // tokens
+    int lo, hi;       // keys that any of them sees
+    int key0, tiles;  // the first tile's first key, tiles (one at least)
 };
 
-__device__ __forceinline__ Unit unit_of(const AttentionParams &p, const Plan &s, const Row &r, int G, int block) {
+template <int KT>
+__device__ __forceinline__ Unit unit_of(const AttentionParams &p, const Plan &s, const Row &r, int block) {
     Unit u;
-    u.rho0 = block * s.rows;
-    u.rho1 = min(u.rho0 + s.rows, r.tokens * G);
-    const int t0 = u.rho0 / G, t1 = (u.rho1 - 1) / G;
+    u.t0 = block * s.tokens;
+    u.t1 = min(u.t0 + s.tokens, r.tokens);
     u.lo = 0;
     u.hi = r.keys;
     if (p.causal) {
-        u.hi = min(u.hi, r.first + t1 + 1);
-        if (p.window > 0) u.lo = max(0, r.first + t0 - p.window + 1);
+        u.hi = min(u.hi, r.first + u.t1);
+        if (p.window > 0) u.lo = max(0, r.first + u.t0 - p.window + 1);
     }
-    u.key0 = u.lo / s.keys * s.keys;
-    u.tiles = u.hi > u.lo ? (u.hi - u.key0 + s.keys - 1) / s.keys : 1;
+    u.key0 = u.lo & -KT;
+    u.tiles = u.hi > u.lo ? (u.hi - u.key0 + KT - 1) / KT : 1;
     return u;
 }
 
-__device__ __forceinline__ int blocks_of(const Plan &s, const Row &r, int G) {
-    return (r.tokens * G + s.rows - 1) / s.rows;
+__device__ __forceinline__ int blocks_of(const Plan &s, const Row &r) {
+    return (int)((unsigned)(r.tokens + s.tokens - 1) / (unsigned)s.tokens);
 }
 
-// Tiles of a row for one key head.
-__device__ __forceinline__ long row_tiles(const AttentionParams &p, const Plan &s, const Row &r, int G) {
-    long n = 0;
-    const int blocks = blocks_of(s, r, G);
-    for (int i = 0; i < blocks; ++i) n += unit_of(p, s, r, G, i).tiles;
-    return n;
-}
-
-// A place in the order of all tiles, and the tiles from there to the CTA's end.
+// A place in the order of all tiles, and the tiles from there to the CTA's end; the other
+// CTAs' are `each` long, and one more before CTA `more`.
 struct Place {
-    int b, hk, block, tile;
-    long left;
+    int b, group, block, tile;
+    long left, each, more;
 };
 
-// Where this CTA's piece starts.  Called by all THREADS threads.
-template <int THREADS>
-__device__ Place find_place(const AttentionParams &p, const Plan &s, int G) {
-    __shared__ long sums[THREADS / 32];
+// Where this CTA's piece starts.  Called by all THREADS threads.  Each warp sums up a stretch
+// of the rows, 32 rows at a time; where rows have many blocks, the lanes share each row's.
+// (One thread a row took 3 us for every 60 blocks of the longest.)
+template <int KT, int THREADS>
+__device__ Place find_place(const AttentionParams &p, const Plan &s) {
+    constexpr int kWarps = THREADS / 32;
+    __shared__ long sums[kWarps];
     __shared__ Place found;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int per = (p.B + THREADS - 1) / THREADS;
-    const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
-    long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += row_tiles(p, s, row_at(p, b), G) * p.Hk;
-    long upto = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-        const long x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
-    }
-    if (lane == 31) sums[warp] = upto;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, groups = p.Hk * s.per_key;
+    const int per = (p.B + kWarps - 1) / kWarps;
+    const int b0 = min(warp * per, p.B), b1 = min(b0 + per, p.B);
+    Row mine{0, 0, 0, 0};  // of lane b % 32
+    // Tiles of 32 rows from b on for one group, a lane each.
+    auto tiles = [&](int b) {
+        mine = b + lane < b1 ? row_at(p, b + lane) : Row{0, 0, 0, 0};
+        const int blocks = blocks_of(s, mine);
+        unsigned wide = __ballot_sync(kAll, blocks > 4);
+        long n = 0;
+        if (blocks <= 4)
+            for (int i = 0; i < blocks; ++i) n += unit_of<KT>(p, s, mine, i).tiles;
+        while (wide != 0) {
+            const int x = __ffs(wide) - 1;
+            wide &= wide - 1;
+            const Row r = row_of_lane(mine, x);
+            const int its = __shfl_sync(kAll, blocks, x);
+            long part = 0;
+            for (int i = lane; i < its; i += 32) part += unit_of<KT>(p, s, r, i).tiles;
+            for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kAll, part, o);
+            if (lane == x) n = part;
+        }
+        return n;
+    };
+    // inclusive sums over the lanes
+    auto scan = [&](long x) {
+        for (int o = 1; o < 32; o <<= 1) {
+            const long y = __shfl_up_sync(kAll, x, o);
+            if (lane >= o) x += y;
+        }
+        return x;
+    };
+    long all = 0;
+    const bool once = b1 - b0 <= 32;
+    long kept = 0;  // the lane's row's tiles, where one look is enough
+    for (int b = b0; b < b1; b += 32) all += kept = tiles(b);
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kAll, all, o);
+    all *= groups;
+    if (lane == 0) sums[warp] = all;
+    if (threadIdx.x == 0) found.left = 0;
     __syncthreads();
     long before = 0, total = 0;
-    for (int w = 0; w < THREADS / 32; ++w) {
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += sums[w];
         total += sums[w];
     }
-    before += upto - mine;
-    // (no more CTAs than tiles: one without a piece never stands between a unit's parts)
-    const long n = max(1l, min((long)s.ctas, total)), c = min((long)blockIdx.x, n);
-    const long from = total * c / n, to = blockIdx.x < n ? total * (c + 1) / n : from;
-    if (threadIdx.x == 0 && from >= to) found.left = 0;
-    if (from < to && before <= from && from < before + mine) {
+    // Equal pieces, the first ones a tile longer; no more CTAs than tiles, so that one without
+    // a piece never stands between a unit's parts.
+    const int c = blockIdx.x;
+    const long each = total >> 31 ? total / s.ctas : (long)((unsigned)total / (unsigned)s.ctas);
+    const long more = total - each * s.ctas;
+    const long from = each * c + min((long)c, more), left = each + (c < more ? 1 : 0);
+    if (left > 0 && before <= from && from < before + all) {
         long rest = from - before;
-        for (int b = b0; b < b1; ++b) {
-            const Row r = row_at(p, b);
-            const long n = row_tiles(p, s, r, G);
-            if (rest >= n * p.Hk) {
-                rest -= n * p.Hk;
+        for (int b = b0; b < b1; b += 32) {
+            const long n = once ? kept : tiles(b), upto = scan(n * groups);
+            const unsigned in = __ballot_sync(kAll, rest < upto);
+            if (in == 0) {
+                rest -= __shfl_sync(kAll, upto, 31);
                 continue;
             }
-            found.b = b;
-            found.hk = (int)(rest / n);
-            rest -= found.hk * n;
-            int i = 0;
-            for (;; ++i) {
-                const int t = unit_of(p, s, r, G, i).tiles;
-                if (rest < t) break;
-                rest -= t;
+            const int x = __ffs(in) - 1;
+            const long of_row = __shfl_sync(kAll, n, x);
+            rest -= __shfl_sync(kAll, upto, x) - of_row * groups;
+            const Row r = row_of_lane(mine, x);
+            int group = 0;
+            if (groups > 1) {
+                group = (rest | of_row) >> 31 ? (int)(rest / of_row) : (int)((unsigned)rest / (unsigned)of_row);
+                rest -= group * of_row;
             }
-            found.block = i;
-            found.tile = (int)rest;
-            found.left = to - from;
+            const int blocks = blocks_of(s, r);
+            for (int i = 0;; i += 32) {
+                const int t = i + lane < blocks ? unit_of<KT>(p, s, r, i + lane).tiles : 0;
+                const long sum = scan(t);
+                const unsigned at = __ballot_sync(kAll, rest < sum);
+                if (at == 0) {
+                    rest -= __shfl_sync(kAll, sum, 31);
+                    continue;
+                }
+                const int y = __ffs(at) - 1;
+                rest -= __shfl_sync(kAll, sum - t, y);
+                if (lane == 0) found = Place{b + x, group, i + y, (int)rest, left, each, more};
+                break;
+            }
             break;
         }
     }
@@ -160,114 +205,114 @@ __device__ Place find_place(const AttentionParams &p, const Plan &s, int G) {
     return found;
 }
 
-// The piece's units one after another.  at() gives the unit at hand, its tiles [tile, end).
+// The piece's units one after another: of the unit at hand the tiles [at.tile, end).
+template <int KT>
 struct Walk {
     Place at;
     Row row;
     Unit unit;
     int end, blocks;
-    int nth;  // of this CTA's units
-    __device__ __forceinline__ void load(const AttentionParams &p, const Plan &s, int G) {
-        unit = unit_of(p, s, row, G, at.block);
+    __device__ __forceinline__ void load(const AttentionParams &p, const Plan &s) {
+        unit = unit_of<KT>(p, s, row, at.block);
         end = (int)min((long)unit.tiles, at.tile + at.left);
     }
-    __device__ __forceinline__ bool start(const AttentionParams &p, const Plan &s, int G, const Place &from) {
+    __device__ __forceinline__ bool start(const AttentionParams &p, const Plan &s, const Place &from) {
         at = from;
-        nth = 0;
         if (at.left <= 0) return false;
         row = row_at(p, at.b);
-        blocks = blocks_of(s, row, G);
-        load(p, s, G);
+        blocks = blocks_of(s, row);
+        load(p, s);
         return true;
     }
-    __device__ __forceinline__ bool next(const AttentionParams &p, const Plan &s, int G) {
+    __device__ __forceinline__ bool next(const AttentionParams &p, const Plan &s) {
         at.left -= end - at.tile;
         if (at.left <= 0) return false;
-        ++nth;
         at.tile = 0;
         if (++at.block == blocks) {
             at.block = 0;
-            if (++at.hk == p.Hk) {
-                at.hk = 0;
+            if (++at.group == p.Hk * s.per_key) {
+                at.group = 0;
                 do {
                     if (++at.b >= p.B) return false;
                     row = row_at(p, at.b);
-                    blocks = blocks_of(s, row, G);
+                    blocks = blocks_of(s, row);
                 } while (blocks == 0);
             }
         }
-        load(p, s, G);
+        load(p, s);
         return true;
     }
-    __device__ __forceinline__ bool whole() const { return at.tile == 0 && end == unit.tiles; }
-    // Which of the CTA's two parts a cut unit leaves.
-    __device__ __forceinline__ int part() const { return at.tile > 0 ? 0 : 1; }
+    // 0, 1: the CTA's part that the cut unit leaves; -1: the unit is whole.
+    __device__ __forceinline__ int part() const { return at.tile > 0 ? 0 : end < unit.tiles ? 1 : -1; }
+    __device__ __forceinline__ int key_head(const Plan &s) const { return s.per_key == 1 ? at.group : at.group / s.per_key; }
+    // First query head of the group, and its heads.
+    __device__ __forceinline__ int head0(const AttentionParams &p, const Plan &s) const {
+        const int k = key_head(s);
+        return k * (p.Hq / p.Hk) + (at.group - k * s.per_key) * s.gs;
+    }
+    __device__ __forceinline__ int heads(const AttentionParams &p, const Plan &s) const {
+        return min(s.gs, (key_head(s) + 1) * (p.Hq / p.Hk) - head0(p, s));
+    }
+    // What the CTA leaves for the join, after its last unit (one thread).
+    __device__ __forceinline__ Cut cut(const AttentionParams &p, const Plan &s) const {
+        Cut c{};
+        if (part() != 1) return c;
+        c.row0 = (row.tok0 + unit.t0) * p.Hq + head0(p, s);
+        c.tokens = unit.t1 - unit.t0;
+        c.heads = heads(p, s);
+        // CTAs from here on: pieces of each + 1 tiles up to CTA `more`, then of each
+        const long rest = unit.tiles - end, longer = max(0l, at.more - (long)(blockIdx.x + 1));
+        const long in = longer * (at.each + 1);
+        c.parts = 1 + (int)(rest <= in ? (rest + at.each) / (at.each + 1) : longer + (rest - in + at.each - 1) / at.each);
+        return c;
+    }
 };
 
-// What the CTA leaves for the join, written by one thread (Place `from` as found).
-__device__ inline void write_cut(const AttentionParams &p, const Plan &s, int G, const Place &from) {
-    Cut c{};
-    Walk w;
-    if (w.start(p, s, G, from)) {
-        if (w.at.tile > 0) c.head = w.end == w.unit.tiles ? 1 : 2;
-        do {
-            if (w.at.tile == 0 && w.end < w.unit.tiles) {
-                c.tail = 1;
-                c.b = w.at.b;
-                c.hk = w.at.hk;
-                c.block = w.at.block;
-            }
-        } while (w.next(p, s, G));
-    }
-    *s.cut(blockIdx.x) = c;
-}
-
 // Joins the parts of cut units.  Grid (ctas, slices): CTA x takes the unit that CTA x of the
-// attention left a tail of, a warp a query row; maxima are those of scores times log2 e.
+// attention began and did not end, a warp a query row; maxima are those of scores times log2 e.
 template <typename T>
 __global__ void __launch_bounds__(256) join_kernel(const AttentionParams p, const Plan s) {
     tc::grid_dependency_wait();
     const Cut c = *s.cut(blockIdx.x);
-    if (!c.tail) return;
-    const int G = p.Hq / p.Hk;
-    const Row r = row_at(p, c.b);
-    const Unit u = unit_of(p, s, r, G, c.block);
-    const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
-    // the CTA in which the unit ends
-    int last = blockIdx.x + 1;
-    while (last < s.ctas - 1 && s.cut(last)->head == 2) ++last;
-    const int n = u.rho1 - u.rho0, per = s.d / 32;
-    for (int i = blockIdx.y * warps + threadIdx.x / 32; i < n; i += gridDim.y * warps) {
+    const int lane = threadIdx.x % 32, warps = blockDim.x / 32, per = s.d / 32;
+    for (int i = blockIdx.y * warps + threadIdx.x / 32; i < c.tokens * s.gs; i += gridDim.y * warps) {
+        const int t = i / s.gs, g = i - t * s.gs;
+        if (g >= c.heads) continue;
+        auto stats = [&](int x) { return x < c.parts ? s.stats(blockIdx.x + x, x == 0)[i] : make_float2(kNone, 0.f); };
         float top = kNone;
-        for (int x = blockIdx.x + lane; x <= last; x += 32)
-            top = fmaxf(top, s.stats(x, x == (int)blockIdx.x)[i].x);
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int x = lane; x < c.parts; x += 32) top = fmaxf(top, stats(x).x);
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
         const float safe = top == kNone ? 0.f : top;
         float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int x = blockIdx.x; x <= last; ++x) {
-            const int part = x == (int)blockIdx.x;
-            const float2 ml = s.stats(x, part)[i];
-            const float *o = s.sums(x, part) + (size_t)i * s.d + lane * per;
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-            if (per == 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(o);
-                v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-            } else if (per == 2) {
-                const float2 f = *reinterpret_cast<const float2 *>(o);
-                v[0] = f.x, v[1] = f.y;
-            } else {
-                v[0] = o[0];
+        for (int x0 = 0; x0 < c.parts; x0 += 32) {
+            const float2 ml = stats(x0 + lane);
+            const float mine = exp2f(ml.x - safe);
+            sum = fmaf(mine, ml.y, sum);
+#pragma unroll 8
+            for (int x = x0; x < min(c.parts, x0 + 32); ++x) {
+                const float *o = s.sums(blockIdx.x + x, x == 0) + (size_t)i * s.d + lane * per;
+                float v[4] = {0.f, 0.f, 0.f, 0.f};
+                if (per == 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(o);
+                    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+                } else if (per == 2) {
+                    const float2 f = *reinterpret_cast<const float2 *>(o);
+                    v[0] = f.x, v[1] = f.y;
+                } else {
+                    v[0] = o[0];
+                }
+                const float w = __shfl_sync(kAll, mine, x - x0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] = fmaf(w, v[e], acc[e]);
             }
-            const float w = exp2f(ml.x - safe);
-            sum = fmaf(w, ml.y, sum);
-            for (int e = 0; e < 4; ++e) acc[e] = fmaf(w, v[e], acc[e]);
         }
-        const int rho = u.rho0 + i, t = rho / G;
-        const long at = (r.tok0 + t) * p.Hq + c.hk * G + (rho - t * G);
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+        const long at = c.row0 + (long)t * p.Hq + g;
         const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;  // (a NaN stays one)
         T *out = reinterpret_cast<T *>(p.out) + at * p.d + lane * per;
-        for (int e = 0; e < per; ++e) st_out(out + e, acc[e] * inv);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < per) st_out(out + e, acc[e] * inv);
         if (p.lse != nullptr && lane == 0) p.lse[at] = (safe + log2f(sum)) * 0.69314718055994530942f;
     }
 }
@@ -275,22 +320,36 @@ __global__ void __launch_bounds__(256) join_kernel(const AttentionParams p, cons
 // Launched behind an attention kernel, while it still runs.
 cudaError_t launch_join(const AttentionParams &p, const Plan &s, cudaStream_t stream);
 
-// Plans of the two kernels.
+// Units of up to `rows` query rows.
+inline Plan plan_of(int Hq, int Hk, int d, int rows, int ctas) {
+    Plan s{};
+    const int G = Hq / Hk;
+    s.per_key = (G + rows - 1) / rows;
+    s.gs = (G + s.per_key - 1) / s.per_key;
+    s.tokens = rows / s.gs;
+    s.ctas = ctas;
+    s.d = d;
+    return s;
+}
+// Tokens of a row on average (packed rows' own lengths are only on the device).
+inline long mean_tokens(int B, int T, bool varlen) { return varlen ? ((long)T + B - 1) / (B > 0 ? B : 1) : T; }
+
 Plan plan_simt(int B, int T, int Hq, int Hk, int d, bool varlen);
 cudaError_t launch_attention_simt(const AttentionParams &p, const Plan &s, cudaStream_t stream);
-// 16-bit tensors that TMA can address, with pages of a multiple of 8 slots and up to 128
-// query heads a key head.
+// 16-bit tensors that TMA can address, with pages of a multiple of 8 slots.
 bool tc_takes(const AttentionParams &p);
 Plan plan_tc(int B, int T, int Hq, int Hk, int d, bool varlen);
 cudaError_t launch_attention_tc(const AttentionParams &p, const Plan &s, cudaStream_t stream);
 
 }  // namespace attn
 
-// Tensor maps of 16-bit tensors, 128-byte swizzle, boxes of 64 features (zeros past d):
-// [tokens][H][d] with `heads` x `tokens` boxes; [pages][heads][slots][d] with boxes of `rows`
-// slots.  Strides in elements.
-bool encode_heads_map(CUtensorMap *m, const void *ptr, bool bf16, int d, int H, long tokens, int64_t head_stride,
-                      int64_t token_stride, int box_heads, int box_tokens);
-bool encode_pages_map(CUtensorMap *m, const void *ptr, bool bf16, int d, int slots, int heads, int pages,
-                      int64_t slot_stride, int64_t head_stride, int64_t page_stride, int rows);
+// Tensor maps of 16-bit tensors, 128-byte swizzle, 64 features to a 128-byte row (zeros past
+// d).  Queries [tokens][H][d]: boxes of `heads` x `tokens` rows of 64 features.
+bool encode_heads_map(CUtensorMap *m, const void *ptr, bool bf16, int d, int H, long tokens, int64_t token_stride,
+                      int box_heads, int box_tokens);
+// A cache's pages, as [count][slots / 8][d / 64][8 slots][64]: boxes of `rows` slots with all
+// their features, 8 slots of 64 features next to each other.  `unit`: elements from one
+// index of the first dimension to the next.
+bool encode_pages_map(CUtensorMap *m, const void *ptr, bool bf16, int d, int slots, int64_t slot_stride, int64_t count,
+                      int64_t unit, int rows);
 }  // namespace gdn

@@ -35,9 +35,14 @@ __global__ void __launch_bounds__(Shape<M>::kThreads) simt_kernel(const Attentio
     float *sk = sq + M * D;                        // [KT][D + 4]
     float *sv = sk + KT * (D + 4);                 // [KT][D]
     float *sp = sv + KT * D;                       // [M][KT + 4]
-    const int G = p.Hq / p.Hk, tx = threadIdx.x % TX, ty = threadIdx.x / TX;
-    const Place from = find_place<THREADS>(p, s, G);
-    if (threadIdx.x == 0) write_cut(p, s, G, from);
+    const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
+    const Place from = find_place<KT, THREADS>(p, s);
+    int tt[4], gg[4];  // token and head of the thread's rows in the unit
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        tt[i] = (ty * 4 + i) / s.gs;
+        gg[i] = ty * 4 + i - tt[i] * s.gs;
+    }
     const float scale2 = p.scale * tc::kLog2e;
     // Rows of D elements from global to shared memory as fp32; src(row) is the address or
     // nullptr (zeros).
@@ -54,15 +59,17 @@ __global__ void __launch_bounds__(Shape<M>::kThreads) simt_kernel(const Attentio
             *reinterpret_cast<float4 *>(dst + r * stride + c) = x;
         }
     };
-    Walk w;
-    for (bool more = w.start(p, s, G, from); more; more = w.next(p, s, G)) {
+    Walk<KT> w;
+    Cut cut{};
+    for (bool more = w.start(p, s, from); more; more = w.next(p, s)) {
         const Unit &u = w.unit;
-        const int n = u.rho1 - u.rho0;
+        const int n = u.t1 - u.t0, heads = w.heads(p, s), head0 = w.head0(p, s), hk = w.key_head(s);
+        cut = w.cut(p, s);
         __syncthreads();
         fill(sq, D, M, [&](int r) -> const T * {
-            if (r >= n) return nullptr;
-            const int rho = u.rho0 + r, t = rho / G;
-            return reinterpret_cast<const T *>(p.q) + (w.row.tok0 + t) * p.qs + (int64_t)(w.at.hk * G + rho - t * G) * D;
+            const int t = r / s.gs, g = r - t * s.gs;
+            if (t >= n || g >= heads) return nullptr;
+            return reinterpret_cast<const T *>(p.q) + (w.row.tok0 + u.t0 + t) * p.qs + (int64_t)(head0 + g) * D;
         });
         float m[4], l[4], o[4][NC];
         int lo[4], hi[4];  // keys that a row sees
@@ -72,7 +79,7 @@ __global__ void __launch_bounds__(Shape<M>::kThreads) simt_kernel(const Attentio
             l[i] = 0.f;
 #pragma unroll
             for (int c = 0; c < NC; ++c) o[i][c] = 0.f;
-            const int r = ty * 4 + i, at = w.row.first + (u.rho0 + min(r, n - 1)) / G;
+            const int at = w.row.first + u.t0 + min(tt[i], n - 1);
             lo[i] = p.causal && p.window > 0 ? max(0, at - p.window + 1) : 0;
             hi[i] = p.causal ? min(w.row.keys, at + 1) : w.row.keys;
         }
@@ -90,7 +97,7 @@ __global__ void __launch_bounds__(Shape<M>::kThreads) simt_kernel(const Attentio
                         return nullptr;
                     }
                     return reinterpret_cast<const T *>(pages) + id * p.page_stride +
-                           (int64_t)(k - pg * p.page_size) * p.slot_stride + w.at.hk * p.head_stride;
+                           (int64_t)(k - pg * p.page_size) * p.slot_stride + hk * p.head_stride;
                 };
             };
             fill(sk, D + 4, KT, page(p.k_pages));
@@ -178,10 +185,9 @@ __global__ void __launch_bounds__(Shape<M>::kThreads) simt_kernel(const Attentio
 #pragma unroll
             for (int d = TX / 2; d > 0; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
             const int r = ty * 4 + i;
-            if (r >= n) continue;
-            if (w.whole()) {
-                const int rho = u.rho0 + r, t = rho / G;
-                const long at = (w.row.tok0 + t) * p.Hq + w.at.hk * G + (rho - t * G);
+            if (tt[i] >= n || gg[i] >= heads) continue;
+            if (w.part() < 0) {
+                const long at = (w.row.tok0 + u.t0 + tt[i]) * p.Hq + head0 + gg[i];
                 const float inv = l[i] > 0.f ? 1.f / l[i] : l[i] == 0.f ? 0.f : l[i];  // (a NaN stays one)
                 T *out = reinterpret_cast<T *>(p.out) + at * D;
 #pragma unroll
@@ -196,6 +202,7 @@ __global__ void __launch_bounds__(Shape<M>::kThreads) simt_kernel(const Attentio
             }
         }
     }
+    if (threadIdx.x == 0) *s.cut(blockIdx.x) = cut;
 }
 
 template <typename T, int D, int M>
@@ -214,7 +221,7 @@ cudaError_t launch_m(const AttentionParams &p, const Plan &s, cudaStream_t strea
 
 template <typename T>
 cudaError_t launch_t(const AttentionParams &p, const Plan &s, cudaStream_t stream) {
-    const bool few = s.rows == 16;
+    const bool few = s.rows() <= 16;
     switch (p.d) {
         case 32: return few ? launch_m<T, 32, 16>(p, s, stream) : launch_m<T, 32, 64>(p, s, stream);
         case 64: return few ? launch_m<T, 64, 16>(p, s, stream) : launch_m<T, 64, 64>(p, s, stream);
@@ -225,7 +232,8 @@ cudaError_t launch_t(const AttentionParams &p, const Plan &s, cudaStream_t strea
 template <typename T>
 cudaError_t launch_join_t(const AttentionParams &p, const Plan &s, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)s.ctas, (unsigned)std::max(1, s.rows / 32));
+    const long most = std::min<long>(s.rows(), (long)p.T * s.gs);  // query rows of a unit
+    cfg.gridDim = dim3((unsigned)s.ctas, (unsigned)((most + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -249,16 +257,10 @@ cudaError_t launch_attention_simt(const AttentionParams &p, const Plan &s, cudaS
     return p.dt == GDN_F16 ? launch_t<__half>(p, s, stream) : launch_t<__nv_bfloat16>(p, s, stream);
 }
 
-// Query rows a unit: 16 where a row of the batch has no more on average (packed rows' own
-// lengths are only on the device), else 64.
+// Query rows a unit: 16 where a row of the batch has no more on average, else 64.
 Plan plan_simt(int B, int T, int Hq, int Hk, int d, bool varlen) {
-    const long mean = varlen ? ((long)T + B - 1) / std::max(B, 1) : T;
-    Plan s{};
-    s.rows = mean * (Hq / Hk) <= 16 ? 16 : 64;
-    s.keys = s.rows == 16 ? Shape<16>::KT : Shape<64>::KT;
-    s.ctas = 2 * sm_count_of_current_device();
-    s.d = d;
-    return s;
+    const int rows = mean_tokens(B, T, varlen) * (Hq / Hk) <= 16 ? 16 : 64;
+    return plan_of(Hq, Hk, d, rows, 2 * sm_count_of_current_device());
 }
 
 }  // namespace attn

@@ -1297,12 +1297,12 @@ long max_chunks_of(int B, int T, bool varlen) {
 
 }  // namespace
 
-bool encode_heads_map(CUtensorMap *m, const void *ptr, bool bf16, int d, int H, long tokens, int64_t head_stride,
-                      int64_t token_stride, int box_heads, int box_tokens) {
+bool encode_heads_map(CUtensorMap *m, const void *ptr, bool bf16, int d, int H, long tokens, int64_t token_stride,
+                      int box_heads, int box_tokens) {
     EncodeTiledFn enc = encode_fn();
     if (enc == nullptr) return false;
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)tokens};
-    cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)token_stride * 2};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)token_stride * 2};
     cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
     cuuint32_t es[3] = {1, 1, 1};
     return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
@@ -1310,17 +1310,16 @@ bool encode_heads_map(CUtensorMap *m, const void *ptr, bool bf16, int d, int H, 
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-bool encode_pages_map(CUtensorMap *m, const void *ptr, bool bf16, int d, int slots, int heads, int pages,
-                      int64_t slot_stride, int64_t head_stride, int64_t page_stride, int rows) {
+bool encode_pages_map(CUtensorMap *m, const void *ptr, bool bf16, int d, int slots, int64_t slot_stride, int64_t count,
+                      int64_t unit, int rows) {
     EncodeTiledFn enc = encode_fn();
     if (enc == nullptr) return false;
-    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)slots, (cuuint64_t)heads, (cuuint64_t)pages};
-    // (the stride of a dimension of one says nothing, and may be 0)
-    cuuint64_t strides[3] = {(cuuint64_t)(slots > 1 ? slot_stride : d) * 2, (cuuint64_t)(heads > 1 ? head_stride : d) * 2,
-                             (cuuint64_t)(pages > 1 ? page_stride : d) * 2};
-    cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
-    cuuint32_t es[4] = {1, 1, 1, 1};
-    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+    const int halves = (d + 63) / 64;
+    cuuint64_t dims[5] = {(cuuint64_t)(d < 64 ? d : 64), 8, (cuuint64_t)halves, (cuuint64_t)slots / 8, (cuuint64_t)count};
+    cuuint64_t strides[4] = {(cuuint64_t)slot_stride * 2, 128, (cuuint64_t)slot_stride * 16, (cuuint64_t)unit * 2};
+    cuuint32_t box[5] = {64, 8, (cuuint32_t)halves, (cuuint32_t)rows / 8, 1};
+    cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
                const_cast<void *>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
