@@ -103,11 +103,12 @@ __device__ __forceinline__ int blocks_of(const Plan &s, const Row &r) {
 struct Place {
     int b, group, block, tile;
     long left, each, more;
+    Row row;  // of b
 };
 
-// Where this CTA's piece starts.  Called by all THREADS threads.  Each warp sums up a stretch
-// of the rows, 32 rows at a time; where rows have many blocks, the lanes share each row's.
-// (One thread a row took 3 us for every 60 blocks of the longest.)
+// Where this CTA's piece starts.  Each warp sums up a stretch of the rows, 32 rows at a time;
+// where rows have many blocks, the lanes share each row's.  (One thread a row took 3 us for
+// every 60 blocks of the longest.)  Called by all THREADS threads.
 template <int KT, int THREADS>
 __device__ Place find_place(const AttentionParams &p, const Plan &s) {
     constexpr int kWarps = THREADS / 32;
@@ -195,7 +196,7 @@ __device__ Place find_place(const AttentionParams &p, const Plan &s) {
                 }
                 const int y = __ffs(at) - 1;
                 rest -= __shfl_sync(kAll, sum - t, y);
-                if (lane == 0) found = Place{b + x, group, i + y, (int)rest, left, each, more};
+                if (lane == 0) found = Place{b + x, group, i + y, (int)rest, left, each, more, r};
                 break;
             }
             break;
@@ -219,7 +220,7 @@ struct Walk {
     __device__ __forceinline__ bool start(const AttentionParams &p, const Plan &s, const Place &from) {
         at = from;
         if (at.left <= 0) return false;
-        row = row_at(p, at.b);
+        row = at.row;
         blocks = blocks_of(s, row);
         load(p, s);
         return true;

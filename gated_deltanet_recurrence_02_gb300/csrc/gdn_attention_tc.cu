@@ -25,11 +25,10 @@ namespace {
 using namespace tc;
 
 constexpr int KT = 128;             // keys of a tile
-constexpr int kThreads = 384;
-// registers a thread: 168 at launch, of which the third warpgroup gives 96 to the others
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr int kThreads = 512;
+// registers a thread: 128 at launch, of which two warpgroups give 72 each to the others
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 56;
 constexpr uint32_t kBlock = 16384;  // 128 rows of 64 elements
-constexpr uint32_t tS = 0, tO = 256;  // TMEM: S (and P in its place) and O of a slot, 128 columns each
 constexpr uint32_t kTmemCols = 512;
 constexpr float kGrowth = 8.f;      // of the maximum's exponent, before O follows
 constexpr int kUnits = 4;           // units ahead
@@ -40,14 +39,20 @@ constexpr int kUnits = 4;           // units ahead
 enum Mode { kPair, kOne };
 
 // Shared memory: queries (blocks of 64 features, 128 rows each; kPair: both slots' of a unit,
-// kOne: of two units in turn), the ring of tiles (8 keys x 64 features a kilobyte; a row of 8
-// keys has all its features together), and what the warps tell each other.
-template <int NB>
+// kOne: of two units in turn), the rings of tiles of keys and of values (8 keys x 64 features
+// a kilobyte, all features of 8 keys together), and what the warps tell each other.
+template <int NB, int MODE>
 struct Layout {
+    // TMEM columns: S of the slots, 128 each, and O.  For heads of up to 64 there is room for P
+    // of its own: the next tile's S can follow as soon as the last one has been read.  (Else P
+    // takes S's place, and S waits for the product with it.)
+    static constexpr bool kOwnP = NB == 1;
+    static constexpr uint32_t tS = 0, tO = 256, kO = 64 * NB;
+    static constexpr uint32_t tP = kOwnP ? 384 : tS, kP = kOwnP ? 64 : 128;  // 64 columns used
     static constexpr uint32_t kTile = NB * kBlock;
-    static constexpr int NS = NB == 2 ? 5 : 10;            // tiles of keys or values in flight
-    static constexpr uint32_t oKv = 2 * kTile;
-    static constexpr uint32_t oMerge = oKv + NS * kTile;   // [128] maxima and sums of slot 1 (kOne)
+    static constexpr int NK = NB == 2 ? 3 : 5, NV = NB == 2 ? 2 : 5;  // tiles of keys, and of values, in flight
+    static constexpr uint32_t oK = 2 * kTile, oV = oK + NK * kTile;
+    static constexpr uint32_t oMerge = oV + NV * kTile;    // [128] maxima and sums of slot 1 (kOne)
     static constexpr uint32_t oWork = oMerge + 1024;       // [kUnits] Work
     static constexpr uint32_t oBar = oWork + kUnits * 96;
     static constexpr uint32_t kSmem = oBar + 384 + 1024;   // + alignment slack
@@ -97,12 +102,20 @@ struct Half16<__half> {
     }
 };
 
-// Order in which a piece's n tiles of keys and values go through the ring: the issuing warp's
-// order of use.  kPair: K0 V0 K1 V1 ..; kOne, one tile of scores ahead: K0 K1 V0 K2 V1 K3 ..
-template <int MODE>
-__device__ __forceinline__ int seq_k(int i) { return MODE == kPair ? 2 * i : i == 0 ? 0 : 2 * i - 1; }
-template <int MODE>
-__device__ __forceinline__ int seq_v(int i, int n) { return MODE == kPair || i == n - 1 ? 2 * i + 1 : 2 * i + 2; }
+// Four lanes' four values, transposed: value r of lane t (of four in a row) to value t of lane r.
+__device__ __forceinline__ void transpose4(uint32_t (&v)[4], int lane) {
+#pragma unroll
+    for (int b = 1; b <= 2; b <<= 1) {
+        const bool up = (lane & b) != 0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (r & b) continue;
+            const uint32_t got = __shfl_xor_sync(kAll, up ? v[r] : v[r | b], b);
+            if (up) v[r] = got;
+            else v[r | b] = got;
+        }
+    }
+}
 
 // The unit at hand of a walk.
 template <int MODE>
@@ -142,38 +155,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                  const __grid_constant__ CUtensorMap mv) {
     using H = Half16<E>;
-    using L = Layout<NB>;
-    constexpr int NS = L::NS;
+    using L = Layout<NB, MODE>;
+    constexpr int NK = L::NK, NV = L::NV;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_align1k(smem_raw);
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::oBar), *empty = full + NS;
-    uint64_t *u_full = empty + NS, *u_empty = u_full + kUnits;
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(sm + L::oBar), *k_empty = k_full + NK;
+    uint64_t *v_full = k_empty + NK, *v_empty = v_full + NV;
+    uint64_t *u_full = v_empty + NV, *u_empty = u_full + kUnits;
     uint64_t *q_full = u_empty + kUnits, *q_free = q_full + 2;  // (kPair: the first of each)
-    uint64_t *s_full = q_free + 2, *p_ready = s_full + 2, *o_done = p_ready + 2;  // of a slot each
+    // of a slot each: S is there, has been read (kOwnP), P is there, O has been added to
+    uint64_t *s_full = q_free + 2, *s_free = s_full + 2, *p_ready = s_free + 2, *o_done = p_ready + 2;
     uint64_t *other = o_done + 2, *merged = other + 1, *drain = other + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(other + 3);
     Work *works = reinterpret_cast<Work *>(sm + L::oWork);
     const int warp = __shfl_sync(kAll, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
-        }
+        for (int i = 0; i < 2 * (NK + NV); ++i) mbar_init(&k_full[i], 1);  // both rings'
         for (int i = 0; i < kUnits; ++i) {
             mbar_init(&u_full[i], 1);
-            mbar_init(&u_empty[i], 8 + 3);  // softmax warps, two that load, one that issues MMAs
+            mbar_init(&u_empty[i], 8 + 2 + (L::kOwnP ? 2 : 1));  // softmax, loading, issuing warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&q_free[i], 1);
             mbar_init(&s_full[i], 1);
+            mbar_init(&s_free[i], 4);
             mbar_init(&p_ready[i], 4);
             mbar_init(&o_done[i], 1);
         }
         mbar_init(other, 4);
         mbar_init(merged, 4);
-        mbar_init(drain, 1);
+        mbar_init(drain, L::kOwnP ? 2 : 1);
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -187,8 +200,9 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
     fence_after_sync();
     const uint32_t tm = __shfl_sync(kAll, *tmem_slot, 0);
     bool ok = true;
-    // Waits run out p.limit nanoseconds after the warp's last unit or tile came.  A wait of a
-    // whole warp, for a barrier's n-th completion (from 0): the same outcome in every lane.
+    // Waits run out p.limit nanoseconds after the warp's last unit came (a tile takes about a
+    // microsecond).  A wait of a whole warp, for a barrier's n-th completion (from 0): the same
+    // outcome in every lane.
     uint32_t since = globaltimer_lo();
     auto wait = [&](uint64_t *bar, int n) {
         return __all_sync(kAll, mbar_wait_since(bar, (uint32_t)n & 1u, since, p.limit)) != 0;
@@ -211,13 +225,13 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
         regs_inc<kSoftmaxRegs>();
         const int s = warp >> 2, r = (warp & 3) * 32 + lane;  // slot, row of the slot
         const int t = r / p.plan.gs, g = r - t * p.plan.gs;   // its token in the slot, its head in the group
-        const uint32_t ts = tm + ((uint32_t)((warp & 3) * 32) << 16) + tS + 128 * s;
-        const uint32_t to = tm + ((uint32_t)((warp & 3) * 32) << 16) + tO + 128 * s;
+        const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t ts = lanes + L::tS + 128 * s, tp = lanes + L::tP + L::kP * s, to = lanes + L::tO + L::kO * s;
         float2 *merge = reinterpret_cast<float2 *>(sm + L::oMerge);
         const float2 c2 = make_float2(p.c, p.c);
         const int slot_t = MODE == kPair ? s * p.slot_tokens : 0;
         const int row = slot_t * p.plan.gs + r;  // of the unit
-        int item = 0, done = 0, merges = 0;
+        int item = 0, merges = 0;
         Work x;
 #pragma unroll 1
         for (int u = 0; next_unit(u, x); ++u) {
@@ -238,9 +252,13 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
 #pragma unroll 1
             for (int i = i0; i < i1; i += MODE == kPair ? 1 : 2, ++item) {
                 if (!(ok = wait(&s_full[s], item))) break;
-                since = globaltimer_lo();
                 fence_after_sync();
                 if (idle) {
+                    if (L::kOwnP) {
+                        arrive(&s_free[s]);
+                        // (this S may be there before the other warps' last P is)
+                        if (item > 0 && !(ok = wait(&p_ready[s], item - 1))) break;
+                    }
                     arrive(&p_ready[s]);
                     continue;
                 }
@@ -248,6 +266,10 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
 #pragma unroll
                 for (int j = 0; j < 4; ++j) tmem_ld32_async(ts + 32 * j, v[j]);
                 tmem_wait_ld();
+                if (L::kOwnP) {
+                    fence_before_sync();
+                    arrive(&s_free[s]);
+                }
                 const int a = lo - (x.key0 + i * KT), e = hi - (x.key0 + i * KT);
                 if (__any_sync(kAll, e < KT)) {
 #pragma unroll
@@ -272,24 +294,25 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                     const float keep = grow ? ex2_approx(m - now) : 1.f;
                     m = grow ? now : m;
                     if (i != i0) {
-                        // the slot's last product is done: S was issued behind it
+                        // (else the slot's last product is done: S was issued behind it)
+                        if (L::kOwnP) {
+                            if (!(ok = wait(&o_done[s], item - 1))) break;
+                            fence_after_sync();
+                        }
                         l *= keep;
                         const float2 k2 = make_float2(keep, keep);
+#pragma unroll 1
+                        for (int j = 0; j < p.d; j += 16) {
+                            uint32_t o[16];
+                            tmem_ld16_async(to + j, o);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 4 * NB; ++j) {
-                            if (16 * j < p.d) {
-                                uint32_t o[16];
-                                tmem_ld16_async(to + 16 * j, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 16; k += 2) {
-                                    const float2 y =
-                                        __fmul2_rn(k2, make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])));
-                                    o[k] = __float_as_uint(y.x);
-                                    o[k + 1] = __float_as_uint(y.y);
-                                }
-                                tmem_st16(to + 16 * j, o);
+                            for (int k = 0; k < 16; k += 2) {
+                                const float2 y = __fmul2_rn(k2, make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])));
+                                o[k] = __float_as_uint(y.x);
+                                o[k + 1] = __float_as_uint(y.y);
                             }
+                            tmem_st16(to + j, o);
                         }
                     }
                 }
@@ -308,8 +331,13 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                         sum[(k >> 1) & 1] = __fadd2_rn(sum[(k >> 1) & 1], y);
                         pk[k / 2] = H::pack2(y.x, y.y);
                     }
-                    tmem_st16(ts + 16 * j, pk);
+                    if (L::kOwnP && j == 0 && i != i0) {  // the last P has been used
+                        if (!(ok = wait(&o_done[s], item - 1))) break;
+                        fence_after_sync();
+                    }
+                    tmem_st16(tp + 16 * j, pk);
                 }
+                if (!ok) break;
                 tmem_wait_st();
                 fence_before_sync();
                 arrive(&p_ready[s]);
@@ -319,8 +347,7 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
             if (!ok) break;
             const bool any = i1 > i0;  // the slot has sums of its own
             if (any) {
-                if (!(ok = wait(&o_done[s], done))) break;
-                ++done;
+                if (!(ok = wait(&o_done[s], item - 1))) break;
                 fence_after_sync();
             }
             float f0 = 1.f, f1 = 0.f;  // factors of this slot's sums, and of the other's (kOne)
@@ -350,38 +377,79 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                 f0 *= inv;
                 f1 *= inv;
                 const long at = (x.tok0 + slot_t + t) * p.Hq + x.head0 + g;
-                E *out = reinterpret_cast<E *>(p.out) + at * p.d;
-                float *left = p.plan.sums(blockIdx.x, x.part & 1) + row * p.d;
-#pragma unroll 1
-                for (int j = 0; j < p.d; j += 16) {
-                    uint32_t o[16], o1[16];
-                    float y[16];
-                    if (any) tmem_ld16_async(to + j, o);
-                    if (both) tmem_ld16_async(to + 128 + j, o1);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        y[k] = any ? __uint_as_float(o[k]) * f0 : 0.f;
-                        if (both) y[k] = fmaf(__uint_as_float(o1[k]), f1, y[k]);
-                    }
-                    if (mine && whole) {
-#pragma unroll
-                        for (int k = 0; k < 16; k += 8)
-                            *reinterpret_cast<uint4 *>(out + j + k) =
-                                make_uint4(H::pack2(y[k], y[k + 1]), H::pack2(y[k + 2], y[k + 3]),
-                                           H::pack2(y[k + 4], y[k + 5]), H::pack2(y[k + 6], y[k + 7]));
-                    } else if (mine) {
-#pragma unroll
-                        for (int k = 0; k < 16; k += 4)
-                            *reinterpret_cast<float4 *>(left + j + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
-                    }
-                }
-                fence_before_sync();
                 if (mine) {
                     if (!whole) p.plan.stats(blockIdx.x, x.part)[row] = make_float2(m - H::kShift, l);
                     else if (p.lse != nullptr)
                         p.lse[at] = ((m == kNone ? 0.f : m - H::kShift) + log2f(l)) * 0.69314718055994530942f;
                 }
+                // O leaves TMEM as fragments, lane 4 g + t: columns 2 t, 2 t + 1 of every 8 of rows
+                // g and g + 8, and is transposed between four lanes, which then write 8 columns
+                // each: 8 rows a store.  (A row a lane, stores of 32 rows took 2 us a unit, parts
+                // in fp32 5 us.)
+                const unsigned there = __ballot_sync(kAll, mine);
+                char *to_row = whole ? static_cast<char *>(p.out) + at * p.d * (long)sizeof(E)
+                                     : reinterpret_cast<char *>(p.plan.sums(blockIdx.x, x.part & 1) + row * p.d);
+#pragma unroll 1
+                for (int turn = 0; turn < 2 * NB; ++turn) {  // 16 rows, 64 columns
+                    const int c = turn / NB, col = turn % NB * 64;
+                    if ((there >> (16 * c) & 0xffff) == 0) continue;
+                    const uint32_t from = to + ((uint32_t)(16 * c) << 16) + col;
+                    float2 y[2][2][4];  // of rows g and g + 8: 32 columns a time, 8 r + 2 t
+                    __syncwarp();
+#pragma unroll
+                    for (int part = 0; part < (MODE == kOne ? 2 : 1); ++part) {
+                        if (part == 1 && !both) break;
+                        uint32_t o[2][16];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            if (32 * q < p.d) tmem_ld_16x32(from + part * L::kO + 32 * q, o[q]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float f = __shfl_sync(kAll, part ? f1 : f0, 16 * c + 8 * h + (lane >> 2));
+#pragma unroll
+                            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) {
+                                    const float2 v = make_float2(__uint_as_float(o[q][4 * r + 2 * h]),
+                                                                 __uint_as_float(o[q][4 * r + 2 * h + 1]));
+                                    // (without sums of its own the slot's columns hold anything)
+                                    if (part == 0) y[h][q][r] = any ? __fmul2_rn(v, make_float2(f, f)) : make_float2(0.f, 0.f);
+                                    else y[h][q][r] = __ffma2_rn(v, make_float2(f, f), y[h][q][r]);
+                                }
+                        }
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int of = 16 * c + 8 * h + (lane >> 2);
+                        char *dst = reinterpret_cast<char *>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(to_row), of)) +
+                                    (col + 8 * (lane & 3)) * (whole ? sizeof(E) : sizeof(float));
+                        const bool write = there >> of & 1;
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            if (32 * q >= p.d) break;
+                            if (whole) {
+                                uint32_t v[4];
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) v[r] = H::pack2(y[h][q][r].x, y[h][q][r].y);
+                                transpose4(v, lane);
+                                if (write) *reinterpret_cast<uint4 *>(dst + 64 * q) = make_uint4(v[0], v[1], v[2], v[3]);
+                            } else {
+                                uint32_t a[4], b[4];
+#pragma unroll
+                                for (int r = 0; r < 4; ++r)
+                                    a[r] = __float_as_uint(y[h][q][r].x), b[r] = __float_as_uint(y[h][q][r].y);
+                                transpose4(a, lane);
+                                transpose4(b, lane);
+                                if (write) {
+                                    *reinterpret_cast<uint4 *>(dst + 128 * q) = make_uint4(a[0], b[0], a[1], b[1]);
+                                    *reinterpret_cast<uint4 *>(dst + 128 * q + 16) = make_uint4(a[2], b[2], a[3], b[3]);
+                                }
+                            }
+                        }
+                    }
+                }
+                fence_before_sync();
             }
             if (both) arrive(merged);
         }
@@ -395,8 +463,10 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
             const int boxes = KT / p.box;
             // This lane's box of a tile.  Its page is read a tile ahead.
             const int first = lane * p.box;
-            int base = 0;                   // loads of the units so far, of both warps
-            uint32_t mine = 0, parity = 0;  // stages that this warp has loaded last, and their phases
+            uint64_t *full = values ? v_full : k_full, *empty = values ? v_empty : k_empty;
+            uint8_t *ring = sm + (values ? L::oV : L::oK);
+            const int stages = values ? NV : NK;
+            int st = 0, round = 0;  // of the ring
             Work x;
 #pragma unroll 1
             for (int u = 0; next_unit(u, x); ++u) {
@@ -409,38 +479,36 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                 int ahead = page_of(0);
 #pragma unroll 1
                 for (int i = 0; i < x.n; ++i) {
-                    const int at = base + (values ? seq_v<MODE>(i, x.n) : seq_k<MODE>(i)), st = at % NS;
                     const int k0 = x.key0 + i * KT, k = k0 + first;
                     const int b0 = (max(x.lo, k0) - k0) / p.box, b1 = (min(x.hi - k0, KT) + p.box - 1) / p.box;
-                    const int page = ahead;
+                    int index = p.none;  // of this lane's box (one past all: zeros)
+                    if (lane >= b0 && lane < b1) {
+                        if (ahead >= 0 && ahead < p.num_pages) index = ahead * p.page_step + x.hk * p.head_step;
+                        else atomicOr(p.err, (uint32_t)GDN_DEVERR_BAD_INDEX);
+                    }
+                    const int slot = (int)((unsigned)k % (unsigned)p.page_size) >> 3;
                     ahead = page_of(i + 1);
-                    if (at >= NS && !(ok = wait(&empty[st], at / NS - 1))) break;
-                    since = globaltimer_lo();
+                    if (round > 0 && !(ok = wait(&empty[st], round - 1))) break;
                     if (leader) mbar_arrive_expect_tx(&full[st], (uint32_t)((b1 - b0) * p.box * 128 * NB));
                     __syncwarp();
-                    mine |= 1u << st;
-                    parity = (parity & ~(1u << st)) | ((uint32_t)(at / NS) & 1u) << st;
-                    if (lane >= b0 && lane < b1) {
-                        int index = p.none;  // (out of the tensor: zeros)
-                        if (page >= 0 && page < p.num_pages) index = page * p.page_step + x.hk * p.head_step;
-                        else atomicOr(p.err, (uint32_t)GDN_DEVERR_BAD_INDEX);
-                        tma_load_5d(sm + L::oKv + st * L::kTile + first * 128 * NB, values ? &mv : &mk, 0, 0, 0,
-                                    (int)((unsigned)k % (unsigned)p.page_size) >> 3, index, &full[st]);
-                    }
+                    uint8_t *dst = ring + st * L::kTile;
+                    // (by the converged warp, a box after the other: lanes that issue their own
+                    // box each take 60 ns for it)
+#pragma unroll 2
+                    for (int y = b0; y < b1; ++y)
+                        tma_load_5d_warp(leader, dst + y * p.box * (128 * NB), values ? &mv : &mk, 0, 0, 0,
+                                         __shfl_sync(kAll, slot, y), __shfl_sync(kAll, index, y), &full[st]);
                     __syncwarp();
+                    if (++st == stages) st = 0, ++round;
                 }
                 if (!ok) break;
-                base += 2 * x.n;
             }
-            // The copies in flight land before the CTA ends, whoever gave up.  (To the end: the
-            // last ones of both warps.  Given up: this warp's own; a stage that the other one
-            // has filled since may take the wait its time.)
+            // The copies in flight land before the CTA ends, whoever gave up.
             __syncwarp();
 #pragma unroll 1
-            for (int y = 0; y < NS; ++y) {
-                const int at = base - 1 - y;
-                if (ok && at >= 0) mbar_wait(&full[at % NS], (uint32_t)(at / NS) & 1u, kDefaultWaitNs / 8);
-                if (!ok && (mine >> y & 1)) mbar_wait(&full[y], parity >> y & 1, kDefaultWaitNs / 8);
+            for (int y = 0; y < stages; ++y) {
+                const int n = y < st ? round : round - 1;  // the stage's last load
+                if (n >= 0) mbar_wait(&full[y], (uint32_t)n & 1u, kDefaultWaitNs / 8);
             }
         } else if (warp == 11) {
             // =================== units, and their queries ================
@@ -455,10 +523,7 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                 since = globaltimer_lo();
                 Work x;
                 x.n = -1;
-                if (more) {
-                    x = work_of<MODE>(p, w);
-                    cut = w.cut(p, p.plan);
-                }
+                if (more) x = work_of<MODE>(p, w);
                 if (lane == 0) works[u % kUnits] = x;
                 arrive(&u_full[u % kUnits]);
                 if (!more) break;
@@ -476,101 +541,116 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                     __syncwarp();
                     ++live;
                 }
+                cut = w.cut(p, p.plan);
                 more = w.next(p, p.plan);
             }
             if (lane == 0) *p.plan.cut(blockIdx.x) = cut;
             // (a barrier's last completion: older ones are not told from none)
             for (int x = max(0, live - (MODE == kOne ? 2 : 1)); x < live; ++x)
                 mbar_wait(&q_full[MODE == kOne ? x & 1 : 0], (uint32_t)(MODE == kOne ? x >> 1 : x) & 1u, kDefaultWaitNs / 8);
-        } else {
+        } else if (warp == 9 || (warp == 12 && L::kOwnP)) {
             // ============================ MMAs ===========================
+            // One warp issues all, slot after slot, so that one slot's softmax runs under the
+            // other's products (a warp a slot: both ran in step, 4100 tokens over 32100 keys took
+            // 1403 us, not 1225).  Where P has its own place a second one issues the sums: an
+            // MMA and a commit cost their issuer some 40 cycles each, and the products of d = 64
+            // are over in 260.
+            const bool does_scores = !L::kOwnP || warp == 9, does_sums = !L::kOwnP || warp == 12;
             // (a negative scale: of the scores' queries)
             const uint32_t id_s = idesc_f16(128, KT, false, false, H::kBf16) | (p.scale < 0.f ? 1u << 13 : 0u);
             const uint32_t id_o = idesc_f16(128, p.d, false, true, H::kBf16);
-            const uint32_t s0 = smem_u32(sm);
-            int base = 0, live = 0, items[2] = {0, 0};
+            const uint64_t q0 = desc_sw128(smem_u32(sm), 16, 1024);
+            const uint64_t k0 = desc_sw128(smem_u32(sm) + L::oK, 16, NB * 1024);
+            const uint64_t v0 = desc_sw128(smem_u32(sm) + L::oV, 1024, NB * 1024);
+            int live = 0, asked[2] = {0, 0}, items[2] = {0, 0};  // of a slot: scores, sums so far
+            int kst = 0, kround = 0, vst = 0, vround = 0;        // of the rings
             Work x;
 #pragma unroll 1
             for (int u = 0; next_unit(u, x); ++u) {
                 if (x.n == 0) continue;
                 const int n = x.n, buf = MODE == kOne ? live & 1 : 0;
-                if (!(ok = wait(&q_full[buf], MODE == kOne ? live >> 1 : live))) break;
-                int k_seen = -1, v_seen = -1;
-                // S of slot s = Q K_i^T; the tile goes back behind its last product
-                auto scores = [&](int s, int i, bool last) {
-                    const int at = base + seq_k<MODE>(i), st = at % NS;
-                    if (i != k_seen && !(ok = wait(&full[st], at / NS))) return;
-                    k_seen = i;
-                    since = globaltimer_lo();
+                if (does_scores && !(ok = wait(&q_full[buf], MODE == kOne ? live >> 1 : live))) break;
+                auto has = [&](int s, int i) {
+                    return MODE == kOne ? i >= 0 && i < n && (i & 1) == s
+                                        : i >= (s ? x.a[1] : x.a[0]) && i < (s ? x.e[1] : x.e[0]);
+                };
+                auto next = [&](int &st, int &round, int stages) {
+                    if (++st == stages) st = 0, ++round;
+                };
+                // S of slot s = Q K_i^T, of the tile of keys at hand; `first`, `last`: of its uses
+                auto scores = [&](int s, bool first, bool last) {
+                    if (first && !(ok = wait(&k_full[kst], kround))) return;
+                    if (L::kOwnP) {
+                        const int before = s ? asked[1] : asked[0];
+                        if (before > 0 && !(ok = wait(&s_free[s], before - 1))) return;
+                        if (s) ++asked[1];
+                        else ++asked[0];
+                    }
                     fence_after_sync();
-                    const uint64_t qd = desc_sw128(s0 + (MODE == kOne ? buf : s) * L::kTile, 16, 1024);
-                    const uint64_t kd = desc_sw128(s0 + L::oKv + st * L::kTile, 16, NB * 1024);
+                    const uint64_t qd = desc_add(q0, (MODE == kOne ? buf : s) * L::kTile), kd = desc_add(k0, kst * L::kTile);
 #pragma unroll
                     for (int k = 0; k < 4 * NB; ++k)
                         if (16 * k < p.d)
-                            mma_f16_warp(leader, tm + tS + 128 * s, desc_add(qd, (k >> 2) * kBlock + (k & 3) * 32),
+                            mma_f16_warp(leader, tm + L::tS + 128 * s, desc_add(qd, (k >> 2) * kBlock + (k & 3) * 32),
                                          desc_add(kd, (k >> 2) * 1024 + (k & 3) * 32), id_s, k > 0);
                     mma_commit_warp(leader, &s_full[s]);
-                    if (last) mma_commit_warp(leader, &empty[st]);
+                    if (last) {
+                        mma_commit_warp(leader, &k_empty[kst]);
+                        next(kst, kround, NK);
+                    }
                 };
-                // O of slot s += P V_i
-                auto sums = [&](int s, int i, bool first, bool last, bool end) {
-                    const int at = base + seq_v<MODE>(i, n), st = at % NS;
-                    if (i != v_seen) {
-                        if (!(ok = wait(&full[st], at / NS))) return;
+                // O of slot s += P V_i, of the tile of values at hand
+                auto sums = [&](int s, int i, bool first, bool last) {
+                    if (first) {
+                        if (!(ok = wait(&v_full[vst], vround))) return;
                         // Values of keys that no query of the unit sees: zeros, whatever was
                         // there (their weights are 0, but 0 times NaN is not).
-                        const int k0 = x.key0 + i * KT;
-                        const int r0 = max(0, x.lo - k0), r1 = min(KT, x.hi - k0);
+                        const int key = x.key0 + i * KT;
+                        const int r0 = max(0, x.lo - key), r1 = min(KT, x.hi - key);
                         if (r0 > 0 || r1 < KT) {
-                            uint8_t *v = sm + L::oKv + st * L::kTile;
+                            uint8_t *v = sm + L::oV + vst * L::kTile;
 #pragma unroll 1
-                            for (int e = lane; e < (r0 + KT - r1) * 8 * NB; e += 32) {
-                                int row = e / (8 * NB);
+                            for (int y = lane; y < (r0 + KT - r1) * 8 * NB; y += 32) {
+                                int row = y / (8 * NB);
                                 row = row < r0 ? row : row - r0 + r1;
-                                *reinterpret_cast<uint4 *>(v + (row >> 3) * (NB * 1024) + (e / 8 % NB) * 1024 +
-                                                           (row & 7) * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                                *reinterpret_cast<uint4 *>(v + (row >> 3) * (NB * 1024) + (y / 8 % NB) * 1024 +
+                                                           (row & 7) * 128 + (y & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                             }
                             fence_proxy_async();
                             __syncwarp();
                         }
-                        v_seen = i;
                     }
-                    if (!(ok = wait(&p_ready[s], items[s]))) return;
-                    ++items[s];
-                    since = globaltimer_lo();
+                    if (!(ok = wait(&p_ready[s], s ? items[1] : items[0]))) return;
+                    if (s) ++items[1];
+                    else ++items[0];
                     fence_after_sync();
-                    const uint64_t vd = desc_sw128(s0 + L::oKv + st * L::kTile, 1024, NB * 1024);
+                    const uint64_t vd = desc_add(v0, vst * L::kTile);
+                    const uint32_t more = has(s, i - (MODE == kPair ? 1 : 2));
 #pragma unroll
                     for (int k = 0; k < KT / 16; ++k)
-                        mma_f16_ta_warp(leader, tm + tO + 128 * s, tm + tS + 128 * s + 8 * k, desc_add(vd, k * NB * 2048),
-                                        id_o, !first || k > 0);
-                    if (last) mma_commit_warp(leader, &empty[st]);
-                    if (end) mma_commit_warp(leader, &o_done[s]);
-                };
-                if constexpr (MODE == kPair) {
-                    auto has = [&](int s, int i) { return i >= (s ? x.a[1] : x.a[0]) && i < (s ? x.e[1] : x.e[0]); };
-                    // Turn y: sums of tile (y / 2) - 1 for slot y % 2, then its scores of the next
-#pragma unroll 1
-                    for (int y = 0; ok && y < 2 * n + 2; ++y) {
-                        const int s = y & 1, i = (y >> 1) - 1;
-                        if (has(s, i)) sums(s, i, !has(s, i - 1), s == 1 || !has(1, i), !has(s, i + 1));
-                        if (ok && has(s, i + 1)) scores(s, i + 1, s == 1 || !has(1, i + 1));
-                        // the unit's last scores are issued
-                        if (ok && y == 2 * n - 1) mma_commit_warp(leader, q_free);
+                        mma_f16_ta_warp(leader, tm + L::tO + L::kO * s, tm + L::tP + L::kP * s + 8 * k,
+                                        desc_add(vd, k * NB * 2048), id_o, k > 0 ? 1u : more);
+                    mma_commit_warp(leader, &o_done[s]);
+                    if (last) {
+                        mma_commit_warp(leader, &v_empty[vst]);
+                        next(vst, vround, NV);
                     }
-                } else {
-                    // Turn y: sums of tile y - 2, then scores of tile y, for slot y % 2
+                };
+                // Turn y, for slot s = y % 2: sums of tile i, and scores of the slot's next tile.
+                // (kOne: i = y - 2, the tiles in turn; kPair: both slots have tile i = y / 2 - 1.)
 #pragma unroll 1
-                    for (int y = 0; ok && y < n + 2; ++y) {
-                        const int s = y & 1, i = y - 2;
-                        if (i >= 0) sums(s, i, i < 2, true, i >= n - 2);
-                        if (ok && y < n) scores(s, y, true);
-                        if (ok && y == n - 1) mma_commit_warp(leader, &q_free[buf]);
+                for (int y = 0; ok && y < (MODE == kOne ? n + 2 : 2 * n + 2); ++y) {
+                    const int s = y & 1, i = MODE == kOne ? y - 2 : (y >> 1) - 1, to_come = MODE == kOne ? y : i + 1;
+                    const bool both_sums = MODE == kPair && has(0, i) && has(1, i);
+                    const bool both_scores = MODE == kPair && has(0, to_come) && has(1, to_come);
+                    if (does_sums && has(s, i)) sums(s, i, !both_sums || s == 0, !both_sums || s == 1);
+                    if (does_scores && ok) {
+                        if (has(s, to_come)) scores(s, !both_scores || s == 0, !both_scores || s == 1);
+                        // the unit's last scores are issued
+                        if (ok && y == (MODE == kOne ? n : 2 * n) - 1) mma_commit_warp(leader, &q_free[buf]);
                     }
                 }
                 if (!ok) break;
-                base += 2 * n;
                 ++live;
             }
             mma_commit_warp(leader, drain);  // nothing may be in flight when TMEM is given back
@@ -587,7 +667,7 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
 template <typename E, int NB, int MODE>
 cudaError_t launch_mode(const TcParams &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                         cudaStream_t stream) {
-    constexpr uint32_t bytes = Layout<NB>::kSmem;
+    constexpr uint32_t bytes = Layout<NB, MODE>::kSmem;
     cudaError_t e = set_smem_once<attention_kernel<E, NB, MODE>>((int)bytes);
     if (e != cudaSuccess) return e;
     attention_kernel<E, NB, MODE><<<p.plan.ctas, kThreads, bytes, stream>>>(p, mq, mk, mv);

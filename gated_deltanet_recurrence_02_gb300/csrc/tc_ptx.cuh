@@ -150,13 +150,14 @@ __device__ __forceinline__ void tma_load_3d_warp(uint32_t leader, void *dst, con
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "r"(leader)
         : "memory");
 }
-// One box of a five-dimensional map, by the calling thread.
-__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4,
-                                            uint64_t *bar) {
+// One box of a five-dimensional map, by a whole converged warp.
+__device__ __forceinline__ void tma_load_5d_warp(uint32_t leader, void *dst, const CUtensorMap *map, int c0, int c1,
+                                                 int c2, int c3, int c4, uint64_t *bar) {
     asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %8, 0;\n\t"
+        "@e cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n}\n" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar)), "r"(leader)
         : "memory");
 }
 // Contiguous global -> shared copy; both addresses 16-byte aligned, bytes % 16 == 0.

@@ -92,6 +92,14 @@ def test_many_ragged_rows(gdn, dtype):
     check(gdn, new, lens, 4, 2, 64, 16, dtype, tail=3)
 
 
+@pytest.mark.parametrize("new,longest,d,Hq", [(1, 1500, 128, 8), (1, 1500, 64, 8), (3, 700, 128, 12), (90, 400, 128, 8), (90, 400, 64, 8)])
+def test_many_rows_a_CTA(gdn, new, longest, d, Hq):
+    """Rows of up to a dozen tiles, several of them and parts of others for each CTA."""
+    g = torch.Generator().manual_seed(6)
+    lens = [int(x) for x in torch.randint(1, longest, (300 if new < 10 else 60,), generator=g)]
+    check(gdn, [new] * len(lens), lens, Hq, 2, d, 16, "bf16", packed=False)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_keys_of_growing_size(gdn, dtype):
     """The maximum grows tile after tile, so everything summed before is scaled down."""
