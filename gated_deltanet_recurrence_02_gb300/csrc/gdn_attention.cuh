@@ -2,8 +2,9 @@
 //
 // A unit is (row b, group of query heads that share a key head, block of tokens): its query
 // rows are rho = t gs + g, gs heads a token, so that all of them read a tile of keys once.
-// All units' tiles in a row, in the order of b, group, block, are cut into equal pieces, one
-// a CTA, so that no lengths, however ragged, leave CTAs idle.  Lengths are on the device, so
+// All units' tiles in a row, in the order of b, group, block, each unit with a few more in
+// front for what it costs to begin and end, are cut into equal pieces, one a CTA, so that no
+// lengths, however ragged, leave CTAs idle.  Lengths are on the device, so
 // each CTA finds its piece there: a sum over the rows and a search along the one it starts
 // in.  A unit that a cut goes through leaves its parts (unscaled sums, maxima, sums of
 // weights) in the workspace, at most two a CTA: the end of a unit that an earlier CTA began
@@ -34,6 +35,8 @@ struct alignas(16) Cut {
 struct Plan {
     int tokens, gs;      // tokens of a unit, query heads of a group
     int per_key;         // groups of a key head
+    int over;            // tiles that a unit's beginning and end cost
+    int least_log2;      // tiles of a piece, the least
     int ctas, d;
     uint8_t *ws;
     __host__ __device__ int rows() const { return tokens * gs; }
@@ -99,7 +102,7 @@ __device__ __forceinline__ int blocks_of(const Plan &s, const Row &r) {
 }
 
 // A place in the order of all tiles, and the tiles from there to the CTA's end; the other
-// CTAs' are `each` long, and one more before CTA `more`.
+// pieces are `each` long, and one more before CTA `more`.
 struct Place {
     int b, group, block, tile;
     long left, each, more;
@@ -125,14 +128,14 @@ __device__ Place find_place(const AttentionParams &p, const Plan &s) {
         unsigned wide = __ballot_sync(kAll, blocks > 4);
         long n = 0;
         if (blocks <= 4)
-            for (int i = 0; i < blocks; ++i) n += unit_of<KT>(p, s, mine, i).tiles;
+            for (int i = 0; i < blocks; ++i) n += unit_of<KT>(p, s, mine, i).tiles + s.over;
         while (wide != 0) {
             const int x = __ffs(wide) - 1;
             wide &= wide - 1;
             const Row r = row_of_lane(mine, x);
             const int its = __shfl_sync(kAll, blocks, x);
             long part = 0;
-            for (int i = lane; i < its; i += 32) part += unit_of<KT>(p, s, r, i).tiles;
+            for (int i = lane; i < its; i += 32) part += unit_of<KT>(p, s, r, i).tiles + s.over;
             for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kAll, part, o);
             if (lane == x) n = part;
         }
@@ -161,12 +164,12 @@ __device__ Place find_place(const AttentionParams &p, const Plan &s) {
         if (w < warp) before += sums[w];
         total += sums[w];
     }
-    // Equal pieces, the first ones a tile longer; no more CTAs than tiles, so that one without
-    // a piece never stands between a unit's parts.
+    // Equal pieces of at least `least`, the first ones a tile longer
     const int c = blockIdx.x;
-    const long each = total >> 31 ? total / s.ctas : (long)((unsigned)total / (unsigned)s.ctas);
-    const long more = total - each * s.ctas;
-    const long from = each * c + min((long)c, more), left = each + (c < more ? 1 : 0);
+    const int n_ctas = (int)min((long)s.ctas, max(1l, total >> s.least_log2));
+    const long each = total >> 31 ? total / n_ctas : (long)((unsigned)total / (unsigned)n_ctas);
+    const long more = total - each * n_ctas;
+    const long from = each * c + min((long)c, more), left = c < n_ctas ? each + (c < more ? 1 : 0) : 0;
     if (left > 0 && before <= from && from < before + all) {
         long rest = from - before;
         for (int b = b0; b < b1; b += 32) {
@@ -187,7 +190,7 @@ __device__ Place find_place(const AttentionParams &p, const Plan &s) {
             }
             const int blocks = blocks_of(s, r);
             for (int i = 0;; i += 32) {
-                const int t = i + lane < blocks ? unit_of<KT>(p, s, r, i + lane).tiles : 0;
+                const int t = i + lane < blocks ? unit_of<KT>(p, s, r, i + lane).tiles + s.over : 0;
                 const long sum = scan(t);
                 const unsigned at = __ballot_sync(kAll, rest < sum);
                 if (at == 0) {
@@ -196,7 +199,10 @@ __device__ Place find_place(const AttentionParams &p, const Plan &s) {
                 }
                 const int y = __ffs(at) - 1;
                 rest -= __shfl_sync(kAll, sum - t, y);
-                if (lane == 0) found = Place{b + x, group, i + y, (int)rest, left, each, more, r};
+                // (in what a unit has in front: at its first tile, the rest of that gone)
+                const int ahead = max(0, s.over - (int)min(rest, 1l << 30));
+                if (lane == 0)
+                    found = Place{b + x, group, i + y, (int)max(0l, rest - s.over), left - ahead, each, more, r};
                 break;
             }
             break;
@@ -226,7 +232,7 @@ struct Walk {
         return true;
     }
     __device__ __forceinline__ bool next(const AttentionParams &p, const Plan &s) {
-        at.left -= end - at.tile;
+        at.left -= end - at.tile + s.over;
         if (at.left <= 0) return false;
         at.tile = 0;
         if (++at.block == blocks) {
@@ -261,7 +267,8 @@ struct Walk {
         c.row0 = (row.tok0 + unit.t0) * p.Hq + head0(p, s);
         c.tokens = unit.t1 - unit.t0;
         c.heads = heads(p, s);
-        // CTAs from here on: pieces of each + 1 tiles up to CTA `more`, then of each
+        // CTAs from here on: pieces of each + 1 tiles up to CTA `more`, then of each (all of
+        // them the unit's tiles)
         const long rest = unit.tiles - end, longer = max(0l, at.more - (long)(blockIdx.x + 1));
         const long in = longer * (at.each + 1);
         c.parts = 1 + (int)(rest <= in ? (rest + at.each) / (at.each + 1) : longer + (rest - in + at.each - 1) / at.each);
@@ -322,12 +329,14 @@ __global__ void __launch_bounds__(256) join_kernel(const AttentionParams p, cons
 cudaError_t launch_join(const AttentionParams &p, const Plan &s, cudaStream_t stream);
 
 // Units of up to `rows` query rows.
-inline Plan plan_of(int Hq, int Hk, int d, int rows, int ctas) {
+inline Plan plan_of(int Hq, int Hk, int d, int rows, int ctas, int over, int least_log2) {
     Plan s{};
     const int G = Hq / Hk;
     s.per_key = (G + rows - 1) / rows;
     s.gs = (G + s.per_key - 1) / s.per_key;
     s.tokens = rows / s.gs;
+    s.over = over;
+    s.least_log2 = least_log2;
     s.ctas = ctas;
     s.d = d;
     return s;

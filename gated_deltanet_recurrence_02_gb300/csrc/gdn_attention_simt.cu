@@ -260,7 +260,7 @@ cudaError_t launch_attention_simt(const AttentionParams &p, const Plan &s, cudaS
 // Query rows a unit: 16 where a row of the batch has no more on average, else 64.
 Plan plan_simt(int B, int T, int Hq, int Hk, int d, bool varlen) {
     const int rows = mean_tokens(B, T, varlen) * (Hq / Hk) <= 16 ? 16 : 64;
-    return plan_of(Hq, Hk, d, rows, 2 * sm_count_of_current_device());
+    return plan_of(Hq, Hk, d, rows, 2 * sm_count_of_current_device(), 1, 1);
 }
 
 }  // namespace attn

@@ -5,13 +5,14 @@
 //     S = Q K^T,  m' = max(m, max_j S_j),  P_j = 2^{c S_j - c m'}
 //     l <- 2^{c (m - m')} l + sum_j P_j,   O <- 2^{c (m - m')} O + P V
 // and O / l at the end.  S and O are fp32 in TMEM, a query row to a lane, so a thread has a
-// whole row of a tile: no reduction crosses threads.  m follows the true maximum only when
-// that has grown by more than 8 in the exponent: weights of up to 2^8 are as exact, and most
-// tiles then leave O where it is.
+// whole row of a tile: no reduction crosses threads.  Any m will do that keeps the weights in
+// range, so a tile is first weighed with the m of the tiles before it, and m looked for only
+// where the row's sum of weights passes 2^15: most tiles need no maximum, and leave O where
+// it is.
 //
 // Roundings: P to the inputs' type for the tensor cores, the result once; l sums the weights
 // in fp32 before their rounding.  fp16 weights are scaled by 2^7, so that they keep full
-// precision down to 2^-21 of the largest and stay below 2^15.
+// precision down to 2^-21 of the largest (with m anew).
 #include <algorithm>
 #include <cstring>
 #include <numeric>
@@ -29,8 +30,9 @@ constexpr int kThreads = 512;
 // registers a thread: 128 at launch, of which two warpgroups give 72 each to the others
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 56;
 constexpr uint32_t kBlock = 16384;  // 128 rows of 64 elements
+constexpr uint32_t tS = 0, tO = 256;  // TMEM: S (and P in its place) and O of a slot, 128 columns each
 constexpr uint32_t kTmemCols = 512;
-constexpr float kGrowth = 8.f;      // of the maximum's exponent, before O follows
+constexpr float kMost = 32768.f;    // sum of a row's weights of a tile without a new maximum
 constexpr int kUnits = 4;           // units ahead
 
 // Two ways to use the two slots (S and O in TMEM and a warpgroup each):
@@ -41,14 +43,8 @@ enum Mode { kPair, kOne };
 // Shared memory: queries (blocks of 64 features, 128 rows each; kPair: both slots' of a unit,
 // kOne: of two units in turn), the rings of tiles of keys and of values (8 keys x 64 features
 // a kilobyte, all features of 8 keys together), and what the warps tell each other.
-template <int NB, int MODE>
+template <int NB>
 struct Layout {
-    // TMEM columns: S of the slots, 128 each, and O.  For heads of up to 64 there is room for P
-    // of its own: the next tile's S can follow as soon as the last one has been read.  (Else P
-    // takes S's place, and S waits for the product with it.)
-    static constexpr bool kOwnP = NB == 1;
-    static constexpr uint32_t tS = 0, tO = 256, kO = 64 * NB;
-    static constexpr uint32_t tP = kOwnP ? 384 : tS, kP = kOwnP ? 64 : 128;  // 64 columns used
     static constexpr uint32_t kTile = NB * kBlock;
     static constexpr int NK = NB == 2 ? 3 : 5, NV = NB == 2 ? 2 : 5;  // tiles of keys, and of values, in flight
     static constexpr uint32_t oK = 2 * kTile, oV = oK + NK * kTile;
@@ -155,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                  const __grid_constant__ CUtensorMap mv) {
     using H = Half16<E>;
-    using L = Layout<NB, MODE>;
+    using L = Layout<NB>;
     constexpr int NK = L::NK, NV = L::NV;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_align1k(smem_raw);
@@ -163,8 +159,7 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
     uint64_t *v_full = k_empty + NK, *v_empty = v_full + NV;
     uint64_t *u_full = v_empty + NV, *u_empty = u_full + kUnits;
     uint64_t *q_full = u_empty + kUnits, *q_free = q_full + 2;  // (kPair: the first of each)
-    // of a slot each: S is there, has been read (kOwnP), P is there, O has been added to
-    uint64_t *s_full = q_free + 2, *s_free = s_full + 2, *p_ready = s_free + 2, *o_done = p_ready + 2;
+    uint64_t *s_full = q_free + 2, *p_ready = s_full + 2, *o_done = p_ready + 2;  // of a slot each
     uint64_t *other = o_done + 2, *merged = other + 1, *drain = other + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(other + 3);
     Work *works = reinterpret_cast<Work *>(sm + L::oWork);
@@ -174,19 +169,18 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
         for (int i = 0; i < 2 * (NK + NV); ++i) mbar_init(&k_full[i], 1);  // both rings'
         for (int i = 0; i < kUnits; ++i) {
             mbar_init(&u_full[i], 1);
-            mbar_init(&u_empty[i], 8 + 2 + (L::kOwnP ? 2 : 1));  // softmax, loading, issuing warps
+            mbar_init(&u_empty[i], 8 + 3);  // softmax, loading, issuing warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&q_free[i], 1);
             mbar_init(&s_full[i], 1);
-            mbar_init(&s_free[i], 4);
             mbar_init(&p_ready[i], 4);
             mbar_init(&o_done[i], 1);
         }
         mbar_init(other, 4);
         mbar_init(merged, 4);
-        mbar_init(drain, L::kOwnP ? 2 : 1);
+        mbar_init(drain, 1);
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -226,7 +220,7 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
         const int s = warp >> 2, r = (warp & 3) * 32 + lane;  // slot, row of the slot
         const int t = r / p.plan.gs, g = r - t * p.plan.gs;   // its token in the slot, its head in the group
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t ts = lanes + L::tS + 128 * s, tp = lanes + L::tP + L::kP * s, to = lanes + L::tO + L::kO * s;
+        const uint32_t ts = lanes + tS + 128 * s, to = lanes + tO + 128 * s;
         float2 *merge = reinterpret_cast<float2 *>(sm + L::oMerge);
         const float2 c2 = make_float2(p.c, p.c);
         const int slot_t = MODE == kPair ? s * p.slot_tokens : 0;
@@ -254,11 +248,6 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                 if (!(ok = wait(&s_full[s], item))) break;
                 fence_after_sync();
                 if (idle) {
-                    if (L::kOwnP) {
-                        arrive(&s_free[s]);
-                        // (this S may be there before the other warps' last P is)
-                        if (item > 0 && !(ok = wait(&p_ready[s], item - 1))) break;
-                    }
                     arrive(&p_ready[s]);
                     continue;
                 }
@@ -266,10 +255,6 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
 #pragma unroll
                 for (int j = 0; j < 4; ++j) tmem_ld32_async(ts + 32 * j, v[j]);
                 tmem_wait_ld();
-                if (L::kOwnP) {
-                    fence_before_sync();
-                    arrive(&s_free[s]);
-                }
                 const int a = lo - (x.key0 + i * KT), e = hi - (x.key0 + i * KT);
                 if (__any_sync(kAll, e < KT)) {
 #pragma unroll
@@ -281,68 +266,68 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                     for (int j = 0; j < KT; ++j)
                         if (j < a) v[j >> 5][j & 31] = 0xff800000u;
                 }
-                float top[4];
+                // The weights, relative to the maximum as it was; where a row's sum comes out too
+                // large (and for the first tile), once more with the maximum taken anew.
+                bool anew = i == i0;
+                float2 sum[2];
+                while (true) {
+                    if (anew) {
+                        float top[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) top[j] = __uint_as_float(v[j][0]);
+                        for (int j = 0; j < 4; ++j) top[j] = __uint_as_float(v[j][0]);
 #pragma unroll
-                for (int k = 1; k < 32; ++k)
+                        for (int k = 1; k < 32; ++k)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) top[j] = fmaxf(top[j], __uint_as_float(v[j][k]));
-                const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.c;
-                const bool grow = now - m > kGrowth;  // (from none: always, unless there is still none)
-                if (__any_sync(kAll, grow)) {
-                    const float keep = grow ? ex2_approx(m - now) : 1.f;
-                    m = grow ? now : m;
-                    if (i != i0) {
-                        // (else the slot's last product is done: S was issued behind it)
-                        if (L::kOwnP) {
-                            if (!(ok = wait(&o_done[s], item - 1))) break;
-                            fence_after_sync();
-                        }
-                        l *= keep;
-                        const float2 k2 = make_float2(keep, keep);
+                            for (int j = 0; j < 4; ++j) top[j] = fmaxf(top[j], __uint_as_float(v[j][k]));
+                        const float now = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.c, m);
+                        if (i != i0) {
+                            // (the slot's last product is done: S was issued behind it)
+                            const float keep = now == kNone ? 1.f : ex2_approx(m - now);
+                            l *= keep;
+                            const float2 k2 = make_float2(keep, keep);
 #pragma unroll 1
-                        for (int j = 0; j < p.d; j += 16) {
-                            uint32_t o[16];
-                            tmem_ld16_async(to + j, o);
-                            tmem_wait_ld();
+                            for (int j = 0; j < p.d; j += 16) {
+                                uint32_t o[16];
+                                tmem_ld16_async(to + j, o);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 16; k += 2) {
-                                const float2 y = __fmul2_rn(k2, make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])));
-                                o[k] = __float_as_uint(y.x);
-                                o[k + 1] = __float_as_uint(y.y);
+                                for (int k = 0; k < 16; k += 2) {
+                                    const float2 y =
+                                        __fmul2_rn(k2, make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])));
+                                    o[k] = __float_as_uint(y.x);
+                                    o[k + 1] = __float_as_uint(y.y);
+                                }
+                                tmem_st16(to + j, o);
                             }
-                            tmem_st16(to + j, o);
                         }
+                        m = now;
                     }
-                }
-                // (held finite: without keys so far weights are 0)
-                const float off = H::kShift - fmaxf(m, -3.4028235e38f);
-                const float2 off2 = make_float2(off, off);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    // (held finite: without keys so far, a score that there is makes the sum infinite)
+                    const float off = H::kShift - fmaxf(m, -3.4028235e38f);
+                    const float2 off2 = make_float2(off, off);
+                    sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t pk[16];
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        float2 y = __ffma2_rn(make_float2(__uint_as_float(v[j][k]), __uint_as_float(v[j][k + 1])), c2, off2);
-                        y.x = ex2_approx(y.x);
-                        y.y = ex2_approx(y.y);
-                        sum[(k >> 1) & 1] = __fadd2_rn(sum[(k >> 1) & 1], y);
-                        pk[k / 2] = H::pack2(y.x, y.y);
+                        for (int k = 0; k < 32; k += 2) {
+                            float2 y = __ffma2_rn(make_float2(__uint_as_float(v[j][k]), __uint_as_float(v[j][k + 1])), c2, off2);
+                            y.x = ex2_approx(y.x);
+                            y.y = ex2_approx(y.y);
+                            sum[(k >> 1) & 1] = __fadd2_rn(sum[(k >> 1) & 1], y);
+                            pk[k / 2] = H::pack2(y.x, y.y);
+                        }
+                        tmem_st16(ts + 16 * j, pk);
                     }
-                    if (L::kOwnP && j == 0 && i != i0) {  // the last P has been used
-                        if (!(ok = wait(&o_done[s], item - 1))) break;
-                        fence_after_sync();
-                    }
-                    tmem_st16(tp + 16 * j, pk);
+                    sum[0] = __fadd2_rn(sum[0], sum[1]);
+                    sum[0].x += sum[0].y;
+                    if (anew || !__any_sync(kAll, mine && !(sum[0].x <= kMost))) break;
+                    anew = true;
                 }
-                if (!ok) break;
                 tmem_wait_st();
                 fence_before_sync();
                 arrive(&p_ready[s]);
-                sum[0] = __fadd2_rn(sum[0], sum[1]);
-                l += sum[0].x + sum[0].y;
+                l += sum[0].x;
             }
             if (!ok) break;
             const bool any = i1 > i0;  // the slot has sums of its own
@@ -402,7 +387,7 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                         uint32_t o[2][16];
 #pragma unroll
                         for (int q = 0; q < 2; ++q)
-                            if (32 * q < p.d) tmem_ld_16x32(from + part * L::kO + 32 * q, o[q]);
+                            if (32 * q < p.d) tmem_ld_16x32(from + part * 128 + 32 * q, o[q]);
                         tmem_wait_ld();
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -548,28 +533,25 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
             // (a barrier's last completion: older ones are not told from none)
             for (int x = max(0, live - (MODE == kOne ? 2 : 1)); x < live; ++x)
                 mbar_wait(&q_full[MODE == kOne ? x & 1 : 0], (uint32_t)(MODE == kOne ? x >> 1 : x) & 1u, kDefaultWaitNs / 8);
-        } else if (warp == 9 || (warp == 12 && L::kOwnP)) {
+        } else if (warp == 9) {
             // ============================ MMAs ===========================
             // One warp issues all, slot after slot, so that one slot's softmax runs under the
             // other's products (a warp a slot: both ran in step, 4100 tokens over 32100 keys took
-            // 1403 us, not 1225).  Where P has its own place a second one issues the sums: an
-            // MMA and a commit cost their issuer some 40 cycles each, and the products of d = 64
-            // are over in 260.
-            const bool does_scores = !L::kOwnP || warp == 9, does_sums = !L::kOwnP || warp == 12;
+            // 1403 us, not 1180).
             // (a negative scale: of the scores' queries)
             const uint32_t id_s = idesc_f16(128, KT, false, false, H::kBf16) | (p.scale < 0.f ? 1u << 13 : 0u);
             const uint32_t id_o = idesc_f16(128, p.d, false, true, H::kBf16);
             const uint64_t q0 = desc_sw128(smem_u32(sm), 16, 1024);
             const uint64_t k0 = desc_sw128(smem_u32(sm) + L::oK, 16, NB * 1024);
             const uint64_t v0 = desc_sw128(smem_u32(sm) + L::oV, 1024, NB * 1024);
-            int live = 0, asked[2] = {0, 0}, items[2] = {0, 0};  // of a slot: scores, sums so far
-            int kst = 0, kround = 0, vst = 0, vround = 0;        // of the rings
+            int live = 0, items[2] = {0, 0};               // of a slot: sums so far
+            int kst = 0, kround = 0, vst = 0, vround = 0;  // of the rings
             Work x;
 #pragma unroll 1
             for (int u = 0; next_unit(u, x); ++u) {
                 if (x.n == 0) continue;
                 const int n = x.n, buf = MODE == kOne ? live & 1 : 0;
-                if (does_scores && !(ok = wait(&q_full[buf], MODE == kOne ? live >> 1 : live))) break;
+                if (!(ok = wait(&q_full[buf], MODE == kOne ? live >> 1 : live))) break;
                 auto has = [&](int s, int i) {
                     return MODE == kOne ? i >= 0 && i < n && (i & 1) == s
                                         : i >= (s ? x.a[1] : x.a[0]) && i < (s ? x.e[1] : x.e[0]);
@@ -580,18 +562,12 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                 // S of slot s = Q K_i^T, of the tile of keys at hand; `first`, `last`: of its uses
                 auto scores = [&](int s, bool first, bool last) {
                     if (first && !(ok = wait(&k_full[kst], kround))) return;
-                    if (L::kOwnP) {
-                        const int before = s ? asked[1] : asked[0];
-                        if (before > 0 && !(ok = wait(&s_free[s], before - 1))) return;
-                        if (s) ++asked[1];
-                        else ++asked[0];
-                    }
                     fence_after_sync();
                     const uint64_t qd = desc_add(q0, (MODE == kOne ? buf : s) * L::kTile), kd = desc_add(k0, kst * L::kTile);
 #pragma unroll
                     for (int k = 0; k < 4 * NB; ++k)
                         if (16 * k < p.d)
-                            mma_f16_warp(leader, tm + L::tS + 128 * s, desc_add(qd, (k >> 2) * kBlock + (k & 3) * 32),
+                            mma_f16_warp(leader, tm + tS + 128 * s, desc_add(qd, (k >> 2) * kBlock + (k & 3) * 32),
                                          desc_add(kd, (k >> 2) * 1024 + (k & 3) * 32), id_s, k > 0);
                     mma_commit_warp(leader, &s_full[s]);
                     if (last) {
@@ -628,7 +604,7 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                     const uint32_t more = has(s, i - (MODE == kPair ? 1 : 2));
 #pragma unroll
                     for (int k = 0; k < KT / 16; ++k)
-                        mma_f16_ta_warp(leader, tm + L::tO + L::kO * s, tm + L::tP + L::kP * s + 8 * k,
+                        mma_f16_ta_warp(leader, tm + tO + 128 * s, tm + tS + 128 * s + 8 * k,
                                         desc_add(vd, k * NB * 2048), id_o, k > 0 ? 1u : more);
                     mma_commit_warp(leader, &o_done[s]);
                     if (last) {
@@ -643,12 +619,10 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                     const int s = y & 1, i = MODE == kOne ? y - 2 : (y >> 1) - 1, to_come = MODE == kOne ? y : i + 1;
                     const bool both_sums = MODE == kPair && has(0, i) && has(1, i);
                     const bool both_scores = MODE == kPair && has(0, to_come) && has(1, to_come);
-                    if (does_sums && has(s, i)) sums(s, i, !both_sums || s == 0, !both_sums || s == 1);
-                    if (does_scores && ok) {
-                        if (has(s, to_come)) scores(s, !both_scores || s == 0, !both_scores || s == 1);
-                        // the unit's last scores are issued
-                        if (ok && y == (MODE == kOne ? n : 2 * n) - 1) mma_commit_warp(leader, &q_free[buf]);
-                    }
+                    if (has(s, i)) sums(s, i, !both_sums || s == 0, !both_sums || s == 1);
+                    if (ok && has(s, to_come)) scores(s, !both_scores || s == 0, !both_scores || s == 1);
+                    // the unit's last scores are issued
+                    if (ok && y == (MODE == kOne ? n : 2 * n) - 1) mma_commit_warp(leader, &q_free[buf]);
                 }
                 if (!ok) break;
                 ++live;
@@ -667,7 +641,7 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
 template <typename E, int NB, int MODE>
 cudaError_t launch_mode(const TcParams &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                         cudaStream_t stream) {
-    constexpr uint32_t bytes = Layout<NB, MODE>::kSmem;
+    constexpr uint32_t bytes = Layout<NB>::kSmem;
     cudaError_t e = set_smem_once<attention_kernel<E, NB, MODE>>((int)bytes);
     if (e != cudaSuccess) return e;
     attention_kernel<E, NB, MODE><<<p.plan.ctas, kThreads, bytes, stream>>>(p, mq, mk, mv);
@@ -715,8 +689,11 @@ bool tc_takes(const AttentionParams &p) {
 }
 
 Plan plan_tc(int B, int T, int Hq, int Hk, int d, bool varlen) {
-    Plan s = plan_of(Hq, Hk, d, 128, sm_count_of_current_device());
-    if (mean_tokens(B, T, varlen) > s.tokens) s.tokens *= 2;  // two blocks a unit
+    Plan s = plan_of(Hq, Hk, d, 128, sm_count_of_current_device(), 1, 1);
+    if (mean_tokens(B, T, varlen) > s.tokens) {
+        s.tokens *= 2;  // two blocks a unit
+        s.over = 2;
+    }
     return s;
 }
 
