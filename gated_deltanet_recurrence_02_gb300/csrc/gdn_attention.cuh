@@ -34,7 +34,7 @@ struct alignas(16) Cut {
 // sums [ctas][2][rows][d].
 struct Plan {
     int tokens, gs;      // tokens of a unit, query heads of a group
-    int per_key;         // groups of a key head
+    int per_key, G;      // groups, and query heads, of a key head
     int over;            // tiles that a unit's beginning and end cost
     int least_log2;      // tiles of a piece, the least
     int ctas, d;
@@ -159,10 +159,11 @@ __device__ Place find_place(const AttentionParams &p, const Plan &s) {
     if (threadIdx.x == 0) found.left = 0;
     __syncthreads();
     long before = 0, total = 0;
-#pragma unroll 1
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sums[w];
-        total += sums[w];
+        const long x = sums[w];
+        if (w < warp) before += x;
+        total += x;
     }
     // Equal pieces of at least `least`, the first ones a tile longer
     const int c = blockIdx.x;
@@ -255,10 +256,10 @@ struct Walk {
     // First query head of the group, and its heads.
     __device__ __forceinline__ int head0(const AttentionParams &p, const Plan &s) const {
         const int k = key_head(s);
-        return k * (p.Hq / p.Hk) + (at.group - k * s.per_key) * s.gs;
+        return k * s.G + (at.group - k * s.per_key) * s.gs;
     }
     __device__ __forceinline__ int heads(const AttentionParams &p, const Plan &s) const {
-        return min(s.gs, (key_head(s) + 1) * (p.Hq / p.Hk) - head0(p, s));
+        return min(s.gs, (key_head(s) + 1) * s.G - head0(p, s));
     }
     // What the CTA leaves for the join, after its last unit (one thread).
     __device__ __forceinline__ Cut cut(const AttentionParams &p, const Plan &s) const {
@@ -276,52 +277,76 @@ struct Walk {
     }
 };
 
-// Joins the parts of cut units.  Grid (ctas, slices): CTA x takes the unit that CTA x of the
-// attention began and did not end, a warp a query row; maxima are those of scores times log2 e.
-template <typename T>
+// Joins the parts of cut units; maxima are those of scores times log2 e.  Grid (ctas, slices):
+// CTA x takes the unit that CTA x of the attention began and did not end, a warp four query
+// rows at a time (eight parts each a look: most units have two), so that all their loads are
+// on their way together; D / 32 columns a lane.
+template <typename T, int D>
 __global__ void __launch_bounds__(256) join_kernel(const AttentionParams p, const Plan s) {
+    constexpr int kRows = 4, kLook = 32 / kRows, W = D / 32;
+    struct alignas(4 * W) Cols {
+        float v[W];
+    };
     tc::grid_dependency_wait();
     const Cut c = *s.cut(blockIdx.x);
-    const int lane = threadIdx.x % 32, warps = blockDim.x / 32, per = s.d / 32;
-    for (int i = blockIdx.y * warps + threadIdx.x / 32; i < c.tokens * s.gs; i += gridDim.y * warps) {
-        const int t = i / s.gs, g = i - t * s.gs;
-        if (g >= c.heads) continue;
-        auto stats = [&](int x) { return x < c.parts ? s.stats(blockIdx.x + x, x == 0)[i] : make_float2(kNone, 0.f); };
-        float top = kNone;
-        for (int x = lane; x < c.parts; x += 32) top = fmaxf(top, stats(x).x);
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    const int lane = threadIdx.x % 32, n = c.tokens * s.gs;
+    const int first = (blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32) * kRows, step = gridDim.y * (blockDim.x / 32) * kRows;
+    for (int i0 = first; i0 < n; i0 += step) {
+        const int mine = min(i0 + lane / kLook, n - 1);  // the row whose statistics the lane reads
+        auto stats = [&](int x) {
+            x += lane % kLook;
+            return x < c.parts ? s.stats(blockIdx.x + x, x == 0)[mine] : make_float2(kNone, 0.f);
+        };
+        auto over = [&](float x, auto f) {  // over the lanes of a row
+            for (int o = kLook / 2; o > 0; o >>= 1) x = f(x, __shfl_xor_sync(kAll, x, o));
+            return x;
+        };
+        float2 ml = stats(0);
+        float top = ml.x;
+        for (int x = kLook; x < c.parts; x += kLook) top = fmaxf(top, stats(x).x);
+        top = over(top, [](float a, float b) { return fmaxf(a, b); });
         const float safe = top == kNone ? 0.f : top;
-        float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int x0 = 0; x0 < c.parts; x0 += 32) {
-            const float2 ml = stats(x0 + lane);
-            const float mine = exp2f(ml.x - safe);
-            sum = fmaf(mine, ml.y, sum);
-#pragma unroll 8
-            for (int x = x0; x < min(c.parts, x0 + 32); ++x) {
-                const float *o = s.sums(blockIdx.x + x, x == 0) + (size_t)i * s.d + lane * per;
-                float v[4] = {0.f, 0.f, 0.f, 0.f};
-                if (per == 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(o);
-                    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-                } else if (per == 2) {
-                    const float2 f = *reinterpret_cast<const float2 *>(o);
-                    v[0] = f.x, v[1] = f.y;
-                } else {
-                    v[0] = o[0];
-                }
-                const float w = __shfl_sync(kAll, mine, x - x0);
+        float sum = 0.f, acc[kRows][W];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int e = 0; e < W; ++e) acc[r][e] = 0.f;
+        for (int x0 = 0; x0 < c.parts; x0 += kLook) {
+            if (x0 > 0) ml = stats(x0);
+            const float weight = exp2f(ml.x - safe);
+            sum = fmaf(weight, ml.y, sum);
+#pragma unroll 4
+            for (int x = x0; x < min(c.parts, x0 + kLook); ++x) {
+                Cols v[kRows];
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+                    v[r] = *reinterpret_cast<const Cols *>(s.sums(blockIdx.x + x, x == 0) +
+                                                           (size_t)min(i0 + r, n - 1) * D + lane * W);
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const float w = __shfl_sync(kAll, weight, r * kLook + x - x0);
+#pragma unroll
+                    for (int e = 0; e < W; ++e) acc[r][e] = fmaf(w, v[r].v[e], acc[r][e]);
+                }
             }
         }
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-        const long at = c.row0 + (long)t * p.Hq + g;
+        sum = over(sum, [](float a, float b) { return a + b; });
+        const float lse = (safe + log2f(sum)) * 0.69314718055994530942f;
         const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;  // (a NaN stays one)
-        T *out = reinterpret_cast<T *>(p.out) + at * p.d + lane * per;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (e < per) st_out(out + e, acc[e] * inv);
-        if (p.lse != nullptr && lane == 0) p.lse[at] = (safe + log2f(sum)) * 0.69314718055994530942f;
+        for (int r = 0; r < kRows; ++r) {
+            const float f = __shfl_sync(kAll, inv, r * kLook), log_sum = __shfl_sync(kAll, lse, r * kLook);
+            const int i = i0 + r, t = i / s.gs, g = i - t * s.gs;
+            if (i >= n || g >= c.heads) continue;
+            const long at = c.row0 + (long)t * p.Hq + g;
+            struct alignas(sizeof(T) * W) Out {
+                T v[W];
+            } out;
+#pragma unroll
+            for (int e = 0; e < W; ++e) st_out(&out.v[e], acc[r][e] * f);
+            *reinterpret_cast<Out *>(reinterpret_cast<T *>(p.out) + at * D + lane * W) = out;
+            if (p.lse != nullptr && lane == 0) p.lse[at] = log_sum;
+        }
     }
 }
 
@@ -331,9 +356,9 @@ cudaError_t launch_join(const AttentionParams &p, const Plan &s, cudaStream_t st
 // Units of up to `rows` query rows.
 inline Plan plan_of(int Hq, int Hk, int d, int rows, int ctas, int over, int least_log2) {
     Plan s{};
-    const int G = Hq / Hk;
-    s.per_key = (G + rows - 1) / rows;
-    s.gs = (G + s.per_key - 1) / s.per_key;
+    s.G = Hq / Hk;
+    s.per_key = (s.G + rows - 1) / rows;
+    s.gs = (s.G + s.per_key - 1) / s.per_key;
     s.tokens = rows / s.gs;
     s.over = over;
     s.least_log2 = least_log2;

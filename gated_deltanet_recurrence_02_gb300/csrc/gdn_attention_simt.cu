@@ -229,11 +229,12 @@ cudaError_t launch_t(const AttentionParams &p, const Plan &s, cudaStream_t strea
     }
 }
 
-template <typename T>
-cudaError_t launch_join_t(const AttentionParams &p, const Plan &s, cudaStream_t stream) {
+template <typename T, int D>
+cudaError_t launch_join_d(const AttentionParams &p, const Plan &s, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
+    // (a warp has four rows at a time, a CTA eight warps; no more CTAs than run at once)
     const long most = std::min<long>(s.rows(), (long)p.T * s.gs);  // query rows of a unit
-    cfg.gridDim = dim3((unsigned)s.ctas, (unsigned)((most + 7) / 8));
+    cfg.gridDim = dim3((unsigned)s.ctas, (unsigned)std::min<long>((most + 31) / 32, 4));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -241,8 +242,17 @@ cudaError_t launch_join_t(const AttentionParams &p, const Plan &s, cudaStream_t 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<T>, p, s);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<T, D>, p, s);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_join_t(const AttentionParams &p, const Plan &s, cudaStream_t stream) {
+    switch (p.d) {
+        case 32: return launch_join_d<T, 32>(p, s, stream);
+        case 64: return launch_join_d<T, 64>(p, s, stream);
+        default: return launch_join_d<T, 128>(p, s, stream);
+    }
 }
 
 }  // namespace

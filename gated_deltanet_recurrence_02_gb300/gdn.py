@@ -614,10 +614,21 @@ def gdn_accept_drafts(target_probs, draft_probs, draft_tokens, uniform, *, draft
     return tokens, emitted_count
 
 
-def _int32(t, what: str):
-    """Pointer of a contiguous int32 tensor on the device."""
-    if t.dtype != torch.int32:
-        raise ValueError(f"{what} is int32")
+def _heads(t, N: int, H: int, d: int):
+    """Pointer and token stride (elements) of heads [N, H, d] whose tokens are contiguous
+    (slices of wider rows among them)."""
+    s0, s1, s2 = t.stride()
+    if not t.is_cuda:
+        raise ValueError("libgdn takes device tensors")
+    if (s2 != 1 and d != 1) or (s1 != d and H != 1):
+        raise ValueError("the elements of a token must be contiguous")
+    return t.data_ptr(), s0 if N > 1 else H * d
+
+
+def _ints(t, shape, what: str):
+    """Pointer of a contiguous int32 tensor of this shape."""
+    if t.dtype != torch.int32 or t.shape != shape:
+        raise ValueError(f"{what} is int32 {list(shape)}")
     return _p(t)
 
 
@@ -626,18 +637,17 @@ def _turn_args(inv_freq, positions, axes, N: int, d: int):
     half = inv_freq.shape[0]
     if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or 2 * half > d:
         raise ValueError("inv_freq is float32 [R / 2], R of at most a head's size")
-    A = 1
-    pp = ap = None
+    A, pp, ap = 1, None, None
     if positions is not None:
         if positions.dim() == 2:
             A = positions.shape[0]
-        if positions.shape[-1] != N or positions.dim() > 2 or A < 1:
-            raise ValueError("positions is int32 [N] or [A, N]")
-        pp = _int32(positions, "positions")
-    if axes is not None:
-        if axes.shape != (half,):
-            raise ValueError("axes is int32 [R / 2]")
-        ap = _int32(axes, "axes")
+            if A < 1:
+                raise ValueError("positions is int32 [N] or [A, N], A of one at least")
+            pp = _ints(positions, (A, N), "positions")
+        else:
+            pp = _ints(positions, (N,), "positions")
+        if axes is not None:
+            ap = _ints(axes, (half,), "axes")
     return _p(inv_freq), pp, ap, 2 * half, A
 
 
@@ -651,14 +661,14 @@ def gdn_rotary(x, positions, inv_freq, *, axes=None, pairs: bool = False, invers
     shape, dtype = x.shape, x.dtype
     N, H, d = shape
     fp, pp, ap, R, A = _turn_args(inv_freq, positions, axes, N, d)
+    xp, xs = _heads(x, N, H, d)
     if out is None:
         out = _empty(shape, dtype, x.device, stream)
         op, os_ = out.data_ptr(), H * d
     else:
         if out.shape != shape or out.dtype != dtype:
             raise ValueError("out must have the shape and the dtype of x")
-        op, os_ = _rows(out, 2)
-    xp, xs = _rows(x, 2)
+        op, os_ = _heads(out, N, H, d)
     flags = (GDN_ROTARY_PAIRS if pairs else 0) | (GDN_ROTARY_INVERSE if inverse else 0)
     st = lib().gdn_rotary(xp, op, pp, ap, fp, N, H, d, R, A, xs, os_, flags, _DT[dtype], _stream(stream))
     if st:
@@ -670,27 +680,26 @@ def _page_args(k_pages, v_pages, page_table, kv_lens, B: int, dtype):
     """Shape, pointers and strides of a cache [num_pages, page_size, Hk, d] (any order of the
     first three dimensions in memory), with its table and its lengths."""
     pages, page_size, Hk, d = shape = k_pages.shape
-    strides = k_pages.stride()
+    s0, s1, s2, s3 = strides = k_pages.stride()
     if v_pages.shape != shape or v_pages.stride() != strides:
         raise ValueError("k_pages and v_pages are [num_pages, page_size, Hk, d] with the same strides")
     if k_pages.dtype != dtype or v_pages.dtype != dtype:
         raise ValueError("the pages must have the dtype of the tokens")
-    if strides[3] != 1 and d != 1:
+    if s3 != 1 and d != 1:
         raise ValueError("the elements of a slot's head must be contiguous")
     if not (k_pages.is_cuda and v_pages.is_cuda):
         raise ValueError("libgdn takes device tensors")
-    if page_table.dim() != 2 or page_table.shape[0] != B or kv_lens.shape != (B,):
-        raise ValueError("page_table is int32 [B, max_pages], kv_lens int32 [B]")
-    return (Hk, d, k_pages.data_ptr(), v_pages.data_ptr(), _int32(page_table, "page_table"),
-            _int32(kv_lens, "kv_lens"), (pages, page_size, page_table.shape[1], *strides[:3]))
+    if page_table.dim() != 2:
+        raise ValueError("page_table is int32 [B, max_pages]")
+    width = page_table.shape[1]
+    return (Hk, d, k_pages.data_ptr(), v_pages.data_ptr(), _ints(page_table, (B, width), "page_table"),
+            _ints(kv_lens, (B,), "kv_lens"), pages, page_size, width, s0, s1, s2)
 
 
 def _row_count(total: int, B: int, T, cu_seqlens):
     """T argument and pointer of the rows of `total` tokens."""
     if cu_seqlens is not None:
-        if cu_seqlens.shape != (B + 1,):
-            raise ValueError("cu_seqlens is int32 [B + 1]")
-        return total, _int32(cu_seqlens, "cu_seqlens")
+        return total, _ints(cu_seqlens, (B + 1,), "cu_seqlens")
     if T is None:
         T = total // B if B else 0
     if B * T > total or T < 0:
@@ -704,43 +713,41 @@ def gdn_paged_append(k, v, k_pages, v_pages, page_table, kv_lens, *, B: int, T: 
     """New tokens' keys and values [total_T, Hk, d] into the cache's pages
     [num_pages, page_size, Hk, d], row b's at the positions that end at kv_lens[b].  With
     inv_freq the keys, and the queries q [total_T, Hq, d], are rotated on the way, by
-    `positions` or by their positions in the cache (see gdn_rotary).  Returns the
-    rotated queries (q_out, which may be q), or None without q."""
+    `positions` (see gdn_rotary; of the B * T tokens where rows are uniform) or by their
+    positions in the cache.  Returns the rotated queries (q_out, which may be q), or None
+    without q."""
     N, Hk, d = shape = k.shape
     dtype = k.dtype
     if v.shape != shape or v.dtype != dtype:
         raise ValueError("v must have the shape and the dtype of k")
-    ph, pd, kp, vp, tp, lp, pages = _page_args(k_pages, v_pages, page_table, kv_lens, B, dtype)
-    if (ph, pd) != (Hk, d):
+    ph, pd, kp, vp, tp, lp, pages, size, width, s0, s1, s2 = _page_args(k_pages, v_pages, page_table, kv_lens, B, dtype)
+    if ph != Hk or pd != d:
         raise ValueError("the pages must have the heads of k")
     T, cp = _row_count(N, B, T, cu_seqlens)
     fp = pp = ap = None
     R, A = 0, 1
     if inv_freq is not None:
-        # (uniform rows may end before the tensor does; positions has their number)
         fp, pp, ap, R, A = _turn_args(inv_freq, positions, axes, N if cp is not None else B * T, d)
-        if pp is None and ap is not None:
-            ap = None  # the cache position on every axis
     Hq, qp, qs, op, os_ = 0, None, 0, None, 0
     if q is not None:
-        if q.shape[0] != N or q.shape[2] != d or q.dtype != dtype:
+        n, Hq, e = q_shape = q.shape
+        if n != N or e != d or q.dtype != dtype:
             raise ValueError("q is [total_T, Hq, d] in the dtype of k")
-        Hq = q.shape[1]
-        qp, qs = _rows(q, 2)
+        qp, qs = _heads(q, N, Hq, d)
         if q_out is None:
-            q_out = _empty(q.shape, dtype, q.device, stream)
+            q_out = _empty(q_shape, dtype, q.device, stream)
             op, os_ = q_out.data_ptr(), Hq * d
         else:
-            if q_out.shape != q.shape or q_out.dtype != dtype:
+            if q_out.shape != q_shape or q_out.dtype != dtype:
                 raise ValueError("q_out must have the shape and the dtype of q")
-            op, os_ = _rows(q_out, 2)
+            op, os_ = _heads(q_out, N, Hq, d)
     elif q_out is not None:
         raise ValueError("q_out goes with q")
-    xk, ks = _rows(k, 2)
-    xv, vs = _rows(v, 2)
+    xk, ks = _heads(k, N, Hk, d)
+    xv, vs = _heads(v, N, Hk, d)
     st = lib().gdn_paged_append(qp, xk, xv, op, kp, vp, tp, lp, cp, pp, ap, fp, B, T, Hq, Hk, d, R, A,
-                                qs, ks, vs, os_, *pages, GDN_ROTARY_PAIRS if pairs else 0, _DT[dtype],
-                                _stream(stream))
+                                qs, ks, vs, os_, pages, size, width, s0, s1, s2,
+                                GDN_ROTARY_PAIRS if pairs else 0, _DT[dtype], _stream(stream))
     if st:
         _check(st, "gdn_paged_append")
     return q_out
@@ -756,36 +763,43 @@ def gdn_paged_attention(q, k_pages, v_pages, page_table, kv_lens, *, B: int, T: 
                         window: int = 0, out=None, lse=None, want_lse: bool = False, workspace=None,
                         stream=None):
     """Attention of new tokens q [total_T, Hq, d] (rows may be slices) over the
-    cache, row b's last one at position kv_lens[b] - 1: over the keys up to a query's own (with a window, the last `window` of
-    them), or over all keys of the row without `causal`.  scale is d ** -0.5 by
-    default.  Returns (out, lse); lse [total_T, Hq] (None unless wanted) is the log of the sum of
-    weights."""
+    cache, row b's last one at position kv_lens[b] - 1: over the keys up to a query's own (with
+    a window, the last `window` of them), or over all keys of the row without `causal`.  scale
+    is d ** -0.5 by default.  Returns (out, lse); lse [total_T, Hq] (None unless wanted) is the
+    log of the sum of weights."""
     N, Hq, d = shape = q.shape
     dtype = q.dtype
-    Hk, pd, kp, vp, tp, lp, pages = _page_args(k_pages, v_pages, page_table, kv_lens, B, dtype)
+    Hk, pd, kp, vp, tp, lp, pages, size, width, s0, s1, s2 = _page_args(k_pages, v_pages, page_table, kv_lens, B, dtype)
     if pd != d:
         raise ValueError("the pages must have the head size of q")
     T, cp = _row_count(N, B, T, cu_seqlens)
+    qp, qs = _heads(q, N, Hq, d)
+    device = q.device
     if out is None:
-        out = _empty(shape, dtype, q.device, stream)
+        out = _empty(shape, dtype, device, stream)
+        op = out.data_ptr()
     elif out.shape != shape or out.dtype != dtype:
         raise ValueError("out must have the shape and the dtype of q")
+    else:
+        op = _p(out)
     if lse is None:
         if want_lse:
-            lse = _empty((N, Hq), torch.float32, q.device, stream)
+            lse = _empty((N, Hq), torch.float32, device, stream)
     elif lse.shape != (N, Hq) or lse.dtype != torch.float32:
         raise ValueError("lse is float32 [total_T, Hq]")
-    L = lib()
+    L, code = lib(), _DT[dtype]
     if workspace is None:
-        need = L.gdn_paged_attention_workspace_size(B, T, Hq, Hk, d, _DT[dtype], int(cp is not None))
-        if 0 < need < 1 << 62:
-            workspace = _empty(need, torch.uint8, q.device, stream, scratch=True)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    qp, qs = _rows(q, 2)
-    st = L.gdn_paged_attention(qp, kp, vp, tp, lp, cp, _p(out), _p(lse), B, T, Hq, Hk, d, qs, *pages,
-                               d ** -0.5 if scale is None else scale, window,
-                               0 if causal else GDN_ATTENTION_FULL, _DT[dtype], _p(workspace), ws_bytes,
-                               _stream(stream))
+        ws_bytes = L.gdn_paged_attention_workspace_size(B, T, Hq, Hk, d, code, cp is not None)
+        if 0 < ws_bytes < 1 << 62:
+            workspace = _empty(ws_bytes, torch.uint8, device, stream, scratch=True)
+            wp = workspace.data_ptr()
+        else:
+            wp = None
+    else:
+        wp, ws_bytes = _p(workspace), workspace.numel() * workspace.element_size()
+    st = L.gdn_paged_attention(qp, kp, vp, tp, lp, cp, op, _p(lse), B, T, Hq, Hk, d, qs, pages, size, width,
+                               s0, s1, s2, d ** -0.5 if scale is None else scale, window,
+                               0 if causal else GDN_ATTENTION_FULL, code, wp, ws_bytes, _stream(stream))
     if st:
         _check(st, "gdn_paged_attention")
     return out, lse
