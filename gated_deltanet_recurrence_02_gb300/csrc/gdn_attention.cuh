@@ -371,7 +371,7 @@ inline long mean_tokens(int B, int T, bool varlen) { return varlen ? ((long)T + 
 
 Plan plan_simt(int B, int T, int Hq, int Hk, int d, bool varlen);
 cudaError_t launch_attention_simt(const AttentionParams &p, const Plan &s, cudaStream_t stream);
-// 16-bit tensors that TMA can address, with pages of a multiple of 8 slots.
+// 16-bit tensors whose addresses and strides are multiples of 16 bytes.
 bool tc_takes(const AttentionParams &p);
 Plan plan_tc(int B, int T, int Hq, int Hk, int d, bool varlen);
 cudaError_t launch_attention_tc(const AttentionParams &p, const Plan &s, cudaStream_t stream);

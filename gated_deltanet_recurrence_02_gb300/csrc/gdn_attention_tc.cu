@@ -163,13 +163,21 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
     uint64_t *other = o_done + 2, *merged = other + 1, *drain = other + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(other + 3);
     Work *works = reinterpret_cast<Work *>(sm + L::oWork);
+    const bool gather = p.box < 8;  // pages that TMA boxes do not fit
     const int warp = __shfl_sync(kAll, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2 * (NK + NV); ++i) mbar_init(&k_full[i], 1);  // both rings'
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(&k_full[i], gather ? 2 : 1);
+            mbar_init(&k_empty[i], 1);
+        }
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(&v_full[i], gather ? 2 : 1);
+            mbar_init(&v_empty[i], 1);
+        }
         for (int i = 0; i < kUnits; ++i) {
             mbar_init(&u_full[i], 1);
-            mbar_init(&u_empty[i], 8 + 3);  // softmax, loading, issuing warps
+            mbar_init(&u_empty[i], 8 + 3 + (gather ? 2 : 0));  // softmax, loading, issuing warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
@@ -442,10 +450,90 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
     } else {
         regs_dec<kOtherRegs>();
         const uint32_t leader = elect_leader();
-        if (warp == 8 || warp == 10) {
+        if (gather && (warp & 1) == 0) {
+            // ====== loads, keys or values: pages of any size, 16 bytes a lane ======
+            // Two warps a tile, 64 rows each.  The copies are this thread's own writes: it waits
+            // for them and passes them to the tensor cores' side with a fence, a tile behind.
+            constexpr int kCols = 8 * NB;  // 16-byte columns of a row (of 32 elements: 4)
+            const bool values = (warp & 2) != 0;
+            const int r0 = warp >= 12 ? 64 : 0;
+            uint64_t *full = values ? v_full : k_full, *empty = values ? v_empty : k_empty;
+            const char *pages = static_cast<const char *>(values ? p.v_pages : p.k_pages);
+            uint8_t *ring = sm + (values ? L::oV : L::oK);
+            const int stages = values ? NV : NK;
+            int st = 0, round = 0, pending = -1;  // of the ring; the stage that is not handed on yet
+            auto hand_on = [&]() {
+                if (pending < 0) return;
+                fence_proxy_async();
+                arrive(&full[pending]);
+                pending = -1;
+            };
+            auto landed = [&]() {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                hand_on();
+            };
+            Work x;
+#pragma unroll 1
+            for (int u = 0; next_unit(u, x); ++u) {
+                const int32_t *table = p.page_table + (int64_t)x.b * p.max_pages;
+                // Pages of the lane's rows (lane, lane + 32 of the warp's), read a tile ahead
+                auto page_of = [&](int i, int h) {
+                    const int k = x.key0 + i * KT + r0 + 32 * h + lane;
+                    return i < x.n && k >= x.lo && k < x.hi ? table[(unsigned)k / (unsigned)p.page_size] : -1;
+                };
+                int ahead[2] = {page_of(0, 0), page_of(0, 1)};
+#pragma unroll 1
+                for (int i = 0; i < x.n; ++i) {
+                    const int k0 = x.key0 + i * KT + r0;
+                    long row[2];  // bytes into the pages; -1: left out, -2: zeros
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int k = k0 + 32 * h + lane, page = ahead[h];
+                        row[h] = -1;
+                        if (k >= x.lo && k < x.hi) {
+                            row[h] = -2;
+                            if (page >= 0 && page < p.num_pages)
+                                row[h] = 2 * (page * p.page_stride + (long)((unsigned)k % (unsigned)p.page_size) * p.slot_stride +
+                                              x.hk * p.head_stride);
+                            else atomicOr(p.err, (uint32_t)GDN_DEVERR_BAD_INDEX);
+                        }
+                        ahead[h] = page_of(i + 1, h);
+                    }
+                    if (round > 0) {
+                        if (!mbar_test_wait(&empty[st], (uint32_t)(round - 1) & 1u)) landed();
+                        __syncwarp();
+                        if (!(ok = wait(&empty[st], round - 1))) break;
+                    }
+                    uint8_t *dst = ring + st * L::kTile + (r0 >> 3) * (NB * 1024);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll 4
+                        for (int y = 0; y < kCols; ++y) {
+                            const int at = y * 32 + lane, r = at / kCols, c = at % kCols;  // row of 32, column
+                            const long from = __shfl_sync(kAll, row[h], r);
+                            if (from == -1 || 8 * c >= p.d) continue;
+                            const int q = 32 * h + r;
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                             smem_u32(dst + (q >> 3) * (NB * 1024) + (c >> 3) * 1024 + sw128_chunk(q & 7, c & 7))),
+                                         "l"(pages + (from < 0 ? 0 : from + 16 * c)), "r"(from < 0 ? 0 : 16)
+                                         : "memory");
+                        }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    if (pending >= 0) {
+                        asm volatile("cp.async.wait_group 1;" ::: "memory");
+                        hand_on();
+                    }
+                    pending = st;
+                    if (++st == stages) st = 0, ++round;
+                }
+                if (!ok) break;
+                landed();
+            }
+            landed();
+        } else if (warp == 8 || warp == 10) {
             // ================== loads: keys, or values ===================
             const bool values = warp == 10;
-            const int boxes = KT / p.box;
+            const int boxes = KT / p.box;  // (pages of a multiple of 8 slots)
             // This lane's box of a tile.  Its page is read a tile ahead.
             const int first = lane * p.box;
             uint64_t *full = values ? v_full : k_full, *empty = values ? v_empty : k_empty;
@@ -677,8 +765,8 @@ Steps steps_of(const AttentionParams &p) {
 }  // namespace
 
 bool tc_takes(const AttentionParams &p) {
-    if (p.dt == GDN_F32 || p.page_size % 8 != 0 || p.num_pages == 0) return false;
-    // tensor maps: addresses and strides of 16 bytes, strides below 2^40 bytes, indexes of 31 bits
+    if (p.dt == GDN_F32 || p.num_pages == 0) return false;
+    // tensor maps, and 16-byte copies: addresses and strides of 16 bytes, strides below 2^40 bytes, indexes of 31 bits
     const uint64_t all = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k_pages) |
                          reinterpret_cast<uintptr_t>(p.v_pages) |
                          (uint64_t)(p.qs | p.page_stride | p.slot_stride | p.head_stride) * 2;
@@ -713,9 +801,12 @@ cudaError_t launch_attention_tc(const AttentionParams &pp, const Plan &plan, cud
     const long total = p.cu_seqlens != nullptr ? (long)p.T : (long)p.B * p.T;
     const bool bf = p.dt == GDN_BF16;
     CUtensorMap mq, mk, mv;
-    if (!encode_heads_map(&mq, p.q, bf, p.d, p.Hq, total, p.qs, plan.gs, p.slot_tokens) ||
-        !encode_pages_map(&mk, p.k_pages, bf, p.d, p.page_size, p.slot_stride, x.count, x.unit, p.box) ||
-        !encode_pages_map(&mv, p.v_pages, bf, p.d, p.page_size, p.slot_stride, x.count, x.unit, p.box))
+    memset(&mk, 0, sizeof(mk));
+    memset(&mv, 0, sizeof(mv));
+    if (!encode_heads_map(&mq, p.q, bf, p.d, p.Hq, total, p.qs, plan.gs, p.slot_tokens)) return cudaErrorInvalidValue;
+    if (p.box >= 8 &&
+        (!encode_pages_map(&mk, p.k_pages, bf, p.d, p.page_size, p.slot_stride, x.count, x.unit, p.box) ||
+         !encode_pages_map(&mv, p.v_pages, bf, p.d, p.page_size, p.slot_stride, x.count, x.unit, p.box)))
         return cudaErrorInvalidValue;
     if (p.d == 128)
         return bf ? launch_nb<__nv_bfloat16, 2>(p, mq, mk, mv, stream) : launch_nb<__half, 2>(p, mq, mk, mv, stream);
