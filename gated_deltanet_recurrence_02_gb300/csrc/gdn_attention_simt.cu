@@ -9,8 +9,11 @@
 // and o / l at the end; all in fp32.  A key that a query does not see gets no weight and its
 // values are not added, whatever they hold.  A row without keys gives 0 and a log of -inf.
 //
-// A CTA of 64 (or, for few rows, 16) query rows holds them, a tile of keys and one of values
-// in shared memory; a thread has four rows of a few keys, then of a few output features.
+// Two kernels.  Of up to 16 query rows (single tokens, a few drafts), bound by HBM: a warp
+// streams keys and values through registers, four features a lane, and has all rows' queries
+// and sums in registers too.  Of up to 64: a CTA holds them, a tile of keys and one of values
+// in shared memory, bound by the FMA units; a thread has four rows of a few keys, then of a
+// few output features.
 #include <algorithm>
 
 #include "gdn_attention.cuh"
@@ -19,16 +22,225 @@ namespace gdn {
 namespace attn {
 namespace {
 
-template <int M>
-struct Shape {
-    static constexpr int TX = M == 64 ? 16 : 32;       // threads along keys and features
-    static constexpr int kThreads = M / 4 * TX;
-    static constexpr int KT = M == 64 ? 32 : 64;       // keys of a tile
-};
+constexpr int kLanes = 16;        // threads along keys and features
+constexpr int kThreads = 256;
+constexpr int kRows = 64, kKeys = 32;  // query rows, keys of a tile
+constexpr int kStreamKeys = 64;   // of a tile, where keys are streamed
 
-template <typename T, int D, int M>
-__global__ void __launch_bounds__(Shape<M>::kThreads) simt_kernel(const AttentionParams p, const Plan s, bool vectors) {
-    constexpr int TX = Shape<M>::TX, KT = Shape<M>::KT, THREADS = Shape<M>::kThreads;
+// Four elements of a row in fp32; `vectors`: 16 (or, of 16 bits, 8) bytes aligned.
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *g, bool vectors) {
+    if (vectors) return ld4(g);
+    return make_float4(ld_f(g), ld_f(g + 1), ld_f(g + 2), ld_f(g + 3));
+}
+
+// Up to R query rows.  A key takes D / 4 lanes, so a warp has K = 128 / D keys at a time and
+// U times as many on their way; the warps of a CTA take the piece's keys in turn.  Each group
+// of lanes has sums and maxima of its own, joined at the unit's end through shared memory.
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) stream_kernel(const AttentionParams p, const Plan s,
+                                                                           const Divisor page_size, bool vectors) {
+    constexpr int L = D / 4, K = 32 / L, U = R == 4 ? 4 : 2, kWarps = kThreads / 32, kGroups = kWarps * K;
+    constexpr int O = R > L ? R / L : 1;  // rows whose scores end up in a lane
+    extern __shared__ float4 smem4[];
+    float4 *parts = smem4;                                                       // [kGroups][R][L]
+    float2 *part_stats = reinterpret_cast<float2 *>(smem4 + kGroups * R * L);    // [kGroups][R]
+    const Place from = find_place<kStreamKeys, kThreads>(p, s);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, in = lane % L, sub = lane / L;
+    const float scale2 = p.scale * tc::kLog2e;
+    // The lane's rows own0 .. own0 + O - 1 (others of the group may have the same): row bits
+    // from the top are lane bits from the top of the group's.
+    int own0 = 0;
+#pragma unroll
+    for (int n = R, o = L / 2; n > 1 && o > 0; n /= 2, o /= 2) own0 += in & o ? n / 2 : 0;
+    auto owner = [](int r) {  // a lane of the group that has row r
+        int x = 0;
+#pragma unroll
+        for (int n = R, o = L / 2; n > 1 && o > 0; n /= 2, o /= 2) {
+            if (r >= n / 2) x += o, r -= n / 2;
+        }
+        return x;
+    };
+    Walk<kStreamKeys> w;
+    Cut cut{};
+    for (bool more = w.start(p, s, from); more; more = w.next(p, s)) {
+        const Unit &u = w.unit;
+        const int n = u.t1 - u.t0, heads = w.heads(p, s), head0 = w.head0(p, s), hk = w.key_head(s);
+        cut = w.cut(p, s);
+        float4 q[R], acc[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int t = r / s.gs, g = r - t * s.gs;
+            q[r] = acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t < n && g < heads) {
+                q[r] = load4(reinterpret_cast<const T *>(p.q) + (w.row.tok0 + u.t0 + t) * p.qs + (int64_t)(head0 + g) * D + 4 * in,
+                             vectors);
+                q[r] = make_float4(q[r].x * scale2, q[r].y * scale2, q[r].z * scale2, q[r].w * scale2);
+            }
+        }
+        float m[O], l[O];
+        int lo[O], hi[O];  // keys that a row sees
+        int all_lo = 0, all_hi = 0x7fffffff;  // that all of them see
+#pragma unroll
+        for (int o = 0; o < O; ++o) {
+            m[o] = kNone;
+            l[o] = 0.f;
+        }
+        auto sees = [&](int r, int &a, int &b) {
+            const int at = w.row.first + u.t0 + min(r / s.gs, n - 1);
+            a = p.causal && p.window > 0 ? max(0, at - p.window + 1) : 0;
+            b = p.causal ? min(w.row.keys, at + 1) : w.row.keys;
+        };
+#pragma unroll
+        for (int o = 0; o < O; ++o) sees(own0 + o, lo[o], hi[o]);
+        {
+            int a, b;
+            sees((n - 1) * s.gs, all_lo, b);
+            sees(0, a, all_hi);
+        }
+        const int k1 = min(u.hi, u.key0 + w.end * kStreamKeys);
+        int k0 = max(u.lo, u.key0 + w.at.tile * kStreamKeys) + warp * (K * U);
+        const int32_t *table = p.page_table + (int64_t)w.at.b * p.max_pages;
+        // Pages of the group's next keys, read a turn ahead
+        int page[U];
+        auto pages_of = [&](int k) {
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int key = k + j * K + sub;
+                page[j] = key < k1 ? table[page_size.div((uint32_t)key)] : -1;
+            }
+        };
+        pages_of(k0);
+        for (; k0 < k1; k0 += kWarps * K * U) {
+            float4 kk[U], vv[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int key = k0 + j * K + sub, id = page[j];
+                kk[j] = vv[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (id >= 0 && id < p.num_pages) {
+                    const uint32_t slot = (uint32_t)key - page_size.div((uint32_t)key) * page_size.d;
+                    const int64_t at = id * p.page_stride + (int64_t)slot * p.slot_stride + hk * p.head_stride + 4 * in;
+                    kk[j] = load4(reinterpret_cast<const T *>(p.k_pages) + at, vectors);
+                    vv[j] = load4(reinterpret_cast<const T *>(p.v_pages) + at, vectors);
+                } else if (key < k1) {
+                    atomicOr(p.err, (uint32_t)GDN_DEVERR_BAD_INDEX);
+                }
+            }
+            pages_of(k0 + kWarps * K * U);
+            float x[U][O];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                float v[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    v[r] = fmaf(q[r].x, kk[j].x, fmaf(q[r].y, kk[j].y, fmaf(q[r].z, kk[j].z, q[r].w * kk[j].w)));
+                // Sums over the group's lanes, in each step of half as many rows
+                int rows = R;
+#pragma unroll
+                for (int o = L / 2; o > 0; o /= 2) {
+                    if (rows > 1) {
+                        rows /= 2;
+                        const bool up = (in & o) != 0;
+#pragma unroll
+                        for (int r = 0; r < R / 2; ++r) {
+                            if (r >= rows) break;
+                            const float got = __shfl_xor_sync(kAll, up ? v[r] : v[r + rows], o);
+                            v[r] = (up ? v[r + rows] : v[r]) + got;
+                        }
+                    } else {
+                        v[0] += __shfl_xor_sync(kAll, v[0], o);
+                    }
+                }
+                const int key = k0 + j * K + sub;
+#pragma unroll
+                for (int o = 0; o < O; ++o) x[j][o] = key < k1 && key >= lo[o] && key < hi[o] ? v[o] : kNone;
+            }
+            // (the maximum that weights are relative to follows the true one when that has grown
+            // by more than 8 in the exponent)
+            bool grow = false;
+            float now[O], keep[O];
+#pragma unroll
+            for (int o = 0; o < O; ++o) {
+                now[o] = m[o];
+#pragma unroll
+                for (int j = 0; j < U; ++j) now[o] = fmaxf(now[o], x[j][o]);
+                grow |= now[o] - m[o] > 8.f;
+            }
+            if (__any_sync(kAll, grow)) {
+#pragma unroll
+                for (int o = 0; o < O; ++o) {
+                    keep[o] = now[o] == kNone ? 1.f : exp2f(m[o] - now[o]);
+                    m[o] = now[o];
+                    l[o] *= keep[o];
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float f = __shfl_sync(kAll, keep[r % O], sub * L + owner(r));
+                    acc[r] = make_float4(acc[r].x * f, acc[r].y * f, acc[r].z * f, acc[r].w * f);
+                }
+            }
+            const bool tested = k0 < all_lo || k0 + K * U > all_hi;  // a row may not see a key
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                float e[O];
+#pragma unroll
+                for (int o = 0; o < O; ++o) {
+                    e[o] = m[o] == kNone ? 0.f : exp2f(x[j][o] - m[o]);
+                    l[o] += e[o];
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float f = __shfl_sync(kAll, e[r % O], sub * L + owner(r));
+                    if (tested && f == 0.f) continue;  // (what a hidden key's values are does not matter)
+                    acc[r] = make_float4(fmaf(f, vv[j].x, acc[r].x), fmaf(f, vv[j].y, acc[r].y),
+                                         fmaf(f, vv[j].z, acc[r].z), fmaf(f, vv[j].w, acc[r].w));
+                }
+            }
+        }
+        __syncthreads();  // the last unit's parts have been read
+        const int group = warp * K + sub;
+#pragma unroll
+        for (int r = 0; r < R; ++r) parts[(group * R + r) * L + in] = acc[r];
+#pragma unroll
+        for (int o = 0; o < O; ++o) part_stats[group * R + own0 + o] = make_float2(m[o], l[o]);
+        __syncthreads();
+        for (int e = threadIdx.x; e < R * L; e += kThreads) {
+            const int r = e / L, c = e % L, t = r / s.gs, g = r - t * s.gs;
+            if (t >= n || g >= heads) continue;
+            float top = kNone;
+            for (int y = 0; y < kGroups; ++y) top = fmaxf(top, part_stats[y * R + r].x);
+            const float safe = top == kNone ? 0.f : top;
+            float sum = 0.f;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int y = 0; y < kGroups; ++y) {
+                const float2 ml = part_stats[y * R + r];
+                const float4 v = parts[(y * R + r) * L + c];
+                const float f = exp2f(ml.x - safe);
+                sum = fmaf(f, ml.y, sum);
+                a = make_float4(fmaf(f, v.x, a.x), fmaf(f, v.y, a.y), fmaf(f, v.z, a.z), fmaf(f, v.w, a.w));
+            }
+            if (w.part() < 0) {
+                const long at = (w.row.tok0 + u.t0 + t) * p.Hq + head0 + g;
+                const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;  // (a NaN stays one)
+                T *out = reinterpret_cast<T *>(p.out) + at * D + 4 * c;
+                st_out(out, a.x * inv);
+                st_out(out + 1, a.y * inv);
+                st_out(out + 2, a.z * inv);
+                st_out(out + 3, a.w * inv);
+                if (p.lse != nullptr && c == 0) p.lse[at] = (safe + log2f(sum)) * 0.69314718055994530942f;
+            } else {
+                *reinterpret_cast<float4 *>(s.sums(blockIdx.x, w.part()) + (size_t)r * D + 4 * c) = a;
+                if (c == 0) s.stats(blockIdx.x, w.part())[r] = make_float2(top, sum);
+            }
+        }
+    }
+    if (threadIdx.x == 0) *s.cut(blockIdx.x) = cut;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) simt_kernel(const AttentionParams p, const Plan s, bool vectors) {
+    constexpr int TX = kLanes, KT = kKeys, THREADS = kThreads, M = kRows;
     constexpr int NK = KT / TX, NC = D / TX, VC = NC < 4 ? NC : 4;
     extern __shared__ float4 smem4[];
     float *sq = reinterpret_cast<float *>(smem4);  // [M][D]
@@ -53,8 +265,7 @@ __global__ void __launch_bounds__(Shape<M>::kThreads) simt_kernel(const Attentio
             const T *g = src(r);
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (g != nullptr) {
-                if (vectors) x = ld4(g + c);
-                else x = make_float4(ld_f(g + c), ld_f(g + c + 1), ld_f(g + c + 2), ld_f(g + c + 3));
+                x = load4(g + c, vectors);
             }
             *reinterpret_cast<float4 *>(dst + r * stride + c) = x;
         }
@@ -205,27 +416,44 @@ __global__ void __launch_bounds__(Shape<M>::kThreads) simt_kernel(const Attentio
     if (threadIdx.x == 0) *s.cut(blockIdx.x) = cut;
 }
 
-template <typename T, int D, int M>
-cudaError_t launch_m(const AttentionParams &p, const Plan &s, cudaStream_t stream) {
-    using S = Shape<M>;
-    constexpr int bytes = (M * D + S::KT * (2 * D + 4) + M * (S::KT + 4)) * (int)sizeof(float);
-    cudaError_t e = set_smem_once<simt_kernel<T, D, M>>(bytes);
+template <typename T, int D, int R>
+cudaError_t launch_stream(const AttentionParams &p, const Plan &s, bool vectors, cudaStream_t stream) {
+    constexpr int bytes = kThreads / 32 * (R * 128 * (int)sizeof(float) + 128 / D * R * (int)sizeof(float2));
+    cudaError_t e = set_smem_once<stream_kernel<T, D, R>>(bytes);
     if (e != cudaSuccess) return e;
+    stream_kernel<T, D, R><<<s.ctas, kThreads, bytes, stream>>>(p, s, Divisor((uint32_t)p.page_size), vectors);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const AttentionParams &p, const Plan &s, cudaStream_t stream) {
     const uintptr_t all = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k_pages) |
                           reinterpret_cast<uintptr_t>(p.v_pages) |
                           (uintptr_t)(p.qs | p.page_stride | p.slot_stride | p.head_stride) * sizeof(T);
-    simt_kernel<T, D, M><<<s.ctas, S::kThreads, bytes, stream>>>(p, s, (all & (4 * sizeof(T) - 1)) == 0);
-    e = cudaGetLastError();
+    const bool vectors = (all & (4 * sizeof(T) - 1)) == 0;
+    cudaError_t e;
+    if (s.rows() <= 4) {
+        e = launch_stream<T, D, 4>(p, s, vectors, stream);
+    } else if (s.rows() <= 8) {
+        e = launch_stream<T, D, 8>(p, s, vectors, stream);
+    } else if (s.rows() <= 16) {
+        e = launch_stream<T, D, 16>(p, s, vectors, stream);
+    } else {
+        constexpr int bytes = (kRows * D + kKeys * (2 * D + 4) + kRows * (kKeys + 4)) * (int)sizeof(float);
+        e = set_smem_once<simt_kernel<T, D>>(bytes);
+        if (e != cudaSuccess) return e;
+        simt_kernel<T, D><<<s.ctas, kThreads, bytes, stream>>>(p, s, vectors);
+        e = cudaGetLastError();
+    }
     return e != cudaSuccess ? e : launch_join(p, s, stream);
 }
 
 template <typename T>
 cudaError_t launch_t(const AttentionParams &p, const Plan &s, cudaStream_t stream) {
-    const bool few = s.rows() <= 16;
     switch (p.d) {
-        case 32: return few ? launch_m<T, 32, 16>(p, s, stream) : launch_m<T, 32, 64>(p, s, stream);
-        case 64: return few ? launch_m<T, 64, 16>(p, s, stream) : launch_m<T, 64, 64>(p, s, stream);
-        default: return few ? launch_m<T, 128, 16>(p, s, stream) : launch_m<T, 128, 64>(p, s, stream);
+        case 32: return launch_d<T, 32>(p, s, stream);
+        case 64: return launch_d<T, 64>(p, s, stream);
+        default: return launch_d<T, 128>(p, s, stream);
     }
 }
 
@@ -267,10 +495,14 @@ cudaError_t launch_attention_simt(const AttentionParams &p, const Plan &s, cudaS
     return p.dt == GDN_F16 ? launch_t<__half>(p, s, stream) : launch_t<__nv_bfloat16>(p, s, stream);
 }
 
-// Query rows a unit: 16 where a row of the batch has no more on average, else 64.
+// Query rows a unit: 4, 8 or 16 where a row of the batch has no more on average, else 64.
 Plan plan_simt(int B, int T, int Hq, int Hk, int d, bool varlen) {
-    const int rows = mean_tokens(B, T, varlen) * (Hq / Hk) <= 16 ? 16 : 64;
-    return plan_of(Hq, Hk, d, rows, 2 * sm_count_of_current_device(), 1, 1);
+    const long rows = mean_tokens(B, T, varlen) * (Hq / Hk);
+    const int sms = sm_count_of_current_device();
+    if (rows <= 4) return plan_of(Hq, Hk, d, 4, 2 * sms, 1, 1);
+    if (rows <= 8) return plan_of(Hq, Hk, d, 8, 2 * sms, 1, 1);
+    if (rows <= 16) return plan_of(Hq, Hk, d, 16, sms, 1, 1);
+    return plan_of(Hq, Hk, d, kRows, 2 * sms, 1, 1);
 }
 
 }  // namespace attn

@@ -25,23 +25,6 @@ constexpr int kInFlight = 2;      // vectors a thread
 constexpr int kMaxTokens = 128;   // a CTA at a time
 constexpr int kMaxAngles = 2048;  // of them together (but those of one token)
 
-// n / d for any 32-bit n by a multiplication: T. Granlund and P. Montgomery, "Division by
-// invariant integers using multiplication" (1994), figure 4.1.
-struct Divisor {
-    uint32_t m, s1, s2, d;
-    explicit Divisor(uint32_t d_) : d(d_) {
-        uint32_t l = 0;
-        while (l < 32 && (1ull << l) < d) ++l;
-        m = (uint32_t)((((1ull << l) - d) << 32) / d + 1);
-        s1 = l < 1 ? l : 1;
-        s2 = l < 1 ? 0 : l - 1;
-    }
-    __device__ __forceinline__ uint32_t div(uint32_t n) const {
-        const uint32_t t = __umulhi(m, n);
-        return (t + ((n - t) >> s1)) >> s2;
-    }
-};
-
 struct RotaryShape {
     int tokens;        // a CTA at a time
     int turned;        // vectors of a head that turn (with their second halves)

@@ -65,6 +65,11 @@ CASES = [
     dict(new=[50], lens=[90], Hq=4, Hk=2, d=64, page=16, slack=3),            # rows on no boundary
     dict(new=[2], lens=[400], Hq=200, Hk=1, d=64, page=16),                   # very wide groups
     dict(new=[3], lens=[300], Hq=64, Hk=2, d=128, page=16),
+    dict(new=[1, 1], lens=[700, 333], Hq=5, Hk=1, d=128, page=20, packed=False),  # 5 rows of 8
+    dict(new=[3], lens=[500], Hq=3, Hk=1, d=32, page=24, packed=False),       # 9 rows of 16
+    dict(new=[2], lens=[500], Hq=4, Hk=2, d=32, page=12, packed=False),       # 4 rows
+    dict(new=[1] * 9, lens=[100] * 9, Hq=8, Hk=1, d=64, page=20, packed=False, window=30),
+    dict(new=[2, 2], lens=[1, 9], Hq=4, Hk=1, d=128, page=16, packed=False, causal=False),
     dict(new=[100, 20], lens=[400, 20], Hq=4, Hk=2, d=64, page=16, window=1),
     dict(new=[100, 20], lens=[400, 20], Hq=4, Hk=2, d=128, page=16, window=37),
     dict(new=[300], lens=[900], Hq=8, Hk=2, d=64, page=64, window=256),
