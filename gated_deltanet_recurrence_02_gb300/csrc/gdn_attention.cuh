@@ -64,7 +64,8 @@ __device__ __forceinline__ Row row_at(const AttentionParams &p, int b) {
     Row r;
     row_range(p.cu_seqlens, b, p.T, r.tok0, r.tokens);
     const int len = max(p.kv_lens[b], 0);
-    const long room = (long)p.max_pages * p.page_size;
+    // (sums of a key's number and a tile's size stay below 2^31)
+    const long room = min((long)p.max_pages * p.page_size, 0x7fffff00l);
     r.keys = len < room ? len : (int)room;
     r.first = len - r.tokens;
     return r;

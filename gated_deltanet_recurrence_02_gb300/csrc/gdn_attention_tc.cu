@@ -213,9 +213,12 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
-    // The u-th unit; false past the last one.
+    // The u-th unit; false past the last one.  (A limit below a microsecond, a test's, gives up
+    // where it is not there yet, which the first one never is.)
     auto next_unit = [&](int u, Work &x) {
-        if (!(ok = wait(&u_full[u % kUnits], u / kUnits))) return false;
+        ok = p.limit >= 1000 ? wait(&u_full[u % kUnits], u / kUnits)
+                             : __all_sync(kAll, mbar_test_wait(&u_full[u % kUnits], (uint32_t)(u / kUnits) & 1u)) != 0;
+        if (!ok) return false;
         since = globaltimer_lo();
         x = works[u % kUnits];
         arrive(&u_empty[u % kUnits]);
