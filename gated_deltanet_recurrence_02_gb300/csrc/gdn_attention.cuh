@@ -121,61 +121,52 @@ __device__ Place find_place(const AttentionParams &p, const Plan &s) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, groups = p.Hk * s.per_key;
     const int per = (p.B + kWarps - 1) / kWarps;
     const int b0 = min(warp * per, p.B), b1 = min(b0 + per, p.B);
-    Row mine{0, 0, 0, 0};  // of lane b % 32
-    // Tiles of 32 rows from b on for one group, a lane each.
-    auto tiles = [&](int b) {
-        mine = b + lane < b1 ? row_at(p, b + lane) : Row{0, 0, 0, 0};
-        const int blocks = blocks_of(s, mine);
-        unsigned wide = __ballot_sync(kAll, blocks > 4);
-        long n = 0;
-        if (blocks <= 4)
-            for (int i = 0; i < blocks; ++i) n += unit_of<KT>(p, s, mine, i).tiles + s.over;
-        while (wide != 0) {
-            const int x = __ffs(wide) - 1;
-            wide &= wide - 1;
-            const Row r = row_of_lane(mine, x);
-            const int its = __shfl_sync(kAll, blocks, x);
-            long part = 0;
-            for (int i = lane; i < its; i += 32) part += unit_of<KT>(p, s, r, i).tiles + s.over;
-            for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kAll, part, o);
-            if (lane == x) n = part;
-        }
-        return n;
-    };
     // inclusive sums over the lanes
     auto scan = [&](long x) {
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
             const long y = __shfl_up_sync(kAll, x, o);
             if (lane >= o) x += y;
         }
         return x;
     };
-    long all = 0;
-    const bool once = b1 - b0 <= 32;
-    long kept = 0;  // the lane's row's tiles, where one look is enough
-    for (int b = b0; b < b1; b += 32) all += kept = tiles(b);
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kAll, all, o);
-    all *= groups;
-    if (lane == 0) sums[warp] = all;
     if (threadIdx.x == 0) found.left = 0;
-    __syncthreads();
-    long before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const long x = sums[w];
-        if (w < warp) before += x;
-        total += x;
-    }
-    // Equal pieces of at least `least`, the first ones a tile longer
-    const int c = blockIdx.x;
-    const int n_ctas = (int)min((long)s.ctas, max(1l, total >> s.least_log2));
-    const long each = total >> 31 ? total / n_ctas : (long)((unsigned)total / (unsigned)n_ctas);
-    const long more = total - each * n_ctas;
-    const long from = each * c + min((long)c, more), left = c < n_ctas ? each + (c < more ? 1 : 0) : 0;
-    if (left > 0 && before <= from && from < before + all) {
-        long rest = from - before;
+    // Two passes over the rows, 32 a time: what they come to, and (by the warp that has the
+    // piece's start) where that is.  Each in the same code: a launch finds the instruction
+    // cache empty, and waits for every line of it.
+    Row mine{0, 0, 0, 0};  // of lane b % 32
+    long n = 0, all = 0, rest = -1, left = 0, each = 0, more = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
         for (int b = b0; b < b1; b += 32) {
-            const long n = once ? kept : tiles(b), upto = scan(n * groups);
+            if (pass == 0 || b1 - b0 > 32) {
+                // tiles of 32 rows from b on for one group, a lane each
+                mine = b + lane < b1 ? row_at(p, b + lane) : Row{0, 0, 0, 0};
+                const int blocks = blocks_of(s, mine);
+                unsigned some = __ballot_sync(kAll, blocks > 0);
+                const bool wide = __any_sync(kAll, blocks > 4);  // the lanes share each row's blocks
+                n = 0;
+                do {
+                    const int x = wide ? __ffs(some) - 1 : lane;
+                    const Row r = row_of_lane(mine, max(x, 0));
+                    const int its = __shfl_sync(kAll, blocks, max(x, 0));
+                    long part = 0;
+#pragma unroll 1
+                    for (int i = wide ? lane : 0; i < its; i += wide ? 32 : 1) part += unit_of<KT>(p, s, r, i).tiles + s.over;
+                    if (wide) {
+#pragma unroll 1
+                        for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kAll, part, o);
+                    }
+                    if (!wide || lane == x) n = part;
+                    some &= some - 1;
+                } while (wide && some != 0);
+            }
+            const long upto = scan(n * groups);
+            if (pass == 0) {
+                all += __shfl_sync(kAll, upto, 31);
+                continue;
+            }
             const unsigned in = __ballot_sync(kAll, rest < upto);
             if (in == 0) {
                 rest -= __shfl_sync(kAll, upto, 31);
@@ -185,30 +176,51 @@ __device__ Place find_place(const AttentionParams &p, const Plan &s) {
             const long of_row = __shfl_sync(kAll, n, x);
             rest -= __shfl_sync(kAll, upto, x) - of_row * groups;
             const Row r = row_of_lane(mine, x);
-            int group = 0;
+            int group = 0, block = 0;
             if (groups > 1) {
                 group = (rest | of_row) >> 31 ? (int)(rest / of_row) : (int)((unsigned)rest / (unsigned)of_row);
                 rest -= group * of_row;
             }
             const int blocks = blocks_of(s, r);
-            for (int i = 0;; i += 32) {
-                const int t = i + lane < blocks ? unit_of<KT>(p, s, r, i + lane).tiles + s.over : 0;
-                const long sum = scan(t);
-                const unsigned at = __ballot_sync(kAll, rest < sum);
-                if (at == 0) {
-                    rest -= __shfl_sync(kAll, sum, 31);
-                    continue;
+            if (blocks > 1) {
+#pragma unroll 1
+                for (int i = 0;; i += 32) {
+                    const int t = i + lane < blocks ? unit_of<KT>(p, s, r, i + lane).tiles + s.over : 0;
+                    const long sum = scan(t);
+                    const unsigned at = __ballot_sync(kAll, rest < sum);
+                    if (at == 0) {
+                        rest -= __shfl_sync(kAll, sum, 31);
+                        continue;
+                    }
+                    const int y = __ffs(at) - 1;
+                    rest -= __shfl_sync(kAll, sum - t, y);
+                    block = i + y;
+                    break;
                 }
-                const int y = __ffs(at) - 1;
-                rest -= __shfl_sync(kAll, sum - t, y);
-                // (in what a unit has in front: at its first tile, the rest of that gone)
-                const int ahead = max(0, s.over - (int)min(rest, 1l << 30));
-                if (lane == 0)
-                    found = Place{b + x, group, i + y, (int)max(0l, rest - s.over), left - ahead, each, more, r};
-                break;
             }
+            // (in what a unit has in front: at its first tile, the rest of that gone)
+            const int ahead = max(0, s.over - (int)min(rest, 1l << 30));
+            if (lane == 0) found = Place{b + x, group, block, (int)max(0l, rest - s.over), left - ahead, each, more, r};
             break;
         }
+        if (pass == 1) break;
+        if (lane == 0) sums[warp] = all;
+        __syncthreads();
+        long before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const long x = sums[w];
+            if (w < warp) before += x;
+            total += x;
+        }
+        // Equal pieces of at least 2^least_log2, the first ones a tile longer
+        const int c = blockIdx.x;
+        const int n_ctas = (int)min((long)s.ctas, max(1l, total >> s.least_log2));
+        each = total >> 31 ? total / n_ctas : (long)((unsigned)total / (unsigned)n_ctas);
+        more = total - each * n_ctas;
+        left = c < n_ctas ? each + (c < more ? 1 : 0) : 0;
+        rest = each * c + min((long)c, more) - before;
+        if (left <= 0 || rest < 0 || rest >= all) break;
     }
     __syncthreads();
     return found;
