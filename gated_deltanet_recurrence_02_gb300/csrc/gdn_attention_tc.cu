@@ -55,9 +55,12 @@ struct Layout {
 };
 
 struct TcParams : AttentionParams {
+    explicit TcParams(const AttentionParams &p) : AttentionParams(p), page_size_((uint32_t)p.page_size) {}
     Plan plan;
     int slot_tokens;        // tokens of a slot
     int box;                // keys of a TMA box: the power of two in the page size
+    Divisor page_size_;     // by the page's slots
+    int box_log2;
     int page_step, head_step, none;  // a page's and a head's index in the maps, and one past all
     float c;                // |scale| log2 e
     uint32_t limit;         // of waits, ns: wait_ns, 4 s at most
@@ -482,7 +485,7 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                 // Pages of the lane's rows (lane, lane + 32 of the warp's), read a tile ahead
                 auto page_of = [&](int i, int h) {
                     const int k = x.key0 + i * KT + r0 + 32 * h + lane;
-                    return i < x.n && k >= x.lo && k < x.hi ? table[(unsigned)k / (unsigned)p.page_size] : -1;
+                    return i < x.n && k >= x.lo && k < x.hi ? table[p.page_size_.div((uint32_t)k)] : -1;
                 };
                 int ahead[2] = {page_of(0, 0), page_of(0, 1)};
 #pragma unroll 1
@@ -496,7 +499,7 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                         if (k >= x.lo && k < x.hi) {
                             row[h] = -2;
                             if (page >= 0 && page < p.num_pages)
-                                row[h] = 2 * (page * p.page_stride + (long)((unsigned)k % (unsigned)p.page_size) * p.slot_stride +
+                                row[h] = 2 * (page * p.page_stride + (long)p.page_size_.rest((uint32_t)k) * p.slot_stride +
                                               x.hk * p.head_stride);
                             else atomicOr(p.err, (uint32_t)GDN_DEVERR_BAD_INDEX);
                         }
@@ -549,20 +552,20 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                 const int32_t *table = p.page_table + (int64_t)x.b * p.max_pages;
                 auto page_of = [&](int i) {
                     const int k = x.key0 + i * KT + first;
-                    return i < x.n && lane < boxes && k + p.box > x.lo && k < x.hi ? table[(unsigned)k / (unsigned)p.page_size]
+                    return i < x.n && lane < boxes && k + p.box > x.lo && k < x.hi ? table[p.page_size_.div((uint32_t)k)]
                                                                                    : -1;
                 };
                 int ahead = page_of(0);
 #pragma unroll 1
                 for (int i = 0; i < x.n; ++i) {
                     const int k0 = x.key0 + i * KT, k = k0 + first;
-                    const int b0 = (max(x.lo, k0) - k0) / p.box, b1 = (min(x.hi - k0, KT) + p.box - 1) / p.box;
+                    const int b0 = (max(x.lo, k0) - k0) >> p.box_log2, b1 = (min(x.hi - k0, KT) + p.box - 1) >> p.box_log2;
                     int index = p.none;  // of this lane's box (one past all: zeros)
                     if (lane >= b0 && lane < b1) {
                         if (ahead >= 0 && ahead < p.num_pages) index = ahead * p.page_step + x.hk * p.head_step;
                         else atomicOr(p.err, (uint32_t)GDN_DEVERR_BAD_INDEX);
                     }
-                    const int slot = (int)((unsigned)k % (unsigned)p.page_size) >> 3;
+                    const int slot = (int)p.page_size_.rest((uint32_t)k) >> 3;
                     ahead = page_of(i + 1);
                     if (round > 0 && !(ok = wait(&empty[st], round - 1))) break;
                     if (leader) mbar_arrive_expect_tx(&full[st], (uint32_t)((b1 - b0) * p.box * 128 * NB));
@@ -789,11 +792,12 @@ Plan plan_tc(int B, int T, int Hq, int Hk, int d, bool varlen) {
 }
 
 cudaError_t launch_attention_tc(const AttentionParams &pp, const Plan &plan, cudaStream_t stream) {
-    TcParams p{};
-    static_cast<AttentionParams &>(p) = pp;
+    TcParams p(pp);
     p.plan = plan;
     p.slot_tokens = 128 / plan.gs;
     p.box = std::min(KT, p.page_size & -p.page_size);
+    p.box_log2 = 0;
+    while (1 << p.box_log2 < p.box) ++p.box_log2;
     const Steps x = steps_of(pp);
     p.page_step = (int)x.page;
     p.head_step = (int)x.head;

@@ -275,6 +275,7 @@ struct Divisor {
         const uint32_t t = __umulhi(m, n);
         return (t + ((n - t) >> s1)) >> s2;
     }
+    __device__ __forceinline__ uint32_t rest(uint32_t n) const { return n - div(n) * d; }
 };
 
 __device__ __forceinline__ float ld_f(const float *p) { return *p; }

@@ -1319,9 +1319,14 @@ bool encode_pages_map(CUtensorMap *m, const void *ptr, bool bf16, int d, int slo
     cuuint64_t strides[4] = {(cuuint64_t)slot_stride * 2, 128, (cuuint64_t)slot_stride * 16, (cuuint64_t)unit * 2};
     cuuint32_t box[5] = {64, 8, (cuuint32_t)halves, (cuuint32_t)rows / 8, 1};
     cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    // (no more than a head's row: next to it may lie another head's, which this CTA does not
+    // read; with 256 bytes 32 rows of 8192 keys of d = 64 took 136 us)
+    const CUtensorMapL2promotion promotion = d >= 128  ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                             : d >= 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                       : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
     return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
                const_cast<void *>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_SWIZZLE_128B, promotion,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
