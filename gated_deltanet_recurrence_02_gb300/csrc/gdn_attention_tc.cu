@@ -5,14 +5,13 @@
 //     S = Q K^T,  m' = max(m, max_j S_j),  P_j = 2^{c S_j - c m'}
 //     l <- 2^{c (m - m')} l + sum_j P_j,   O <- 2^{c (m - m')} O + P V
 // and O / l at the end.  S and O are fp32 in TMEM, a query row to a lane, so a thread has a
-// whole row of a tile: no reduction crosses threads.  Any m will do that keeps the weights in
-// range, so a tile is first weighed with the m of the tiles before it, and m looked for only
-// where the row's sum of weights passes 2^15: most tiles need no maximum, and leave O where
-// it is.
+// whole row of a tile: no reduction crosses threads.  m follows the true maximum only when
+// that has grown by more than 8 in the exponent: weights of up to 2^8 are as exact, and most
+// tiles then leave O where it is.
 //
 // Roundings: P to the inputs' type for the tensor cores, the result once; l sums the weights
 // in fp32 before their rounding.  fp16 weights are scaled by 2^7, so that they keep full
-// precision down to 2^-21 of the largest (with m anew).
+// precision down to 2^-21 of the largest and stay below 2^15.
 #include <algorithm>
 #include <cstring>
 #include <numeric>
@@ -32,7 +31,7 @@ constexpr int kSoftmaxRegs = 200, kOtherRegs = 56;
 constexpr uint32_t kBlock = 16384;  // 128 rows of 64 elements
 constexpr uint32_t tS = 0, tO = 256;  // TMEM: S (and P in its place) and O of a slot, 128 columns each
 constexpr uint32_t kTmemCols = 512;
-constexpr float kMost = 32768.f;    // sum of a row's weights of a tile without a new maximum
+constexpr float kGrowth = 8.f;      // of the maximum's exponent, before O follows
 constexpr int kUnits = 4;           // units ahead
 
 // Two ways to use the two slots (S and O in TMEM and a warpgroup each):
@@ -280,68 +279,59 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                     for (int j = 0; j < KT; ++j)
                         if (j < a) v[j >> 5][j & 31] = 0xff800000u;
                 }
-                // The weights, relative to the maximum as it was; where a row's sum comes out too
-                // large (and for the first tile), once more with the maximum taken anew.
-                bool anew = i == i0;
-                float2 sum[2];
-                while (true) {
-                    if (anew) {
-                        float top[4];
+                float top[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) top[j] = __uint_as_float(v[j][0]);
+                for (int j = 0; j < 4; ++j) top[j] = __uint_as_float(v[j][0]);
 #pragma unroll
-                        for (int k = 1; k < 32; ++k)
+                for (int k = 1; k < 32; ++k)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) top[j] = fmaxf(top[j], __uint_as_float(v[j][k]));
-                        const float now = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.c, m);
-                        if (i != i0) {
-                            // (the slot's last product is done: S was issued behind it)
-                            const float keep = now == kNone ? 1.f : ex2_approx(m - now);
-                            l *= keep;
-                            const float2 k2 = make_float2(keep, keep);
+                    for (int j = 0; j < 4; ++j) top[j] = fmaxf(top[j], __uint_as_float(v[j][k]));
+                const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.c;
+                const bool grow = now - m > kGrowth;  // (from none: always, unless there is still none)
+                if (__any_sync(kAll, grow)) {
+                    const float keep = grow ? ex2_approx(m - now) : 1.f;
+                    m = grow ? now : m;
+                    if (i != i0) {
+                        // (the slot's last product is done: S was issued behind it)
+                        l *= keep;
+                        const float2 k2 = make_float2(keep, keep);
 #pragma unroll 1
-                            for (int j = 0; j < p.d; j += 16) {
-                                uint32_t o[16];
-                                tmem_ld16_async(to + j, o);
-                                tmem_wait_ld();
+                        for (int j = 0; j < p.d; j += 16) {
+                            uint32_t o[16];
+                            tmem_ld16_async(to + j, o);
+                            tmem_wait_ld();
 #pragma unroll
-                                for (int k = 0; k < 16; k += 2) {
-                                    const float2 y =
-                                        __fmul2_rn(k2, make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])));
-                                    o[k] = __float_as_uint(y.x);
-                                    o[k + 1] = __float_as_uint(y.y);
-                                }
-                                tmem_st16(to + j, o);
+                            for (int k = 0; k < 16; k += 2) {
+                                const float2 y = __fmul2_rn(k2, make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])));
+                                o[k] = __float_as_uint(y.x);
+                                o[k + 1] = __float_as_uint(y.y);
                             }
+                            tmem_st16(to + j, o);
                         }
-                        m = now;
                     }
-                    // (held finite: without keys so far, a score that there is makes the sum infinite)
-                    const float off = H::kShift - fmaxf(m, -3.4028235e38f);
-                    const float2 off2 = make_float2(off, off);
-                    sum[0] = sum[1] = make_float2(0.f, 0.f);
+                }
+                // (held finite: without keys so far weights are 0)
+                const float off = H::kShift - fmaxf(m, -3.4028235e38f);
+                const float2 off2 = make_float2(off, off);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t pk[16];
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t pk[16];
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            float2 y = __ffma2_rn(make_float2(__uint_as_float(v[j][k]), __uint_as_float(v[j][k + 1])), c2, off2);
-                            y.x = ex2_approx(y.x);
-                            y.y = ex2_approx(y.y);
-                            sum[(k >> 1) & 1] = __fadd2_rn(sum[(k >> 1) & 1], y);
-                            pk[k / 2] = H::pack2(y.x, y.y);
-                        }
-                        tmem_st16(ts + 16 * j, pk);
+                    for (int k = 0; k < 32; k += 2) {
+                        float2 y = __ffma2_rn(make_float2(__uint_as_float(v[j][k]), __uint_as_float(v[j][k + 1])), c2, off2);
+                        y.x = ex2_approx(y.x);
+                        y.y = ex2_approx(y.y);
+                        sum[(k >> 1) & 1] = __fadd2_rn(sum[(k >> 1) & 1], y);
+                        pk[k / 2] = H::pack2(y.x, y.y);
                     }
-                    sum[0] = __fadd2_rn(sum[0], sum[1]);
-                    sum[0].x += sum[0].y;
-                    if (anew || !__any_sync(kAll, mine && !(sum[0].x <= kMost))) break;
-                    anew = true;
+                    tmem_st16(ts + 16 * j, pk);
                 }
                 tmem_wait_st();
                 fence_before_sync();
                 arrive(&p_ready[s]);
-                l += sum[0].x;
+                sum[0] = __fadd2_rn(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
             }
             if (!ok) break;
             const bool any = i1 > i0;  // the slot has sums of its own
