@@ -70,6 +70,11 @@ __device__ __forceinline__ Row row_at(const AttentionParams &p, int b) {
     r.first = len - r.tokens;
     return r;
 }
+// The first key that the window of a query at position `at` leaves it (before the first
+// position, where a query has no keys at all: no sum here passes 32 bits).
+__device__ __forceinline__ int window_start(const AttentionParams &p, int at) {
+    return p.causal && p.window > 0 ? max(0, max(0, at) - p.window + 1) : 0;
+}
 __device__ __forceinline__ Row row_of_lane(const Row &r, int lane) {
     return Row{__shfl_sync(kAll, r.tok0, lane), __shfl_sync(kAll, r.tokens, lane), __shfl_sync(kAll, r.keys, lane),
                __shfl_sync(kAll, r.first, lane)};
@@ -87,12 +92,9 @@ __device__ __forceinline__ Unit unit_of(const AttentionParams &p, const Plan &s,
     Unit u;
     u.t0 = block * s.tokens;
     u.t1 = min(u.t0 + s.tokens, r.tokens);
-    u.lo = 0;
+    u.lo = window_start(p, r.first + u.t0);
     u.hi = r.keys;
-    if (p.causal) {
-        u.hi = min(u.hi, r.first + u.t1);
-        if (p.window > 0) u.lo = max(0, r.first + u.t0 - p.window + 1);
-    }
+    if (p.causal) u.hi = min(u.hi, r.first + u.t1);
     u.key0 = u.lo & -KT;
     u.tiles = u.hi > u.lo ? (u.hi - u.key0 + KT - 1) / KT : 1;
     return u;

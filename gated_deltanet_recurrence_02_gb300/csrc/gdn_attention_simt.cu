@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) stream_kernel(const 
         }
         auto sees = [&](int r, int &a, int &b) {
             const int at = w.row.first + u.t0 + min(r / s.gs, n - 1);
-            a = p.causal && p.window > 0 ? max(0, at - p.window + 1) : 0;
+            a = window_start(p, at);
             b = p.causal ? min(w.row.keys, at + 1) : w.row.keys;
         };
 #pragma unroll
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads) simt_kernel(const AttentionParams p,
 #pragma unroll
             for (int c = 0; c < NC; ++c) o[i][c] = 0.f;
             const int at = w.row.first + u.t0 + min(tt[i], n - 1);
-            lo[i] = p.causal && p.window > 0 ? max(0, at - p.window + 1) : 0;
+            lo[i] = window_start(p, at);
             hi[i] = p.causal ? min(w.row.keys, at + 1) : w.row.keys;
         }
         for (int tile = w.at.tile; tile < w.end; ++tile) {

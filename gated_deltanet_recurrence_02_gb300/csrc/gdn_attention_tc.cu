@@ -139,7 +139,7 @@ __device__ __forceinline__ Work work_of(const TcParams &p, const Walk<KT> &w) {
         int lo = u.lo, hi = u.hi;
         if (MODE == kPair && p.causal) {
             hi = min(hi, x.pos + t + x.tokens[s]);
-            if (p.window > 0) lo = max(lo, x.pos + t - p.window + 1);
+            lo = max(lo, window_start(p, x.pos + t));
         }
         const bool any = x.n > 0 && x.tokens[s] > 0 && hi > lo;
         x.a[s] = any ? min(x.n, max(0, (lo - x.key0) >> 7)) : 0;
@@ -251,7 +251,7 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                 if (p.causal) {
                     const int at = x.pos + slot_t + t;
                     hi = min(hi, at + 1);
-                    if (p.window > 0) lo = max(0, at - p.window + 1);
+                    lo = window_start(p, at);
                 }
             }
             float m = kNone, l = 0.f;  // m: c times the score that weights are relative to
