@@ -9,11 +9,13 @@
 // and o / l at the end; all in fp32.  A key that a query does not see gets no weight and its
 // values are not added, whatever they hold.  A row without keys gives 0 and a log of -inf.
 //
-// Two kernels.  Of up to 16 query rows (single tokens, a few drafts), bound by HBM: a warp
+// Two kernels.  Of up to 8 query rows (single tokens, a few drafts), bound by HBM: a warp
 // streams keys and values through registers, four features a lane, and has all rows' queries
-// and sums in registers too.  Of up to 64: a CTA holds them, a tile of keys and one of values
-// in shared memory, bound by the FMA units; a thread has four rows of a few keys, then of a
-// few output features.
+// and sums in registers too.  Single tokens of 64 rows over 2000 keys, 4 of 16 heads, d = 128,
+// fp32: 106 us, 4.9 TB/s.  Of up to 64: a CTA holds them, a tile of keys and one of values
+// in shared memory, bound by the FMA units and the shared memory that feeds them; a thread has
+// four rows of a few keys, then of a few output features.  4 x 1000 tokens over 2000 keys each,
+// the same heads: 1.69 ms, 39 TFLOP/s.
 #include <algorithm>
 
 #include "gdn_attention.cuh"
@@ -38,21 +40,21 @@ __device__ __forceinline__ float4 load4(const T *g, bool vectors) {
 // U times as many on their way; the warps of a CTA take the piece's keys in turn.  Each group
 // of lanes has sums and maxima of its own, joined at the unit's end through shared memory.
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) stream_kernel(const AttentionParams p, const Plan s,
-                                                                           const Divisor page_size, bool vectors) {
+__global__ void __launch_bounds__(kThreads, 2) stream_kernel(const AttentionParams p, const Plan s,
+                                                              const Divisor page_size, bool vectors) {
     constexpr int L = D / 4, K = 32 / L, U = R == 4 ? 4 : 2, kWarps = kThreads / 32, kGroups = kWarps * K;
-    constexpr int O = R > L ? R / L : 1;  // rows whose scores end up in a lane
+    static_assert(R <= L, "the scores of one row end up in a lane");
     extern __shared__ float4 smem4[];
     float4 *parts = smem4;                                                       // [kGroups][R][L]
     float2 *part_stats = reinterpret_cast<float2 *>(smem4 + kGroups * R * L);    // [kGroups][R]
     const Place from = find_place<kStreamKeys, kThreads>(p, s);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, in = lane % L, sub = lane / L;
     const float scale2 = p.scale * tc::kLog2e;
-    // The lane's rows own0 .. own0 + O - 1 (others of the group may have the same): row bits
-    // from the top are lane bits from the top of the group's.
-    int own0 = 0;
+    // The lane's row (others of the group may have the same): row bits from the top are lane
+    // bits from the top of the group's.
+    int own = 0;
 #pragma unroll
-    for (int n = R, o = L / 2; n > 1 && o > 0; n /= 2, o /= 2) own0 += in & o ? n / 2 : 0;
+    for (int n = R, o = L / 2; n > 1 && o > 0; n /= 2, o /= 2) own += in & o ? n / 2 : 0;
     auto owner = [](int r) {  // a lane of the group that has row r
         int x = 0;
 #pragma unroll
@@ -78,21 +80,15 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) stream_kernel(const 
                 q[r] = make_float4(q[r].x * scale2, q[r].y * scale2, q[r].z * scale2, q[r].w * scale2);
             }
         }
-        float m[O], l[O];
-        int lo[O], hi[O];  // keys that a row sees
+        float m = kNone, l = 0.f;
+        int lo, hi;                           // keys that the lane's row sees
         int all_lo = 0, all_hi = 0x7fffffff;  // that all of them see
-#pragma unroll
-        for (int o = 0; o < O; ++o) {
-            m[o] = kNone;
-            l[o] = 0.f;
-        }
         auto sees = [&](int r, int &a, int &b) {
             const int at = w.row.first + u.t0 + min(r / s.gs, n - 1);
             a = window_start(p, at);
             b = p.causal ? min(w.row.keys, at + 1) : w.row.keys;
         };
-#pragma unroll
-        for (int o = 0; o < O; ++o) sees(own0 + o, lo[o], hi[o]);
+        sees(own, lo, hi);
         {
             int a, b;
             sees((n - 1) * s.gs, all_lo, b);
@@ -127,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) stream_kernel(const 
                 }
             }
             pages_of(k0 + kWarps * K * U);
-            float x[U][O];
+            float x[U];
 #pragma unroll
             for (int j = 0; j < U; ++j) {
                 float v[R];
@@ -152,45 +148,31 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) stream_kernel(const 
                     }
                 }
                 const int key = k0 + j * K + sub;
-#pragma unroll
-                for (int o = 0; o < O; ++o) x[j][o] = key < k1 && key >= lo[o] && key < hi[o] ? v[o] : kNone;
+                x[j] = key < k1 && key >= lo && key < hi ? v[0] : kNone;
             }
             // (the maximum that weights are relative to follows the true one when that has grown
             // by more than 8 in the exponent)
-            bool grow = false;
-            float now[O], keep[O];
+            float now = m;
 #pragma unroll
-            for (int o = 0; o < O; ++o) {
-                now[o] = m[o];
-#pragma unroll
-                for (int j = 0; j < U; ++j) now[o] = fmaxf(now[o], x[j][o]);
-                grow |= now[o] - m[o] > 8.f;
-            }
-            if (__any_sync(kAll, grow)) {
-#pragma unroll
-                for (int o = 0; o < O; ++o) {
-                    keep[o] = now[o] == kNone ? 1.f : exp2f(m[o] - now[o]);
-                    m[o] = now[o];
-                    l[o] *= keep[o];
-                }
+            for (int j = 0; j < U; ++j) now = fmaxf(now, x[j]);
+            if (__any_sync(kAll, now - m > 8.f)) {
+                const float keep = now == kNone ? 1.f : exp2f(m - now);
+                m = now;
+                l *= keep;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float f = __shfl_sync(kAll, keep[r % O], sub * L + owner(r));
+                    const float f = __shfl_sync(kAll, keep, sub * L + owner(r));
                     acc[r] = make_float4(acc[r].x * f, acc[r].y * f, acc[r].z * f, acc[r].w * f);
                 }
             }
             const bool tested = k0 < all_lo || k0 + K * U > all_hi;  // a row may not see a key
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                float e[O];
-#pragma unroll
-                for (int o = 0; o < O; ++o) {
-                    e[o] = m[o] == kNone ? 0.f : exp2f(x[j][o] - m[o]);
-                    l[o] += e[o];
-                }
+                const float e = m == kNone ? 0.f : exp2f(x[j] - m);
+                l += e;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float f = __shfl_sync(kAll, e[r % O], sub * L + owner(r));
+                    const float f = __shfl_sync(kAll, e, sub * L + owner(r));
                     if (tested && f == 0.f) continue;  // (what a hidden key's values are does not matter)
                     acc[r] = make_float4(fmaf(f, vv[j].x, acc[r].x), fmaf(f, vv[j].y, acc[r].y),
                                          fmaf(f, vv[j].z, acc[r].z), fmaf(f, vv[j].w, acc[r].w));
@@ -201,8 +183,7 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) stream_kernel(const 
         const int group = warp * K + sub;
 #pragma unroll
         for (int r = 0; r < R; ++r) parts[(group * R + r) * L + in] = acc[r];
-#pragma unroll
-        for (int o = 0; o < O; ++o) part_stats[group * R + own0 + o] = make_float2(m[o], l[o]);
+        part_stats[group * R + own] = make_float2(m, l);
         __syncthreads();
         for (int e = threadIdx.x; e < R * L; e += kThreads) {
             const int r = e / L, c = e % L, t = r / s.gs, g = r - t * s.gs;
@@ -436,8 +417,6 @@ cudaError_t launch_d(const AttentionParams &p, const Plan &s, cudaStream_t strea
         e = launch_stream<T, D, 4>(p, s, vectors, stream);
     } else if (s.rows() <= 8) {
         e = launch_stream<T, D, 8>(p, s, vectors, stream);
-    } else if (s.rows() <= 16) {
-        e = launch_stream<T, D, 16>(p, s, vectors, stream);
     } else {
         constexpr int bytes = (kRows * D + kKeys * (2 * D + 4) + kRows * (kKeys + 4)) * (int)sizeof(float);
         e = set_smem_once<simt_kernel<T, D>>(bytes);
@@ -495,14 +474,16 @@ cudaError_t launch_attention_simt(const AttentionParams &p, const Plan &s, cudaS
     return p.dt == GDN_F16 ? launch_t<__half>(p, s, stream) : launch_t<__nv_bfloat16>(p, s, stream);
 }
 
-// Query rows a unit: 4, 8 or 16 where a row of the batch has no more on average, else 64.
+// Query rows a unit.  Four are streamed at the rate of their bytes, eight at half of it (the
+// sums over the lanes), so eight are the better from five rows on, and 64 by the other kernel
+// once the rows of a key head fill six units of eight.  64 rows of the batch over 2000 keys,
+// 4 key heads, d = 128, fp32, us by units of 4, 8, 64: of 4 query rows 106, 156, 679; of 8
+// 198, 159, 680; of 20 469, 434, 677; of 32 742, 574, 682.  At 40 rows 8 and 64 meet (d = 128:
+// 351 and 354, d = 64: 193 and 194), at 48 they are 438 and 355.  (16 rows a unit took what two
+// units of 8 take.)
 Plan plan_simt(int B, int T, int Hq, int Hk, int d, bool varlen) {
     const long rows = mean_tokens(B, T, varlen) * (Hq / Hk);
-    const int sms = sm_count_of_current_device();
-    if (rows <= 4) return plan_of(Hq, Hk, d, 4, 2 * sms, 1, 1);
-    if (rows <= 8) return plan_of(Hq, Hk, d, 8, 2 * sms, 1, 1);
-    if (rows <= 16) return plan_of(Hq, Hk, d, 16, sms, 1, 1);
-    return plan_of(Hq, Hk, d, kRows, 2 * sms, 1, 1);
+    return plan_of(Hq, Hk, d, rows <= 4 ? 4 : rows <= 40 ? 8 : kRows, 2 * sm_count_of_current_device(), 1, 1);
 }
 
 }  // namespace attn

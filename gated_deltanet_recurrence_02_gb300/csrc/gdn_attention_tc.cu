@@ -772,10 +772,18 @@ bool tc_takes(const AttentionParams &p) {
            steps_of(p).count < (1ll << 31) - 1;
 }
 
+// One block a unit, or two that share its tiles: two where there are as many blocks as CTAs.
+// With fewer every unit is cut, and pairs have twice the rows to leave and to join; with more,
+// tiles are fetched half as often and the slots' sums need no adding up.  us with one and with
+// two a unit, 4 of 16 heads, tokens of a row after 2000 others:
+//     d = 64:  1 x 512 (64 blocks)  22, 26;   8 x 128 (128)  26, 28;   64 x 512 (4096)  371, 328
+//     d = 128: 1 x 512              27, 29;   8 x 128        34, 32;   64 x 512         774, 456
 Plan plan_tc(int B, int T, int Hq, int Hk, int d, bool varlen) {
-    Plan s = plan_of(Hq, Hk, d, 128, sm_count_of_current_device(), 1, 1);
-    if (mean_tokens(B, T, varlen) > s.tokens) {
-        s.tokens *= 2;  // two blocks a unit
+    const int ctas = sm_count_of_current_device();
+    Plan s = plan_of(Hq, Hk, d, 128, ctas, 1, 1);
+    const long mean = mean_tokens(B, T, varlen), blocks = (mean + s.tokens - 1) / s.tokens;
+    if (blocks > 1 && blocks * B * Hk * s.per_key >= ctas) {
+        s.tokens *= 2;
         s.over = 2;
     }
     return s;
