@@ -10,6 +10,8 @@
 // weights) in the workspace, at most two a CTA: the end of a unit that an earlier CTA began
 // (part 0) and the start of one that a later CTA goes on with (part 1).  The join, a second
 // kernel, adds the parts up in the order of the keys, so the result does not depend on timing.
+// (16 prompts of 200 to 2000 tokens, 4 of 32 heads, d = 64: 240 us with units counted by their
+// tiles alone, 199 with what begins and ends them.)
 #pragma once
 
 #include "gdn_internal.cuh"

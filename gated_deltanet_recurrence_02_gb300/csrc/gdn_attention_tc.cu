@@ -12,6 +12,21 @@
 // Roundings: P to the inputs' type for the tensor cores, the result once; l sums the weights
 // in fp32 before their rounding.  fp16 weights are scaled by 2^7, so that they keep full
 // precision down to 2^-21 of the largest and stay below 2^15.
+//
+// Roles.  Two warpgroups for the softmax, one for each of two slots (S, P in its place, and O
+// in TMEM); of the other warps one walks through the CTA's units and fetches their queries,
+// one fetches tiles of keys and one of values (TMA; two each by 16-byte copies for pages that
+// are no multiple of 8 slots: 4 x 1000 tokens over 2000 keys, d = 64, take 84 us with pages of
+// 20 slots and 57 with 16), one issues all products, a slot's under the other's softmax.
+//
+// Bounds, and what the kernel comes to on the device.  Single tokens: the bytes of the cache,
+// 32 rows over 8192 keys, 8 of 32 heads, 164 us at d = 128 (6.5 TB/s), 99 at d = 64 (5.4).
+// Long chunks at d = 128: the tensor cores, 4100 tokens over 32100 keys, 32 heads, 1.18 ms,
+// 1.70 PFLOP/s.  At d = 64 the chain of a tile, S, maximum, exponentials, P, O, some 2400
+// cycles for two slots' tiles where the tensor cores and the exponentials need 1050 each.
+// Short calls: 4 to 5 us until the first tile has arrived and 4 to 6 for the join.  Two warps for
+// the halves of a row (16 for the softmax), which swap their maxima, took a third longer at
+// d = 128 and a tenth at d = 64.
 #include <algorithm>
 #include <cstring>
 #include <numeric>
@@ -620,8 +635,7 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
         } else if (warp == 9) {
             // ============================ MMAs ===========================
             // One warp issues all, slot after slot, so that one slot's softmax runs under the
-            // other's products (a warp a slot: both ran in step, 4100 tokens over 32100 keys took
-            // 1403 us, not 1180).
+            // other's products (a warp a slot: both ran in step, 1403 us where one takes 1183).
             // (a negative scale: of the scores' queries)
             const uint32_t id_s = idesc_f16(128, KT, false, false, H::kBf16) | (p.scale < 0.f ? 1u << 13 : 0u);
             const uint32_t id_o = idesc_f16(128, p.d, false, true, H::kBf16);
