@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Optional
 
 import torch
@@ -153,6 +154,21 @@ def _empty(shape, dtype, device, stream, scratch: bool = False):
     if not scratch:
         t.record_stream(current)
     return t
+
+
+# Workspaces that a thread keeps for its calls on the default stream, by device: (tensor,
+# pointer, bytes).  The default stream runs them one after the other, is never captured and
+# never ends; and another thread's calls, whose launches might come in between, have one of
+# their own.  (An allocation behind a launch takes 5 to 7 us of the GB300's host, the rest of
+# an attention call 12.)  Calls on other streams allocate.
+_kept = threading.local()
+
+
+def _keep(nbytes: int, device):
+    """Make the thread's workspace on the default stream of the current device one of nbytes."""
+    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    kept = _kept.__dict__[_device()] = (t, t.data_ptr(), nbytes)
+    return kept
 
 
 def _codes(q, alpha, conventions: int):
@@ -620,6 +636,8 @@ def _heads(t, N: int, H: int, d: int):
     s0, s1, s2 = t.stride()
     if not t.is_cuda:
         raise ValueError("libgdn takes device tensors")
+    if t.get_device() != _device():
+        raise ValueError("the tensors must be on the current device")
     if (s2 != 1 and d != 1) or (s1 != d and H != 1):
         raise ValueError("the elements of a token must be contiguous")
     return t.data_ptr(), s0 if N > 1 else H * d
@@ -788,18 +806,24 @@ def gdn_paged_attention(q, k_pages, v_pages, page_table, kv_lens, *, B: int, T: 
     elif lse.shape != (N, Hq) or lse.dtype != torch.float32:
         raise ValueError("lse is float32 [total_T, Hq]")
     L, code = lib(), _DT[dtype]
-    if workspace is None:
+    handle = _stream(stream)
+    if workspace is not None:
+        wp, ws_bytes = _p(workspace), workspace.numel() * workspace.element_size()
+    else:
+        kept = _kept.__dict__.get(_device()) if not handle else None
         ws_bytes = L.gdn_paged_attention_workspace_size(B, T, Hq, Hk, d, code, cp is not None)
-        if 0 < ws_bytes < 1 << 62:
+        if kept is not None and ws_bytes <= kept[2]:
+            wp = kept[1]
+        elif not 0 < ws_bytes < 1 << 62:
+            wp = None
+        elif not handle and not _stream(None):
+            wp = _keep(ws_bytes, device)[1]
+        else:
             workspace = _empty(ws_bytes, torch.uint8, device, stream, scratch=True)
             wp = workspace.data_ptr()
-        else:
-            wp = None
-    else:
-        wp, ws_bytes = _p(workspace), workspace.numel() * workspace.element_size()
     st = L.gdn_paged_attention(qp, kp, vp, tp, lp, cp, op, _p(lse), B, T, Hq, Hk, d, qs, pages, size, width,
                                s0, s1, s2, d ** -0.5 if scale is None else scale, window,
-                               0 if causal else GDN_ATTENTION_FULL, code, wp, ws_bytes, _stream(stream))
+                               0 if causal else GDN_ATTENTION_FULL, code, wp, ws_bytes, handle)
     if st:
         _check(st, "gdn_paged_attention")
     return out, lse
