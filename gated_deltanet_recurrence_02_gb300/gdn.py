@@ -19,7 +19,7 @@ import torch
 
 from . import build as _build
 
-GDN_OK = 0
+GDN_OK, GDN_ERR_WORKSPACE = 0, 7
 GDN_F32, GDN_F16, GDN_BF16 = 0, 1, 2
 GDN_DEVERR_BAD_INDEX, GDN_DEVERR_TIMEOUT = 1, 2
 # input conventions (include/gdn.h): OR'd into dtype_qkv / dtype_gate
@@ -807,23 +807,39 @@ def gdn_paged_attention(q, k_pages, v_pages, page_table, kv_lens, *, B: int, T: 
         raise ValueError("lse is float32 [total_T, Hq]")
     L, code = lib(), _DT[dtype]
     handle = _stream(stream)
+    kept = None
     if workspace is not None:
         wp, ws_bytes = _p(workspace), workspace.numel() * workspace.element_size()
     else:
-        kept = _kept.__dict__.get(_device()) if not handle else None
-        ws_bytes = L.gdn_paged_attention_workspace_size(B, T, Hq, Hk, d, code, cp is not None)
-        if kept is not None and ws_bytes <= kept[2]:
-            wp = kept[1]
-        elif not 0 < ws_bytes < 1 << 62:
-            wp = None
-        elif not handle and not _stream(None):
-            wp = _keep(ws_bytes, device)[1]
+        if not handle:
+            kept = _kept.__dict__.get(_device())
+        if kept is not None:
+            workspace, wp, ws_bytes = kept
         else:
+            ws_bytes = L.gdn_paged_attention_workspace_size(B, T, Hq, Hk, d, code, cp is not None)
+            wp = None
+            if not 0 < ws_bytes < 1 << 62:
+                pass
+            elif not handle and not _stream(None):
+                workspace, wp, _ = _keep(ws_bytes, device)
+            else:
+                workspace = _empty(ws_bytes, torch.uint8, device, stream, scratch=True)
+                wp = workspace.data_ptr()
+    if scale is None:
+        scale = d ** -0.5
+    flags = 0 if causal else GDN_ATTENTION_FULL
+    lp_out = _p(lse)
+    st = L.gdn_paged_attention(qp, kp, vp, tp, lp, cp, op, lp_out, B, T, Hq, Hk, d, qs, pages, size, width,
+                               s0, s1, s2, scale, window, flags, code, wp, ws_bytes, handle)
+    if st == GDN_ERR_WORKSPACE and kept is not None:  # (nothing was launched: with one that is large enough)
+        ws_bytes = L.gdn_paged_attention_workspace_size(B, T, Hq, Hk, d, code, cp is not None)
+        if _stream(None):
             workspace = _empty(ws_bytes, torch.uint8, device, stream, scratch=True)
             wp = workspace.data_ptr()
-    st = L.gdn_paged_attention(qp, kp, vp, tp, lp, cp, op, _p(lse), B, T, Hq, Hk, d, qs, pages, size, width,
-                               s0, s1, s2, d ** -0.5 if scale is None else scale, window,
-                               0 if causal else GDN_ATTENTION_FULL, code, wp, ws_bytes, handle)
+        else:
+            workspace, wp, _ = _keep(ws_bytes, device)
+        st = L.gdn_paged_attention(qp, kp, vp, tp, lp, cp, op, lp_out, B, T, Hq, Hk, d, qs, pages, size, width,
+                                   s0, s1, s2, scale, window, flags, code, wp, ws_bytes, handle)
     if st:
         _check(st, "gdn_paged_attention")
     return out, lse

@@ -77,3 +77,27 @@ def test_a_captured_call_next_to_eager_ones(gdn):
         eager = [gdn.gdn_paged_attention(*cases[1][0], B=1)[0] for _ in range(20)]
         torch.cuda.synchronize()
         assert all(torch.equal(y, want[0]) for y in captured) and all(torch.equal(y, want[1]) for y in eager)
+
+
+def test_the_default_stream_named_from_another(gdn):
+    """stream=0 with another one current: the kept workspace, none yet, and one that is too small."""
+    small, large = case(*SIZES[2], seed=2), case(*SIZES[1], seed=1)
+    torch.cuda.synchronize()
+
+    def calls():
+        torch.cuda.set_device(0)
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            results.append((gdn.gdn_paged_attention(*small[0], B=1, stream=0)[0], small))
+        results.append((gdn.gdn_paged_attention(*small[0], B=1)[0], small))
+        with torch.cuda.stream(side):
+            results.append((gdn.gdn_paged_attention(*large[0], B=1, stream=0)[0], large))
+        torch.cuda.synchronize()
+
+    results = []
+    t = threading.Thread(target=calls)  # (with no workspace kept)
+    t.start()
+    t.join()
+    assert len(results) == 3
+    for y, (_, o, bound) in results:
+        near(y, o, bound)
