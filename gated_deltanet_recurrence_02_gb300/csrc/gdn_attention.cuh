@@ -297,18 +297,27 @@ struct Walk {
 // Joins the parts of cut units; maxima are those of scores times log2 e.  Grid (ctas, slices):
 // CTA x takes the unit that CTA x of the attention began and did not end, a warp four query
 // rows at a time (eight parts each a look: most units have two), so that all their loads are
-// on their way together; D / 32 columns a lane.
+// on their way together; D / 32 columns a lane.  Where there are no more than 16 rows, two to
+// eight warps share their parts and are added up in order through shared memory: a single
+// token over a long cache leaves few rows and many parts (8000 keys, 4 of 16 heads, d = 128:
+// the whole call 24 us with one warp for a row's parts, 16 so; 30000 keys 30 and 20).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) join_kernel(const AttentionParams p, const Plan s) {
-    constexpr int kRows = 4, kLook = 32 / kRows, W = D / 32;
+    constexpr int kRows = 4, kLook = 32 / kRows, W = D / 32, kWarps = 8;
     struct alignas(4 * W) Cols {
         float v[W];
     };
+    __shared__ Cols shared[kWarps][kRows][32];
+    __shared__ float shared_sum[kWarps][kRows];
     tc::grid_dependency_wait();
     const Cut c = *s.cut(blockIdx.x);
-    const int lane = threadIdx.x % 32, n = c.tokens * s.gs;
-    const int first = (blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32) * kRows, step = gridDim.y * (blockDim.x / 32) * kRows;
-    for (int i0 = first; i0 < n; i0 += step) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, n = c.tokens * s.gs;
+    // Warps that share four rows' parts (then all rows are had in one turn)
+    const int split = gridDim.y > 1 || c.parts <= kLook ? 1 : n <= 4 ? 8 : n <= 8 ? 4 : n <= 16 ? 2 : 1;
+    const int share = warp % split, per = (c.parts + split - 1) / split;
+    const int x_begin = share * per, x_end = min(c.parts, x_begin + per);
+    const int first = (blockIdx.y * kWarps + warp) / split * kRows, step = gridDim.y * kWarps * kRows;
+    for (int i0 = first; i0 < (split > 1 ? first + 1 : n); i0 += step) {
         const int mine = min(i0 + lane / kLook, n - 1);  // the row whose statistics the lane reads
         auto stats = [&](int x) {
             x += lane % kLook;
@@ -318,9 +327,9 @@ __global__ void __launch_bounds__(256) join_kernel(const AttentionParams p, cons
             for (int o = kLook / 2; o > 0; o >>= 1) x = f(x, __shfl_xor_sync(kAll, x, o));
             return x;
         };
-        float2 ml = stats(0);
-        float top = ml.x;
-        for (int x = kLook; x < c.parts; x += kLook) top = fmaxf(top, stats(x).x);
+        float top = kNone;
+#pragma unroll 4
+        for (int x = 0; x < c.parts; x += kLook) top = fmaxf(top, stats(x).x);
         top = over(top, [](float a, float b) { return fmaxf(a, b); });
         const float safe = top == kNone ? 0.f : top;
         float sum = 0.f, acc[kRows][W];
@@ -328,12 +337,12 @@ __global__ void __launch_bounds__(256) join_kernel(const AttentionParams p, cons
         for (int r = 0; r < kRows; ++r)
 #pragma unroll
             for (int e = 0; e < W; ++e) acc[r][e] = 0.f;
-        for (int x0 = 0; x0 < c.parts; x0 += kLook) {
-            if (x0 > 0) ml = stats(x0);
+        for (int x0 = x_begin; x0 < x_end; x0 += kLook) {
+            const float2 ml = x0 + lane % kLook < x_end ? stats(x0) : make_float2(kNone, 0.f);
             const float weight = exp2f(ml.x - safe);
             sum = fmaf(weight, ml.y, sum);
 #pragma unroll 4
-            for (int x = x0; x < min(c.parts, x0 + kLook); ++x) {
+            for (int x = x0; x < min(x_end, x0 + kLook); ++x) {
                 Cols v[kRows];
 #pragma unroll
                 for (int r = 0; r < kRows; ++r)
@@ -348,6 +357,25 @@ __global__ void __launch_bounds__(256) join_kernel(const AttentionParams p, cons
             }
         }
         sum = over(sum, [](float a, float b) { return a + b; });
+        if (split > 1) {
+            if (share > 0) {
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+                    for (int e = 0; e < W; ++e) shared[warp][r][lane].v[e] = acc[r][e];
+                }
+                if (lane % kLook == 0) shared_sum[warp][lane / kLook] = sum;
+            }
+            __syncthreads();
+            if (share > 0) break;
+            for (int y = warp + 1; y < warp + split; ++y) {
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) acc[r][e] += shared[y][r][lane].v[e];
+                sum += shared_sum[y][lane / kLook];
+            }
+        }
         const float lse = (safe + log2f(sum)) * 0.69314718055994530942f;
         const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;  // (a NaN stays one)
 #pragma unroll

@@ -794,12 +794,9 @@ bool tc_takes(const AttentionParams &p) {
 //     d = 128: 1 x 512              27, 29;   8 x 128        34, 32;   64 x 512         774, 456
 Plan plan_tc(int B, int T, int Hq, int Hk, int d, bool varlen) {
     const int ctas = sm_count_of_current_device();
-    Plan s = plan_of(Hq, Hk, d, 128, ctas, 1, 1);
+    Plan s = plan_of(Hq, Hk, d, 128, ctas, 2, 1);
     const long mean = mean_tokens(B, T, varlen), blocks = (mean + s.tokens - 1) / s.tokens;
-    if (blocks > 1 && blocks * B * Hk * s.per_key >= ctas) {
-        s.tokens *= 2;
-        s.over = 2;
-    }
+    if (blocks > 1 && blocks * B * Hk * s.per_key >= ctas) s.tokens *= 2;
     return s;
 }
 
