@@ -297,23 +297,27 @@ struct Walk {
 // Joins the parts of cut units; maxima are those of scores times log2 e.  Grid (ctas, slices):
 // CTA x takes the unit that CTA x of the attention began and did not end, a warp four query
 // rows at a time (eight parts each a look: most units have two), so that all their loads are
-// on their way together; D / 32 columns a lane.  Where there are no more than 16 rows, two to
-// eight warps share their parts and are added up in order through shared memory: a single
-// token over a long cache leaves few rows and many parts (8000 keys, 4 of 16 heads, d = 128:
-// the whole call 24 us with one warp for a row's parts, 16 so; 30000 keys 30 and 20).
-template <typename T, int D>
+// on their way together; D / 32 columns a lane.
+//
+// SHARE: of no more than 16 rows two to eight warps share the parts and are added up in order
+// through shared memory, for a single token over a long cache leaves few rows and many parts
+// (8000 keys, 4 of 16 heads, d = 128: the whole call 24 us with one warp for a row's parts, 16
+// so; 30000 keys 30 and 20).  Not for other calls: with shared memory the join's CTAs no longer
+// start next to the attention's (3 rows of up to 65 tokens, fp32: 22 us, without it 16).
+template <typename T, int D, bool SHARE>
 __global__ void __launch_bounds__(256) join_kernel(const AttentionParams p, const Plan s) {
     constexpr int kRows = 4, kLook = 32 / kRows, W = D / 32, kWarps = 8;
     struct alignas(4 * W) Cols {
         float v[W];
     };
-    __shared__ Cols shared[kWarps][kRows][32];
-    __shared__ float shared_sum[kWarps][kRows];
+    __shared__ Cols shared[SHARE ? kWarps : 1][kRows][32];
+    __shared__ float shared_sum[SHARE ? kWarps : 1][kRows];
     tc::grid_dependency_wait();
     const Cut c = *s.cut(blockIdx.x);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, n = c.tokens * s.gs;
     // Warps that share four rows' parts (then all rows are had in one turn)
-    const int split = gridDim.y > 1 || c.parts <= kLook ? 1 : n <= 4 ? 8 : n <= 8 ? 4 : n <= 16 ? 2 : 1;
+    const int split = !SHARE || c.parts <= kLook ? 1 : n <= 4 ? 8 : n <= 8 ? 4 : n <= 16 ? 2 : 1;
+    if (split > 1 && blockIdx.y > 0) return;
     const int share = warp % split, per = (c.parts + split - 1) / split;
     const int x_begin = share * per, x_end = min(c.parts, x_begin + per);
     const int first = (blockIdx.y * kWarps + warp) / split * kRows, step = gridDim.y * kWarps * kRows;
@@ -327,9 +331,10 @@ __global__ void __launch_bounds__(256) join_kernel(const AttentionParams p, cons
             for (int o = kLook / 2; o > 0; o >>= 1) x = f(x, __shfl_xor_sync(kAll, x, o));
             return x;
         };
-        float top = kNone;
+        const float2 ml0 = stats(0);
+        float top = ml0.x;
 #pragma unroll 4
-        for (int x = 0; x < c.parts; x += kLook) top = fmaxf(top, stats(x).x);
+        for (int x = kLook; x < c.parts; x += kLook) top = fmaxf(top, stats(x).x);
         top = over(top, [](float a, float b) { return fmaxf(a, b); });
         const float safe = top == kNone ? 0.f : top;
         float sum = 0.f, acc[kRows][W];
@@ -338,7 +343,8 @@ __global__ void __launch_bounds__(256) join_kernel(const AttentionParams p, cons
 #pragma unroll
             for (int e = 0; e < W; ++e) acc[r][e] = 0.f;
         for (int x0 = x_begin; x0 < x_end; x0 += kLook) {
-            const float2 ml = x0 + lane % kLook < x_end ? stats(x0) : make_float2(kNone, 0.f);
+            float2 ml = x0 == 0 ? ml0 : stats(x0);
+            if (x0 + lane % kLook >= x_end) ml = make_float2(kNone, 0.f);
             const float weight = exp2f(ml.x - safe);
             sum = fmaf(weight, ml.y, sum);
 #pragma unroll 4
@@ -357,7 +363,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttentionParams p, cons
             }
         }
         sum = over(sum, [](float a, float b) { return a + b; });
-        if (split > 1) {
+        if (SHARE && split > 1) {
             if (share > 0) {
 #pragma unroll
                 for (int r = 0; r < kRows; ++r) {

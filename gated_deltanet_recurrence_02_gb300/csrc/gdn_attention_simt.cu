@@ -436,8 +436,8 @@ cudaError_t launch_t(const AttentionParams &p, const Plan &s, cudaStream_t strea
     }
 }
 
-template <typename T, int D>
-cudaError_t launch_join_d(const AttentionParams &p, const Plan &s, cudaStream_t stream) {
+template <typename T, int D, bool SHARE>
+cudaError_t launch_join_s(const AttentionParams &p, const Plan &s, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     // (a warp has four rows at a time, a CTA eight warps; no more CTAs than run at once)
     const long most = std::min<long>(s.rows(), (long)p.T * s.gs);  // query rows of a unit
@@ -449,8 +449,14 @@ cudaError_t launch_join_d(const AttentionParams &p, const Plan &s, cudaStream_t 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<T, D>, p, s);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<T, D, SHARE>, p, s);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_join_d(const AttentionParams &p, const Plan &s, cudaStream_t stream) {
+    return mean_tokens(p.B, p.T, p.cu_seqlens != nullptr) * s.gs <= 16 ? launch_join_s<T, D, true>(p, s, stream)
+                                                                       : launch_join_s<T, D, false>(p, s, stream);
 }
 
 template <typename T>
