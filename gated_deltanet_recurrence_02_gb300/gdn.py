@@ -784,7 +784,8 @@ def gdn_paged_attention(q, k_pages, v_pages, page_table, kv_lens, *, B: int, T: 
     cache, row b's last one at position kv_lens[b] - 1: over the keys up to a query's own (with
     a window, the last `window` of them), or over all keys of the row without `causal`.  scale
     is d ** -0.5 by default.  Returns (out, lse); lse [total_T, Hq] (None unless wanted) is the
-    log of the sum of weights."""
+    log of the sum of weights.  Without `workspace` calls on the default stream use one that
+    the thread keeps, others allocate."""
     N, Hq, d = shape = q.shape
     dtype = q.dtype
     Hk, pd, kp, vp, tp, lp, pages, size, width, s0, s1, s2 = _page_args(k_pages, v_pages, page_table, kv_lens, B, dtype)
