@@ -511,8 +511,8 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
                         ahead[h] = page_of(i + 1, h);
                     }
                     if (round > 0) {
-                        if (!mbar_test_wait(&empty[st], (uint32_t)(round - 1) & 1u)) landed();
-                        __syncwarp();
+                        // (all lanes or none: it holds the warp's barrier and its one arrival)
+                        if (__any_sync(kAll, !mbar_test_wait(&empty[st], (uint32_t)(round - 1) & 1u))) landed();
                         if (!(ok = wait(&empty[st], round - 1))) break;
                     }
                     uint8_t *dst = ring + st * L::kTile + (r0 >> 3) * (NB * 1024);
