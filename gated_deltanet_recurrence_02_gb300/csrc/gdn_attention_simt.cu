@@ -165,10 +165,13 @@ __global__ void __launch_bounds__(kThreads, 2) stream_kernel(const AttentionPara
                     acc[r] = make_float4(acc[r].x * f, acc[r].y * f, acc[r].z * f, acc[r].w * f);
                 }
             }
+            // (no maximum yet: every key so far is hidden, x = -infinity and no weight, or NaN, which
+            // a maximum passes over and the weight keeps)
+            const float safe = m == kNone ? 0.f : m;
             const bool tested = k0 < all_lo || k0 + K * U > all_hi;  // a row may not see a key
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                const float e = m == kNone ? 0.f : exp2f(x[j] - m);
+                const float e = exp2f(x[j] - safe);
                 l += e;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
