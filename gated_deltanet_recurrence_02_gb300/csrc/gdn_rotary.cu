@@ -8,7 +8,8 @@
 // Angles.  p f_i in fp32 is off by 2^-24 of itself, 0.06 rad at a position of a million.
 // Here f_i / 2 pi is held as a 64-bit fraction of a turn, formed in double once per CTA
 // and frequency; p times it, modulo 2^64, is the angle modulo a turn, exact but for the
-// 2^-52 of the fraction's own rounding.  Its upper 32 bits go to sincospi as half turns.
+// 2^-52 of the fraction's own rounding.  Of its upper 32 bits the distance from the nearest
+// quarter of a turn goes to sincospi, as half turns.
 //
 // One pass: every element is read and written once, and bound by HBM.  A CTA takes a few
 // tokens at a time: it starts to load their vectors (V elements, 16 bytes where alignment and
@@ -228,10 +229,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) rotary_kernel(const RotaryPar
         for (int e = threadIdx.x; e < tokens * half; e += kThreads) {
             const int t = (int)s.per_half.div(e), i = e - t * half;
             const int pos = APPEND && p.pos == nullptr ? place[t].pos : p.pos[axis[i] * p.N + n0 + t];
-            const int32_t frac = (int32_t)((turns[i] * (uint64_t)(int64_t)pos) >> 32);
-            float c, sn;
-            sincospif((float)frac * 0x1p-31f, &sn, &c);
-            if (p.flags & GDN_ROTARY_INVERSE) sn = -sn;
+            // In units of 2^-32 turns: the nearest quarter, and no more than an eighth of a turn
+            // from there, so that the 24 bits of fp32 hold the small angle to 2^-24 of itself.
+            const uint32_t frac = (uint32_t)((turns[i] * (uint64_t)(int64_t)pos) >> 32);
+            const uint32_t quarter = (frac + 0x20000000u) >> 30;
+            float c0, s0;
+            sincospif((float)(int32_t)(frac - (quarter << 30)) * 0x1p-31f, &s0, &c0);
+            float c = quarter & 1 ? s0 : c0, sn = quarter & 1 ? c0 : s0;
+            if (quarter == 1 || quarter == 2) c = -c;
+            if ((quarter >= 2) != ((p.flags & GDN_ROTARY_INVERSE) != 0)) sn = -sn;
             if constexpr (V == 1) {
                 angle2[e] = make_float2(c, sn);
             } else {

@@ -481,8 +481,8 @@ GDN_API int gdn_accept_drafts(const void *target_probs, const void *draft_probs,
  * Pair i < R / 2 of every head of token n turns by phi = positions[axes[i]][n] * inv_freq[i]:
  *     (x1, x2) -> (x1 cos phi - x2 sin phi, x2 cos phi + x1 sin phi)
  * and elements from R on are copied.  Angles are formed in whole turns, off by no more
- * than 2^-50 of themselves, 2^-31 turns and the fp32 sine's last bit, at any position;
- * the result is rounded once.
+ * than 2^-50 of themselves and 2^-31 turns at any position, their sines and cosines by two
+ * and a half units in the last place besides; the result is rounded once.
  *  x, out      element (n, h, i) at [n * stride + h * d + i], aligned to their element
  *              (vectors of up to 16 bytes where addresses, strides and widths allow).
  *              out may be exactly x (same stride); else it overlaps no input.
