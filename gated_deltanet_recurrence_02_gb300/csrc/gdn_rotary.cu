@@ -104,7 +104,7 @@ __device__ Place place_of(const RotaryParams &p, int64_t n) {
         t = (int)(n - tok0);
     }
     x.row = b;
-    const int64_t pos = (int64_t)p.kv_lens[b] - len + t;
+    const int64_t pos = (int64_t)max(p.kv_lens[b], 0) - len + t;
     x.pos = (int)pos;
     if (pos < 0) return x;  // before the cache's first position: kept nowhere
     const uint32_t page = (uint32_t)pos / (uint32_t)p.page_size;
