@@ -630,24 +630,40 @@ def gdn_accept_drafts(target_probs, draft_probs, draft_tokens, uniform, *, draft
     return tokens, emitted_count
 
 
+def _here(t) -> int:
+    """Pointer of a tensor on the current device, the one that the kernels run on."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError("libgdn takes device tensors")
+    if device != _device():
+        raise ValueError("the tensors must be on the current device")
+    return t.data_ptr()
+
+
+def _whole(t) -> Optional[int]:
+    """Pointer of a contiguous tensor on the current device, or None."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("libgdn takes contiguous tensors")
+    return _here(t)
+
+
 def _heads(t, N: int, H: int, d: int):
     """Pointer and token stride (elements) of heads [N, H, d] whose tokens are contiguous
     (slices of wider rows among them)."""
     s0, s1, s2 = t.stride()
-    if not t.is_cuda:
-        raise ValueError("libgdn takes device tensors")
-    if t.get_device() != _device():
-        raise ValueError("the tensors must be on the current device")
+    at = _here(t)
     if (s2 != 1 and d != 1) or (s1 != d and H != 1):
         raise ValueError("the elements of a token must be contiguous")
-    return t.data_ptr(), s0 if N > 1 else H * d
+    return at, s0 if N > 1 else H * d
 
 
 def _ints(t, shape, what: str):
     """Pointer of a contiguous int32 tensor of this shape."""
     if t.dtype != torch.int32 or t.shape != shape:
         raise ValueError(f"{what} is int32 {list(shape)}")
-    return _p(t)
+    return _whole(t)
 
 
 def _turn_args(inv_freq, positions, axes, N: int, d: int):
@@ -666,7 +682,7 @@ def _turn_args(inv_freq, positions, axes, N: int, d: int):
             pp = _ints(positions, (N,), "positions")
         if axes is not None:
             ap = _ints(axes, (half,), "axes")
-    return _p(inv_freq), pp, ap, 2 * half, A
+    return _whole(inv_freq), pp, ap, 2 * half, A
 
 
 def gdn_rotary(x, positions, inv_freq, *, axes=None, pairs: bool = False, inverse: bool = False,
@@ -705,12 +721,10 @@ def _page_args(k_pages, v_pages, page_table, kv_lens, B: int, dtype):
         raise ValueError("the pages must have the dtype of the tokens")
     if s3 != 1 and d != 1:
         raise ValueError("the elements of a slot's head must be contiguous")
-    if not (k_pages.is_cuda and v_pages.is_cuda):
-        raise ValueError("libgdn takes device tensors")
     if page_table.dim() != 2:
         raise ValueError("page_table is int32 [B, max_pages]")
     width = page_table.shape[1]
-    return (Hk, d, k_pages.data_ptr(), v_pages.data_ptr(), _ints(page_table, (B, width), "page_table"),
+    return (Hk, d, _here(k_pages), _here(v_pages), _ints(page_table, (B, width), "page_table"),
             _ints(kv_lens, (B,), "kv_lens"), pages, page_size, width, s0, s1, s2)
 
 
@@ -800,7 +814,7 @@ def gdn_paged_attention(q, k_pages, v_pages, page_table, kv_lens, *, B: int, T: 
     elif out.shape != shape or out.dtype != dtype:
         raise ValueError("out must have the shape and the dtype of q")
     else:
-        op = _p(out)
+        op = _whole(out)
     if lse is None:
         if want_lse:
             lse = _empty((N, Hq), torch.float32, device, stream)
@@ -810,7 +824,7 @@ def gdn_paged_attention(q, k_pages, v_pages, page_table, kv_lens, *, B: int, T: 
     handle = _stream(stream)
     kept = None
     if workspace is not None:
-        wp, ws_bytes = _p(workspace), workspace.numel() * workspace.element_size()
+        wp, ws_bytes = _whole(workspace), workspace.numel() * workspace.element_size()
     else:
         if not handle:
             kept = _kept.__dict__.get(_device())
@@ -829,7 +843,7 @@ def gdn_paged_attention(q, k_pages, v_pages, page_table, kv_lens, *, B: int, T: 
     if scale is None:
         scale = d ** -0.5
     flags = 0 if causal else GDN_ATTENTION_FULL
-    lp_out = _p(lse)
+    lp_out = _whole(lse)
     st = L.gdn_paged_attention(qp, kp, vp, tp, lp, cp, op, lp_out, B, T, Hq, Hk, d, qs, pages, size, width,
                                s0, s1, s2, scale, window, flags, code, wp, ws_bytes, handle)
     if st == GDN_ERR_WORKSPACE and kept is not None:  # (nothing was launched: with one that is large enough)
