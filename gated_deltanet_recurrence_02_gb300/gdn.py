@@ -666,6 +666,12 @@ def _ints(t, shape, what: str):
     return _whole(t)
 
 
+def _fits(sizes: int) -> None:
+    """Sizes, or'd together, that C ints hold (ctypes would hand on their lower 32 bits)."""
+    if sizes > 0x7fffffff:
+        raise ValueError("the sizes of a call must be below 2^31")
+
+
 def _turn_args(inv_freq, positions, axes, N: int, d: int):
     """Pointers of inv_freq, positions and axes, R and A of a rotation of N tokens."""
     half = inv_freq.shape[0]
@@ -695,6 +701,7 @@ def gdn_rotary(x, positions, inv_freq, *, axes=None, pairs: bool = False, invers
     shape, dtype = x.shape, x.dtype
     N, H, d = shape
     fp, pp, ap, R, A = _turn_args(inv_freq, positions, axes, N, d)
+    _fits(H | d | A)
     xp, xs = _heads(x, N, H, d)
     if out is None:
         out = _empty(shape, dtype, x.device, stream)
@@ -775,6 +782,7 @@ def gdn_paged_append(k, v, k_pages, v_pages, page_table, kv_lens, *, B: int, T: 
             op, os_ = _heads(q_out, N, Hq, d)
     elif q_out is not None:
         raise ValueError("q_out goes with q")
+    _fits(N | Hq | Hk | d | A | pages | size | width)
     xk, ks = _heads(k, N, Hk, d)
     xv, vs = _heads(v, N, Hk, d)
     st = lib().gdn_paged_append(qp, xk, xv, op, kp, vp, tp, lp, cp, pp, ap, fp, B, T, Hq, Hk, d, R, A,
@@ -806,6 +814,7 @@ def gdn_paged_attention(q, k_pages, v_pages, page_table, kv_lens, *, B: int, T: 
     if pd != d:
         raise ValueError("the pages must have the head size of q")
     T, cp = _row_count(N, B, T, cu_seqlens)
+    _fits(N | Hq | Hk | d | pages | size | width | window)
     qp, qs = _heads(q, N, Hq, d)
     device = q.device
     if out is None:

@@ -76,3 +76,48 @@ def test_each_tensor_is_on_the_current_device(calls, name, which):
     with pytest.raises(ValueError, match="current device"):
         getattr(gdn, name)(**args, **kw)
     assert not calls
+
+
+class Long(On):
+    """More tokens, heads or pages than 32 bits count, as the shape has it."""
+
+    def __init__(self, t, **sizes):
+        super().__init__(t)
+        shape = list(t.shape)
+        for at, n in sizes.items():
+            shape[int(at[1:])] = n
+        self.shape = torch.Size(shape)
+
+    def stride(self):
+        return self.t.stride()
+
+    def is_contiguous(self):
+        return True
+
+
+BIG = 2**32 + 3  # the 32 bits of a C int would be 3
+
+
+@pytest.mark.parametrize("name,change,kw", [
+    ("gdn_rotary", dict(x=dict(_1=BIG), out=dict(_1=BIG)), {}),
+    ("gdn_rotary", dict(positions=dict(_0=BIG)), {}),
+    ("gdn_paged_append", dict(k=dict(_0=BIG), v=dict(_0=BIG), q=dict(_0=BIG), q_out=dict(_0=BIG), positions=dict(_1=BIG)), {}),
+    ("gdn_paged_append", dict(q=dict(_1=BIG), q_out=dict(_1=BIG)), {}),
+    ("gdn_paged_append", dict(k_pages=dict(_0=BIG), v_pages=dict(_0=BIG)), {}),
+    ("gdn_paged_append", dict(k_pages=dict(_1=BIG), v_pages=dict(_1=BIG)), {}),
+    ("gdn_paged_append", dict(page_table=dict(_1=BIG)), {}),
+    ("gdn_paged_append", dict(positions=dict(_0=BIG)), {}),
+    ("gdn_paged_attention", dict(q=dict(_0=BIG), out=dict(_0=BIG), lse=dict(_0=BIG)), {}),
+    ("gdn_paged_attention", dict(q=dict(_1=BIG), out=dict(_1=BIG), lse=dict(_1=BIG)), {}),
+    ("gdn_paged_attention", dict(k_pages=dict(_0=BIG), v_pages=dict(_0=BIG)), {}),
+    ("gdn_paged_attention", dict(page_table=dict(_1=BIG)), {}),
+    ("gdn_paged_attention", {}, dict(window=BIG)),
+    ("gdn_paged_attention", {}, dict(window=2**31)),
+])
+def test_sizes_that_a_c_int_does_not_hold(calls, name, change, kw):
+    """They are refused, not cut to their lower 32 bits."""
+    tensors, rest = CALLS[name]
+    args = {n: Long(t, **change[n]) if n in change else On(t) for n, t in tensors.items()}
+    with pytest.raises(ValueError, match="2\\^31"):
+        getattr(gdn, name)(**args, **rest, **kw)
+    assert not calls
