@@ -65,7 +65,14 @@ struct Layout {
     static constexpr uint32_t oMerge = oV + NV * kTile;    // [128] maxima and sums of slot 1 (kOne)
     static constexpr uint32_t oWork = oMerge + 1024;       // [kUnits] Work
     static constexpr uint32_t oBar = oWork + kUnits * 96;
-    static constexpr uint32_t kSmem = oBar + 384 + 1024;   // + alignment slack
+    // Barriers, each kind behind the one before; then the address that TMEM's allocation writes
+    static constexpr int bKFull = 0, bKEmpty = bKFull + NK, bVFull = bKEmpty + NK, bVEmpty = bVFull + NV;
+    static constexpr int bUFull = bVEmpty + NV, bUEmpty = bUFull + kUnits, bQFull = bUEmpty + kUnits;
+    static constexpr int bQFree = bQFull + 2, bSFull = bQFree + 2, bPReady = bSFull + 2, bODone = bPReady + 2;
+    static constexpr int bOther = bODone + 2, bMerged = bOther + 1, bDrain = bMerged + 1, kBars = bDrain + 1;
+    static constexpr uint32_t oTmem = oBar + 8 * kBars;
+    static constexpr uint32_t kSmem = oTmem + 16 + 1024;   // + alignment slack
+    static_assert(kSmem <= 227 * 1024, "a CTA has no more shared memory");
 };
 
 struct TcParams : AttentionParams {
@@ -172,13 +179,13 @@ attention_kernel(const TcParams p, const __grid_constant__ CUtensorMap mq, const
     constexpr int NK = L::NK, NV = L::NV;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_align1k(smem_raw);
-    uint64_t *k_full = reinterpret_cast<uint64_t *>(sm + L::oBar), *k_empty = k_full + NK;
-    uint64_t *v_full = k_empty + NK, *v_empty = v_full + NV;
-    uint64_t *u_full = v_empty + NV, *u_empty = u_full + kUnits;
-    uint64_t *q_full = u_empty + kUnits, *q_free = q_full + 2;  // (kPair: the first of each)
-    uint64_t *s_full = q_free + 2, *p_ready = s_full + 2, *o_done = p_ready + 2;  // of a slot each
-    uint64_t *other = o_done + 2, *merged = other + 1, *drain = other + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(other + 3);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::oBar);
+    uint64_t *k_full = bars + L::bKFull, *k_empty = bars + L::bKEmpty, *v_full = bars + L::bVFull;
+    uint64_t *v_empty = bars + L::bVEmpty, *u_full = bars + L::bUFull, *u_empty = bars + L::bUEmpty;
+    uint64_t *q_full = bars + L::bQFull, *q_free = bars + L::bQFree;  // (kPair: the first of each)
+    uint64_t *s_full = bars + L::bSFull, *p_ready = bars + L::bPReady, *o_done = bars + L::bODone;  // of a slot each
+    uint64_t *other = bars + L::bOther, *merged = bars + L::bMerged, *drain = bars + L::bDrain;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::oTmem);
     Work *works = reinterpret_cast<Work *>(sm + L::oWork);
     const bool gather = p.box < 8;  // pages that TMA boxes do not fit
     const int warp = __shfl_sync(kAll, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
