@@ -401,7 +401,8 @@ __global__ void __launch_bounds__(256) join_kernel(const AttentionParams p, cons
     }
 }
 
-// Launched behind an attention kernel, while it still runs.
+// Launched behind an attention kernel, while it still runs, which hides the launch.  (Its CTAs
+// start where that one's have left: a CTA of the tensor-core kernel has all registers.)
 cudaError_t launch_join(const AttentionParams &p, const Plan &s, cudaStream_t stream);
 
 // Units of up to `rows` query rows.

@@ -1,21 +1,23 @@
 // gdn_attention_simt.cu -- attention over a paged cache on the CUDA cores: fp32, and 16-bit
-// tensors whose strides or page size the tensor-core kernel does not take.  Also the join of
-// both kernels' cut units and the choice between them.
+// tensors whose addresses or strides are no multiples of 16 bytes.  Also the join of both
+// kernels' cut units and the choice between them.
 //
 // Per query row, over tiles of keys, with running maximum m and sum l (both of scores times
 // scale log2 e, so that weights are powers of two):
 //     x_j = scale log2 e q.k_j,  m' = max(m, max_j x_j),  w_j = 2^{x_j - m'}
 //     l <- 2^{m - m'} l + sum_j w_j,   o <- 2^{m - m'} o + sum_j w_j v_j
 // and o / l at the end; all in fp32.  A key that a query does not see gets no weight and its
-// values are not added, whatever they hold.  A row without keys gives 0 and a log of -inf.
+// values are not added, whatever they hold.  A row without keys gives 0 and a log of -inf; a
+// score that is NaN makes its row NaN.
 //
-// Two kernels.  Of up to 8 query rows (single tokens, a few drafts), bound by HBM: a warp
-// streams keys and values through registers, four features a lane, and has all rows' queries
-// and sums in registers too.  Single tokens of 64 rows over 2000 keys, 4 of 16 heads, d = 128,
-// fp32: 106 us, 4.9 TB/s.  Of up to 64: a CTA holds them, a tile of keys and one of values
-// in shared memory, bound by the FMA units and the shared memory that feeds them; a thread has
-// four rows of a few keys, then of a few output features.  4 x 1000 tokens over 2000 keys each,
-// the same heads: 1.69 ms, 39 TFLOP/s.
+// Two kernels.  Of up to 8 query rows (single tokens, a few drafts): a warp streams keys and
+// values through registers, four features a lane, and has all rows' queries and sums in
+// registers too.  Of up to 4 rows bound by HBM, single tokens of 64 rows over 2000 keys, 4 of
+// 16 heads, d = 128, fp32: 105 us, 5.0 TB/s; of 8 by the sums over the lanes, 159 us for the
+// same bytes.  Of up to 64: a CTA holds them, a tile of keys and one of values in shared
+// memory, bound by the shared memory that feeds the FMA units (six 16-byte loads for 32 FMAs);
+// a thread has four rows of a few keys, then of a few output features.  4 x 1000 tokens over
+// 2000 keys each, the same heads: 1.69 ms, 39 TFLOP/s.
 #include <algorithm>
 
 #include "gdn_attention.cuh"
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 2) stream_kernel(const AttentionPara
                 x[j] = key < k1 && key >= lo && key < hi ? v[0] : kNone;
             }
             // (the maximum that weights are relative to follows the true one when that has grown
-            // by more than 8 in the exponent)
+            // by more than 8 in the exponent, as in the tensor-core kernel)
             float now = m;
 #pragma unroll
             for (int j = 0; j < U; ++j) now = fmaxf(now, x[j]);

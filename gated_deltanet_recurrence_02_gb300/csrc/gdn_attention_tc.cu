@@ -6,7 +6,9 @@
 //     l <- 2^{c (m - m')} l + sum_j P_j,   O <- 2^{c (m - m')} O + P V
 // and O / l at the end.  S and O are fp32 in TMEM, a query row to a lane, so a thread has a
 // whole row of a tile: no reduction crosses threads.  m follows the true maximum only when
-// that has grown by more than 8 in the exponent: weights of up to 2^8 are as exact, and most
+// that has grown by more than 8 in the exponent (running maximum and sum: M. Milakov and
+// N. Gimelshein, "Online normalizer calculation for softmax" (2018); that the maximum may lag
+// is known from published attention kernels): weights of up to 2^8 are as exact, and most
 // tiles then leave O where it is.
 //
 // Roundings: P to the inputs' type for the tensor cores, the result once; l sums the weights
@@ -16,13 +18,15 @@
 // Roles.  Two warpgroups for the softmax, one for each of two slots (S, P in its place, and O
 // in TMEM); of the other warps one walks through the CTA's units and fetches their queries,
 // one fetches tiles of keys and one of values (TMA; two each by 16-byte copies for pages that
-// are no multiple of 8 slots: 4 x 1000 tokens over 2000 keys, d = 64, take 84 us with pages of
-// 20 slots and 57 with 16), one issues all products, a slot's under the other's softmax.
+// are no multiple of 8 slots: 4 x 1000 tokens over 2000 keys, 8 of 32 heads, d = 64, take 84 us
+// with pages of 20 slots and 73 with 16; single tokens of 64 rows over 2000 keys, 4 of 16 heads,
+// d = 128, 74 and 53), one issues all products, a slot's under the other's softmax.
 //
 // Bounds, and what the kernel comes to on the device.  Single tokens: the bytes of the cache,
-// 32 rows over 8192 keys, 8 of 32 heads, 164 us at d = 128 (6.5 TB/s), 99 at d = 64 (5.4).
-// Long chunks at d = 128: the tensor cores, 4100 tokens over 32100 keys, 32 heads, 1.18 ms,
-// 1.70 PFLOP/s.  At d = 64 the chain of a tile, S, maximum, exponentials, P, O, some 2400
+// 32 rows over 8192 keys, 8 of 32 heads, 165 us at d = 128 (6.5 TB/s), 99 at d = 64 (5.4; up to
+// 120 on a card that has just run long chunks), 74 at d = 32 (3.6).
+// Long chunks at d = 128: the tensor cores, 4100 tokens over 32100 keys, 32 heads, 1.17 ms,
+// 1.73 PFLOP/s.  At d = 64 the chain of a tile, S, maximum, exponentials, P, O, some 2400
 // cycles for two slots' tiles where the tensor cores and the exponentials need 1050 each.
 // Short calls: 4 to 5 us until the first tile has arrived and 4 to 6 for the join.  Two warps for
 // the halves of a row (16 for the softmax), which swap their maxima, took a third longer at

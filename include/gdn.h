@@ -468,7 +468,8 @@ GDN_API int gdn_accept_drafts(const void *target_probs, const void *draft_probs,
  *              read.  One outside [0, num_pages) sets GDN_DEVERR_BAD_INDEX.
  *  kv_lens     int32 [B], device: keys of the row, its new tokens included.  The row's
  *              T_b new tokens are at positions kv_lens[b] - T_b ... kv_lens[b] - 1.
- *              (Negative lengths count as 0; keys past max_pages * page_size do not exist.)
+ *              (Negative lengths count as 0; keys past max_pages * page_size do not exist,
+ *              and attention takes none past 2^31 - 256.)
  * Rows are uniform or packed as above (cu_seqlens); tokens that no row owns are left
  * alone.  dtype is one of GDN_F32, GDN_F16, GDN_BF16 for everything that is not int32.
  */
@@ -527,11 +528,12 @@ GDN_API int gdn_paged_append(const void *q, const void *k, const void *v, void *
  * p = kv_lens[b] - T_b + t, with key head h / (Hq / Hk):
  *     w_j = e^{scale q.k_j},  out = sum_j w_j v_j / sum_j w_j,  lse = log sum_j w_j
  * over the keys j <= p, with a window only j > p - window, and with GDN_ATTENTION_FULL
- * over all j < kv_lens[b].  A query without keys gives out 0 and lse -infinity.
+ * over all j < kv_lens[b].  A query without keys gives out 0 and lse -infinity, one with a
+ * score that is NaN gives NaN.
  * Precondition: a query's largest score (scale q.k) is below 2^20 in magnitude; others may
  * be as low as they like.
  *  q           [total_T, Hq, d], rows q_stride elements apart (>= Hq * d).
- *  out         [total_T, Hq, d], dense.       lse   fp32 [total_T, Hq] or NULL.
+ *  out         [total_T, Hq, d], dense, 16-byte aligned.   lse   fp32 [total_T, Hq] or NULL.
  *  window      0: none.  Not with GDN_ATTENTION_FULL.
  *  d           32, 64 or 128.       Hq % Hk = 0.       B <= 65535; total_T * Hq < 2^31.
  *  workspace   gdn_paged_attention_workspace_size() bytes for the same sizes and the
