@@ -169,3 +169,51 @@ CUDA_CORES = [  # of up to 4, 8 and 64 query rows a unit
 def test_the_cuda_cores(gdn, case, d, dtype, slack):  # noqa: F811
     """Rows of queries that begin on a boundary of 8 (fp32: 16) bytes and no wider, and on none."""
     check(gdn, d=d, dtype=dtype, slack=slack, **case)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("page", [1000, 1001, 1024])
+@pytest.mark.parametrize("B,Hk,T", [(1, 1, 1), (1, 2, 40), (3, 2, 5), (3, 1, 300)])
+def test_rows_that_are_one_page_each(gdn, B, Hk, T, page, dtype):  # noqa: F811
+    """A cache without paging, [B, length, Hk, d]: as many pages as rows, one of them alone too."""
+    dt, d, Hq = DT[dtype], 64, 4 * Hk
+    k, v = (torch.randn(B, page, Hk, d, device="cuda").to(dt) for _ in range(2))
+    q = torch.randn(B * T, Hq, d, device="cuda").to(dt)
+    lens = [page, 700, 333][:B]
+    table = int32([[b] for b in range(B)])
+    out, _ = gdn.gdn_paged_attention(q, k, v, table, int32(lens), B=B)
+    for b, n in enumerate(lens):
+        r = slice(b * T, b * T + T)
+        o, _, bound, _ = attend(q[r], k[b, :n], v[b, :n], n - T, d ** -0.5)
+        near(out[r], o, bound)
+    # and appended to in place: a row's last T positions
+    new = [torch.randn(B * T, Hk, d, device="cuda").to(dt) for _ in range(2)]
+    want = [x.clone() for x in (k, v)]
+    for x, y in zip(want, new):
+        for b, n in enumerate(lens):
+            x[b, n - T:n] = y[b * T:b * T + T]
+    gdn.gdn_paged_append(*new, k, v, table, int32(lens), B=B)
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1]) and gdn.gdn_device_errors() == 0
+
+
+def test_two_graphs_replayed_at_once(gdn):  # noqa: F811
+    """Each captured with a workspace of its own, replayed on two streams at the same time."""
+    Hq, Hk, d = 8, 2, 128
+    calls, graphs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for i, (n, T) in enumerate(((3000, 1), (1500, 200))):
+        cache = Cache([n], Hk, d, 16, torch.bfloat16, seed=i)
+        q = torch.randn(T, Hq, d, device="cuda").to(torch.bfloat16)
+        args = (q, cache.k, cache.v, cache.table, int32([n]))
+        calls.append((args, gdn.gdn_paged_attention(*args, B=1)[0]))
+    for args, _ in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = [gdn.gdn_paged_attention(*args, B=1)[0] for _ in range(10)]
+        graphs.append((graph, outs))
+    for _ in range(10):
+        for s, (graph, _) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for (_, want), (_, outs) in zip(calls, graphs):
+            assert all(torch.equal(x, want) for x in outs)
